@@ -9,6 +9,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <string>
 
 #include "moe.h"
@@ -303,6 +304,63 @@ int dispatch_launch(const char* fn, int T, int H, int E, int k, int dtype, const
   return hip_status(timed(MOE_K_DISPATCH_ROWS, s,
                           [&] { return moe::launch_dispatch_rows(T, H, k, esize_of(dtype), x, inv_perm, x_sorted, s); }),
                     fn);
+}
+
+int check_aligned(const char* fn, const char* name, const void* p) {
+  REQUIRE(((uintptr_t)p & 15) == 0, MOE_ERR_INVALID_ARGUMENT, "%s: %s must be 16-byte aligned", fn, name);
+  return MOE_OK;
+}
+
+// A buffer of a call: NULL ones overlap nothing.
+struct Span {
+  const char* name;
+  const void* p;
+  int64_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  if (a.p == nullptr || b.p == nullptr) return false;
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  return x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+}
+
+// Output `out` shares no memory with `others`, but may be one of them exactly
+// where `in_place` (each of its elements is then read before it is written).
+int check_output(const char* fn, const Span& out, std::initializer_list<Span> others, bool in_place) {
+  for (const Span& o : others)
+    REQUIRE(!overlap(out, o) || (in_place && out.p == o.p && out.bytes == o.bytes), MOE_ERR_INVALID_ARGUMENT,
+            "%s: %s overlaps %s", fn, out.name, o.name);
+  return MOE_OK;
+}
+
+int check_workspace(const char* fn, size_t need, const void* ws, size_t ws_bytes) {
+  REQUIRE(ws_bytes >= need, MOE_ERR_WORKSPACE_TOO_SMALL, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need);
+  REQUIRE(need == 0 || ws != nullptr, MOE_ERR_INVALID_ARGUMENT, "%s: workspace must not be NULL", fn);
+  return check_aligned(fn, "workspace", ws);
+}
+
+int check_score(const char* fn, int score, float scale) {
+  REQUIRE(score == MOE_SCORE_SOFTMAX || score == MOE_SCORE_SIGMOID, MOE_ERR_INVALID_ARGUMENT,
+          "%s: score %d is neither MOE_SCORE_SOFTMAX nor MOE_SCORE_SIGMOID", fn, score);
+  REQUIRE(std::isfinite(scale), MOE_ERR_INVALID_ARGUMENT, "%s: scale must be finite", fn);
+  return MOE_OK;
+}
+
+int check_norm(const char* fn, int T, int H, int dtype) {
+  REQUIRE(T >= 1, MOE_ERR_INVALID_ARGUMENT, "%s: T=%d must be >= 1", fn, T);
+  int rc = check_dtype(fn, dtype);
+  if (rc || (rc = check_row_width(fn, "H", H))) return rc;
+  REQUIRE(H <= moe::kLayerNormMaxWidth, MOE_ERR_UNSUPPORTED, "%s: H=%d exceeds %d", fn, H, moe::kLayerNormMaxWidth);
+  return MOE_OK;
+}
+
+int check_linear(const char* fn, int T, int I, int O, int dtype, int act) {
+  REQUIRE(T >= 1, MOE_ERR_INVALID_ARGUMENT, "%s: T=%d must be >= 1", fn, T);
+  int rc = check_dtype(fn, dtype);
+  if (rc || (rc = check_row_width(fn, "I", I)) || (rc = check_row_width(fn, "O", O))) return rc;
+  REQUIRE(I <= moe::kLinearMaxWidth && O <= moe::kLinearMaxWidth, MOE_ERR_UNSUPPORTED, "%s: I=%d or O=%d exceeds %d",
+          fn, I, O, moe::kLinearMaxWidth);
+  REQUIRE(act >= MOE_ACT_NONE && act <= MOE_ACT_SILU, MOE_ERR_INVALID_ARGUMENT, "%s: unknown activation %d", fn, act);
+  return MOE_OK;
 }
 
 }  // namespace
@@ -782,6 +840,223 @@ int moe_compact_pairs_cap(int T, int H, int F, int E, int k, int dtype, int cap,
   const int es = esize_of(dtype);
   return hip_status(moe::launch_gather_rows(kept_offsets + E, kept_src, (int)bound64, x_sorted, x_kept, H * es, a_save,
                                             a_kept, F * es, h_save, h_kept, 2 * F * es, s),
+                    fn);
+}
+
+int moe_route_scored(int T, int E, int k, int score, int n_groups, int top_groups, int group_top, int renormalize,
+                     float scale, const float* logits, const float* bias, int32_t* topk_idx, float* topk_w,
+                     void* stream) {
+  const char* fn = "moe_route_scored";
+  int rc = check_routing_dims(fn, T, E, k);
+  if (rc || (rc = check_score(fn, score, scale))) return rc;
+  REQUIRE(n_groups >= 1 && E % n_groups == 0, MOE_ERR_INVALID_ARGUMENT, "%s: n_groups=%d does not divide E=%d", fn,
+          n_groups, E);
+  REQUIRE(n_groups <= 16, MOE_ERR_UNSUPPORTED, "%s: n_groups=%d exceeds 16", fn, n_groups);
+  REQUIRE(top_groups >= 1 && top_groups <= n_groups, MOE_ERR_INVALID_ARGUMENT, "%s: top_groups=%d is not in 1..%d", fn,
+          top_groups, n_groups);
+  const int size = E / n_groups;
+  REQUIRE((group_top == 1 || group_top == 2) && group_top <= size, MOE_ERR_INVALID_ARGUMENT,
+          "%s: group_top=%d must be 1 or 2, at most the group size %d", fn, group_top, size);
+  REQUIRE(k <= top_groups * size, MOE_ERR_INVALID_ARGUMENT, "%s: k=%d exceeds the %d experts of %d groups", fn, k,
+          top_groups * size, top_groups);
+  NONNULL(logits);
+  NONNULL(topk_idx);
+  NONNULL(topk_w);
+  hipStream_t s = as_stream(stream);
+  return hip_status(timed(MOE_K_ROUTE_SCORED, s,
+                          [&] {
+                            return moe::launch_route_scored(T, E, k, score, n_groups, top_groups, group_top,
+                                                            renormalize != 0, scale, logits, bias, topk_idx, topk_w, s);
+                          }),
+                    fn);
+}
+
+int moe_route_scored_bwd(int T, int E, int k, int score, int renormalize, float scale, const float* logits,
+                         const int32_t* topk_idx, const float* dg, float* dlogits, void* stream) {
+  const char* fn = "moe_route_scored_bwd";
+  int rc = check_routing_dims(fn, T, E, k);
+  if (rc || (rc = check_score(fn, score, scale))) return rc;
+  NONNULL(logits);
+  NONNULL(topk_idx);
+  NONNULL(dg);
+  NONNULL(dlogits);
+  const int64_t row = (int64_t)T * E * 4, sel = (int64_t)T * k * 4;
+  if ((rc = check_output(fn, {"dlogits", dlogits, row},
+                         {{"logits", logits, row}, {"topk_idx", topk_idx, sel}, {"dg", dg, sel}}, false)))
+    return rc;
+  hipStream_t s = as_stream(stream);
+  return hip_status(timed(MOE_K_ROUTE_SCORED, s,
+                          [&] {
+                            return moe::launch_route_scored_bwd(T, E, k, score, renormalize != 0, scale, logits,
+                                                                topk_idx, dg, dlogits, s);
+                          }),
+                    fn);
+}
+
+int moe_router_bwd_dlogits(int T, int H, int E, int dtype, const void* x, const void* w_r, const float* dlogits,
+                           void* dw_r, void* dx, int dx_accumulate, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  const char* fn = "moe_router_bwd_dlogits";
+  int rc = check_routing_dims(fn, T, E, 1);
+  if (rc || (rc = check_dtype(fn, dtype)) || (rc = check_row_width(fn, "H", H))) return rc;
+  REQUIRE((int64_t)T * H < ((int64_t)1 << 40), MOE_ERR_UNSUPPORTED, "%s: x too large", fn);
+  NONNULL(x);
+  NONNULL(w_r);
+  NONNULL(dlogits);
+  NONNULL(dw_r);
+  NONNULL(dx);
+  if ((rc = check_router_workspace(fn, T, H, E, workspace, workspace_bytes))) return rc;
+  hipStream_t s = as_stream(stream);
+  return hip_status(timed(MOE_K_ROUTER_DW, s,
+                          [&] {
+                            return moe::launch_router_bwd_dlogits(T, H, E, esize_of(dtype), x, w_r, dlogits, dw_r, dx,
+                                                                  dx_accumulate != 0, workspace, s);
+                          }),
+                    fn);
+}
+
+int moe_layernorm_fwd(int T, int H, int dtype, float eps, const void* x, const void* gamma, const void* beta, void* y,
+                      float* mean, float* rstd, void* stream) {
+  const char* fn = "moe_layernorm_fwd";
+  int rc = check_norm(fn, T, H, dtype);
+  if (rc) return rc;
+  REQUIRE(eps >= 0.0f && std::isfinite(eps), MOE_ERR_INVALID_ARGUMENT, "%s: eps must be finite and not negative", fn);
+  NONNULL(x);
+  NONNULL(gamma);
+  NONNULL(y);
+  REQUIRE((mean == nullptr) == (rstd == nullptr), MOE_ERR_INVALID_ARGUMENT,
+          "%s: mean and rstd must both be given or both be NULL", fn);
+  const int es = esize_of(dtype);
+  const int64_t row = (int64_t)T * H * es, col = (int64_t)H * es;
+  if ((rc = check_aligned(fn, "x", x)) || (rc = check_aligned(fn, "gamma", gamma)) ||
+      (rc = check_aligned(fn, "beta", beta)) || (rc = check_aligned(fn, "y", y)) ||
+      (rc = check_output(fn, {"y", y, row}, {{"x", x, row}}, true)) ||
+      (rc = check_output(fn, {"y", y, row},
+                         {{"gamma", gamma, col}, {"beta", beta, col}, {"mean", mean, 4ll * T}, {"rstd", rstd, 4ll * T}}, false)))
+    return rc;
+  hipStream_t s = as_stream(stream);
+  return hip_status(
+      timed(MOE_K_LAYERNORM, s, [&] { return moe::launch_layernorm_fwd(T, H, es, eps, x, gamma, beta, y, mean, rstd, s); }),
+      fn);
+}
+
+size_t moe_layernorm_workspace_bytes(int T, int H) {
+  if (T < 1 || H < 1 || H > moe::kLayerNormMaxWidth) return 0;
+  return moe::layernorm_workspace_bytes(T, H);
+}
+
+int moe_layernorm_bwd(int T, int H, int dtype, const void* x, const void* gamma, const float* mean, const float* rstd,
+                      const void* dy, const void* dx_add, void* dx, void* dgamma, void* dbeta, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_layernorm_bwd";
+  int rc = check_norm(fn, T, H, dtype);
+  if (rc) return rc;
+  NONNULL(x);
+  NONNULL(gamma);
+  NONNULL(mean);
+  NONNULL(rstd);
+  NONNULL(dy);
+  NONNULL(dx);
+  NONNULL(dgamma);
+  const int es = esize_of(dtype);
+  const int64_t row = (int64_t)T * H * es, col = (int64_t)H * es;
+  const Span sx{"x", x, row}, sgamma{"gamma", gamma, col}, sdy{"dy", dy, row}, sadd{"dx_add", dx_add, row};
+  const Span sdx{"dx", dx, row}, sdg{"dgamma", dgamma, col}, sdb{"dbeta", dbeta, col};
+  const Span smean{"mean", mean, 4ll * T}, srstd{"rstd", rstd, 4ll * T};
+  if ((rc = check_aligned(fn, "x", x)) || (rc = check_aligned(fn, "gamma", gamma)) ||
+      (rc = check_aligned(fn, "dy", dy)) || (rc = check_aligned(fn, "dx_add", dx_add)) ||
+      (rc = check_aligned(fn, "dx", dx)) || (rc = check_output(fn, sdx, {sx, sdy, sadd}, true)) ||
+      (rc = check_output(fn, sdx, {sgamma, smean, srstd, sdg, sdb}, false)) ||
+      (rc = check_output(fn, sdg, {sx, sgamma, sdy, sadd, sdb}, false)) ||
+      (rc = check_output(fn, sdb, {sx, sgamma, sdy, sadd}, false)) ||
+      (rc = check_workspace(fn, moe::layernorm_workspace_bytes(T, H), workspace, workspace_bytes)))
+    return rc;
+  hipStream_t s = as_stream(stream);
+  return hip_status(timed(MOE_K_LAYERNORM, s,
+                          [&] {
+                            return moe::launch_layernorm_bwd(T, H, es, x, gamma, mean, rstd, dy, dx_add, dx, dgamma,
+                                                             dbeta, workspace, s);
+                          }),
+                    fn);
+}
+
+size_t moe_linear_workspace_bytes(int T, int I, int O, int dtype) {
+  if (T < 1 || I < 1 || O < 1 || I > moe::kLinearMaxWidth || O > moe::kLinearMaxWidth || esize_of(dtype) == 0) return 0;
+  return moe::linear_workspace_bytes(T, I, O, esize_of(dtype));
+}
+
+int moe_linear_fwd(int T, int I, int O, int dtype, int act, const void* x, const void* w, const void* bias,
+                   const void* mul, const void* residual, void* z_save, void* y, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_linear_fwd";
+  int rc = check_linear(fn, T, I, O, dtype, act);
+  if (rc) return rc;
+  NONNULL(x);
+  NONNULL(w);
+  NONNULL(y);
+  const int es = esize_of(dtype);
+  const int64_t in = (int64_t)T * I * es, out = (int64_t)T * O * es;
+  const Span sx{"x", x, in}, sw{"w", w, (int64_t)I * O * es}, sb{"bias", bias, (int64_t)O * es};
+  const Span sm{"mul", mul, out}, sr{"residual", residual, out}, sz{"z_save", z_save, out}, sy{"y", y, out};
+  if ((rc = check_aligned(fn, "x", x)) || (rc = check_aligned(fn, "w", w)) || (rc = check_aligned(fn, "bias", bias)) ||
+      (rc = check_aligned(fn, "mul", mul)) || (rc = check_aligned(fn, "residual", residual)) ||
+      (rc = check_aligned(fn, "z_save", z_save)) || (rc = check_aligned(fn, "y", y)) ||
+      (rc = check_output(fn, sy, {sm, sr}, true)) || (rc = check_output(fn, sy, {sx, sw, sb, sz}, false)) ||
+      (rc = check_output(fn, sz, {sx, sw, sb, sm, sr}, false)) ||
+      (rc = check_workspace(fn, moe::linear_workspace_bytes(T, I, O, es), workspace, workspace_bytes)))
+    return rc;
+  const moe::LinearArgs g{T, I, O, act, x, w};
+  hipStream_t s = as_stream(stream);
+  return hip_status(
+      timed(MOE_K_LINEAR_FWD, s,
+            [&] { return moe::launch_linear_fwd(g, es, bias, mul, residual, z_save, y, workspace, s); }),
+      fn);
+}
+
+int moe_linear_bwd(int T, int I, int O, int dtype, int act, const void* x, const void* w, const void* z,
+                   const void* mul, const void* dy, void* dz, const void* dx_add, void* dx, void* dw, void* dbias,
+                   void* dmul, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_linear_bwd";
+  int rc = check_linear(fn, T, I, O, dtype, act);
+  if (rc) return rc;
+  const bool plain = act == MOE_ACT_NONE && mul == nullptr;  // dz = dy
+  NONNULL(dy);
+  if (dx != nullptr) NONNULL(w);
+  if (dw != nullptr) NONNULL(x);
+  if (!plain) {
+    NONNULL(z);
+    NONNULL(dz);
+  } else {
+    z = dz = nullptr;
+  }
+  REQUIRE((mul == nullptr) == (dmul == nullptr), MOE_ERR_INVALID_ARGUMENT,
+          "%s: mul and dmul must both be given or both be NULL", fn);
+  REQUIRE(dx != nullptr || dx_add == nullptr, MOE_ERR_INVALID_ARGUMENT, "%s: dx_add without dx", fn);
+  REQUIRE(dx != nullptr || dw != nullptr || dbias != nullptr || dmul != nullptr, MOE_ERR_INVALID_ARGUMENT,
+          "%s: no gradient is wanted", fn);
+  const int es = esize_of(dtype);
+  const int64_t in = (int64_t)T * I * es, out = (int64_t)T * O * es, wide = (int64_t)I * O * es;
+  const Span sx{"x", dw != nullptr ? x : nullptr, in}, sw{"w", dx != nullptr ? w : nullptr, wide}, sz{"z", z, out};
+  const Span sm{"mul", mul, out}, sdy{"dy", dy, out}, sdz{"dz", dz, out}, sadd{"dx_add", dx_add, in};
+  const Span sdx{"dx", dx, in}, sdw{"dw", dw, wide}, sdb{"dbias", dbias, (int64_t)O * es}, sdm{"dmul", dmul, out};
+  for (const Span& b : {sx, sw, sz, sm, sdy, sdz, sadd, sdx, sdw, sdb, sdm})
+    if ((rc = check_aligned(fn, b.name, b.p))) return rc;
+  if ((rc = check_output(fn, sdz, {sdy, sz, sm}, true)) || (rc = check_output(fn, sdz, {sx, sw, sadd}, false)) ||
+      (rc = check_output(fn, sdm, {sdy, sz, sm}, true)) ||
+      (rc = check_output(fn, sdm, {sx, sw, sdz, sadd}, false)) ||
+      (rc = check_output(fn, sdx, {sadd}, true)) ||
+      (rc = check_output(fn, sdx, {sx, sw, sz, sm, sdy, sdz, sdw, sdb, sdm}, false)) ||
+      (rc = check_output(fn, sdw, {sx, sw, sz, sm, sdy, sdz, sadd, sdb, sdm}, false)) ||
+      (rc = check_output(fn, sdb, {sx, sw, sz, sm, sdy, sdz, sadd, sdm}, false)) ||
+      (rc = check_workspace(fn, moe::linear_workspace_bytes(T, I, O, es), workspace, workspace_bytes)))
+    return rc;
+  const moe::LinearArgs g{T, I, O, act, x, w};
+  hipStream_t s = as_stream(stream);
+  return hip_status(timed(MOE_K_LINEAR_BWD, s,
+                          [&] {
+                            return moe::launch_linear_bwd(g, es, z, mul, dy, dz, dx_add, dx, dw, dbias, dmul,
+                                                          workspace, s);
+                          }),
                     fn);
 }
 

@@ -210,6 +210,40 @@ hipError_t launch_router_bwd(int T, int H, int E, int k, int esize, const void* 
                              const int32_t* idx, const float* w, const float* dg, float* dlogits, void* dw_r,
                              void* dx, bool dx_accumulate, void* ws, hipStream_t stream);
 
+// The two products of the router's backward for a given dlogits.
+hipError_t launch_router_bwd_dlogits(int T, int H, int E, int esize, const void* x, const void* w_r,
+                                     const float* dlogits, void* dw_r, void* dx, bool dx_accumulate, void* ws,
+                                     hipStream_t stream);
+
+hipError_t launch_route_scored(int T, int E, int k, int score, int n_groups, int top_groups, int group_top,
+                               bool renormalize, float scale, const float* logits, const float* bias, int32_t* idx,
+                               float* w, hipStream_t stream);
+hipError_t launch_route_scored_bwd(int T, int E, int k, int score, bool renormalize, float scale, const float* logits,
+                                   const int32_t* idx, const float* dg, float* dlogits, hipStream_t stream);
+
+constexpr int kLayerNormMaxWidth = 16384;  // a row is held in registers
+size_t layernorm_workspace_bytes(int T, int H);
+hipError_t launch_layernorm_fwd(int T, int H, int esize, float eps, const void* x, const void* gamma, const void* beta,
+                                void* y, float* mean, float* rstd, hipStream_t stream);
+hipError_t launch_layernorm_bwd(int T, int H, int esize, const void* x, const void* gamma, const float* mean,
+                                const float* rstd, const void* dy, const void* dx_add, void* dx, void* dgamma,
+                                void* dbeta, void* ws, hipStream_t stream);
+
+constexpr int kLinearMaxWidth = 1 << 20;
+// Dense product of T rows, I inputs, O outputs: x [T, I], w [I, O].
+struct LinearArgs {
+  int T, I, O;
+  int act;
+  const void* x;
+  const void* w;
+};
+size_t linear_workspace_bytes(int T, int I, int O, int esize);
+hipError_t launch_linear_fwd(const LinearArgs& g, int esize, const void* bias, const void* mul, const void* residual,
+                             void* z, void* y, void* ws, hipStream_t stream);
+hipError_t launch_linear_bwd(const LinearArgs& g, int esize, const void* z, const void* mul, const void* dy, void* dz,
+                             const void* dx_add, void* dx, void* dw, void* dbias, void* dmul, void* ws,
+                             hipStream_t stream);
+
 hipError_t launch_fill_i32(int32_t* a, int64_t n, int32_t v, hipStream_t stream);
 hipError_t launch_compact(int64_t N, int E, int cap, const int32_t* counts, const int32_t* offsets, const int32_t* perm,
                           const float* score, int32_t* kept_counts, int32_t* kept_offsets, int32_t* kept_perm,

@@ -438,6 +438,18 @@ hipError_t gemm(int M, int N, int K, const void* a, int lda, const void* b, int 
   return hipGetLastError();
 }
 
+// dW_r and dx for a given dl = dlogits.
+template <typename T>
+hipError_t router_bwd_products(int T_, int H, int E, const void* x, const void* w_r, const float* dl, void* dw_r,
+                               void* dx, bool dx_acc, float* ws, hipStream_t stream) {
+  // dW_r [H,E] = x^T dl: A(h,t) = x[t*H + h], B(t,e) = dl[t*E + e]; reduction over T
+  hipError_t err = gemm<T, float, T, false, false, false>(H, E, T_, x, H, dl, E, dw_r, ws, true, stream);
+  if (err != hipSuccess) return err;
+  // dx [T,H] (+)= dl W_r^T: A(t,e) = dl[t*E + e], B(e,h) = w_r[h*E + e]; reduction over E only
+  if (dx_acc) return gemm<float, T, T, true, true, true>(T_, H, E, dl, E, w_r, E, dx, nullptr, false, stream);
+  return gemm<float, T, T, true, true, false>(T_, H, E, dl, E, w_r, E, dx, nullptr, false, stream);
+}
+
 template <typename T>
 hipError_t router_bwd_typed(int T_, int H, int E, int k, const void* x, const void* w_r, const int32_t* idx,
                             const float* w, const float* dg, float* dl, void* dw_r, void* dx, bool dx_acc,
@@ -445,12 +457,7 @@ hipError_t router_bwd_typed(int T_, int H, int E, int k, const void* x, const vo
   MOE_LAUNCH(router_dlogits_kernel, dim3((T_ + 3) / 4), dim3(256), 0, stream, T_, E, k, idx, w, dg, dl);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  // dW_r [H,E] = x^T dl: A(h,t) = x[t*H + h], B(t,e) = dl[t*E + e]; reduction over T
-  err = gemm<T, float, T, false, false, false>(H, E, T_, x, H, dl, E, dw_r, ws, true, stream);
-  if (err != hipSuccess) return err;
-  // dx [T,H] (+)= dl W_r^T: A(t,e) = dl[t*E + e], B(e,h) = w_r[h*E + e]; reduction over E only
-  if (dx_acc) return gemm<float, T, T, true, true, true>(T_, H, E, dl, E, w_r, E, dx, nullptr, false, stream);
-  return gemm<float, T, T, true, true, false>(T_, H, E, dl, E, w_r, E, dx, nullptr, false, stream);
+  return router_bwd_products<T>(T_, H, E, x, w_r, dl, dw_r, dx, dx_acc, ws, stream);
 }
 
 }  // namespace
@@ -475,6 +482,14 @@ hipError_t launch_router_bwd(int T, int H, int E, int k, int esize, const void* 
                                    stream);
   return router_bwd_typed<uint16_t>(T, H, E, k, x, w_r, idx, w, dg, dlogits, dw_r, dx, dx_accumulate, (float*)ws,
                                     stream);
+}
+
+hipError_t launch_router_bwd_dlogits(int T, int H, int E, int esize, const void* x, const void* w_r,
+                                     const float* dlogits, void* dw_r, void* dx, bool dx_accumulate, void* ws,
+                                     hipStream_t stream) {
+  if (esize == 4)
+    return router_bwd_products<float>(T, H, E, x, w_r, dlogits, dw_r, dx, dx_accumulate, (float*)ws, stream);
+  return router_bwd_products<uint16_t>(T, H, E, x, w_r, dlogits, dw_r, dx, dx_accumulate, (float*)ws, stream);
 }
 
 }  // namespace moe

@@ -5,18 +5,33 @@ sized once from the host capacities) and ``forward`` / ``backward`` enqueue the
 library calls in order on one stream -- (router logits,) route, dispatch,
 grouped SwiGLU forward, combine; then optionally compaction, backward dx (+ dg),
 dW and the router's backward.  No step here computes anything itself: every
-value comes from libmoe's kernels.
+value comes from libmoe's kernels.  ``MoeBlockBuffers`` puts the layer into its
+block the same way: layer norm, router with scored routing, routed experts, and
+a gated shared expert whose last product adds the routed sum.
 """
 from __future__ import annotations
+
+import dataclasses
 
 import torch
 
 from . import moe
 
 
+@dataclasses.dataclass(frozen=True)
+class ScoredRouting:
+    """How moe_route_scored chooses and weighs (its arguments of these names)."""
+    score: int = moe.MOE_SCORE_SIGMOID
+    n_groups: int = 1
+    top_groups: int = 1
+    group_top: int = 1
+    renormalize: bool = True
+    scale: float = 1.0
+
+
 class MoeLayerBuffers:
     def __init__(self, T, H, F, E, k, dtype=torch.bfloat16, device="cuda", rho=None, dw=True, dg=True,
-                 router=False, keep_graph=True, quota_cap=None, gather_rows=None, overlap_dw=False):
+                 router=False, keep_graph=True, quota_cap=None, gather_rows=None, overlap_dw=False, routing=None):
         """rho: quota ratio of the compacted backward (None: no compaction);
         quota_cap: the per-expert quota directly (e.g. from
         moe.moe_quota_cap_for_budget), instead of rho.  keep_graph=False: the
@@ -33,7 +48,10 @@ class MoeLayerBuffers:
         weight gradients run on a second stream (default priority) alongside
         the dX GEMM and the dx sum, from the point where the dx call signals dO
         and dh complete (moe_signal_dh_ready); the caller's stream then waits
-        for them.  Results are the same bit for bit."""
+        for them.  Results are the same bit for bit.  routing: a ScoredRouting;
+        tokens are then routed by scores (moe_route_scored) instead of by the
+        softmax over the selected logits."""
+        self.routing = routing
         self.T, self.H, self.F, self.E, self.k = T, H, F, E, k
         self.keep_graph = keep_graph
         self.N = N = T * k
@@ -99,17 +117,23 @@ class MoeLayerBuffers:
             self.router_ws = em(max(moe.moe_router_workspace_bytes(T, H, E), 16), dt=torch.uint8)
 
     # ------------------------------------------------------------------ forward
-    def forward(self, logits, x, w_gate, w_up, w_down, stream=None, w_r=None, wq=None, wt=None):
+    def forward(self, logits, x, w_gate, w_up, w_down, stream=None, w_r=None, wq=None, wt=None, route_bias=None):
         """With w_r (a layer built with router=True) the logits are x W_r and
         the `logits` argument is ignored.  With wq (moe.Fp8Weights of the same
         frozen weights) the expert GEMMs read the fp8 copy.  With wt
         (moe.Fp8KMajorWeights) both expert GEMMs run on the fp8 matrix cores:
-        the token rows are quantized per row, then gathered on load."""
+        the token rows are quantized per row, then gathered on load.
+        route_bias: the selection bias [E] of a layer with `routing`."""
         self._x = x  # the backward reads token rows through the pair ids
         if w_r is not None:
             moe.moe_router_fwd(x, w_r, self.logits, self.router_ws, stream)
             logits = self.logits
-        moe.moe_route_topk(logits, self.topk_idx, self.topk_w, self.k, stream)
+        if self.routing is not None:
+            moe.moe_route_scored(logits, route_bias, self.topk_idx, self.topk_w, self.k,
+                                 **dataclasses.asdict(self.routing), stream=stream)
+        else:
+            assert route_bias is None, "a selection bias needs a layer with scored routing"
+            moe.moe_route_topk(logits, self.topk_idx, self.topk_w, self.k, stream)
         g = self.gather_rows or wt is not None  # index-only dispatch: the forward gathers x rows itself
         moe.moe_dispatch(self.topk_idx, None if g else x, self.counts, self.offsets, self.perm, self.inv_perm,
                          None if g else self.x_sorted, self.ws, self.E, stream)
@@ -205,7 +229,61 @@ class MoeLayerBuffers:
                                    self.dw_down, self.R, s_dw, x_src=x_src, x_div=k, a_src=a_src)
             if self.overlap_dw:
                 s_main.wait_stream(s_dw)
-        if w_r is not None:
+        if w_r is not None and self.routing is not None:
+            r = self.routing
+            moe.moe_route_scored_bwd(self.logits, self.topk_idx, self.dg, self.dlogits, r.score, r.renormalize, r.scale,
+                                     stream)
+            moe.moe_router_bwd_dlogits(self._x, w_r, self.dlogits, self.dw_r, self.dx, True, self.router_ws, stream)
+        elif w_r is not None:
             moe.moe_router_bwd(self._x, w_r, self.topk_idx, self.topk_w, self.dg, self.dlogits, self.dw_r, self.dx,
                                True, self.router_ws, stream)
+        return self.dx
+
+
+class MoeBlockBuffers:
+    """A MoE block over T tokens of width H, without its skip connection:
+
+        xn = layernorm(x),  y = experts(route(xn W_r), xn) + (silu(xn S_gate) * (xn S_up)) S_down
+
+    E routed experts of width F (top k, chosen by `routing`) and a shared gated
+    expert of width S.  forward / backward take the parameters as a dict:
+    gamma, beta (or None), w_r, w_gate, w_up, w_down, s_gate [H, S], s_up [H, S],
+    s_down [S, H], and route_bias [E] (optional); backward leaves the gradients
+    in `grads` under the same names (the selection bias has none)."""
+
+    def __init__(self, T, H, F, E, k, S, routing=ScoredRouting(), dtype=torch.bfloat16, device="cuda", eps=1e-5):
+        self.layer = L = MoeLayerBuffers(T, H, F, E, k, dtype, device, router=True, routing=routing)
+        self.eps = eps
+        em = lambda *s, dt=dtype: torch.empty(*s, dtype=dt, device=L.device)  # noqa: E731
+        self.xn, self.y, self.dx = em(T, H), em(T, H), em(T, H)
+        self.mean, self.rstd = em(T, dt=torch.float32), em(T, dt=torch.float32)
+        self.up, self.z_gate, self.hidden = em(T, S), em(T, S), em(T, S)
+        self.d_hidden, self.d_up, self.dz = em(T, S), em(T, S), em(T, S)
+        need = max(moe.moe_layernorm_workspace_bytes(T, H), moe.moe_linear_workspace_bytes(T, H, S, dtype),
+                   moe.moe_linear_workspace_bytes(T, S, H, dtype), 16)
+        self.ws = em(need, dt=torch.uint8)  # of one call at a time: they follow each other on one stream
+        self.grads = dict(gamma=em(H), beta=em(H), w_r=L.dw_r, w_gate=L.dw_gate, w_up=L.dw_up, w_down=L.dw_down,
+                          s_gate=em(H, S), s_up=em(H, S), s_down=em(S, H))
+
+    def forward(self, x, p, stream=None):
+        self._x = x
+        moe.moe_layernorm_fwd(x, p["gamma"], p.get("beta"), self.xn, self.mean, self.rstd, self.eps, stream)
+        routed = self.layer.forward(None, self.xn, p["w_gate"], p["w_up"], p["w_down"], stream, w_r=p["w_r"],
+                                    route_bias=p.get("route_bias"))
+        moe.moe_linear_fwd(self.xn, p["s_up"], None, self.up, workspace=self.ws, stream=stream)
+        moe.moe_linear_fwd(self.xn, p["s_gate"], None, self.hidden, act=moe.MOE_ACT_SILU, mul=self.up,
+                           z_save=self.z_gate, workspace=self.ws, stream=stream)
+        moe.moe_linear_fwd(self.hidden, p["s_down"], None, self.y, residual=routed, workspace=self.ws, stream=stream)
+        return self.y
+
+    def backward(self, dy, p, dx_add=None, stream=None):
+        """dx (+ dx_add, the gradient that reaches x past the block) and `grads`."""
+        g, ws, s = self.grads, self.ws, stream
+        dxn = self.layer.backward(dy, p["w_gate"], p["w_up"], p["w_down"], stream=stream, w_r=p["w_r"])
+        moe.moe_linear_bwd(self.hidden, p["s_down"], dy, None, self.d_hidden, g["s_down"], workspace=ws, stream=s)
+        moe.moe_linear_bwd(self.xn, p["s_gate"], self.d_hidden, self.dz, dxn, g["s_gate"], act=moe.MOE_ACT_SILU,
+                           z=self.z_gate, mul=self.up, dmul=self.d_up, dx_add=dxn, workspace=ws, stream=s)
+        moe.moe_linear_bwd(self.xn, p["s_up"], self.d_up, None, dxn, g["s_up"], dx_add=dxn, workspace=ws, stream=s)
+        moe.moe_layernorm_bwd(self._x, p["gamma"], self.mean, self.rstd, dxn, self.dx, g["gamma"],
+                              g["beta"] if p.get("beta") is not None else None, ws, dx_add, s)
         return self.dx

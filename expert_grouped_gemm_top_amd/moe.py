@@ -19,11 +19,14 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmoe.so")
 
 MOE_F32, MOE_BF16 = 0, 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_SILU = range(5)
 _STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARGUMENT", 2: "MOE_ERR_UNSUPPORTED",
            3: "MOE_ERR_WORKSPACE_TOO_SMALL", 4: "MOE_ERR_HIP"}
 
 _lib = None
 _vp, _i, _sz, _d, _i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_double, ctypes.c_int64
+_f = ctypes.c_float
 
 _SIGS = {
     "moe_status_string": ([_i], ctypes.c_char_p),
@@ -56,6 +59,15 @@ _SIGS = {
     "moe_quantize_rows_fp8": ([_i, _i, _vp, _vp, _vp, _vp], _i),
     "moe_transpose_fp8": ([_i, _i, _i, _vp, _vp, _vp], _i),
     "moe_grouped_swiglu_fwd_fp8": ([_i] * 5 + [_vp] * 15, _i),
+    "moe_route_scored": ([_i] * 8 + [_f] + [_vp] * 5, _i),
+    "moe_route_scored_bwd": ([_i] * 5 + [_f] + [_vp] * 5, _i),
+    "moe_router_bwd_dlogits": ([_i] * 4 + [_vp] * 5 + [_i, _vp, _sz, _vp], _i),
+    "moe_layernorm_fwd": ([_i] * 3 + [_f] + [_vp] * 7, _i),
+    "moe_layernorm_workspace_bytes": ([_i, _i], _sz),
+    "moe_layernorm_bwd": ([_i] * 3 + [_vp] * 10 + [_sz, _vp], _i),
+    "moe_linear_workspace_bytes": ([_i] * 4, _sz),
+    "moe_linear_fwd": ([_i] * 5 + [_vp] * 8 + [_sz, _vp], _i),
+    "moe_linear_bwd": ([_i] * 5 + [_vp] * 12 + [_sz, _vp], _i),
 }
 
 
@@ -456,3 +468,137 @@ def moe_compact_pairs(counts, offsets, perm, score, rho, kept_counts, kept_offse
         _ptr(x_kept, "x_kept", d, R * H, allow_none=x_sorted is None),
         _ptr(a_kept, "a_kept", d, R * F, allow_none=a_save is None),
         _ptr(h_kept, "h_kept", d, R * 2 * F, allow_none=h_save is None), _stream(stream)))
+
+
+# ---- the rest of a MoE block ---------------------------------------------------
+
+def _matrix(t, name, shape, dtype, allow_none=False):
+    """The pointer of a contiguous GPU tensor of exactly this shape and type."""
+    if t is None and allow_none:
+        return None
+    p = _ptr(t, name, dtype)
+    if tuple(t.shape) != shape:
+        raise MoeError(f"{name} has shape {tuple(t.shape)}, needs {shape}")
+    return p
+
+
+def _rows(t, name):
+    """The two sizes of a matrix argument."""
+    if t is None:
+        raise MoeError(f"{name} is required")
+    if t.dim() != 2 or t.numel() == 0:
+        raise MoeError(f"{name} must be a matrix with at least one element, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _one_device(*tensors):
+    """Every tensor on the current device: the kernels run there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise MoeError(f"a tensor on {t.device} in a call on the current device cuda:{dev}")
+
+
+def moe_route_scored(logits, bias, topk_idx, topk_w, k: int, score: int = MOE_SCORE_SOFTMAX, n_groups: int = 1,
+                     top_groups: int = 1, group_top: int = 1, renormalize: bool = True, scale: float = 1.0,
+                     stream=None):
+    """Routing by scores: softmax or sigmoid, an optional selection bias [E], the
+    best top_groups of n_groups groups, top-k, weights renormalised or not."""
+    T, E = _rows(logits, "logits")
+    args = (_matrix(logits, "logits", (T, E), F32), _matrix(bias, "bias", (E,), F32, allow_none=True),
+            _matrix(topk_idx, "topk_idx", (T, k), I32), _matrix(topk_w, "topk_w", (T, k), F32))
+    _one_device(logits, bias, topk_idx, topk_w)
+    _check(lib().moe_route_scored(T, E, k, score, n_groups, top_groups, group_top, 1 if renormalize else 0, scale,
+                                  *args, _stream(stream)))
+
+
+def moe_route_scored_bwd(logits, topk_idx, dg, dlogits, score: int = MOE_SCORE_SOFTMAX, renormalize: bool = True,
+                         scale: float = 1.0, stream=None):
+    """dlogits from dg = dL/dtopk_w, the selection held fixed."""
+    T, E = _rows(logits, "logits")
+    k = _rows(topk_idx, "topk_idx")[1]
+    args = (_matrix(logits, "logits", (T, E), F32), _matrix(topk_idx, "topk_idx", (T, k), I32),
+            _matrix(dg, "dg", (T, k), F32), _matrix(dlogits, "dlogits", (T, E), F32))
+    _one_device(logits, topk_idx, dg, dlogits)
+    _check(lib().moe_route_scored_bwd(T, E, k, score, 1 if renormalize else 0, scale, *args, _stream(stream)))
+
+
+def moe_router_bwd_dlogits(x, w_r, dlogits, dw_r, dx, accumulate: bool, workspace=None, stream=None):
+    """moe_router_bwd's two products for a given dlogits."""
+    T, H = _rows(x, "x")
+    E = _rows(w_r, "w_r")[1]
+    d = x.dtype
+    args = (_matrix(x, "x", (T, H), d), _matrix(w_r, "w_r", (H, E), d), _matrix(dlogits, "dlogits", (T, E), F32),
+            _matrix(dw_r, "dw_r", (H, E), d), _matrix(dx, "dx", (T, H), d))
+    _one_device(x, w_r, dlogits, dw_r, dx, workspace)
+    ws, ws_bytes = _ws(workspace)
+    _check(lib().moe_router_bwd_dlogits(T, H, E, _dt(x), *args, 1 if accumulate else 0, ws, ws_bytes,
+                                        _stream(stream)))
+
+
+def moe_layernorm_workspace_bytes(T: int, H: int) -> int:
+    return int(lib().moe_layernorm_workspace_bytes(T, H))
+
+
+def moe_layernorm_fwd(x, gamma, beta, y, mean=None, rstd=None, eps: float = 1e-5, stream=None):
+    """y = (x - mean) rstd gamma + beta over rows of H; beta may be None, mean and
+    rstd [T] fp32 are kept for the backward when given; y may be x."""
+    T, H = _rows(x, "x")
+    d = x.dtype
+    args = (_matrix(x, "x", (T, H), d), _matrix(gamma, "gamma", (H,), d),
+            _matrix(beta, "beta", (H,), d, allow_none=True), _matrix(y, "y", (T, H), d),
+            _matrix(mean, "mean", (T,), F32, allow_none=True), _matrix(rstd, "rstd", (T,), F32, allow_none=True))
+    _one_device(x, gamma, beta, y, mean, rstd)
+    _check(lib().moe_layernorm_fwd(T, H, _dt(x), eps, *args, _stream(stream)))
+
+
+def moe_layernorm_bwd(x, gamma, mean, rstd, dy, dx, dgamma, dbeta, workspace, dx_add=None, stream=None):
+    """dx [+ dx_add], dgamma and dbeta (None: not wanted); dx may be dy, x or dx_add."""
+    T, H = _rows(x, "x")
+    d = x.dtype
+    args = (_matrix(x, "x", (T, H), d), _matrix(gamma, "gamma", (H,), d), _matrix(mean, "mean", (T,), F32),
+            _matrix(rstd, "rstd", (T,), F32), _matrix(dy, "dy", (T, H), d),
+            _matrix(dx_add, "dx_add", (T, H), d, allow_none=True), _matrix(dx, "dx", (T, H), d),
+            _matrix(dgamma, "dgamma", (H,), d), _matrix(dbeta, "dbeta", (H,), d, allow_none=True))
+    _one_device(x, gamma, mean, rstd, dy, dx_add, dx, dgamma, dbeta, workspace)
+    ws, ws_bytes = _ws(workspace)
+    _check(lib().moe_layernorm_bwd(T, H, _dt(x), *args, ws, ws_bytes, _stream(stream)))
+
+
+def moe_linear_workspace_bytes(T: int, I: int, O: int, dtype) -> int:  # noqa: E741
+    return int(lib().moe_linear_workspace_bytes(T, I, O, MOE_F32 if dtype == torch.float32 else MOE_BF16))
+
+
+def moe_linear_fwd(x, w, bias, y, act: int = MOE_ACT_NONE, mul=None, residual=None, z_save=None, workspace=None,
+                   stream=None):
+    """y = act(x w + bias) [* mul] [+ residual]; z_save keeps x w + bias for the
+    backward.  y may be mul or residual."""
+    T, I = _rows(x, "x")  # noqa: E741
+    O = _rows(w, "w")[1]  # noqa: E741
+    d = x.dtype
+    opt = dict(allow_none=True)
+    args = (_matrix(x, "x", (T, I), d), _matrix(w, "w", (I, O), d), _matrix(bias, "bias", (O,), d, **opt),
+            _matrix(mul, "mul", (T, O), d, **opt), _matrix(residual, "residual", (T, O), d, **opt),
+            _matrix(z_save, "z_save", (T, O), d, **opt), _matrix(y, "y", (T, O), d))
+    _one_device(x, w, bias, mul, residual, z_save, y, workspace)
+    ws, ws_bytes = _ws(workspace)
+    _check(lib().moe_linear_fwd(T, I, O, _dt(x), act, *args, ws, ws_bytes, _stream(stream)))
+
+
+def moe_linear_bwd(x, w, dy, dz, dx, dw, dbias=None, act: int = MOE_ACT_NONE, z=None, mul=None, dmul=None, dx_add=None,
+                   workspace=None, stream=None):
+    """Gradients of moe_linear_fwd (the residual's is dy): dx [+ dx_add], dw, dbias,
+    each skipped when None, and dmul with mul.  z (the forward's z_save) and dz
+    (a buffer like dy, or dy or z itself) are needed with an activation or mul."""
+    T, I = _rows(x, "x")  # noqa: E741
+    O = _rows(w, "w")[1]  # noqa: E741
+    d = x.dtype
+    opt = dict(allow_none=True)
+    args = (_matrix(x, "x", (T, I), d), _matrix(w, "w", (I, O), d), _matrix(z, "z", (T, O), d, **opt),
+            _matrix(mul, "mul", (T, O), d, **opt), _matrix(dy, "dy", (T, O), d), _matrix(dz, "dz", (T, O), d, **opt),
+            _matrix(dx_add, "dx_add", (T, I), d, **opt), _matrix(dx, "dx", (T, I), d, **opt),
+            _matrix(dw, "dw", (I, O), d, **opt), _matrix(dbias, "dbias", (O,), d, **opt),
+            _matrix(dmul, "dmul", (T, O), d, **opt))
+    _one_device(x, w, z, mul, dy, dz, dx_add, dx, dw, dbias, dmul, workspace)
+    ws, ws_bytes = _ws(workspace)
+    _check(lib().moe_linear_bwd(T, I, O, _dt(x), act, *args, ws, ws_bytes, _stream(stream)))

@@ -28,6 +28,16 @@
  *   moe_grouped_bwd_dx_fp8w frozen expert weights stored once in fp8 (E4M3),
  *                           and the forward and dx backward reading them
  *
+ * Around the expert path, the rest of a MoE block:
+ *
+ *   moe_route_scored, moe_route_scored_bwd  routing by softmax or sigmoid scores
+ *                           with a selection bias and expert groups, and the
+ *                           logits' gradient
+ *   moe_router_bwd_dlogits  the router's products for a given logits' gradient
+ *   moe_layernorm_fwd, moe_layernorm_bwd    the norm in front of the router
+ *   moe_linear_fwd, moe_linear_bwd          a dense product with bias, activation,
+ *                           gate and residual in its epilogue (shared experts)
+ *
  * Conventions for every call:
  *  - Pointers marked (device) are device pointers owned by the caller; the
  *    library allocates no memory and keeps no pointer after a call returns
@@ -100,6 +110,9 @@ int moe_abi_version(void);
  *   moe_grouped_swiglu_fwd_fp8              R = 0: 0; else 3
  *   moe_router_fwd                          1, plus 1 when its workspace is used
  *   moe_router_bwd                          3, plus 1 when its dW_r reduction is split
+ *   moe_router_bwd_dlogits                  2, plus 1 when its dW_r reduction is split
+ *   moe_route_scored, moe_route_scored_bwd, moe_layernorm_fwd  1
+ *   moe_layernorm_bwd                       2
  * These counts are what a HIP graph of a layer step captures. */
 int64_t moe_launch_count(void);
 
@@ -117,7 +130,11 @@ typedef enum moe_kernel {
   MOE_K_COMPACT = 9,       /* the selection kernel of moe_compact_pairs */
   MOE_K_ROUTER_FWD = 10,   /* moe_router_fwd */
   MOE_K_ROUTER_DW = 11,    /* the dW_r GEMM of moe_router_bwd */
-  MOE_K_COUNT = 12
+  MOE_K_ROUTE_SCORED = 12, /* moe_route_scored, moe_route_scored_bwd */
+  MOE_K_LAYERNORM = 13,    /* moe_layernorm_fwd, moe_layernorm_bwd */
+  MOE_K_LINEAR_FWD = 14,   /* moe_linear_fwd */
+  MOE_K_LINEAR_BWD = 15,   /* moe_linear_bwd */
+  MOE_K_COUNT = 16
 } moe_kernel;
 
 /* Profiling hook.  Arms a one-shot request on the calling thread: the next
@@ -478,6 +495,122 @@ int64_t moe_quota_cap_for_budget(int T, int H, int F, int E, int k, int dtype, i
  * [T*k] fp32 (device, out). */
 int moe_pair_scores(int T, int H, int F, int k, int dtype, const int32_t* inv_perm, const float* topk_w,
                     const void* a_save, const void* dy, float* score, void* stream);
+
+/* ---- the rest of a MoE block ------------------------------------------------ */
+
+typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+/* Routing by scores, with a selection bias and expert groups.  For token t:
+ *   s_e = softmax over all E logits, or sigmoid(l_e)
+ *   c_e = s_e + bias_e               the choice score (bias may be NULL)
+ * The experts lie in n_groups groups of E / n_groups neighbours.  A group is
+ * worth the sum of its group_top (1 or 2) best choice scores; the top_groups
+ * groups of most worth stay (equal worth: the lower group), the experts of the
+ * others count as c = -inf.  topk_idx[t, 0..k) lists the k experts of largest c
+ * (equal c: the lower index).  The weights come from s, not c:
+ *   topk_w[t,j] = scale * s_j, or with `renormalize` scale * s_j / sum_i s_i.
+ * Choices are made exactly: without a bias experts rank as their logits do;
+ * scores that are compared with a bias, or summed for a group, are those of
+ * 64-bit arithmetic.
+ *  - An expert whose logit is -inf is unavailable: c = -inf whatever its bias,
+ *    s = 0.  It adds nothing to its group's worth; a group with no available
+ *    expert is worth -inf.  It is listed only when fewer than k experts are
+ *    left, with weight 0.  A token whose selected scores are all zero has
+ *    weights 0, not NaN.
+ *  - A NaN choice score (or worth) ranks above every number, NaNs by lower index; a softmax
+ *    token with a NaN or +inf logit has NaN scores throughout.
+ * Requires n_groups <= 16, n_groups dividing E, 1 <= top_groups <= n_groups,
+ * group_top <= E / n_groups, k <= top_groups * E / n_groups, scale finite.
+ * logits [T, E] fp32, bias [E] fp32 or NULL (device); topk_idx [T, k] int32,
+ * topk_w [T, k] fp32 (device, out). */
+int moe_route_scored(int T, int E, int k, int score, int n_groups, int top_groups, int group_top, int renormalize,
+                     float scale, const float* logits, const float* bias, int32_t* topk_idx, float* topk_w,
+                     void* stream);
+
+/* Gradient of moe_route_scored's weights with the selection held fixed: with
+ * g = dg (dL/dtopk_w), s the scores and p_j = s_j / sum_i s_i,
+ *   softmax, renormalized:  dl_j = scale p_j (g_j - sum_i p_i g_i)
+ *   sigmoid, renormalized:  the same times (1 - s_j)
+ *   sigmoid:                dl_j = scale g_j s_j (1 - s_j)
+ *   softmax:                dl_e = scale s_e ([e selected] g_e - sum_i s_i g_i) for every e
+ * and zero for the other experts of the first three.  Unavailable experts and
+ * tokens whose selected scores are all zero get zeros.  The bias takes no
+ * gradient (the selection does not pass one).  An index listed twice in a row
+ * counts twice; one outside [0, E) is left out.
+ * logits [T, E] fp32, topk_idx [T, k] int32, dg [T, k] fp32 (device);
+ * dlogits [T, E] fp32 (device, out). */
+int moe_route_scored_bwd(int T, int E, int k, int score, int renormalize, float scale, const float* logits,
+                         const int32_t* topk_idx, const float* dg, float* dlogits, void* stream);
+
+/* The two products of moe_router_bwd for a logits' gradient that is given
+ * (from moe_route_scored_bwd, or any other): dw_r = x^T dlogits and dx (+)=
+ * dlogits W_r^T.  Arguments as there; dlogits [T, E] fp32 is read. */
+int moe_router_bwd_dlogits(int T, int H, int E, int dtype, const void* x, const void* w_r, const float* dlogits,
+                           void* dw_r, void* dx, int dx_accumulate, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* Layer norm over rows of H:
+ *   y = (x - mean) rstd gamma + beta, rstd = 1 / sqrt(var + eps)
+ * with mean and (biased) variance in fp32, the variance from the differences to the mean.
+ * x, y [T, H], gamma [H], beta [H] or NULL, of `dtype` (device); mean, rstd
+ * [T] fp32 (device, out; both or neither may be NULL when no backward follows).  y may be x.  eps >= 0.
+ * Pointers (but mean, rstd) 16-byte aligned.  H <= 16384. */
+int moe_layernorm_fwd(int T, int H, int dtype, float eps, const void* x, const void* gamma, const void* beta, void* y,
+                      float* mean, float* rstd, void* stream);
+
+/* Workspace (device bytes) of moe_layernorm_bwd: fp32 partial sums of dgamma
+ * and dbeta (at most 64 MiB).  Host-only. */
+size_t moe_layernorm_workspace_bytes(int T, int H);
+
+/* Its backward: with xh = (x - mean) rstd and g = dy gamma,
+ *   dx = rstd (g - avg(g) - xh avg(g xh)) [+ dx_add],   averages over the row
+ *   dgamma = sum_t dy xh,  dbeta = sum_t dy
+ * Sums in fp32 in one fixed order.  dx_add [T, H] or NULL (the gradient that reaches x past the norm; it may
+ * be dx); dx [T, H] (may be dy), dgamma [H], dbeta [H] or NULL of `dtype` (device, out);
+ * workspace (device, 16-byte aligned) of at least moe_layernorm_workspace_bytes(T, H).
+ * Calls that may overlap need a workspace each. */
+int moe_layernorm_bwd(int T, int H, int dtype, const void* x, const void* gamma, const float* mean, const float* rstd,
+                      const void* dy, const void* dx_add, void* dx, void* dgamma, void* dbeta, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+typedef enum moe_act {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_GELU = 2,      /* z Phi(z) */
+  MOE_ACT_GELU_TANH = 3, /* its tanh form: z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) */
+  MOE_ACT_SILU = 4
+} moe_act;
+
+/* Workspace (device bytes) that moe_linear_fwd and moe_linear_bwd need for T
+ * rows, I inputs and O outputs: fp32 partial sums of split reductions (0 when none
+ * is split).  Host-only. */
+size_t moe_linear_workspace_bytes(int T, int I, int O, int dtype);
+
+/* Dense product with its epilogue:
+ *   z = x W + bias,   y = act(z) [* mul] [+ residual]
+ * all from the fp32 sums, y (and z_save) rounded once.  x [T, I], w [I, O], bias [O] or NULL, mul and
+ * residual [T, O] or NULL of `dtype` (device); z_save [T, O] or NULL (z for the
+ * backward), y [T, O] (device, out).  y may be mul or residual; z_save and y
+ * overlap nothing else.  With act = SILU and mul = x W_up this is a gated expert's hidden row; with residual =
+ * the routed experts' sum a shared expert's output joins it.
+ * I and O multiples of 8, at most 2^20, pointers 16-byte aligned, workspace of at least moe_linear_workspace_bytes (may
+ * be NULL when that is 0).  Calls that may overlap need a workspace each. */
+int moe_linear_fwd(int T, int I, int O, int dtype, int act, const void* x, const void* w, const void* bias,
+                   const void* mul, const void* residual, void* z_save, void* y, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/* Its backward (the residual's gradient is dy):
+ *   dz = dy [* mul] act'(z),  dmul = dy act(z),
+ *   dx = dz W^T [+ dx_add],  dw = x^T dz,  dbias = sum_t dz
+ * z: the forward's z_save, needed when act is not NONE or mul is given, else
+ * ignored.  dz [T, O] (device, out; of `dtype`: the operand of both products,
+ * so rounded to it; dbias sums the unrounded values) is needed in those cases too, and may be dy or z; without them dz is dy itself and
+ * the argument is ignored.  relu'(0) = 0.  dmul [T, O] is written when mul is given (required then; it may be mul, z or dy).
+ * dx_add [T, I] or NULL (may be dx).  dx and dw may each be NULL (not
+ * wanted), dbias [O] too.  dx overlaps none of the inputs but dx_add. */
+int moe_linear_bwd(int T, int I, int O, int dtype, int act, const void* x, const void* w, const void* z,
+                   const void* mul, const void* dy, void* dz, const void* dx_add, void* dx, void* dw, void* dbias,
+                   void* dmul, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
