@@ -9,6 +9,7 @@
 
 #include "moe_common.h"
 #include "moe_launch.h"
+#include "moe_lds32.h"
 #include "moe_rows.h"
 
 namespace moe {
@@ -69,61 +70,378 @@ __device__ __forceinline__ void act_both(int act, float z, float& value, float& 
   }
 }
 
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ float load1(const uint16_t* p) { return bf2f(*p); }
-
-// C [M, N] = A B over K, then the epilogue.  A(m, k) = a[m sam + k sak], B(k, n) = b[k sbk + n sbn].
+// C [M, N] = A B over K, then the epilogue.  Either operand may lie with k
+// contiguous ("KC": a[m lda + k], b[n ldb + k]) or with its own index contiguous
+// (a[k lda + m], b[k ldb + n]).
 struct LinearProduct {
   int M, N, K;
   const void* a;
-  int64_t sam, sak;
+  int64_t lda;
   const void* b;
-  int64_t sbk, sbn;
+  int64_t ldb;
   int act;
   const void *bias, *mul, *residual;
   void *z, *out;
+  int slice;    // k per slice of a split reduction, a multiple of the kernels' stage depth (>= K: not split)
+  float* part;  // split: fp32 partials [slices][M][N]
 };
 
-// 64 x 64 outputs per workgroup, 4 x 4 per thread, 16 k per stage.
+// The epilogue of eight neighbouring outputs, from their fp32 sums.
 template <typename T>
-__global__ __launch_bounds__(256) void linear_product_kernel(LinearProduct g) {
-  __shared__ float s_a[16][65], s_b[16][65];
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int m0 = blockIdx.x * 64, n0 = blockIdx.y * 64;
-  const T* a = (const T*)g.a;
-  const T* b = (const T*)g.b;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < g.K; k0 += 16) {
-    for (int q = tid; q < 64 * 16; q += 256) {
-      const int am = g.sak == 1 ? q >> 4 : q & 63, ak = g.sak == 1 ? q & 15 : q >> 6;
-      s_a[ak][am] = m0 + am < g.M && k0 + ak < g.K ? load1(a + (m0 + am) * g.sam + (k0 + ak) * g.sak) : 0.0f;
-      const int bn = g.sbk == 1 ? q >> 4 : q & 63, bk = g.sbk == 1 ? q & 15 : q >> 6;
-      s_b[bk][bn] = n0 + bn < g.N && k0 + bk < g.K ? load1(b + (k0 + bk) * g.sbk + (n0 + bn) * g.sbn) : 0.0f;
+__device__ __forceinline__ void finish8(const LinearProduct& g, int64_t m, int n, float (&v)[8]) {
+  const int64_t at = m * g.N + n;
+  float u[8];
+  if (g.bias != nullptr) {
+    load8((const T*)g.bias + n, u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += u[j];
+  }
+  if (g.z != nullptr) store8((T*)g.z + at, v);
+  if (g.act != kActNone) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = act_value(g.act, v[j]);
+  }
+  if (g.mul != nullptr) {
+    load8((const T*)g.mul + at, u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= u[j];
+  }
+  if (g.residual != nullptr) {
+    load8((const T*)g.residual + at, u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += u[j];
+  }
+  store8((T*)g.out + at, v);
+}
+
+// Eight outputs of a tile: to the slice's partials or through the epilogue.
+template <typename T>
+__device__ __forceinline__ void leave8(const LinearProduct& g, int slice, int64_t m, int n, float (&v)[8]) {
+  if (g.part != nullptr) store8(g.part + ((int64_t)slice * g.M + m) * g.N + n, v);
+  else finish8<T>(g, m, n, v);
+}
+
+// Adds the slices of a split reduction in order, then the epilogue.
+template <typename T>
+__global__ __launch_bounds__(256) void linear_slices_kernel(LinearProduct g, int slices) {
+  const int runs = g.N / 8;
+  const int64_t total = (int64_t)g.M * runs, MN = (int64_t)g.M * g.N;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    float v[8], u[8];
+    load8(g.part + 8 * i, v);
+    for (int s = 1; s < slices; ++s) {
+      load8(g.part + s * MN + 8 * i, u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += u[j];
     }
-    __syncthreads();
+    finish8<T>(g, i / runs, 8 * (int)(i % runs), v);
+  }
+}
+
+// Row and column tile of workgroup `wg`: each XCD walks a contiguous range of
+// the tiles; groups of up to `depth` row tiles x all column tiles, column-major
+// within a group, so that tiles resident together share operands in L2.
+__device__ __forceinline__ void tile_of(int wg, int mtiles, int ntiles, int depth, int& mt, int& nt) {
+  const int item = xcd_item(wg, mtiles * ntiles);
+  const int grp = item / (depth * ntiles), within = item - grp * depth * ntiles;
+  const int gm = min(depth, mtiles - depth * grp);
+  mt = depth * grp + within % gm;
+  nt = within / gm;
+}
+
+// ---- bf16 on the 32x32x16 matrix core ------------------------------------------
+
+// 16-byte chunk position in a [row][64 k] LDS tile (128-byte rows): 16 rows of
+// one fragment read fall in distinct bank groups.
+__device__ __forceinline__ int kc_key(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
+
+// One operand's stage: ROWS x BK elements by direct global->LDS loads, INS per
+// wave.  KC: LDS [row][BK]; otherwise LDS [BK][ROWS].  Chunks outside the
+// operand come from zeros (TAIL; rows of a KC operand past its end re-read the
+// last row and reach only outputs that are not stored).
+template <bool KC, int ROWS, int BK, int NW, bool TAIL>
+struct Loader {
+  static constexpr int INS = ROWS * BK * 2 / 1024 / NW;
+  static_assert(ROWS * BK * 2 == INS * 1024 * NW, "whole loads");
+  const uint16_t* src[INS];
+  int k[INS];    // k of this lane's chunk within the stage
+  bool ok[INS];  // inside the operand's rows
+  int64_t step;  // elements per k
+  __device__ void init(const void* base, int64_t ld, int r0, int rows, int w, int l) {
+    step = KC ? 1 : ld;
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
+    for (int i = 0; i < INS; ++i) {
+      if (KC) {
+        const int row = (512 / BK) * (INS * w + i) + l / (BK / 8);
+        const int chunk = kc_key(row, l % (BK / 8));
+        k[i] = 8 * chunk;
+        ok[i] = true;
+        src[i] = (const uint16_t*)base + (int64_t)min(r0 + row, rows - 1) * ld + 8 * chunk;
+      } else {
+        k[i] = (512 / ROWS) * (INS * w + i) + l / (ROWS / 8);
+        const int c = r0 + 8 * ((l % (ROWS / 8)) ^ nn_swz(k[i]));
+        ok[i] = c < rows;
+        src[i] = (const uint16_t*)base + (int64_t)k[i] * ld + (ok[i] ? c : 0);
+      }
+    }
+  }
+  __device__ void issue(int k0, int K, unsigned char* tile, int w) const {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < INS; ++i) {
+      const uint16_t* p = src[i] + k0 * step;
+      if (TAIL && (!ok[i] || k0 + k[i] >= K)) p = zero_chunk();
+      g2lds(p, tile + 1024 * (INS * w + i));
+    }
+  }
+};
+
+template <bool KC, int ROWS, int BK>
+__device__ __forceinline__ u32x4 tile_frag(const unsigned char* tile, int sub, int row0) {
+  if (KC) {
+    const int row = row0 + (__lane_id() & 31);
+    return *(const u32x4*)(tile + row * (2 * BK) + 16 * kc_key(row, 2 * sub + (__lane_id() >> 5)));
+  } else {
+    return tr_frag32(tile, 2 * ROWS, sub, row0);
+  }
+}
+
+// Workgroup = BM x BN outputs, NW waves laid out WM x (NW / WM), two LDS stages
+// of 64 k.  A stage is waited for before the last 16 k of the one in front, so
+// its first fragments are read under those products, and its successor's loads
+// go out in two halves before the next two runs of products.
+template <bool AKC, bool BKC, int BM, int BN, int NW, int WM, bool TAIL>
+__global__ __launch_bounds__(64 * NW, (BM + BN) <= 256 ? 2 : NW / 4) void linear_tile_kernel(LinearProduct g, int depth) {
+  constexpr int BK = 64, SUBS = BK / 16;
+  constexpr int TM = BM / WM, TN = BN / (NW / WM), MI = TM / 32, NJ = TN / 32;
+  constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, STAGE = A_BYTES + B_BYTES;
+  extern __shared__ __attribute__((aligned(16))) unsigned char s_dyn[];
+  const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, l32 = l & 31, hk = l >> 5;
+  const int wm = w % WM, wn = w / WM;
+  int mt, nt;
+  tile_of(blockIdx.x, (g.M + BM - 1) / BM, (g.N + BN - 1) / BN, depth, mt, nt);
+  const int m0 = mt * BM, n0 = nt * BN;
+  const int kb = blockIdx.y * g.slice, ke = min(g.K, kb + g.slice);
+
+  Loader<AKC, BM, BK, NW, TAIL> la;
+  Loader<BKC, BN, BK, NW, TAIL> lb;
+  la.init(g.a, g.lda, m0, g.M, w, l);
+  lb.init(g.b, g.ldb, n0, g.N, w, l);
+  auto issue_a = [&](int s) { la.issue(kb + s * BK, g.K, s_dyn + (s & 1) * STAGE, w); };
+  auto issue_b = [&](int s) { lb.issue(kb + s * BK, g.K, s_dyn + (s & 1) * STAGE + A_BYTES, w); };
+
+  f32x16 acc[MI][NJ];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(s_a[k][ty + 16 * i], s_b[k][tx + 16 * j], acc[i][j]);
-    __syncthreads();
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  struct Frags {
+    u32x4 a[MI], b[NJ];
+  };
+  auto products = [&](const Frags& cur, const unsigned char* st, int next_sub, Frags& nxt) {
+    __builtin_amdgcn_s_setprio(1);
+    if (next_sub >= 0) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i) nxt.a[i] = tile_frag<AKC, BM, BK>(st, next_sub, TM * wm + 32 * i);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) nxt.b[j] = tile_frag<BKC, BN, BK>(st + A_BYTES, next_sub, TN * wn + 32 * j);
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int i = 0; i < MI; ++i) acc[i][j] = mfma32(cur.b[j], cur.a[i], acc[i][j]);
+    constexpr int READS = ((AKC ? 1 : 2) * MI + (BKC ? 1 : 2) * NJ + MI * NJ - 1) / (MI * NJ);
+#pragma unroll
+    for (int q = 0; q < MI * NJ; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);      // one product
+      __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);  // its share of the LDS reads
+    }
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  const int steps = (ke - kb + BK - 1) / BK;
+  static_assert(SUBS == 4, "four runs of products per stage");
+  Frags f0, f1;
+  issue_a(0);
+  issue_b(0);
+  wait_vmcnt<0>();
+  barrier_no_fence();
+  if (steps > 1) {
+    issue_a(1);
+    issue_b(1);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < MI; ++i) f0.a[i] = tile_frag<AKC, BM, BK>(s_dyn, 0, TM * wm + 32 * i);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (m >= g.M || n >= g.N) continue;
-      const size_t at = (size_t)m * g.N + n;
-      float z = acc[i][j];
-      if (g.bias != nullptr) z += load1((const T*)g.bias + n);
-      float y = act_value(g.act, z);
-      if (g.mul != nullptr) y *= load1((const T*)g.mul + at);
-      if (g.residual != nullptr) y += load1((const T*)g.residual + at);
-      if (g.z != nullptr) store1((T*)g.z + at, z);
-      store1((T*)g.out + at, y);
+  for (int j = 0; j < NJ; ++j) f0.b[j] = tile_frag<BKC, BN, BK>(s_dyn + A_BYTES, 0, TN * wn + 32 * j);
+  products(f0, s_dyn, 1, f1);
+  products(f1, s_dyn, 2, f0);
+  products(f0, s_dyn, 3, f1);
+  for (int s = 1; s < steps; ++s) {
+    const unsigned char* st = s_dyn + (s & 1) * STAGE;
+    wait_vmcnt<0>();                      // stage s has landed (the only loads in flight)
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's reads of stage s - 1 are done
+    barrier_no_fence();                   // ... and every wave's: its buffer can take stage s + 1
+    if (s + 1 < steps) issue_a(s + 1);
+    products(f1, st, 0, f0);
+    if (s + 1 < steps) issue_b(s + 1);
+    products(f0, st, 1, f1);
+    products(f1, st, 2, f0);
+    products(f0, st, 3, f1);
+  }
+  products(f1, s_dyn, -1, f0);
+
+  // The fp32 tile leaves through the idle stage buffers, HC columns at a time
+  // ([row][HC], 16-byte chunk c of row r at c ^ (r & 15)), so that the epilogue
+  // reads and writes runs of eight neighbouring outputs.  Register r of
+  // acc[i][j] is row TM wm + 32 i + l32, column TN wn + 32 j + 8 (r / 4) + 4 hk + r % 4.
+  constexpr int FIT = 2 * STAGE / (BM * 4);
+  constexpr int HC = FIT >= BN ? BN : (FIT >= 128 ? 128 : 64);
+  static_assert(BM * HC * 4 <= 2 * STAGE && HC % TN == 0 && BN % HC == 0, "staging");
+  float* s_f = reinterpret_cast<float*>(s_dyn);
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's last fragment reads are done
+#pragma unroll
+  for (int part = 0; part < BN / HC; ++part) {
+    barrier_no_fence();  // every wave is done with the stage buffers / the previous part
+    if (TN * wn / HC == part) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int row = TM * wm + 32 * i + l32, col = TN * wn - HC * part + 32 * j + 8 * q + 4 * hk;
+            *(f32x4*)(s_f + row * HC + 4 * ((col >> 2) ^ (row & 15))) =
+                f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+          }
     }
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the staged values are written
+    barrier_no_fence();
+#pragma unroll 2
+    for (int it = tid; it < BM * HC / 8; it += 64 * NW) {
+      const int row = it / (HC / 8), c8 = it % (HC / 8);
+      const int m = m0 + row, n = n0 + HC * part + 8 * c8;
+      if (m >= g.M || n >= g.N) continue;  // N is a multiple of 8: a run is all in or all out
+      const f32x4 lo = *(const f32x4*)(s_f + row * HC + 4 * ((2 * c8) ^ (row & 15)));
+      const f32x4 hi = *(const f32x4*)(s_f + row * HC + 4 * ((2 * c8 + 1) ^ (row & 15)));
+      float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      leave8<uint16_t>(g, blockIdx.y, m, n, v);
+    }
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's reads of the staged rows are done
+  }
+}
+
+// ---- fp32 on the 32x32x2 matrix core ---------------------------------------------
+
+// D = first x second + D: lane l supplies row / column l % 32 of k = l / 32; the
+// registers of D lie as for mfma32.
+__device__ __forceinline__ f32x16 mfma32_f32(float first, float second, f32x16 acc) {
+  return __builtin_amdgcn_mfma_f32_32x32x2f32(first, second, acc, 0, 0, 0);
+}
+
+// Workgroup = BT x BT outputs, four waves of (BT / 2)^2, 16 k per LDS stage, the
+// next stage's values loaded into registers under the products.
+template <bool AKC, bool BKC, int BT>
+__global__ __launch_bounds__(256) void linear_f32_kernel(LinearProduct g, int depth) {
+  constexpr int BK = 16, PITCH = BT + 32, NB = BT / 64;  // 32 x 32 blocks per wave side
+  constexpr int QUADS = BT * BK / 4 / 256;               // 16-byte loads per thread and operand
+  __shared__ __attribute__((aligned(16))) float s_a[BK * PITCH], s_b[BK * PITCH];
+  const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, l32 = l & 31, hk = l >> 5;
+  const int wm = w & 1, wn = w >> 1;
+  int mt, nt;
+  tile_of(blockIdx.x, (g.M + BT - 1) / BT, (g.N + BT - 1) / BT, depth, mt, nt);
+  const int m0 = mt * BT, n0 = nt * BT;
+  const int kb = blockIdx.y * g.slice, ke = min(g.K, kb + g.slice);
+  f32x4 ra[QUADS], rb[QUADS];
+  // four neighbouring elements of an operand; those outside are zero (the contiguous extent is a multiple of 4)
+  auto fetch = [&](auto kc, const void* base, int64_t ld, int r0, int rows, int k0, f32x4 (&v)[QUADS]) {
+#pragma unroll
+    for (int i = 0; i < QUADS; ++i) {
+      const int q = tid + 256 * i;
+      int r, k;
+      if constexpr (decltype(kc)::value) {
+        r = r0 + q / (BK / 4);
+        k = k0 + 4 * (q % (BK / 4));
+      } else {
+        k = k0 + q / (BT / 4);
+        r = r0 + 4 * (q % (BT / 4));
+      }
+      const bool in = r < rows && k < ke;
+      const int64_t at = decltype(kc)::value ? r * ld + k : k * ld + r;
+      v[i] = in ? *(const f32x4*)((const float*)base + at) : f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+  };
+  auto put = [&](auto kc, float* s, const f32x4 (&v)[QUADS]) {
+#pragma unroll
+    for (int i = 0; i < QUADS; ++i) {
+      const int q = tid + 256 * i;
+      if constexpr (decltype(kc)::value) {
+        const int r = q / (BK / 4), k = 4 * (q % (BK / 4));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[(k + j) * PITCH + r] = v[i][j];
+      } else {
+        *(f32x4*)(s + (q / (BT / 4)) * PITCH + 4 * (q % (BT / 4))) = v[i];
+      }
+    }
+  };
+  using A = std::integral_constant<bool, AKC>;
+  using B = std::integral_constant<bool, BKC>;
+  f32x16 acc[NB][NB];
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  fetch(A{}, g.a, g.lda, m0, g.M, kb, ra);
+  fetch(B{}, g.b, g.ldb, n0, g.N, kb, rb);
+  for (int k0 = kb; k0 < ke; k0 += BK) {
+    put(A{}, s_a, ra);
+    put(B{}, s_b, rb);
+    __syncthreads();
+    if (k0 + BK < ke) {
+      fetch(A{}, g.a, g.lda, m0, g.M, k0 + BK, ra);
+      fetch(B{}, g.b, g.ldb, n0, g.N, k0 + BK, rb);
+    }
+#pragma unroll
+    for (int k = 0; k < BK; k += 2) {
+      float fa[NB], fb[NB];
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        fa[i] = s_a[(k + hk) * PITCH + 32 * (NB * wm + i) + l32];
+        fb[i] = s_b[(k + hk) * PITCH + 32 * (NB * wn + i) + l32];
+      }
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int i = 0; i < NB; ++i) acc[i][j] = mfma32_f32(fb[j], fa[i], acc[i][j]);
+    }
+    __syncthreads();
+  }
+  // lane pairs l, l + 32 hold the two halves of eight neighbouring columns of one
+  // row: they swap quads so that each holds whole runs
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int m = m0 + 32 * (NB * wm + i) + l32;
+        const int n = n0 + 32 * (NB * wn + j) + 16 * p + 8 * hk;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // quads 2 p (columns + 0..7) and 2 p + 1 (columns + 8..15): lane half 0 keeps the first run, half 1 the second
+          const float mine0 = acc[i][j][8 * p + e], mine1 = acc[i][j][8 * p + 4 + e];
+          const float give = hk ? mine0 : mine1;
+          const float got = __shfl_xor(give, 32, kWave);
+          v[e] = hk ? got : mine0;
+          v[4 + e] = hk ? mine1 : got;
+        }
+        if (m < g.M && n < g.N) leave8<float>(g, blockIdx.y, m, n, v);
+      }
 }
 
 // dz, dmul and the column sums of dz.  Workgroup = 32 runs of eight columns x 8
@@ -190,10 +508,83 @@ int dz_slots(int T, int O) {
   return std::max(1, std::min((T + 7) / 8, 1024 / std::min(cols, 1024)));
 }
 
+// ---- launchers -------------------------------------------------------------------
+
 template <typename T>
-hipError_t product(const LinearProduct& g, hipStream_t stream) {
-  MOE_LAUNCH((linear_product_kernel<T>), dim3((g.M + 63) / 64, (g.N + 63) / 64), dim3(256), 0, stream, g);
+hipError_t add_slices(const LinearProduct& g, hipStream_t stream) {
+  const int slices = (g.K + g.slice - 1) / g.slice;
+  const int64_t runs = (int64_t)g.M * (g.N / 8);
+  MOE_LAUNCH((linear_slices_kernel<T>), dim3((unsigned)std::min<int64_t>((runs + 255) / 256, 4096)), dim3(256), 0,
+             stream, g, slices);
   return hipGetLastError();
+}
+
+// What runs a product: the tile, and the slices of its reduction.
+struct Plan {
+  int tile;    // rows of the workgroup tile: 256 or 128 (bf16), 128 or 64 (fp32)
+  int slices;
+  int slice;   // k per slice
+};
+
+constexpr int kCus = 256;
+
+Plan plan_of(int M, int N, int K, int esize) {
+  Plan p{};
+  auto tiles = [&](int t) { return (int64_t)((M + t - 1) / t) * ((N + t - 1) / t); };
+  const int big = esize == 2 ? 256 : 128, small = big / 2, stage = esize == 2 ? 64 : 16;
+  p.tile = tiles(big) >= 3 * kCus / 2 ? big : small;
+  const int64_t have = tiles(p.tile);
+  int64_t s = std::max<int64_t>(1, kCus / have);
+  s = std::min<int64_t>(s, std::max(1, K / (esize == 2 ? 512 : 128)));
+  s = std::min<int64_t>(s, 16);
+  p.slice = (int)((((int64_t)K + s - 1) / s + stage - 1) / stage * stage);
+  p.slices = (K + p.slice - 1) / p.slice;
+  return p;
+}
+
+size_t plan_bytes(int M, int N, int K, int esize) {
+  const Plan p = plan_of(M, N, K, esize);
+  return p.slices > 1 ? (size_t)p.slices * M * N * sizeof(float) : 0;
+}
+
+template <bool AKC, bool BKC, int BM, int BN, int NW, int WM, bool TAIL>
+hipError_t launch_tiles(const LinearProduct& g, int slices, hipStream_t stream) {
+  constexpr size_t lds = (size_t)2 * (BM + BN) * 64 * 2;
+  auto kern = linear_tile_kernel<AKC, BKC, BM, BN, NW, WM, TAIL>;
+  static PerDeviceOnce once;
+  hipError_t err = allow_dynamic_lds(once, (const void*)kern, lds);
+  if (err != hipSuccess) return err;
+  const int64_t tiles = (int64_t)((g.M + BM - 1) / BM) * ((g.N + BN - 1) / BN);
+  MOE_LAUNCH(kern, dim3((unsigned)tiles, slices), dim3(64 * NW), lds, stream, g, 1024 / BM);
+  return hipGetLastError();
+}
+
+template <bool AKC, bool BKC, int BM, int BN, int NW, int WM>
+hipError_t launch_bf16(const LinearProduct& g, int slices, hipStream_t stream) {
+  const bool tail = g.K % 64 != 0 || (!BKC && g.N % BN != 0) || (!AKC && g.M % BM != 0);
+  return tail ? launch_tiles<AKC, BKC, BM, BN, NW, WM, true>(g, slices, stream)
+              : launch_tiles<AKC, BKC, BM, BN, NW, WM, false>(g, slices, stream);
+}
+
+// AKC, BKC: which operands have k contiguous.
+template <typename T, bool AKC, bool BKC>
+hipError_t product(LinearProduct g, float* ws, hipStream_t stream) {
+  const Plan p = plan_of(g.M, g.N, g.K, sizeof(T));
+  g.slice = p.slice;
+  g.part = p.slices > 1 ? ws : nullptr;
+  hipError_t err;
+  if constexpr (std::is_same<T, float>::value) {
+    const int64_t tiles = (int64_t)((g.M + p.tile - 1) / p.tile) * ((g.N + p.tile - 1) / p.tile);
+    const dim3 grid((unsigned)tiles, p.slices);
+    if (p.tile == 128) MOE_LAUNCH((linear_f32_kernel<AKC, BKC, 128>), grid, dim3(256), 0, stream, g, 8);
+    else MOE_LAUNCH((linear_f32_kernel<AKC, BKC, 64>), grid, dim3(256), 0, stream, g, 8);
+    err = hipGetLastError();
+  } else {
+    err = p.tile == 256 ? launch_bf16<AKC, BKC, 256, 256, 8, 2>(g, p.slices, stream)
+                        : launch_bf16<AKC, BKC, 128, 128, 4, 2>(g, p.slices, stream);
+  }
+  if (err != hipSuccess || p.slices == 1) return err;
+  return add_slices<T>(g, stream);
 }
 
 template <typename T>
@@ -217,30 +608,30 @@ hipError_t linear_bwd_typed(const LinearArgs& g, const void* z, const void* mul,
   }
   const void* d = plain ? dy : dz;
   if (dx != nullptr) {
-    LinearProduct p{T_, I, O, d, O, 1, g.w, 1, O, kActNone, nullptr, nullptr, dx_add, nullptr, dx};
-    hipError_t err = product<T>(p, stream);
+    LinearProduct p{T_, I, O, d, O, g.w, O, kActNone, nullptr, nullptr, dx_add, nullptr, dx, 0, nullptr};
+    hipError_t err = product<T, true, true>(p, ws, stream);
     if (err != hipSuccess) return err;
   }
   if (dw != nullptr) {
-    LinearProduct p{I, O, T_, g.x, 1, I, d, O, 1, kActNone, nullptr, nullptr, nullptr, nullptr, dw};
-    return product<T>(p, stream);
+    LinearProduct p{I, O, T_, g.x, I, d, O, kActNone, nullptr, nullptr, nullptr, nullptr, dw, 0, nullptr};
+    return product<T, false, false>(p, ws, stream);
   }
   return hipSuccess;
 }
 
 }  // namespace
 
+// The partials of one launch at a time: a backward's column sums, then each product's slices.
 size_t linear_workspace_bytes(int T, int I, int O, int esize) {
-  (void)I;
-  (void)esize;
-  return (size_t)dz_slots(T, O) * O * sizeof(float);
+  return std::max({(size_t)dz_slots(T, O) * O * sizeof(float), plan_bytes(T, O, I, esize), plan_bytes(T, I, O, esize),
+                   plan_bytes(I, O, T, esize)});
 }
 
 hipError_t launch_linear_fwd(const LinearArgs& g, int esize, const void* bias, const void* mul, const void* residual,
                              void* z, void* y, void* ws, hipStream_t stream) {
-  (void)ws;
-  const LinearProduct p{g.T, g.O, g.I, g.x, g.I, 1, g.w, g.O, 1, g.act, bias, mul, residual, z, y};
-  return esize == 4 ? product<float>(p, stream) : product<uint16_t>(p, stream);
+  const LinearProduct p{g.T, g.O, g.I, g.x, g.I, g.w, g.O, g.act, bias, mul, residual, z, y, 0, nullptr};
+  return esize == 4 ? product<float, true, false>(p, (float*)ws, stream)
+                    : product<uint16_t, true, false>(p, (float*)ws, stream);
 }
 
 hipError_t launch_linear_bwd(const LinearArgs& g, int esize, const void* z, const void* mul, const void* dy, void* dz,
