@@ -205,12 +205,12 @@ __device__ __forceinline__ u32x4 tile_frag(const unsigned char* tile, int sub, i
   }
 }
 
-// Workgroup = BM x BN outputs, NW waves laid out WM x (NW / WM), two LDS stages
+// Workgroup = BM x BN outputs, NW waves laid out WM x (NW / WM), STAGES LDS stages
 // of 64 k.  A stage is waited for before the last 16 k of the one in front, so
 // its first fragments are read under those products, and its successor's loads
 // go out in two halves before the next two runs of products.
-template <bool AKC, bool BKC, int BM, int BN, int NW, int WM, bool TAIL>
-__global__ __launch_bounds__(64 * NW, (BM + BN) <= 256 ? 2 : NW / 4) void linear_tile_kernel(LinearProduct g, int depth) {
+template <bool AKC, bool BKC, int BM, int BN, int NW, int WM, int STAGES, bool TAIL>
+__global__ __launch_bounds__(64 * NW, NW / 4) void linear_tile_kernel(LinearProduct g, int depth) {
   constexpr int BK = 64, SUBS = BK / 16;
   constexpr int TM = BM / WM, TN = BN / (NW / WM), MI = TM / 32, NJ = TN / 32;
   constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, STAGE = A_BYTES + B_BYTES;
@@ -226,8 +226,10 @@ __global__ __launch_bounds__(64 * NW, (BM + BN) <= 256 ? 2 : NW / 4) void linear
   Loader<BKC, BN, BK, NW, TAIL> lb;
   la.init(g.a, g.lda, m0, g.M, w, l);
   lb.init(g.b, g.ldb, n0, g.N, w, l);
-  auto issue_a = [&](int s) { la.issue(kb + s * BK, g.K, s_dyn + (s & 1) * STAGE, w); };
-  auto issue_b = [&](int s) { lb.issue(kb + s * BK, g.K, s_dyn + (s & 1) * STAGE + A_BYTES, w); };
+  constexpr int INS = Loader<AKC, BM, BK, NW, TAIL>::INS + Loader<BKC, BN, BK, NW, TAIL>::INS;  // loads of a stage
+  // stage s lies in buffer s % STAGES
+  auto issue_a = [&](int s, int buf) { la.issue(kb + s * BK, g.K, s_dyn + buf * STAGE, w); };
+  auto issue_b = [&](int s, int buf) { lb.issue(kb + s * BK, g.K, s_dyn + buf * STAGE + A_BYTES, w); };
 
   f32x16 acc[MI][NJ];
 #pragma unroll
@@ -264,13 +266,16 @@ __global__ __launch_bounds__(64 * NW, (BM + BN) <= 256 ? 2 : NW / 4) void linear
   const int steps = (ke - kb + BK - 1) / BK;
   static_assert(SUBS == 4, "four runs of products per stage");
   Frags f0, f1;
-  issue_a(0);
-  issue_b(0);
-  wait_vmcnt<0>();
+  for (int s = 0; s < STAGES - 1 && s < steps; ++s) {
+    issue_a(s, s);
+    issue_b(s, s);
+  }
+  if (steps >= STAGES - 1) wait_vmcnt<(STAGES - 2) * INS>();  // stage 0 has landed, later ones need not have
+  else wait_vmcnt<0>();
   barrier_no_fence();
-  if (steps > 1) {
-    issue_a(1);
-    issue_b(1);
+  if (steps > STAGES - 1) {
+    issue_a(STAGES - 1, STAGES - 1);
+    issue_b(STAGES - 1, STAGES - 1);
   }
 #pragma unroll
   for (int i = 0; i < MI; ++i) f0.a[i] = tile_frag<AKC, BM, BK>(s_dyn, 0, TM * wm + 32 * i);
@@ -279,17 +284,23 @@ __global__ __launch_bounds__(64 * NW, (BM + BN) <= 256 ? 2 : NW / 4) void linear
   products(f0, s_dyn, 1, f1);
   products(f1, s_dyn, 2, f0);
   products(f0, s_dyn, 3, f1);
+  int buf = 0;  // of stage s - 1, which stage s + STAGES - 1 takes over
   for (int s = 1; s < steps; ++s) {
-    const unsigned char* st = s_dyn + (s & 1) * STAGE;
-    wait_vmcnt<0>();                      // stage s has landed (the only loads in flight)
+    const int next = buf + 1 < STAGES ? buf + 1 : 0;
+    const unsigned char* st = s_dyn + next * STAGE;
+    // stage s has landed; of the stages behind it, STAGES - 2 may be in flight
+    if (STAGES > 2 && s + STAGES - 2 < steps) wait_vmcnt<(STAGES - 2) * INS>();
+    else wait_vmcnt<0>();
     __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's reads of stage s - 1 are done
-    barrier_no_fence();                   // ... and every wave's: its buffer can take stage s + 1
-    if (s + 1 < steps) issue_a(s + 1);
+    barrier_no_fence();                   // ... and every wave's: its buffer can be loaded again
+    const bool more = s + STAGES - 1 < steps;
+    if (more) issue_a(s + STAGES - 1, buf);
     products(f1, st, 0, f0);
-    if (s + 1 < steps) issue_b(s + 1);
+    if (more) issue_b(s + STAGES - 1, buf);
     products(f0, st, 1, f1);
     products(f1, st, 2, f0);
     products(f0, st, 3, f1);
+    buf = next;
   }
   products(f1, s_dyn, -1, f0);
 
@@ -297,9 +308,9 @@ __global__ __launch_bounds__(64 * NW, (BM + BN) <= 256 ? 2 : NW / 4) void linear
   // ([row][HC], 16-byte chunk c of row r at c ^ (r & 15)), so that the epilogue
   // reads and writes runs of eight neighbouring outputs.  Register r of
   // acc[i][j] is row TM wm + 32 i + l32, column TN wn + 32 j + 8 (r / 4) + 4 hk + r % 4.
-  constexpr int FIT = 2 * STAGE / (BM * 4);
+  constexpr int FIT = STAGES * STAGE / (BM * 4);
   constexpr int HC = FIT >= BN ? BN : (FIT >= 128 ? 128 : 64);
-  static_assert(BM * HC * 4 <= 2 * STAGE && HC % TN == 0 && BN % HC == 0, "staging");
+  static_assert(BM * HC * 4 <= STAGES * STAGE && HC % TN == 0 && BN % HC == 0, "staging");
   float* s_f = reinterpret_cast<float*>(s_dyn);
   __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's last fragment reads are done
 #pragma unroll
@@ -547,10 +558,10 @@ size_t plan_bytes(int M, int N, int K, int esize) {
   return p.slices > 1 ? (size_t)p.slices * M * N * sizeof(float) : 0;
 }
 
-template <bool AKC, bool BKC, int BM, int BN, int NW, int WM, bool TAIL>
+template <bool AKC, bool BKC, int BM, int BN, int NW, int WM, int STAGES, bool TAIL>
 hipError_t launch_tiles(const LinearProduct& g, int slices, hipStream_t stream) {
-  constexpr size_t lds = (size_t)2 * (BM + BN) * 64 * 2;
-  auto kern = linear_tile_kernel<AKC, BKC, BM, BN, NW, WM, TAIL>;
+  constexpr size_t lds = (size_t)STAGES * (BM + BN) * 64 * 2;
+  auto kern = linear_tile_kernel<AKC, BKC, BM, BN, NW, WM, STAGES, TAIL>;
   static PerDeviceOnce once;
   hipError_t err = allow_dynamic_lds(once, (const void*)kern, lds);
   if (err != hipSuccess) return err;
@@ -559,11 +570,11 @@ hipError_t launch_tiles(const LinearProduct& g, int slices, hipStream_t stream) 
   return hipGetLastError();
 }
 
-template <bool AKC, bool BKC, int BM, int BN, int NW, int WM>
+template <bool AKC, bool BKC, int BM, int BN, int NW, int WM, int STAGES>
 hipError_t launch_bf16(const LinearProduct& g, int slices, hipStream_t stream) {
   const bool tail = g.K % 64 != 0 || (!BKC && g.N % BN != 0) || (!AKC && g.M % BM != 0);
-  return tail ? launch_tiles<AKC, BKC, BM, BN, NW, WM, true>(g, slices, stream)
-              : launch_tiles<AKC, BKC, BM, BN, NW, WM, false>(g, slices, stream);
+  return tail ? launch_tiles<AKC, BKC, BM, BN, NW, WM, STAGES, true>(g, slices, stream)
+              : launch_tiles<AKC, BKC, BM, BN, NW, WM, STAGES, false>(g, slices, stream);
 }
 
 // AKC, BKC: which operands have k contiguous.
@@ -580,8 +591,8 @@ hipError_t product(LinearProduct g, float* ws, hipStream_t stream) {
     else MOE_LAUNCH((linear_f32_kernel<AKC, BKC, 64>), grid, dim3(256), 0, stream, g, 8);
     err = hipGetLastError();
   } else {
-    err = p.tile == 256 ? launch_bf16<AKC, BKC, 256, 256, 8, 2>(g, p.slices, stream)
-                        : launch_bf16<AKC, BKC, 128, 128, 4, 2>(g, p.slices, stream);
+    err = p.tile == 256 ? launch_bf16<AKC, BKC, 256, 256, 8, 2, 2>(g, p.slices, stream)
+                        : launch_bf16<AKC, BKC, 128, 128, 4, 2, 2>(g, p.slices, stream);
   }
   if (err != hipSuccess || p.slices == 1) return err;
   return add_slices<T>(g, stream);

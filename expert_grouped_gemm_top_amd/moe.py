@@ -472,31 +472,59 @@ def moe_compact_pairs(counts, offsets, perm, score, rho, kept_counts, kept_offse
 
 # ---- the rest of a MoE block ---------------------------------------------------
 
-def _matrix(t, name, shape, dtype, allow_none=False):
-    """The pointer of a contiguous GPU tensor of exactly this shape and type."""
-    if t is None and allow_none:
-        return None
-    p = _ptr(t, name, dtype)
-    if tuple(t.shape) != shape:
-        raise MoeError(f"{name} has shape {tuple(t.shape)}, needs {shape}")
-    return p
-
-
 def _rows(t, name):
     """The two sizes of a matrix argument."""
     if t is None:
         raise MoeError(f"{name} is required")
-    if t.dim() != 2 or t.numel() == 0:
-        raise MoeError(f"{name} must be a matrix with at least one element, got shape {tuple(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != 2 or 0 in shape:
+        raise MoeError(f"{name} must be a matrix with at least one element, got shape {tuple(shape)}")
+    return shape
 
 
-def _one_device(*tensors):
-    """Every tensor on the current device: the kernels run there."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise MoeError(f"a tensor on {t.device} in a call on the current device cuda:{dev}")
+def _addr(t, name, shape, dtype, dev):
+    """The address of a contiguous tensor of exactly this shape and type on the
+    current device `dev`, where the kernels run; None for None.  (A decoding
+    step's calls are bound by the host: one pass of cheap tests, the message
+    only where one fails.)"""
+    if t is None:
+        return None
+    try:
+        if t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.device.index == dev:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _ptr(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise MoeError(f"{name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
+    raise MoeError(f"{name} is on {t.device} in a call on the current device cuda:{dev}")
+
+
+def _need(t, name, shape, dtype, dev):
+    if t is None:
+        raise MoeError(f"{name} is required")
+    return _addr(t, name, shape, dtype, dev)
+
+
+def _space(workspace, dev):
+    """Address and bytes of a workspace."""
+    if workspace is None:
+        return None, 0
+    return _addr(workspace, "workspace", workspace.shape, workspace.dtype, dev), workspace.nbytes
+
+
+def _device(t, name):
+    """The current device, for a call whose first argument is `t`."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise MoeError(f"{name} must be a GPU tensor")
+    return torch.cuda.current_device()
+
+
+def _queue(stream, dev):
+    """The hipStream_t of a call on device `dev`."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def moe_route_scored(logits, bias, topk_idx, topk_w, k: int, score: int = MOE_SCORE_SOFTMAX, n_groups: int = 1,
@@ -504,36 +532,37 @@ def moe_route_scored(logits, bias, topk_idx, topk_w, k: int, score: int = MOE_SC
                      stream=None):
     """Routing by scores: softmax or sigmoid, an optional selection bias [E], the
     best top_groups of n_groups groups, top-k, weights renormalised or not."""
+    dev = _device(logits, "logits")
     T, E = _rows(logits, "logits")
-    args = (_matrix(logits, "logits", (T, E), F32), _matrix(bias, "bias", (E,), F32, allow_none=True),
-            _matrix(topk_idx, "topk_idx", (T, k), I32), _matrix(topk_w, "topk_w", (T, k), F32))
-    _one_device(logits, bias, topk_idx, topk_w)
-    _check(lib().moe_route_scored(T, E, k, score, n_groups, top_groups, group_top, 1 if renormalize else 0, scale,
-                                  *args, _stream(stream)))
+    _check(lib().moe_route_scored(
+        T, E, k, score, n_groups, top_groups, group_top, 1 if renormalize else 0, scale,
+        _need(logits, "logits", (T, E), F32, dev), _addr(bias, "bias", (E,), F32, dev),
+        _need(topk_idx, "topk_idx", (T, k), I32, dev), _need(topk_w, "topk_w", (T, k), F32, dev), _queue(stream, dev)))
 
 
 def moe_route_scored_bwd(logits, topk_idx, dg, dlogits, score: int = MOE_SCORE_SOFTMAX, renormalize: bool = True,
                          scale: float = 1.0, stream=None):
     """dlogits from dg = dL/dtopk_w, the selection held fixed."""
+    dev = _device(logits, "logits")
     T, E = _rows(logits, "logits")
     k = _rows(topk_idx, "topk_idx")[1]
-    args = (_matrix(logits, "logits", (T, E), F32), _matrix(topk_idx, "topk_idx", (T, k), I32),
-            _matrix(dg, "dg", (T, k), F32), _matrix(dlogits, "dlogits", (T, E), F32))
-    _one_device(logits, topk_idx, dg, dlogits)
-    _check(lib().moe_route_scored_bwd(T, E, k, score, 1 if renormalize else 0, scale, *args, _stream(stream)))
+    _check(lib().moe_route_scored_bwd(
+        T, E, k, score, 1 if renormalize else 0, scale, _need(logits, "logits", (T, E), F32, dev),
+        _need(topk_idx, "topk_idx", (T, k), I32, dev), _need(dg, "dg", (T, k), F32, dev),
+        _need(dlogits, "dlogits", (T, E), F32, dev), _queue(stream, dev)))
 
 
 def moe_router_bwd_dlogits(x, w_r, dlogits, dw_r, dx, accumulate: bool, workspace=None, stream=None):
     """moe_router_bwd's two products for a given dlogits."""
+    dev = _device(x, "x")
     T, H = _rows(x, "x")
     E = _rows(w_r, "w_r")[1]
     d = x.dtype
-    args = (_matrix(x, "x", (T, H), d), _matrix(w_r, "w_r", (H, E), d), _matrix(dlogits, "dlogits", (T, E), F32),
-            _matrix(dw_r, "dw_r", (H, E), d), _matrix(dx, "dx", (T, H), d))
-    _one_device(x, w_r, dlogits, dw_r, dx, workspace)
-    ws, ws_bytes = _ws(workspace)
-    _check(lib().moe_router_bwd_dlogits(T, H, E, _dt(x), *args, 1 if accumulate else 0, ws, ws_bytes,
-                                        _stream(stream)))
+    ws, ws_bytes = _space(workspace, dev)
+    _check(lib().moe_router_bwd_dlogits(
+        T, H, E, _dt(x), _need(x, "x", (T, H), d, dev), _need(w_r, "w_r", (H, E), d, dev),
+        _need(dlogits, "dlogits", (T, E), F32, dev), _need(dw_r, "dw_r", (H, E), d, dev),
+        _need(dx, "dx", (T, H), d, dev), 1 if accumulate else 0, ws, ws_bytes, _queue(stream, dev)))
 
 
 def moe_layernorm_workspace_bytes(T: int, H: int) -> int:
@@ -543,26 +572,26 @@ def moe_layernorm_workspace_bytes(T: int, H: int) -> int:
 def moe_layernorm_fwd(x, gamma, beta, y, mean=None, rstd=None, eps: float = 1e-5, stream=None):
     """y = (x - mean) rstd gamma + beta over rows of H; beta may be None, mean and
     rstd [T] fp32 are kept for the backward when given; y may be x."""
-    T, H = _rows(x, "x")
+    dev = _device(x, "x")
+    T, H = rows = _rows(x, "x")
     d = x.dtype
-    args = (_matrix(x, "x", (T, H), d), _matrix(gamma, "gamma", (H,), d),
-            _matrix(beta, "beta", (H,), d, allow_none=True), _matrix(y, "y", (T, H), d),
-            _matrix(mean, "mean", (T,), F32, allow_none=True), _matrix(rstd, "rstd", (T,), F32, allow_none=True))
-    _one_device(x, gamma, beta, y, mean, rstd)
-    _check(lib().moe_layernorm_fwd(T, H, _dt(x), eps, *args, _stream(stream)))
+    _check(lib().moe_layernorm_fwd(
+        T, H, _dt(x), eps, _need(x, "x", rows, d, dev), _need(gamma, "gamma", (H,), d, dev),
+        _addr(beta, "beta", (H,), d, dev), _need(y, "y", rows, d, dev), _addr(mean, "mean", (T,), F32, dev),
+        _addr(rstd, "rstd", (T,), F32, dev), _queue(stream, dev)))
 
 
 def moe_layernorm_bwd(x, gamma, mean, rstd, dy, dx, dgamma, dbeta, workspace, dx_add=None, stream=None):
     """dx [+ dx_add], dgamma and dbeta (None: not wanted); dx may be dy, x or dx_add."""
-    T, H = _rows(x, "x")
+    dev = _device(x, "x")
+    T, H = rows = _rows(x, "x")
     d = x.dtype
-    args = (_matrix(x, "x", (T, H), d), _matrix(gamma, "gamma", (H,), d), _matrix(mean, "mean", (T,), F32),
-            _matrix(rstd, "rstd", (T,), F32), _matrix(dy, "dy", (T, H), d),
-            _matrix(dx_add, "dx_add", (T, H), d, allow_none=True), _matrix(dx, "dx", (T, H), d),
-            _matrix(dgamma, "dgamma", (H,), d), _matrix(dbeta, "dbeta", (H,), d, allow_none=True))
-    _one_device(x, gamma, mean, rstd, dy, dx_add, dx, dgamma, dbeta, workspace)
-    ws, ws_bytes = _ws(workspace)
-    _check(lib().moe_layernorm_bwd(T, H, _dt(x), *args, ws, ws_bytes, _stream(stream)))
+    ws, ws_bytes = _space(workspace, dev)
+    _check(lib().moe_layernorm_bwd(
+        T, H, _dt(x), _need(x, "x", rows, d, dev), _need(gamma, "gamma", (H,), d, dev),
+        _need(mean, "mean", (T,), F32, dev), _need(rstd, "rstd", (T,), F32, dev), _need(dy, "dy", rows, d, dev),
+        _addr(dx_add, "dx_add", rows, d, dev), _need(dx, "dx", rows, d, dev), _need(dgamma, "dgamma", (H,), d, dev),
+        _addr(dbeta, "dbeta", (H,), d, dev), ws, ws_bytes, _queue(stream, dev)))
 
 
 def moe_linear_workspace_bytes(T: int, I: int, O: int, dtype) -> int:  # noqa: E741
@@ -573,16 +602,15 @@ def moe_linear_fwd(x, w, bias, y, act: int = MOE_ACT_NONE, mul=None, residual=No
                    stream=None):
     """y = act(x w + bias) [* mul] [+ residual]; z_save keeps x w + bias for the
     backward.  y may be mul or residual."""
+    dev = _device(x, "x")
     T, I = _rows(x, "x")  # noqa: E741
     O = _rows(w, "w")[1]  # noqa: E741
-    d = x.dtype
-    opt = dict(allow_none=True)
-    args = (_matrix(x, "x", (T, I), d), _matrix(w, "w", (I, O), d), _matrix(bias, "bias", (O,), d, **opt),
-            _matrix(mul, "mul", (T, O), d, **opt), _matrix(residual, "residual", (T, O), d, **opt),
-            _matrix(z_save, "z_save", (T, O), d, **opt), _matrix(y, "y", (T, O), d))
-    _one_device(x, w, bias, mul, residual, z_save, y, workspace)
-    ws, ws_bytes = _ws(workspace)
-    _check(lib().moe_linear_fwd(T, I, O, _dt(x), act, *args, ws, ws_bytes, _stream(stream)))
+    d, out = x.dtype, (T, O)
+    ws, ws_bytes = _space(workspace, dev)
+    _check(lib().moe_linear_fwd(
+        T, I, O, _dt(x), act, _need(x, "x", (T, I), d, dev), _need(w, "w", (I, O), d, dev),
+        _addr(bias, "bias", (O,), d, dev), _addr(mul, "mul", out, d, dev), _addr(residual, "residual", out, d, dev),
+        _addr(z_save, "z_save", out, d, dev), _need(y, "y", out, d, dev), ws, ws_bytes, _queue(stream, dev)))
 
 
 def moe_linear_bwd(x, w, dy, dz, dx, dw, dbias=None, act: int = MOE_ACT_NONE, z=None, mul=None, dmul=None, dx_add=None,
@@ -590,15 +618,13 @@ def moe_linear_bwd(x, w, dy, dz, dx, dw, dbias=None, act: int = MOE_ACT_NONE, z=
     """Gradients of moe_linear_fwd (the residual's is dy): dx [+ dx_add], dw, dbias,
     each skipped when None, and dmul with mul.  z (the forward's z_save) and dz
     (a buffer like dy, or dy or z itself) are needed with an activation or mul."""
+    dev = _device(x, "x")
     T, I = _rows(x, "x")  # noqa: E741
     O = _rows(w, "w")[1]  # noqa: E741
-    d = x.dtype
-    opt = dict(allow_none=True)
-    args = (_matrix(x, "x", (T, I), d), _matrix(w, "w", (I, O), d), _matrix(z, "z", (T, O), d, **opt),
-            _matrix(mul, "mul", (T, O), d, **opt), _matrix(dy, "dy", (T, O), d), _matrix(dz, "dz", (T, O), d, **opt),
-            _matrix(dx_add, "dx_add", (T, I), d, **opt), _matrix(dx, "dx", (T, I), d, **opt),
-            _matrix(dw, "dw", (I, O), d, **opt), _matrix(dbias, "dbias", (O,), d, **opt),
-            _matrix(dmul, "dmul", (T, O), d, **opt))
-    _one_device(x, w, z, mul, dy, dz, dx_add, dx, dw, dbias, dmul, workspace)
-    ws, ws_bytes = _ws(workspace)
-    _check(lib().moe_linear_bwd(T, I, O, _dt(x), act, *args, ws, ws_bytes, _stream(stream)))
+    d, into, out = x.dtype, (T, I), (T, O)
+    ws, ws_bytes = _space(workspace, dev)
+    _check(lib().moe_linear_bwd(
+        T, I, O, _dt(x), act, _need(x, "x", into, d, dev), _need(w, "w", (I, O), d, dev), _addr(z, "z", out, d, dev),
+        _addr(mul, "mul", out, d, dev), _need(dy, "dy", out, d, dev), _addr(dz, "dz", out, d, dev),
+        _addr(dx_add, "dx_add", into, d, dev), _addr(dx, "dx", into, d, dev), _addr(dw, "dw", (I, O), d, dev),
+        _addr(dbias, "dbias", (O,), d, dev), _addr(dmul, "dmul", out, d, dev), ws, ws_bytes, _queue(stream, dev)))
