@@ -155,6 +155,34 @@ __device__ __forceinline__ void tile_of(int wg, int mtiles, int ntiles, int dept
 // one fragment read fall in distinct bank groups.
 __device__ __forceinline__ int kc_key(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
 
+// k row of a [k][ROWS] LDS tile -> XOR on the 16-byte chunk index: the 4 k rows x
+// 4 chunks that half a wave's transpose read covers lie in distinct banks
+// (256-byte rows and longer: every row starts at the same bank; 128-byte rows: every other one).
+template <int ROWS>
+__device__ __forceinline__ int nc_key(int k) {
+  static_assert(ROWS >= 64, "eight chunks at least");
+  return ROWS >= 128 ? 4 * (k & 3) : 4 * ((k >> 1) & 1);
+}
+
+// 32x32x16 operand fragment of rows row0 .. row0 + 31, k 16 sub .. + 15, from a
+// [k][ROWS] tile: in 16-lane group G, lane r points at k 8 (G >> 1) + 4 h +
+// (r >> 2) and rows 16 (G & 1) + 4 (r & 3) .. + 3, and receives 4 consecutive k of one
+// row (half of its 8).
+template <int ROWS>
+__device__ __forceinline__ u32x4 nc_frag(const unsigned char* tile, int sub, int row0) {
+  const int l = __lane_id(), G = l >> 4, r = l & 15;
+  const int row = row0 + 16 * (G & 1) + 4 * (r & 3);
+  v4i16 part[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int k = 16 * sub + 8 * (G >> 1) + 4 * h + (r >> 2);
+    part[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_v4i16*)(tile + k * (2 * ROWS) + 16 * ((row >> 3) ^ nc_key<ROWS>(k)) + 2 * (row & 7)));
+  }
+  const u32x2 lo = __builtin_bit_cast(u32x2, part[0]), hi = __builtin_bit_cast(u32x2, part[1]);
+  return u32x4{lo[0], lo[1], hi[0], hi[1]};
+}
+
 // One operand's stage: ROWS x BK elements by direct global->LDS loads, INS per
 // wave.  KC: LDS [row][BK]; otherwise LDS [BK][ROWS].  Chunks outside the
 // operand come from zeros (TAIL; rows of a KC operand past its end re-read the
@@ -179,7 +207,7 @@ struct Loader {
         src[i] = (const uint16_t*)base + (int64_t)min(r0 + row, rows - 1) * ld + 8 * chunk;
       } else {
         k[i] = (512 / ROWS) * (INS * w + i) + l / (ROWS / 8);
-        const int c = r0 + 8 * ((l % (ROWS / 8)) ^ nn_swz(k[i]));
+        const int c = r0 + 8 * ((l % (ROWS / 8)) ^ nc_key<ROWS>(k[i]));
         ok[i] = c < rows;
         src[i] = (const uint16_t*)base + (int64_t)k[i] * ld + (ok[i] ? c : 0);
       }
@@ -201,21 +229,25 @@ __device__ __forceinline__ u32x4 tile_frag(const unsigned char* tile, int sub, i
     const int row = row0 + (__lane_id() & 31);
     return *(const u32x4*)(tile + row * (2 * BK) + 16 * kc_key(row, 2 * sub + (__lane_id() >> 5)));
   } else {
-    return tr_frag32(tile, 2 * ROWS, sub, row0);
+    return nc_frag<ROWS>(tile, sub, row0);
   }
 }
 
-// Workgroup = BM x BN outputs, NW waves laid out WM x (NW / WM), STAGES LDS stages
-// of 64 k.  A stage is waited for before the last 16 k of the one in front, so
+// Workgroup = BM x BN outputs by KG groups of NW waves, each group laid out
+// WM x (NW / WM) over the tile and taking every KG-th 64 k of the reduction
+// (the groups' sums are added at the end): two waves on a SIMD hide each other's
+// LDS reads and waits without a smaller wave tile.  STAGES LDS stages of KG x
+// 64 k.  A stage is waited for before the last 16 k of the one in front, so
 // its first fragments are read under those products, and its successor's loads
 // go out in two halves before the next two runs of products.
-template <bool AKC, bool BKC, int BM, int BN, int NW, int WM, int STAGES, bool TAIL>
-__global__ __launch_bounds__(64 * NW, NW / 4) void linear_tile_kernel(LinearProduct g, int depth) {
+template <bool AKC, bool BKC, int BM, int BN, int NW, int WM, int KG, int STAGES, bool TAIL>
+__global__ __launch_bounds__(64 * NW * KG, NW * KG / 4) void linear_tile_kernel(LinearProduct g, int depth) {
   constexpr int BK = 64, SUBS = BK / 16;
   constexpr int TM = BM / WM, TN = BN / (NW / WM), MI = TM / 32, NJ = TN / 32;
-  constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, STAGE = A_BYTES + B_BYTES;
+  constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, GROUP = A_BYTES + B_BYTES, STAGE = KG * GROUP;
   extern __shared__ __attribute__((aligned(16))) unsigned char s_dyn[];
-  const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, l32 = l & 31, hk = l >> 5;
+  const int tid = threadIdx.x, l = tid & 63, l32 = l & 31, hk = l >> 5;
+  const int kg = (tid >> 6) / NW, w = (tid >> 6) % NW;
   const int wm = w % WM, wn = w / WM;
   int mt, nt;
   tile_of(blockIdx.x, (g.M + BM - 1) / BM, (g.N + BN - 1) / BN, depth, mt, nt);
@@ -227,9 +259,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void linear_tile_kernel(LinearProd
   la.init(g.a, g.lda, m0, g.M, w, l);
   lb.init(g.b, g.ldb, n0, g.N, w, l);
   constexpr int INS = Loader<AKC, BM, BK, NW, TAIL>::INS + Loader<BKC, BN, BK, NW, TAIL>::INS;  // loads of a stage
-  // stage s lies in buffer s % STAGES
-  auto issue_a = [&](int s, int buf) { la.issue(kb + s * BK, g.K, s_dyn + buf * STAGE, w); };
-  auto issue_b = [&](int s, int buf) { lb.issue(kb + s * BK, g.K, s_dyn + buf * STAGE + A_BYTES, w); };
+  // stage s lies in buffer s % STAGES; a group loads and reads its own part of it
+  unsigned char* const mine = s_dyn + kg * GROUP;
+  auto issue_a = [&](int s, int buf) { la.issue(kb + (s * KG + kg) * BK, ke, mine + buf * STAGE, w); };
+  auto issue_b = [&](int s, int buf) { lb.issue(kb + (s * KG + kg) * BK, ke, mine + buf * STAGE + A_BYTES, w); };
 
   f32x16 acc[MI][NJ];
 #pragma unroll
@@ -263,7 +296,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void linear_tile_kernel(LinearProd
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  const int steps = (ke - kb + BK - 1) / BK;
+  const int steps = (ke - kb + KG * BK - 1) / (KG * BK);
   static_assert(SUBS == 4, "four runs of products per stage");
   Frags f0, f1;
   for (int s = 0; s < STAGES - 1 && s < steps; ++s) {
@@ -278,16 +311,16 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void linear_tile_kernel(LinearProd
     issue_b(STAGES - 1, STAGES - 1);
   }
 #pragma unroll
-  for (int i = 0; i < MI; ++i) f0.a[i] = tile_frag<AKC, BM, BK>(s_dyn, 0, TM * wm + 32 * i);
+  for (int i = 0; i < MI; ++i) f0.a[i] = tile_frag<AKC, BM, BK>(mine, 0, TM * wm + 32 * i);
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) f0.b[j] = tile_frag<BKC, BN, BK>(s_dyn + A_BYTES, 0, TN * wn + 32 * j);
-  products(f0, s_dyn, 1, f1);
-  products(f1, s_dyn, 2, f0);
-  products(f0, s_dyn, 3, f1);
+  for (int j = 0; j < NJ; ++j) f0.b[j] = tile_frag<BKC, BN, BK>(mine + A_BYTES, 0, TN * wn + 32 * j);
+  products(f0, mine, 1, f1);
+  products(f1, mine, 2, f0);
+  products(f0, mine, 3, f1);
   int buf = 0;  // of stage s - 1, which stage s + STAGES - 1 takes over
   for (int s = 1; s < steps; ++s) {
     const int next = buf + 1 < STAGES ? buf + 1 : 0;
-    const unsigned char* st = s_dyn + next * STAGE;
+    const unsigned char* st = mine + next * STAGE;
     // stage s has landed; of the stages behind it, STAGES - 2 may be in flight
     if (STAGES > 2 && s + STAGES - 2 < steps) wait_vmcnt<(STAGES - 2) * INS>();
     else wait_vmcnt<0>();
@@ -302,7 +335,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void linear_tile_kernel(LinearProd
     products(f0, st, 3, f1);
     buf = next;
   }
-  products(f1, s_dyn, -1, f0);
+  products(f1, mine, -1, f0);
 
   // The fp32 tile leaves through the idle stage buffers, HC columns at a time
   // ([row][HC], 16-byte chunk c of row r at c ^ (r & 15)), so that the epilogue
@@ -316,22 +349,27 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void linear_tile_kernel(LinearProd
 #pragma unroll
   for (int part = 0; part < BN / HC; ++part) {
     barrier_no_fence();  // every wave is done with the stage buffers / the previous part
-    if (TN * wn / HC == part) {
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
+    for (int k2 = 0; k2 < KG; ++k2) {  // the groups in turn: the first writes its sums, the others add theirs
+      if (kg == k2 && TN * wn / HC == part) {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
+        for (int i = 0; i < MI; ++i)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int row = TM * wm + 32 * i + l32, col = TN * wn - HC * part + 32 * j + 8 * q + 4 * hk;
-            *(f32x4*)(s_f + row * HC + 4 * ((col >> 2) ^ (row & 15))) =
-                f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-          }
+          for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int row = TM * wm + 32 * i + l32, col = TN * wn - HC * part + 32 * j + 8 * q + 4 * hk;
+              f32x4* at = (f32x4*)(s_f + row * HC + 4 * ((col >> 2) ^ (row & 15)));
+              f32x4 v = f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+              if (k2 > 0) v += *at;
+              *at = v;
+            }
+      }
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the staged values are written
+      barrier_no_fence();
     }
-    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the staged values are written
-    barrier_no_fence();
 #pragma unroll 2
-    for (int it = tid; it < BM * HC / 8; it += 64 * NW) {
+    for (int it = tid; it < BM * HC / 8; it += 64 * NW * KG) {
       const int row = it / (HC / 8), c8 = it % (HC / 8);
       const int m = m0 + row, n = n0 + HC * part + 8 * c8;
       if (m >= g.M || n >= g.N) continue;  // N is a multiple of 8: a run is all in or all out
@@ -530,27 +568,64 @@ hipError_t add_slices(const LinearProduct& g, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// The workgroup tiles, largest first, and what a pass of them over the chip's
+// 256 CUs takes: `step` us per 64 k (`step_few` when at most 160 workgroups run), `round` us for its prologue
+// and epilogue.  Measured on one MI355X with grids of 128, 256 and 512
+// workgroups and reductions of 512, 2048 and 4096 (all three operand layouts
+// within 8 %).  A larger tile moves fewer bytes through LDS per product (at 256
+// workgroups: 256 x 256 1.32 PFLOP/s, 256 x 128 1.14, 128 x 128 1.01, 128 x 64 0.84, 64 x 64 0.61) but
+// leaves CUs idle where the outputs are few: 4099 x 768 over 2048 takes 49 us
+// on 256 x 256, 30 on 256 x 128, 20.9 on 128 x 128, 25.8 on 128 x 64 tiles.
+struct TileCost {
+  int bm, bn;
+  double step, step_few, round;
+};
+enum { kTile256x256 = 0, kTile256x128, kTile128x128, kTile128x64, kTile64x64, kTilesBf16 };
+constexpr TileCost kCostBf16[kTilesBf16] = {
+    {256, 256, 1.62, 1.13, 8.5}, {256, 128, 0.94, 0.74, 4.5}, {128, 128, 0.53, 0.47, 2.6},
+    {128, 64, 0.33, 0.27, 2.0},  {64, 64, 0.22, 0.19, 1.0}};
+// fp32: the same per 16 k
+enum { kTileF128 = 0, kTileF64, kTilesF32 };
+constexpr TileCost kCostF32[kTilesF32] = {{128, 128, 1.10, 1.10, 4.0}, {64, 64, 0.35, 0.30, 2.0}};
+
+constexpr double kLaunchUs = 3.5;              // one more kernel behind another
+constexpr double kSliceBytesPerUs = 4.0e6;     // partials written and read again
+
 // What runs a product: the tile, and the slices of its reduction.
 struct Plan {
-  int tile;    // rows of the workgroup tile: 256 or 128 (bf16), 128 or 64 (fp32)
+  int tile;
   int slices;
-  int slice;   // k per slice
+  int slice;  // k per slice
 };
 
-constexpr int kCus = 256;
-
+// The plan of least estimated time.  Splitting the reduction pays where few
+// tiles meet a long reduction: 2048 x 768 outputs over 4099 rows take 56 us on
+// 128 x 128 tiles, 31 us in two slices with the sum behind them.
 Plan plan_of(int M, int N, int K, int esize) {
-  Plan p{};
-  auto tiles = [&](int t) { return (int64_t)((M + t - 1) / t) * ((N + t - 1) / t); };
-  const int big = esize == 2 ? 256 : 128, small = big / 2, stage = esize == 2 ? 64 : 16;
-  p.tile = tiles(big) >= 3 * kCus / 2 ? big : small;
-  const int64_t have = tiles(p.tile);
-  int64_t s = std::max<int64_t>(1, kCus / have);
-  s = std::min<int64_t>(s, std::max(1, K / (esize == 2 ? 512 : 128)));
-  s = std::min<int64_t>(s, 16);
-  p.slice = (int)((((int64_t)K + s - 1) / s + stage - 1) / stage * stage);
-  p.slices = (K + p.slice - 1) / p.slice;
-  return p;
+  constexpr int kCus = 256, kFew = 160;
+  const bool bf16 = esize == 2;
+  const int stage = bf16 ? 64 : 16, grain = bf16 ? 128 : 16;
+  Plan best{};
+  double best_us = 0.0;
+  for (int c = 0; c < (bf16 ? (int)kTilesBf16 : (int)kTilesF32); ++c) {
+    const TileCost& t = bf16 ? kCostBf16[c] : kCostF32[c];
+    const int64_t tiles = (int64_t)((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
+    for (int want : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      const int slice = ((K + want - 1) / want + grain - 1) / grain * grain;
+      const int slices = (K + slice - 1) / slice;
+      if (want > 1 && (slices == 1 || tiles * want > 2 * kCus)) break;
+      const int64_t groups = tiles * slices, rest = groups % kCus;
+      const double steps = (double)((std::min(K, slice) + stage - 1) / stage);
+      double us = kLaunchUs + (double)(groups / kCus) * (steps * t.step + t.round);
+      if (rest > 0) us += steps * (rest > kFew ? t.step : t.step_few) + t.round;
+      if (slices > 1) us += kLaunchUs + (double)slices * M * N * 8.0 / kSliceBytesPerUs;
+      if (best.slices == 0 || us < best_us) {
+        best = Plan{c, slices, slice};
+        best_us = us;
+      }
+    }
+  }
+  return best;
 }
 
 size_t plan_bytes(int M, int N, int K, int esize) {
@@ -558,23 +633,24 @@ size_t plan_bytes(int M, int N, int K, int esize) {
   return p.slices > 1 ? (size_t)p.slices * M * N * sizeof(float) : 0;
 }
 
-template <bool AKC, bool BKC, int BM, int BN, int NW, int WM, int STAGES, bool TAIL>
+template <bool AKC, bool BKC, int BM, int BN, int NW, int WM, int KG, int STAGES, bool TAIL>
 hipError_t launch_tiles(const LinearProduct& g, int slices, hipStream_t stream) {
-  constexpr size_t lds = (size_t)STAGES * (BM + BN) * 64 * 2;
-  auto kern = linear_tile_kernel<AKC, BKC, BM, BN, NW, WM, STAGES, TAIL>;
+  constexpr size_t lds = (size_t)STAGES * KG * (BM + BN) * 64 * 2;
+  auto kern = linear_tile_kernel<AKC, BKC, BM, BN, NW, WM, KG, STAGES, TAIL>;
   static PerDeviceOnce once;
   hipError_t err = allow_dynamic_lds(once, (const void*)kern, lds);
   if (err != hipSuccess) return err;
   const int64_t tiles = (int64_t)((g.M + BM - 1) / BM) * ((g.N + BN - 1) / BN);
-  MOE_LAUNCH(kern, dim3((unsigned)tiles, slices), dim3(64 * NW), lds, stream, g, 1024 / BM);
+  MOE_LAUNCH(kern, dim3((unsigned)tiles, slices), dim3(64 * NW * KG), lds, stream, g, 1024 / BM);
   return hipGetLastError();
 }
 
-template <bool AKC, bool BKC, int BM, int BN, int NW, int WM, int STAGES>
+template <bool AKC, bool BKC, int BM, int BN, int NW, int WM, int KG, int STAGES>
 hipError_t launch_bf16(const LinearProduct& g, int slices, hipStream_t stream) {
-  const bool tail = g.K % 64 != 0 || (!BKC && g.N % BN != 0) || (!AKC && g.M % BM != 0);
-  return tail ? launch_tiles<AKC, BKC, BM, BN, NW, WM, STAGES, true>(g, slices, stream)
-              : launch_tiles<AKC, BKC, BM, BN, NW, WM, STAGES, false>(g, slices, stream);
+  // whole stages, in every slice: nothing to mask (a stage that ran past the reduction's end would read past the operands)
+  const bool tail = g.K % (64 * KG) != 0 || (slices > 1 && g.slice % (64 * KG) != 0) || (!BKC && g.N % BN != 0) || (!AKC && g.M % BM != 0);
+  return tail ? launch_tiles<AKC, BKC, BM, BN, NW, WM, KG, STAGES, true>(g, slices, stream)
+              : launch_tiles<AKC, BKC, BM, BN, NW, WM, KG, STAGES, false>(g, slices, stream);
 }
 
 // AKC, BKC: which operands have k contiguous.
@@ -585,14 +661,19 @@ hipError_t product(LinearProduct g, float* ws, hipStream_t stream) {
   g.part = p.slices > 1 ? ws : nullptr;
   hipError_t err;
   if constexpr (std::is_same<T, float>::value) {
-    const int64_t tiles = (int64_t)((g.M + p.tile - 1) / p.tile) * ((g.N + p.tile - 1) / p.tile);
-    const dim3 grid((unsigned)tiles, p.slices);
-    if (p.tile == 128) MOE_LAUNCH((linear_f32_kernel<AKC, BKC, 128>), grid, dim3(256), 0, stream, g, 8);
+    const int bt = kCostF32[p.tile].bm;
+    const dim3 grid((unsigned)((int64_t)((g.M + bt - 1) / bt) * ((g.N + bt - 1) / bt)), p.slices);
+    if (p.tile == kTileF128) MOE_LAUNCH((linear_f32_kernel<AKC, BKC, 128>), grid, dim3(256), 0, stream, g, 8);
     else MOE_LAUNCH((linear_f32_kernel<AKC, BKC, 64>), grid, dim3(256), 0, stream, g, 8);
     err = hipGetLastError();
   } else {
-    err = p.tile == 256 ? launch_bf16<AKC, BKC, 256, 256, 8, 2, 2>(g, p.slices, stream)
-                        : launch_bf16<AKC, BKC, 128, 128, 4, 2, 2>(g, p.slices, stream);
+    switch (p.tile) {
+      case kTile256x256: err = launch_bf16<AKC, BKC, 256, 256, 8, 2, 1, 2>(g, p.slices, stream); break;
+      case kTile256x128: err = launch_bf16<AKC, BKC, 256, 128, 8, 4, 1, 3>(g, p.slices, stream); break;
+      case kTile128x128: err = launch_bf16<AKC, BKC, 128, 128, 4, 2, 2, 2>(g, p.slices, stream); break;
+      case kTile128x64: err = launch_bf16<AKC, BKC, 128, 64, 4, 2, 2, 3>(g, p.slices, stream); break;
+      default: err = launch_bf16<AKC, BKC, 64, 64, 4, 2, 2, 4>(g, p.slices, stream); break;
+    }
   }
   if (err != hipSuccess || p.slices == 1) return err;
   return add_slices<T>(g, stream);

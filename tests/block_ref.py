@@ -48,6 +48,13 @@ def within(name, got, ref, bound):
                           f"{np.broadcast_to(bound, off.shape)[at]:.3e}"
 
 
+def mm(a, b):
+    """a @ b in float64, on the GPU where it is large."""
+    if a.shape[0] * a.shape[1] * b.shape[1] < 1 << 28:
+        return a @ b
+    return (torch.from_numpy(np.ascontiguousarray(a)).cuda() @ torch.from_numpy(np.ascontiguousarray(b)).cuda()).cpu().numpy()
+
+
 # ---- routing by scores ----------------------------------------------------------
 
 
@@ -188,7 +195,7 @@ def slope(a, z):
 
 
 def linear(x, w, bias, a, mul=None, residual=None):
-    z = x @ w + (0 if bias is None else bias)
+    z = mm(x, w) + (0 if bias is None else bias)
     y = act(a, z) * (1 if mul is None else mul)
     return y + (0 if residual is None else residual), z
 

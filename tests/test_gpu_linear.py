@@ -42,7 +42,7 @@ def check_forward(v, dtype, act, bias=True, mul=False, residual=False, save=True
     assert (ws[need:] == 0xAB).all(), "written past the workspace"
     m, r = v["mul"] if mul else None, v["residual"] if residual else None
     ry, rz = R.linear(v["x"], v["w"], v["b"] if bias else None, act, m, r)
-    dz = (I + 2) * 2.0 ** -23 * (np.abs(v["x"]) @ np.abs(v["w"]) + np.abs(v["b"]))
+    dz = (I + 2) * 2.0 ** -23 * (R.mm(np.abs(v["x"]), np.abs(v["w"])) + np.abs(v["b"]))
     if save:
         R.within("z", R.host(z), rz, R.U[dtype] * np.abs(rz) + 1.01 * dz)
     val = np.abs(R.act(act, rz))
@@ -65,6 +65,23 @@ def test_forward(T, I, O, dtype):  # noqa: E741
     v = inputs(T, I, O, dtype, T + I + O)
     check_forward(v, dtype, R.NONE, bias=False, save=False)
     check_forward(v, dtype, R.SILU, bias=True, mul=True, residual=True)
+
+
+LARGE = [  # every workgroup tile with and without masked edges, split reductions, more workgroups than CUs
+    (4096, 2048, 4096, "bf16"), (4090, 2040, 4088, "bf16"), (2500, 1024, 2048, "bf16"), (4099, 2048, 768, "bf16"),
+    (700, 1032, 1000, "bf16"), (40, 4096, 512, "bf16"), (9, 4104, 4096, "bf16"), (1500, 520, 1032, "f32"),
+    (70, 3080, 136, "f32"),
+]
+
+
+@pytest.mark.parametrize("T,I,O,dtype", LARGE)
+def test_forward_large(T, I, O, dtype):  # noqa: E741
+    check_forward(inputs(T, I, O, dtype, T + O), dtype, R.GELU_TANH, mul=True, residual=True)
+
+
+@pytest.mark.parametrize("T,I,O,dtype", LARGE + [(4088, 4090 // 8 * 8, 4080, "bf16"), (8192, 4096, 1408, "bf16"), (8195, 64, 72, "bf16")])
+def test_backward_large(T, I, O, dtype):  # noqa: E741
+    check_backward(inputs(T, I, O, dtype, T + O), dtype, R.SILU, mul=True, add=True)
 
 
 @pytest.mark.parametrize("act", range(5))
@@ -116,19 +133,19 @@ def check_backward(v, dtype, act, bias=True, mul=False, add=False, want=("dx", "
     for name, got, left, right, el, er in (("dx", dx, rz, v["w"].T, stored, 0), ("dw", dw, v["x"].T, rz, 0, stored)):
         if got is None:
             continue
-        ref = left @ right
+        ref = R.mm(left, right)
         n = left.shape[1]
-        size = np.abs(left) @ np.abs(right)
+        size = R.mm(np.abs(left), np.abs(right))
         extra = 0
         if name == "dx" and add:
             ref = ref + v["dx_add"]
             extra = 2.0 ** -23 * (np.abs(v["dx_add"]) + np.abs(ref))
-        slip = (el @ np.abs(right) if name == "dx" else np.abs(left) @ er)
+        slip = 0 if plain else (R.mm(el, np.abs(right)) if name == "dx" else R.mm(np.abs(left), er))
         # rounded dz: elementwise at most `slip`; over the whole result the independent roundings (each at
         # most U of its term) add in squares, so the error's norm is at most sqrt(2) U of the result's size
         R.within(name, R.host(got), ref, R.U[dtype] * np.abs(ref) * 1.01 + (n + 2) * 2.0 ** -23 * size + 1.01 * slip + extra)
         if dtype == "bf16" and ref.size > 4096:
-            quad = np.sqrt(((left ** 2) @ (right ** 2)).sum() + (ref ** 2).sum())
+            quad = np.sqrt(((left ** 2).sum(0) * (right ** 2).sum(1)).sum() * (not plain) + (ref ** 2).sum())
             assert np.linalg.norm(R.host(got) - ref) <= 1.01 * R.U[dtype] * quad, name
 
 
