@@ -25,7 +25,6 @@ struct RouteArgs {
   int32_t* idx;
   float* w;
   int per_lane;  // experts per lane, neighbours: ceil(E / 16)
-  int quads;     // per_lane and E are multiples of 4 and the rows 16-byte aligned
   int on_lanes;  // every group is a whole number of lanes
 };
 
@@ -90,28 +89,30 @@ __device__ __forceinline__ float renormalized(float a, bool on, bool poisoned) {
   return sum == 0.0f ? 0.0f : e / sum;
 }
 
-// Sorts v descending (a bitonic network; N a power of two).
+// Sorts v descending (Batcher's odd-even merge sort; N a power of two).
 template <int N>
 __device__ __forceinline__ void sort_down(uint32_t (&v)[N]) {
 #pragma unroll
-  for (int size = 2; size <= N; size *= 2)
+  for (int p = 1; p < N; p *= 2)
 #pragma unroll
-    for (int stride = size / 2; stride > 0; stride /= 2)
+    for (int q = p; q >= 1; q /= 2)
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int j = i ^ stride;
-        if (j > i) {
-          const uint32_t hi = max(v[i], v[j]), lo = min(v[i], v[j]);
-          const bool down = (i & size) == 0;
-          v[i] = down ? hi : lo;
-          v[j] = down ? lo : hi;
-        }
-      }
+      for (int j = q % p; j + q < N; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const uint32_t hi = max(v[i + j], v[i + j + q]), lo = min(v[i + j], v[i + j + q]);
+            v[i + j] = hi;
+            v[i + j + q] = lo;
+          }
 }
+
+// exp(v) on the hardware's exp2: off by at most (1.5 |v| + 2) 2^-24 of the result.
+__device__ __forceinline__ float quick_exp(float v) { return __builtin_amdgcn_exp2f(v * 1.44269504f); }
 
 template <int V>
 struct RouteLds {
-  double value[4][4][kRow * V];  // wave, token of the wave, expert: what groups are weighed by
+  uint64_t value[4][4][kRow * V];  // wave, token of the wave, expert
   int32_t sel[4][4][kRow];
   float group[4][4][kMaxGroups];
 };
@@ -121,184 +122,190 @@ __device__ __forceinline__ void wave_lds_order() {
   __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");  // the wave's LDS writes before its reads
 }
 
-__device__ __forceinline__ double row_max(double v) {
-#pragma unroll
-  for (int o = 8; o >= 1; o >>= 1) v = fmax(v, __shfl_xor(v, o, kRow));
-  return v;
-}
+__device__ __forceinline__ double as_double(uint64_t u) { return __longlong_as_double((long long)u); }
 
-// The choice of the wave's four tokens in 64 bits, whatever their logits hold;
-// fills sel.  For the rare wave whose fp32 choice scores are too close to tell.
-template <int V>
-__device__ void choose_exactly(const RouteArgs& g, const float* lt, int wv, int tok, int li, RouteLds<V>& s) {
-  const int E = g.E, e0 = li * g.per_lane;
-  float l[V];
-  double sc[V];
-  double m = -__builtin_inf();
-  bool nan = false;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = e0 + i;
-    l[i] = i < g.per_lane && e < E ? lt[e] : -__builtin_inff();
-    nan |= l[i] != l[i];
-    m = fmax(m, (double)l[i]);
-  }
-  m = row_max(m);
-  const bool poisoned = g.score == 0 && (((__ballot(nan) >> (kRow * tok)) & 0xffff) != 0 || m == __builtin_inf());
-  double sum = 0.0;
-  for (int i = 0; i < V; ++i) {
-    if (g.score == 0) sc[i] = l[i] > -__builtin_inff() ? exp((double)l[i] - m) : 0.0;
-    else sc[i] = 1.0 / (1.0 + exp(-(double)l[i]));
-    sum += sc[i];
+// The choice of the wave's four tokens in 64 bits, whatever their logits hold:
+// fills sel, uses `value`, returns whether the token has no scores (softmax with
+// a NaN or +inf).  For the few waves that fp32 cannot decide, so kept short: an
+// unrolled form cost every wave its way through a longer program.
+__device__ __forceinline__ bool choose_exactly(const RouteArgs& g, const float* lt, int tok, int li, uint64_t* value,
+                                               int32_t* sel) {
+  const double inf = __builtin_inf();
+  const int e0 = li * g.per_lane, e1 = min(e0 + g.per_lane, g.E);
+  double m = -inf;
+  bool bad = false;
+  for (int e = e0; e < e1; ++e) {
+    bad |= !(lt[e] < __builtin_inff());
+    m = fmax(m, (double)lt[e]);
   }
 #pragma unroll
-  for (int o = 8; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, kRow);
-  uint64_t key[V];
+  for (int o = 8; o >= 1; o >>= 1) m = fmax(m, __shfl_xor(m, o, kRow));
+  const bool poisoned = g.score == 0 && ((__ballot(bad) >> (kRow * tok)) & 0xffff) != 0;
+  double sum = g.score == 0 ? 0.0 : 1.0;
+#pragma unroll 1
+  for (int e = e0; e < e1; ++e) {
+    const double l = lt[e];
+    double s = l == -inf ? 0.0 : exp(g.score == 0 ? l - m : -l);
+    if (g.score == 0) sum += s;
+    else s = l == -inf ? 0.0 : 1.0 / (1.0 + s);
+    value[e] = (uint64_t)__double_as_longlong(s);
+  }
+  if (g.score == 0)
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = e0 + i;
-    key[i] = 0;
-    if (i >= g.per_lane || e >= E) continue;
-    if (g.score == 0) sc[i] = poisoned ? __builtin_nan("") : (sum > 0.0 ? sc[i] / sum : 0.0);
-    const double c = l[i] == -__builtin_inff() ? -__builtin_inf() : sc[i] + (g.bias != nullptr ? (double)g.bias[e] : 0.0);
+    for (int o = 8; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, kRow);
+  const bool two = g.G > 1 && g.group_top == 2;
+#pragma unroll 1
+  for (int e = e0; e < e1; ++e) {
+    const double l = lt[e];
+    double c = poisoned ? __builtin_nan("") : as_double(value[e]) / (sum > 0.0 ? sum : 1.0);
+    if (g.bias != nullptr) c += (double)g.bias[e];
     // without a bias the logits' own order, which rounding of the scores cannot blur
-    const double by = g.bias != nullptr ? c : (double)l[i];
-    key[i] = order_key64(by);
-    s.value[wv][tok][e] = g.group_top == 1 ? by : c;
+    if (g.bias == nullptr && !two) c = l;
+    value[e] = (uint64_t)__double_as_longlong(l == -inf ? -inf : c);
   }
+  wave_lds_order();
+  uint32_t kept = 0xffffu;
+  const int size = g.E / g.G;
   if (g.G > 1) {
-    wave_lds_order();
-    const int size = E / g.G;
-    uint64_t worth = 0;
-    if (li < g.G) {
-      double a = -__builtin_inf(), b = -__builtin_inf();
-      bool bad = false;
+    double a = -inf, b = -inf;
+    bool nan = false;
+    if (li < g.G)
       for (int j = 0; j < size; ++j) {
-        const double v = s.value[wv][tok][li * size + j];
-        bad |= v != v;
+        const double v = as_double(value[li * size + j]);
+        nan |= v != v;
         b = fmax(b, fmin(a, v));
         a = fmax(a, v);
       }
-      worth = order_key64(bad ? __builtin_nan("") : (g.group_top == 2 && b > -__builtin_inf() ? a + b : a));
-    }
+    const uint64_t worth = order_key64(nan ? __builtin_nan("") : (two && b > -inf ? a + b : a));
     int rank = 0;
     for (int j = 0; j < g.G; ++j) {
       const uint64_t o = __shfl(worth, j, kRow);
       rank += (o > worth || (o == worth && j < li)) ? 1 : 0;
     }
-    const uint32_t kept = (uint32_t)(__ballot(li < g.G && rank < g.top_groups) >> (kRow * tok)) & 0xffffu;
-    const uint64_t out = order_key64(-__builtin_inf());
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (key[i] != 0 && !((kept >> ((e0 + i) / size)) & 1)) key[i] = out;
+    kept = (uint32_t)(__ballot(li < g.G && rank < g.top_groups) >> (kRow * tok)) & 0xffffu;
+    wave_lds_order();
+  }
+#pragma unroll 1
+  for (int e = e0; e < e1; ++e) {
+    const double c = g.bias == nullptr ? (double)lt[e] : as_double(value[e]);
+    value[e] = order_key64((kept >> (e / size)) & 1 ? c : -inf);
   }
   for (int r = 0; r < g.k; ++r) {
     uint64_t best = 0;
-    int at = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        at = i;
+    int at = e0;
+#pragma unroll 4
+    for (int e = e0; e < e1; ++e) {
+      const uint64_t v = value[e];
+      if (v > best) {
+        best = v;
+        at = e;
       }
-    int e = e0 + at;
+    }
 #pragma unroll
     for (int o = 8; o >= 1; o >>= 1) {
       const uint64_t ob = __shfl_xor(best, o, kRow);
-      const int oe = __shfl_xor(e, o, kRow);
-      if (ob > best || (ob == best && oe < e)) {
+      const int oe = __shfl_xor(at, o, kRow);
+      if (ob > best || (ob == best && oe < at)) {
         best = ob;
-        e = oe;
+        at = oe;
       }
     }
-    if (li == 0) s.sel[wv][tok][r] = e;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (e0 + i == e) key[i] = 0;
+    if (li == 0) sel[r] = at;
+    if (at >= e0 && at < e1) value[at] = 0;
   }
+  return poisoned;
 }
 
 // Sixteen lanes per token, four tokens per wave; lane i of a token holds the
-// per_lane experts from per_lane i on, V >= per_lane registers.
+// per_lane experts from per_lane i on in V registers (FULL: all of them, E = 16 V).
 //
-// Choice scores are formed in fp32 and packed into 32-bit keys: the order key
-// with its low four bits given to the expert's place in its lane, so that
-// sorting a lane's keys is min and max, and the lanes' best is a maximum over a DPP row; each
-// round the winner's lane moves up.  Such a key is off by at most 2^-19 of the
-// value, the scores by a few 2^-24 (below); where two neighbours of the sorted k + 1 best, or
-// the last kept and the first dropped group, are nearer than those errors reach, or any value is not finite, the wave decides
-// in 64 bits instead (choose_exactly).  So the choice is always the exact one.
-template <int V>
+// The work is VALU instructions, not bytes (a token's logits are read once): a
+// sort of V keys per lane, then k + 1 rounds of a maximum over 16 lanes.  So choice
+// scores are formed in fp32 and packed into 32-bit keys, the order key with its
+// low four bits given to the expert's place in its lane: sorting is min and
+// max, a round a DPP row maximum, after which the winner's lane moves up.  A
+// key is off by at most 2^-19 of its value, the scores by a few 2^-24 (below).
+// Where two neighbours of the sorted k + 1 best are nearer than that, the 16
+// best are ordered by their 64-bit choice scores; where that does not settle
+// it, or a group is in doubt, or a value is not finite, the wave decides over
+// all experts in 64 bits (choose_exactly).  The choice is the exact one on every path.
+template <int V, bool FULL>
 __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs g) {
   __shared__ RouteLds<V> s;
+  const float inf = __builtin_inff();
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, tok = lane >> 4, li = lane & 15;
   const int64_t t = (int64_t)blockIdx.x * 16 + 4 * wv + tok;
   const bool live = t < g.T;
   const float* lt = g.logits + (live ? t : g.T - 1) * g.E;
-  const int E = g.E, k = g.k, e0 = li * g.per_lane;
-  float l[V];
-  if (V >= 4 && g.quads) {
+  const int E = FULL ? kRow * V : g.E, k = g.k, per_lane = FULL ? V : g.per_lane;
+  const int e0 = li * per_lane, n = FULL ? V : min(max(E - e0, 0), per_lane);  // this lane's experts
+  int32_t* sel = s.sel[wv][tok];
+  // V neighbours from p + e0; past the lane's experts any value of the row
+  auto fetch = [&](const float* p, float (&v)[V]) {
+    if (FULL && V >= 4) {
 #pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      const bool in = i < g.per_lane && e0 + i < E;
-      const f32x4 q = in ? *(const f32x4*)(lt + e0 + i) : f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < V; i += 4) {
+        const f32x4 q = *(const f32x4*)(p + e0 + i);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (i + j < V) l[i + j] = in ? q[j] : -__builtin_inff();
+        for (int j = 0; j < 4 && i + j < V; ++j) v[i + j] = q[j];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = p[FULL ? e0 + i : min(e0 + i, E - 1)];
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) l[i] = i < g.per_lane && e0 + i < E ? lt[e0 + i] : -__builtin_inff();
-  }
-  // what the choice needs: scores only where a bias or a sum meets them
-  const bool by_score = g.bias != nullptr || (g.G > 1 && g.group_top == 2);
-  bool odd = false;  // something fp32 cannot decide
-#pragma unroll
-  for (int i = 0; i < V; ++i) odd |= !(l[i] < __builtin_inff());  // NaN or +inf
-  float top = 0.0f, sum = 1.0f, slack = 0.0f;
+  };
   float c[V];
+  fetch(lt, c);
+  if (!FULL)
 #pragma unroll
-  for (int i = 0; i < V; ++i) c[i] = l[i];
+    for (int i = 0; i < V; ++i) c[i] = i < n ? c[i] : -inf;
+  // scores only where a bias or a sum meets them, or the weights need their sum
+  const bool by_score = g.bias != nullptr || (g.G > 1 && g.group_top == 2);
+  float top = 0.0f, sum = 1.0f, slack = 1e-30f;
   if (g.score == 0 && (by_score || !g.renorm)) {
-    float m = l[0];
+    float m = c[0], ex[V];
 #pragma unroll
-    for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
+    for (int i = 1; i < V; ++i) m = fmaxf(m, c[i]);
     top = row_max(m);
-    odd |= top == -__builtin_inff();
     sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      c[i] = __expf(l[i] - top);
-      sum += c[i];
+      ex[i] = quick_exp(c[i] - top);  // a row of -inf: NaN, which goes the exact way
+      sum += ex[i];
     }
     sum = row_add(sum);
-  }
-  if (by_score) {
-    const float inv = __builtin_amdgcn_rcpf(sum);
-    // |error| of a softmax score: (2.5 |d| + 40) 2^-24 s, d its logit's distance from the largest
-    // (argument and result of exp, the sum of E terms, the quotient), at most 2.5 2^-20 of the
-    // largest score 1 / sum; of a sigmoid 5 2^-24.  Twice that between two scores.
-    slack = g.score == 0 ? inv * 0x1p-17f : 0x1p-20f;
+    if (by_score) {
+      const float inv = __builtin_amdgcn_rcpf(sum);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float sc = g.score == 0 ? c[i] * inv : __builtin_amdgcn_rcpf(1.0f + __expf(-l[i]));
-      float b = 0.0f;
-      if (g.bias != nullptr && i < g.per_lane && e0 + i < E) b = g.bias[e0 + i];
-      odd |= !(fabsf(b) < __builtin_inff());
-      c[i] = l[i] == -__builtin_inff() ? -__builtin_inff() : sc + b;
+      for (int i = 0; i < V; ++i) c[i] = c[i] == -inf ? -inf : ex[i] * inv;
+      // |error| of a softmax score: (2.5 |d| + 40) 2^-24 s, d its logit's distance from the largest
+      // (argument and result of exp, the sum of E terms, the quotient), so at most 2.5 2^-20 of
+      // the largest score 1 / sum; twice that between two
+      slack += inv * 0x1p-17f;
     }
-  } else {
+  } else if (by_score) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) c[i] = l[i];
+    for (int i = 0; i < V; ++i) c[i] = c[i] == -inf ? -inf : __builtin_amdgcn_rcpf(1.0f + quick_exp(-c[i]));
+    slack += 0x1p-20f;  // |error| of a sigmoid: at most 5 2^-24
   }
+  if (g.bias != nullptr) {
+    float b[V];
+    fetch(g.bias, b);
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = c[i] == -inf ? -inf : c[i] + b[i];
+  }
+  bool exactly = false;  // fp32 cannot decide
   uint32_t key[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    key[i] = i < g.per_lane && e0 + i < E ? (order_key32(c[i]) & ~15u) | (uint32_t)(15 - i) : 0u;
+  for (int i = 0; i < V; ++i) {
+    exactly |= (FULL || i < n) && __builtin_amdgcn_classf(c[i], 0x203);  // NaN or +inf
+    key[i] = FULL || i < n ? (order_key32(c[i]) & ~15u) | (uint32_t)(15 - i) : 0u;
+  }
   sort_down(key);
   if (g.G > 1) {
-    float a, b = -__builtin_inff();
+    float a, b = -inf;
     const int lpg = kRow / g.G;  // lanes per group, where groups are whole lanes
+    const int size = E / g.G;
     if (g.on_lanes) {
       a = key_value(key[0]);
       if (V > 1) b = key_value(key[V > 1 ? 1 : 0]);
@@ -309,12 +316,11 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs g) {
       }
     } else {
       float* cs = (float*)s.value[wv][tok];
-      const int size = E / g.G;
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (i < g.per_lane && e0 + i < E) cs[e0 + i] = c[i];
+        if (i < n) cs[e0 + i] = c[i];
       wave_lds_order();
-      a = -__builtin_inff();
+      a = -inf;
       if (li < g.G)
         for (int j = 0; j < size; ++j) {
           const float v = cs[li * size + j];
@@ -322,11 +328,12 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs g) {
           a = fmaxf(a, v);
         }
     }
-    const bool two = g.group_top == 2 && b > -__builtin_inff();
+    const bool two = g.group_top == 2 && b > -inf;
     const float worth = two ? a + b : a;
-    const float size_of = a > -__builtin_inff() ? fabsf(a) + (two ? fabsf(b) : 0.0f) : 0.0f;
+    const float size_of = a > -inf ? fabsf(a) + (two ? fabsf(b) : 0.0f) : 0.0f;
     const float near = 2.5f * 0x1p-19f * row_max(size_of) + 2.0f * slack;
-    if (g.on_lanes ? li % lpg == 0 : li < g.G) s.group[wv][tok][g.on_lanes ? li / lpg : li] = worth;
+    const bool has = g.on_lanes || li < g.G;
+    if (g.on_lanes ? (li & (lpg - 1)) == 0 : has) s.group[wv][tok][g.on_lanes ? li / lpg : li] = worth;
     wave_lds_order();
     int above = 0, not_below = -1;  // groups surely above this lane's, and those not surely below but itself
     for (int j = 0; j < g.G; ++j) {
@@ -334,64 +341,82 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs g) {
       above += o > worth + near ? 1 : 0;
       not_below += o < worth - near ? 0 : 1;
     }
-    const bool has = g.on_lanes || li < g.G;
-    bool keep = above < g.top_groups;
-    odd |= has && keep != (not_below < g.top_groups);
-    if (!g.on_lanes) {
+    const bool keep = above < g.top_groups;
+    exactly |= has && keep != (not_below < g.top_groups);
+    if (g.on_lanes) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = keep ? key[i] : (kKeyNegInf & ~15u) | (uint32_t)(15 - i);
+    } else {
       const uint32_t kept = (uint32_t)(__ballot(has && keep) >> (kRow * tok)) & 0xffffu;
-      const int size = E / g.G;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int at = e0 + 15 - (int)(key[i] & 15u);
         if (key[i] != 0 && !((kept >> (at / size)) & 1)) key[i] = (kKeyNegInf & ~15u) | (key[i] & 15u);
       }
       sort_down(key);
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (key[i] != 0 && !keep) key[i] = (kKeyNegInf & ~15u) | (key[i] & 15u);
     }
   }
-  // the k + 1 best in turn; lane r keeps the r-th
-  const int rounds = k < E ? k + 1 : k;
+  // the best in turn: lane r keeps the r-th; equal keys: the lower lane
   uint32_t mine = 0, last = 0;
-  for (int r = 0; r < rounds; ++r) {
-    const uint32_t m = row_max(key[0]);
-    const bool won = key[0] == m;
-    odd |= __popcll(__ballot(won)) != 4;  // two lanes with one key: a tie
-    if (won && r < k) s.sel[wv][tok][r] = e0 + 15 - (int)(m & 15u);
+  auto next_best = [&](int r) {
+    last = row_max(key[0]);
+    const uint64_t same = __ballot(key[0] == last);
+    const uint32_t row = (uint32_t)(same >> (kRow * tok)) & 0xffffu;
+    const bool won = li == __ffs(row) - 1;
+    if (won && r < kRow) sel[r] = e0 + 15 - (int)(last & 15u);
 #pragma unroll
     for (int i = 0; i < V; ++i) key[i] = won ? (i + 1 < V ? key[i + 1] : 0u) : key[i];
-    if (li == r) mine = m;
-    last = m;
-  }
+    mine = li == r ? last : mine;
+  };
+  const int rounds = k < E ? k + 1 : k;
+  for (int r = 0; r < rounds; ++r) next_best(r);
+  auto apart = [&](float hi, float lo) {
+    return hi - lo > 1.25f * 0x1p-19f * fmaxf(fabsf(hi), lo > -inf ? fabsf(lo) : 0.0f) + slack;
+  };
+  bool close = false;
   {
     const float v = key_value(mine & ~15u);
-    uint32_t after = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)mine, 0x101, 0xf, 0xf, false);  // row_shl:1
-    if (li == k - 1) after = last;
-    const float n = key_value(after & ~15u);
-    const float size_of = fmaxf(fabsf(v), n > -__builtin_inff() ? fabsf(n) : 0.0f);
+    uint32_t after = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)mine, 0x101, 0xf, 0xf, false);  // lane li + 1's
+    if (li == kRow - 1) after = last;                                                             // k = 16
     const bool pair = li < k - 1 || (li == k - 1 && k < E);
-    odd |= pair && !(v - n > 1.25f * 0x1p-19f * size_of + slack + 1e-30f);
-    odd |= li < k && !(v > -__builtin_inff());
+    close = pair && !apart(v, key_value(after & ~15u));
+    exactly |= li < k && !(v > -inf);  // an unavailable expert is listed
   }
-  if (__ballot(odd)) choose_exactly<V>(g, lt, wv, tok, li, s);
+  exactly |= close && (k == kRow || (g.score == 0 && g.bias != nullptr));
+  bool poisoned = false;
+  if (__ballot(close || exactly)) {
+    if (!__ballot(exactly)) {
+      // the 16 best (all of them, where E <= 16) by 64-bit choice scores
+      const int cand = min(E, kRow);
+      for (int r = rounds; r < cand; ++r) next_best(r);
+      const float v = key_value(mine & ~15u);
+      exactly = E > kRow && !apart(__shfl(v, k - 1, kRow), __shfl(v, kRow - 1, kRow));
+      wave_lds_order();
+      const int e = li < cand ? sel[li] : 0;
+      const float le = lt[e];
+      double by = (double)le;
+      if (g.bias != nullptr) by = 1.0 / (1.0 + exp(-by)) + (double)g.bias[e];
+      const uint64_t rank_by = li < cand ? order_key64(v > -inf ? by : -__builtin_inf()) : 0;
+      int rank = 0;
+      for (int j = 0; j < cand; ++j) {
+        const uint64_t o = __shfl(rank_by, j, kRow);
+        const int oe = __shfl(e, j, kRow);
+        rank += (o > rank_by || (o == rank_by && oe < e)) ? 1 : 0;
+      }
+      wave_lds_order();
+      if (li < cand && rank < k) sel[rank] = e;
+    }
+    if (__ballot(exactly)) poisoned = choose_exactly(g, lt, tok, li, s.value[wv][tok], sel);
+  }
   wave_lds_order();
   const bool on = li < k;
-  const int e = on ? s.sel[wv][tok][li] : 0;
+  const int e = on ? sel[li] : 0;
   const float le = lt[e];
-  bool poisoned = false;  // softmax: a NaN or +inf anywhere leaves no score
-  if (g.score == 0) {
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < V; ++i) bad |= !(l[i] < __builtin_inff());
-    poisoned = ((__ballot(bad) >> (kRow * tok)) & 0xffff) != 0;
-  }
   float we;
   if (g.renorm) {
     we = renormalized(log_score(g.score, le), on, poisoned);
   } else if (g.score == 0) {
-    we = poisoned ? __builtin_nanf("") : (le > -__builtin_inff() ? expf(le - top) / sum : 0.0f);
+    we = poisoned ? __builtin_nanf("") : (le > -inf ? expf(le - top) / sum : 0.0f);
   } else {
     we = 1.0f / (1.0f + expf(-le));
   }
@@ -477,22 +502,30 @@ __global__ __launch_bounds__(256) void route_scored_bwd_kernel(int T, int E, int
   }
 }
 
+template <int V>
+hipError_t route_launch(const RouteArgs& g, bool aligned, hipStream_t stream) {
+  const dim3 grid((unsigned)(((int64_t)g.T + 15) / 16)), block(256);
+  if (aligned && g.E == kRow * V) MOE_LAUNCH((route_scored_kernel<V, true>), grid, block, 0, stream, g);
+  else MOE_LAUNCH((route_scored_kernel<V, false>), grid, block, 0, stream, g);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_route_scored(int T, int E, int k, int score, int n_groups, int top_groups, int group_top,
                                bool renormalize, float scale, const float* logits, const float* bias, int32_t* idx,
                                float* w, hipStream_t stream) {
-  RouteArgs g{T, E, k, score, n_groups, top_groups, group_top, (int)renormalize, scale, logits, bias, idx, w, 0, 0, 0};
+  RouteArgs g{T, E, k, score, n_groups, top_groups, group_top, (int)renormalize, scale, logits, bias, idx, w, 0, 0};
   g.per_lane = (E + kRow - 1) / kRow;
-  g.quads = g.per_lane % 4 == 0 && E % 4 == 0 && ((uintptr_t)logits & 15) == 0;
   g.on_lanes = E % kRow == 0 && kRow % n_groups == 0;
-  const dim3 grid((unsigned)(((int64_t)T + 15) / 16)), block(256);
-  if (g.per_lane <= 1) MOE_LAUNCH((route_scored_kernel<1>), grid, block, 0, stream, g);
-  else if (g.per_lane <= 2) MOE_LAUNCH((route_scored_kernel<2>), grid, block, 0, stream, g);
-  else if (g.per_lane <= 4) MOE_LAUNCH((route_scored_kernel<4>), grid, block, 0, stream, g);
-  else if (g.per_lane <= 8) MOE_LAUNCH((route_scored_kernel<8>), grid, block, 0, stream, g);
-  else MOE_LAUNCH((route_scored_kernel<16>), grid, block, 0, stream, g);
-  return hipGetLastError();
+  const bool aligned = (((uintptr_t)logits | (uintptr_t)bias) & 15) == 0;
+  switch (g.per_lane) {
+    case 1: return route_launch<1>(g, aligned, stream);
+    case 2: return route_launch<2>(g, aligned, stream);
+    case 3: case 4: return route_launch<4>(g, aligned, stream);
+    case 5: case 6: case 7: case 8: return route_launch<8>(g, aligned, stream);
+    default: return route_launch<16>(g, aligned, stream);
+  }
 }
 
 hipError_t launch_route_scored_bwd(int T, int E, int k, int score, bool renormalize, float scale, const float* logits,
