@@ -124,94 +124,118 @@ __device__ __forceinline__ void wave_lds_order() {
 
 __device__ __forceinline__ double as_double(uint64_t u) { return __longlong_as_double((long long)u); }
 
-// The choice of the wave's four tokens in 64 bits, whatever their logits hold:
+__device__ __forceinline__ double wave_sum64(double v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, kWave);
+  return v;
+}
+
+// The choice of one token in 64 bits by the whole wave, whatever its logits hold:
 // fills sel, uses `value`, returns whether the token has no scores (softmax with
-// a NaN or +inf).  For the few waves that fp32 cannot decide, so kept short: an
-// unrolled form cost every wave its way through a longer program.
-__device__ __forceinline__ bool choose_exactly(const RouteArgs& g, const float* lt, int tok, int li, uint64_t* value,
-                                               int32_t* sel) {
+// a NaN or +inf).  For the few tokens that fp32 cannot decide; lane l holds the
+// experts l + 64 i.
+__device__ __forceinline__ bool choose_exactly(const RouteArgs& g, const float* lt, uint64_t* value, int32_t* sel) {
+  constexpr int P = kMaxExperts / kWave;
   const double inf = __builtin_inf();
-  const int e0 = li * g.per_lane, e1 = min(e0 + g.per_lane, g.E);
-  double m = -inf;
+  const int lane = threadIdx.x & 63;
+  double l[P], c[P], m = -inf;
   bool bad = false;
-  for (int e = e0; e < e1; ++e) {
-    bad |= !(lt[e] < __builtin_inff());
-    m = fmax(m, (double)lt[e]);
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int e = lane + kWave * i;
+    l[i] = e < g.E ? (double)lt[e] : -inf;
+    bad |= !(l[i] < inf);
+    m = fmax(m, l[i]);
   }
 #pragma unroll
-  for (int o = 8; o >= 1; o >>= 1) m = fmax(m, __shfl_xor(m, o, kRow));
-  const bool poisoned = g.score == 0 && ((__ballot(bad) >> (kRow * tok)) & 0xffff) != 0;
-  double sum = g.score == 0 ? 0.0 : 1.0;
-#pragma unroll 1
-  for (int e = e0; e < e1; ++e) {
-    const double l = lt[e];
-    double s = l == -inf ? 0.0 : exp(g.score == 0 ? l - m : -l);
-    if (g.score == 0) sum += s;
-    else s = l == -inf ? 0.0 : 1.0 / (1.0 + s);
-    value[e] = (uint64_t)__double_as_longlong(s);
-  }
-  if (g.score == 0)
-#pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, kRow);
+  for (int o = 32; o >= 1; o >>= 1) m = fmax(m, __shfl_xor(m, o, kWave));
+  const bool poisoned = g.score == 0 && __ballot(bad) != 0;
   const bool two = g.G > 1 && g.group_top == 2;
-#pragma unroll 1
-  for (int e = e0; e < e1; ++e) {
-    const double l = lt[e];
-    double c = poisoned ? __builtin_nan("") : as_double(value[e]) / (sum > 0.0 ? sum : 1.0);
-    if (g.bias != nullptr) c += (double)g.bias[e];
-    // without a bias the logits' own order, which rounding of the scores cannot blur
-    if (g.bias == nullptr && !two) c = l;
-    value[e] = (uint64_t)__double_as_longlong(l == -inf ? -inf : c);
+  if (g.bias != nullptr || two) {
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      c[i] = l[i] == -inf ? 0.0 : exp(g.score == 0 ? l[i] - m : -l[i]);
+      sum += c[i];
+    }
+    if (g.score == 0) sum = wave_sum64(sum);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int e = lane + kWave * i;
+      c[i] = g.score == 0 ? c[i] / (sum > 0.0 ? sum : 1.0) : 1.0 / (1.0 + c[i]);
+      if (poisoned) c[i] = __builtin_nan("");
+      if (g.bias != nullptr) c[i] += (double)g.bias[min(e, g.E - 1)];
+      if (l[i] == -inf) c[i] = -inf;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; ++i) c[i] = l[i];
   }
-  wave_lds_order();
   uint32_t kept = 0xffffu;
   const int size = g.E / g.G;
   if (g.G > 1) {
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (lane + kWave * i < g.E) value[lane + kWave * i] = (uint64_t)__double_as_longlong(c[i]);
+    wave_lds_order();
+    // four lanes per group
+    const int grp = lane & 15;
     double a = -inf, b = -inf;
     bool nan = false;
-    if (li < g.G)
-      for (int j = 0; j < size; ++j) {
-        const double v = as_double(value[li * size + j]);
+    if (grp < g.G)
+#pragma unroll 2
+      for (int j = lane >> 4; j < size; j += 4) {
+        const double v = as_double(value[grp * size + j]);
         nan |= v != v;
         b = fmax(b, fmin(a, v));
         a = fmax(a, v);
       }
+#pragma unroll
+    for (int o = 16; o <= 32; o *= 2) {
+      const double a2 = __shfl_xor(a, o, kWave), b2 = __shfl_xor(b, o, kWave);
+      b = fmax(fmin(a, a2), fmax(b, b2));
+      a = fmax(a, a2);
+      nan |= __shfl_xor((int)nan, o, kWave) != 0;
+    }
     const uint64_t worth = order_key64(nan ? __builtin_nan("") : (two && b > -inf ? a + b : a));
     int rank = 0;
+#pragma unroll 4
     for (int j = 0; j < g.G; ++j) {
       const uint64_t o = __shfl(worth, j, kRow);
-      rank += (o > worth || (o == worth && j < li)) ? 1 : 0;
+      rank += (o > worth || (o == worth && j < grp)) ? 1 : 0;
     }
-    kept = (uint32_t)(__ballot(li < g.G && rank < g.top_groups) >> (kRow * tok)) & 0xffffu;
-    wave_lds_order();
+    kept = (uint32_t)__ballot(grp < g.G && rank < g.top_groups) & 0xffffu;
   }
-#pragma unroll 1
-  for (int e = e0; e < e1; ++e) {
-    const double c = g.bias == nullptr ? (double)lt[e] : as_double(value[e]);
-    value[e] = order_key64((kept >> (e / size)) & 1 ? c : -inf);
+  uint64_t key[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int e = lane + kWave * i;
+    // without a bias the logits' own order, which rounding of the scores cannot blur
+    const double by = g.bias == nullptr ? l[i] : c[i];
+    key[i] = e < g.E ? order_key64((kept >> (e / size)) & 1 ? by : -inf) : 0;
   }
   for (int r = 0; r < g.k; ++r) {
-    uint64_t best = 0;
-    int at = e0;
-#pragma unroll 4
-    for (int e = e0; e < e1; ++e) {
-      const uint64_t v = value[e];
-      if (v > best) {
-        best = v;
-        at = e;
-      }
-    }
+    uint64_t best = key[0];
+    int at = lane;
 #pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) {
-      const uint64_t ob = __shfl_xor(best, o, kRow);
-      const int oe = __shfl_xor(at, o, kRow);
+    for (int i = 1; i < P; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        at = lane + kWave * i;
+      }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) {
+      const uint64_t ob = __shfl_xor(best, o, kWave);
+      const int oe = __shfl_xor(at, o, kWave);
       if (ob > best || (ob == best && oe < at)) {
         best = ob;
         at = oe;
       }
     }
-    if (li == 0) sel[r] = at;
-    if (at >= e0 && at < e1) value[at] = 0;
+    if (lane == 0) sel[r] = at;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (at == lane + kWave * i) key[i] = 0;
   }
   return poisoned;
 }
@@ -227,8 +251,8 @@ __device__ __forceinline__ bool choose_exactly(const RouteArgs& g, const float* 
 // key is off by at most 2^-19 of its value, the scores by a few 2^-24 (below).
 // Where two neighbours of the sorted k + 1 best are nearer than that, the 16
 // best are ordered by their 64-bit choice scores; where that does not settle
-// it, or a group is in doubt, or a value is not finite, the wave decides over
-// all experts in 64 bits (choose_exactly).  The choice is the exact one on every path.
+// it, or a group is in doubt, or a value is not finite, the wave decides that
+// token over all experts in 64 bits (choose_exactly).  The choice is the exact one on every path.
 template <int V, bool FULL>
 __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs g) {
   __shared__ RouteLds<V> s;
@@ -302,13 +326,21 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs g) {
     key[i] = FULL || i < n ? (order_key32(c[i]) & ~15u) | (uint32_t)(15 - i) : 0u;
   }
   sort_down(key);
+  // whether one key's value surely lies above another's
+  auto apart = [&](float hi, float lo) {
+    return hi - lo > 1.25f * 0x1p-19f * fmaxf(fabsf(hi), lo > -inf ? fabsf(lo) : 0.0f) + slack;
+  };
   if (g.G > 1) {
     float a, b = -inf;
     const int lpg = kRow / g.G;  // lanes per group, where groups are whole lanes
     const int size = E / g.G;
     if (g.on_lanes) {
-      a = key_value(key[0]);
-      if (V > 1) b = key_value(key[V > 1 ? 1 : 0]);
+      a = c[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) {
+        b = __builtin_amdgcn_fmed3f(a, b, c[i]);
+        a = fmaxf(a, c[i]);
+      }
       for (int o = 1; o < lpg; o <<= 1) {
         const float a2 = __shfl_xor(a, o, kRow), b2 = __shfl_xor(b, o, kRow);
         b = fmaxf(fminf(a, a2), fmaxf(b, b2));
@@ -331,18 +363,57 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs g) {
     const bool two = g.group_top == 2 && b > -inf;
     const float worth = two ? a + b : a;
     const float size_of = a > -inf ? fabsf(a) + (two ? fabsf(b) : 0.0f) : 0.0f;
-    const float near = 2.5f * 0x1p-19f * row_max(size_of) + 2.0f * slack;
+    // two scores each, and the roundings of two sums with the bias and of their sum
+    const float near = by_score ? 2.0f * slack + 0x1p-21f * row_max(size_of) : 0.0f;
     const bool has = g.on_lanes || li < g.G;
     if (g.on_lanes ? (li & (lpg - 1)) == 0 : has) s.group[wv][tok][g.on_lanes ? li / lpg : li] = worth;
     wave_lds_order();
-    int above = 0, not_below = -1;  // groups surely above this lane's, and those not surely below but itself
+    int above = 0, not_below = 0;  // groups surely above this lane's, and those not surely below
+    const int own = g.on_lanes ? li / lpg : li;
     for (int j = 0; j < g.G; ++j) {
       const float o = s.group[wv][tok][j];
-      above += o > worth + near ? 1 : 0;
-      not_below += o < worth - near ? 0 : 1;
+      if (j == own) continue;
+      if (by_score) {
+        above += o > worth + near ? 1 : 0;
+        not_below += o < worth - near ? 0 : 1;
+      } else {
+        const int is = o > worth || (o == worth && j < own) ? 1 : 0;
+        above += is;
+        not_below += is;
+      }
     }
-    const bool keep = above < g.top_groups;
-    exactly |= has && keep != (not_below < g.top_groups);
+    bool keep = above < g.top_groups;
+    const bool doubt = has && keep != (not_below < g.top_groups);
+    if (V > 1 && g.on_lanes && g.score == 1) {
+      if (__ballot(doubt)) {
+        // the worths again from 64-bit scores of each lane's two best
+        double best[2];
+#pragma unroll 1
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t q = j ? key[1] : key[0];
+          const int e = e0 + 15 - (int)(q & 15u);
+          const double v = 1.0 / (1.0 + exp(-(double)lt[e])) + (g.bias != nullptr ? (double)g.bias[e] : 0.0);
+          best[j] = q > kKeyNegInf ? v : -__builtin_inf();
+        }
+        // the third best may be the second in truth
+        if (V > 2 && !apart(key_value(key[1] & ~15u), key_value(key[V > 2 ? 2 : 0] & ~15u))) exactly = true;
+        double a2 = fmax(best[0], best[1]), b2 = fmin(best[0], best[1]);
+        for (int o = 1; o < lpg; o <<= 1) {
+          const double a3 = __shfl_xor(a2, o, kRow), b3 = __shfl_xor(b2, o, kRow);
+          b2 = fmax(fmin(a2, a3), fmax(b2, b3));
+          a2 = fmax(a2, a3);
+        }
+        const uint64_t worth2 = order_key64(g.group_top == 2 && b2 > -__builtin_inf() ? a2 + b2 : a2);
+        int rank = 0;
+        for (int j = 0; j < g.G; ++j) {
+          const uint64_t o = __shfl(worth2, j * lpg, kRow);
+          rank += (o > worth2 || (o == worth2 && j < own)) ? 1 : 0;
+        }
+        keep = rank < g.top_groups;
+      }
+    } else {
+      exactly |= doubt;
+    }
     if (g.on_lanes) {
 #pragma unroll
       for (int i = 0; i < V; ++i) key[i] = keep ? key[i] : (kKeyNegInf & ~15u) | (uint32_t)(15 - i);
@@ -370,9 +441,6 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs g) {
   };
   const int rounds = k < E ? k + 1 : k;
   for (int r = 0; r < rounds; ++r) next_best(r);
-  auto apart = [&](float hi, float lo) {
-    return hi - lo > 1.25f * 0x1p-19f * fmaxf(fabsf(hi), lo > -inf ? fabsf(lo) : 0.0f) + slack;
-  };
   bool close = false;
   {
     const float v = key_value(mine & ~15u);
@@ -382,15 +450,18 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs g) {
     close = pair && !apart(v, key_value(after & ~15u));
     exactly |= li < k && !(v > -inf);  // an unavailable expert is listed
   }
-  exactly |= close && (k == kRow || (g.score == 0 && g.bias != nullptr));
+  const bool few = k < kRow && (g.score == 1 || g.bias == nullptr);  // the 16 best can settle it
+  exactly |= close && !few;
   bool poisoned = false;
   if (__ballot(close || exactly)) {
-    if (!__ballot(exactly)) {
+    const uint64_t ties = __ballot(close);
+    if (few && ties) {
       // the 16 best (all of them, where E <= 16) by 64-bit choice scores
       const int cand = min(E, kRow);
       for (int r = rounds; r < cand; ++r) next_best(r);
       const float v = key_value(mine & ~15u);
-      exactly = E > kRow && !apart(__shfl(v, k - 1, kRow), __shfl(v, kRow - 1, kRow));
+      const bool settled = E <= kRow || apart(__shfl(v, k - 1, kRow), __shfl(v, kRow - 1, kRow));
+      exactly |= ((ties >> (kRow * tok)) & 0xffffu) != 0 && !settled;
       wave_lds_order();
       const int e = li < cand ? sel[li] : 0;
       const float le = lt[e];
@@ -406,7 +477,14 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs g) {
       wave_lds_order();
       if (li < cand && rank < k) sel[rank] = e;
     }
-    if (__ballot(exactly)) poisoned = choose_exactly(g, lt, tok, li, s.value[wv][tok], sel);
+    const uint64_t open = __ballot(exactly);
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+      if (((open >> (kRow * q)) & 0xffffu) == 0) continue;
+      const int64_t tq = min((int64_t)blockIdx.x * 16 + 4 * wv + q, (int64_t)g.T - 1);
+      const bool none = choose_exactly(g, g.logits + tq * g.E, s.value[wv][q], s.sel[wv][q]);
+      if (q == tok) poisoned = none;
+    }
   }
   wave_lds_order();
   const bool on = li < k;
