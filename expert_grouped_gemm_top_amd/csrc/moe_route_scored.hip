@@ -504,79 +504,114 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs g) {
   }
 }
 
-// One wave per token: lanes j < k hold the selected pairs' terms, then every
-// lane writes its experts' entries once.
+// The backward: sixteen lanes per token as in the forward.  Lanes j < k hold the
+// selected pairs' terms (an index listed twice: each holds the sum of its
+// terms, added in list order), which go through an LDS row of zeros so that
+// every lane writes whole runs of the token's dlogits once.  HBM-bound: the
+// output, and for plain softmax (DENSE, the only one whose gradient reaches
+// every expert) the logits.  QUAD: runs of four experts, every sixteenth run
+// of a lane; otherwise single experts.
+template <bool QUAD, bool DENSE>
 __global__ __launch_bounds__(256) void route_scored_bwd_kernel(int T, int E, int k, int score, int renorm, float scale,
                                                                const float* __restrict__ logits,
                                                                const int32_t* __restrict__ idx,
-                                                               const float* __restrict__ dg,
-                                                               float* __restrict__ dl) {
-  const int lane = threadIdx.x & 63;
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= T) return;  // whole wave
-  const float* lt = logits + (size_t)t * E;
-  const bool dense = score == 0 && !renorm;
-  float m = 0.0f, sum = 1.0f;
-  float l[4];
-  if (dense) {
-    m = -__builtin_inff();
-    bool nan = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = lane + 64 * i;
-      l[i] = e < E ? lt[e] : -__builtin_inff();
-      nan |= l[i] != l[i];
-      m = fmaxf(m, l[i]);
-    }
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, kWave));
-    if (__ballot(nan)) m = __builtin_nanf("");
-    sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      l[i] = l[i] == -__builtin_inff() ? 0.0f : expf(l[i] - m);  // NaN where the row is
-      sum += l[i];
-    }
-    sum = wave_sum(sum);
-  }
+                                                               const float* __restrict__ dg, float* __restrict__ dl) {
+  constexpr int R = QUAD ? 4 : 1, N = kMaxExperts / (kRow * R);  // experts per run, runs per lane
+  __shared__ __attribute__((aligned(16))) float s_d[4][4][kMaxExperts];
+  const float inf = __builtin_inff();
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, tok = lane >> 4, li = lane & 15;
+  const int64_t row = (int64_t)blockIdx.x * 16 + 4 * wv + tok;
+  const bool live = row < T;
+  const int64_t t = live ? row : T - 1;
+  const float* lt = logits + t * E;
+  float* d_row = s_d[wv][tok];
   int e_l = -1;
-  float g = 0.0f, a = -__builtin_inff();
-  if (lane < k) {
-    const int e = idx[(size_t)t * k + lane];
+  float g = 0.0f, a = -inf;
+  if (li < k) {
+    const int e = idx[t * k + li];
     if (e >= 0 && e < E) {
       e_l = e;
-      g = dg[(size_t)t * k + lane];
+      g = dg[t * k + li];
       a = lt[e];
     }
   }
-  float d;
-  float sg = 0.0f;  // dense: sum_i s_i g_i
-  const bool avail = e_l >= 0 && a != -__builtin_inff();
+  float l[N][R];
+  float m = -inf, sum = 1.0f;
+  if (DENSE) {
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = R * (li + kRow * i);
+      if (QUAD) {
+        const f32x4 q = e < E ? *(const f32x4*)(lt + e) : f32x4{-inf, -inf, -inf, -inf};
+#pragma unroll
+        for (int j = 0; j < R; ++j) l[i][j] = q[j];
+      } else {
+        l[i][0] = e < E ? lt[e] : -inf;
+      }
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        nan |= l[i][j] != l[i][j];
+        m = fmaxf(m, l[i][j]);
+      }
+    }
+    m = row_max(m);
+    if ((__ballot(nan) >> (kRow * tok)) & 0xffff) m = __builtin_nanf("");
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        l[i][j] = l[i][j] == -inf ? 0.0f : quick_exp(l[i][j] - m);  // NaN where the row is
+        sum += l[i][j];
+      }
+    sum = row_add(sum);
+  }
+  const bool avail = e_l >= 0 && a != -inf;
   const float s = score == 0 ? 0.0f : 1.0f / (1.0f + expf(-a));
+  float d, sg = 0.0f;  // DENSE: sg = sum_i s_i g_i
   if (renorm) {
-    const float p = renormalized(log_score(score, a), lane < 16 && e_l >= 0, false);
-    float pg = avail ? p * g : 0.0f;
-    pg = wave_sum(lane < 16 ? pg : 0.0f);
+    const float p = renormalized(log_score(score, a), e_l >= 0, false);
+    const float pg = row_add(avail ? p * g : 0.0f);
     d = scale * p * (g - pg) * (score == 0 ? 1.0f : 1.0f - s);
-  } else if (dense) {
+  } else if (DENSE) {
     const float se = avail ? expf(a - m) / sum : 0.0f;
-    sg = wave_sum(avail ? se * g : 0.0f);
+    sg = row_add(avail ? se * g : 0.0f);
     d = scale * se * g;
   } else {
     d = scale * g * s * (1.0f - s);
   }
   if (!avail) d = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int e = lane + 64 * i;
-    float v = 0.0f;
-    if (dense) v = sum == 0.0f ? 0.0f : -scale * (l[i] / sum) * sg;
-    for (int j = 0; j < k; ++j) {
-      const int ej = __builtin_amdgcn_readlane(e_l, j);
-      const float dj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(d), j));
-      if (ej == e) v += dj;
+  for (int i = 0; i < N; ++i) {
+    const int e = R * (li + kRow * i);
+    if (QUAD) *(f32x4*)(d_row + e) = f32x4{0.f, 0.f, 0.f, 0.f};
+    else d_row[e] = 0.0f;
+  }
+  float total = 0.0f;
+  for (int j = 0; j < k; ++j) {
+    const int ej = __shfl(e_l, j, kRow);
+    const float dj = __shfl(d, j, kRow);
+    total += ej == e_l ? dj : 0.0f;
+  }
+  wave_lds_order();
+  if (e_l >= 0) d_row[e_l] = total;
+  wave_lds_order();
+  const float back = DENSE && sum > 0.0f ? -scale * sg / sum : (sum != sum ? sum : 0.0f);
+  float* out = dl + t * E;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int e = R * (li + kRow * i);
+    if (e >= E || !live) continue;
+    if (QUAD) {
+      f32x4 q = *(const f32x4*)(d_row + e);
+      if (DENSE)
+#pragma unroll
+        for (int j = 0; j < R; ++j) q[j] += back * l[i][j];
+      *(f32x4*)(out + e) = q;
+    } else {
+      out[e] = DENSE ? d_row[e] + back * l[i][0] : d_row[e];
     }
-    if (e < E) dl[(size_t)t * E + e] = v;
   }
 }
 
@@ -608,9 +643,14 @@ hipError_t launch_route_scored(int T, int E, int k, int score, int n_groups, int
 
 hipError_t launch_route_scored_bwd(int T, int E, int k, int score, bool renormalize, float scale, const float* logits,
                                    const int32_t* idx, const float* dg, float* dlogits, hipStream_t stream) {
-  MOE_LAUNCH(route_scored_bwd_kernel, dim3((T + 3) / 4), dim3(256), 0, stream, T, E, k, score, (int)renormalize,
-             scale, logits, idx, dg, dlogits);
-  return hipGetLastError();
+  const dim3 grid((unsigned)(((int64_t)T + 15) / 16)), block(256);
+  const bool quad = E % 4 == 0 && (((uintptr_t)logits | (uintptr_t)dlogits) & 15) == 0;
+  auto run = [&](auto kernel) {
+    MOE_LAUNCH(kernel, grid, block, 0, stream, T, E, k, score, (int)renormalize, scale, logits, idx, dg, dlogits);
+    return hipGetLastError();
+  };
+  if (score == 0 && !renormalize) return quad ? run(route_scored_bwd_kernel<true, true>) : run(route_scored_bwd_kernel<false, true>);
+  return quad ? run(route_scored_bwd_kernel<true, false>) : run(route_scored_bwd_kernel<false, false>);
 }
 
 }  // namespace moe
