@@ -21,14 +21,30 @@ enum Act { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu 
 constexpr float kTanhA = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kTanhB = 0.044715f;
 
-// 1 / (1 + exp(-v))
-__device__ __forceinline__ float logistic(float v) { return 1.0f / (1.0f + expf(-v)); }
+// exp(v) and 1 / (1 + exp(-v)) on the hardware's exp2 and reciprocal: relative
+// errors of at most (1.5 |v| + 2) 2^-24 and of that share of exp(-v) plus 2^-22
+// (the library's expf, erfcf and division took 7 of 28 us of a GELU product's
+// epilogue at 4099 x 768).
+__device__ __forceinline__ float quick_exp(float v) { return __builtin_amdgcn_exp2f(v * 1.44269504f); }
+__device__ __forceinline__ float logistic(float v) { return __builtin_amdgcn_rcpf(1.0f + quick_exp(-v)); }
+
+// Phi(z), the normal distribution: erfc(|z| / sqrt 2) / 2 by formula 7.1.26 of
+// Abramowitz and Stegun, erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + p x),
+// |error| <= 1.5e-7, mirrored for z > 0.
+__device__ __forceinline__ float normal_cdf(float z) {
+  const float x = fabsf(z) * 0.70710678f;
+  const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * x);
+  const float poly =
+      t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+  const float tail = 0.5f * poly * quick_exp(-x * x);
+  return z > 0.0f ? 1.0f - tail : tail;
+}
 
 // act(z); NaN stays NaN.
 __device__ __forceinline__ float act_value(int act, float z) {
   switch (act) {
     case kActRelu: return z < 0.0f ? 0.0f : z;
-    case kActGelu: return 0.5f * z * erfcf(-0.70710678118654752f * z);
+    case kActGelu: return z * normal_cdf(z);
     case kActGeluTanh: return z * logistic(2.0f * kTanhA * (z + kTanhB * z * z * z));  // (1 + tanh u) / 2 = logistic(2 u)
     case kActSilu: return z * logistic(z);
     default: return z;
@@ -45,9 +61,9 @@ __device__ __forceinline__ void act_both(int act, float z, float& value, float& 
       return;
     case kActGelu: {
       const float c = z > 30.0f ? 30.0f : (z < -30.0f ? -30.0f : z);
-      const float phi = 0.5f * erfcf(-0.70710678118654752f * c);
+      const float phi = normal_cdf(c);
       value = z * phi;
-      slope = phi + c * 0.3989422804014327f * expf(-0.5f * c * c);
+      slope = phi + c * 0.3989422804014327f * quick_exp(-0.5f * c * c);
       return;
     }
     case kActGeluTanh: {

@@ -32,6 +32,36 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
 __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
   *(u32x4*)p = u32x4{pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]), pack_bf2(v[6], v[7])};
 }
+// The same, past the caches where `stream` (rows that no cache would hold until they are read again).
+__device__ __forceinline__ void store8(float* p, const float (&v)[8], bool stream) {
+  if (!stream) return store8(p, v);
+  __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, (f32x4*)p);
+  __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, (f32x4*)(p + 4));
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8], bool stream) {
+  if (!stream) return store8(p, v);
+  __builtin_nontemporal_store(u32x4{pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]),
+                                    pack_bf2(v[6], v[7])}, (u32x4*)p);
+}
+
+// Eight elements as they lie in memory, to be converted later (a load in flight).
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<float> {
+  f32x4 lo, hi;
+  __device__ __forceinline__ void load(const float* p) {
+    lo = *(const f32x4*)p;
+    hi = *(const f32x4*)(p + 4);
+  }
+  __device__ __forceinline__ float get(int j) const { return j < 4 ? lo[j] : hi[j - 4]; }
+};
+template <>
+struct Raw8<uint16_t> {
+  u32x4 v;
+  __device__ __forceinline__ void load(const uint16_t* p) { v = *(const u32x4*)p; }
+  __device__ __forceinline__ float get(int j) const { return (j & 1) ? bf_hi(v[j >> 1]) : bf_lo(v[j >> 1]); }
+};
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = (uint16_t)f2bf(v); }
 
