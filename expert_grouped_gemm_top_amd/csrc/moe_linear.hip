@@ -5,6 +5,7 @@
 //   dz = dy [* mul] act'(z),  dmul = dy act(z),
 //   dx = dz W^T [+ dx_add],  dW = x^T dz,  dbias = sum_t dz
 #include <algorithm>
+#include <iterator>
 #include <type_traits>
 
 #include "moe_common.h"
@@ -249,26 +250,36 @@ __device__ __forceinline__ u32x4 tile_frag(const unsigned char* tile, int sub, i
   }
 }
 
-// Workgroup = BM x BN outputs by KG groups of NW waves, each group laid out
+// A workgroup tile: BM x BN outputs by KG groups of NW waves, each group laid out
 // WM x (NW / WM) over the tile and taking every KG-th 64 k of the reduction
 // (the groups' sums are added at the end): two waves on a SIMD hide each other's
 // LDS reads and waits without a smaller wave tile.  STAGES LDS stages of KG x
-// 64 k.  A stage is waited for before the last 16 k of the one in front, so
-// its first fragments are read under those products, and its successor's loads
-// go out in two halves before the next two runs of products.
-template <bool AKC, bool BKC, int BM, int BN, int NW, int WM, int KG, int STAGES, bool TAIL>
-__global__ __launch_bounds__(64 * NW * KG, NW * KG / 4) void linear_tile_kernel(LinearProduct g, int depth) {
+// 64 k.  All have eight waves, one workgroup per CU.
+template <int BM_, int BN_, int NW_, int WM_, int KG_, int STAGES_>
+struct Tile {
+  static constexpr int BM = BM_, BN = BN_, NW = NW_, WM = WM_, KG = KG_, STAGES = STAGES_;
+  static constexpr int LDS = STAGES * KG * (BM + BN) * 64 * 2;
+  static_assert(NW * KG == 8 && LDS <= 160 * 1024, "eight waves, one CU's LDS");
+};
+constexpr int kThreads = 512;
+
+// Output tile `tile` of the product over slice `slice` of its reduction.  A stage
+// is waited for before the last 16 k of the one in front, so its first
+// fragments are read under those products, and its successor's loads go out in
+// two halves before the next two runs of products.
+template <bool AKC, bool BKC, typename C, bool TAIL>
+__device__ __forceinline__ void tile_product(const LinearProduct& g, int tile, int slice, unsigned char* s_dyn) {
+  constexpr int BM = C::BM, BN = C::BN, NW = C::NW, WM = C::WM, KG = C::KG, STAGES = C::STAGES;
   constexpr int BK = 64, SUBS = BK / 16;
   constexpr int TM = BM / WM, TN = BN / (NW / WM), MI = TM / 32, NJ = TN / 32;
   constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, GROUP = A_BYTES + B_BYTES, STAGE = KG * GROUP;
-  extern __shared__ __attribute__((aligned(16))) unsigned char s_dyn[];
   const int tid = threadIdx.x, l = tid & 63, l32 = l & 31, hk = l >> 5;
   const int kg = (tid >> 6) / NW, w = (tid >> 6) % NW;
   const int wm = w % WM, wn = w / WM;
   int mt, nt;
-  tile_of(blockIdx.x, (g.M + BM - 1) / BM, (g.N + BN - 1) / BN, depth, mt, nt);
+  tile_of(tile, (g.M + BM - 1) / BM, (g.N + BN - 1) / BN, 1024 / BM, mt, nt);
   const int m0 = mt * BM, n0 = nt * BN;
-  const int kb = blockIdx.y * g.slice, ke = min(g.K, kb + g.slice);
+  const int kb = slice * g.slice, ke = min(g.K, kb + g.slice);
 
   Loader<AKC, BM, BK, NW, TAIL> la;
   Loader<BKC, BN, BK, NW, TAIL> lb;
@@ -392,7 +403,7 @@ __global__ __launch_bounds__(64 * NW * KG, NW * KG / 4) void linear_tile_kernel(
       const f32x4 lo = *(const f32x4*)(s_f + row * HC + 4 * ((2 * c8) ^ (row & 15)));
       const f32x4 hi = *(const f32x4*)(s_f + row * HC + 4 * ((2 * c8 + 1) ^ (row & 15)));
       float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      leave8<uint16_t>(g, blockIdx.y, m, n, v);
+      leave8<uint16_t>(g, slice, m, n, v);
     }
     __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's reads of the staged rows are done
   }
@@ -406,43 +417,39 @@ __device__ __forceinline__ f32x16 mfma32_f32(float first, float second, f32x16 a
   return __builtin_amdgcn_mfma_f32_32x32x2f32(first, second, acc, 0, 0, 0);
 }
 
-// Workgroup = BT x BT outputs, four waves of (BT / 2)^2, 16 k per LDS stage, the
-// next stage's values loaded into registers under the products.
-template <bool AKC, bool BKC, int BT>
-__global__ __launch_bounds__(256) void linear_f32_kernel(LinearProduct g, int depth) {
-  constexpr int BK = 16, PITCH = BT + 32, NB = BT / 64;  // 32 x 32 blocks per wave side
-  constexpr int QUADS = BT * BK / 4 / 256;               // 16-byte loads per thread and operand
-  __shared__ __attribute__((aligned(16))) float s_a[BK * PITCH], s_b[BK * PITCH];
-  const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, l32 = l & 31, hk = l >> 5;
-  const int wm = w & 1, wn = w >> 1;
-  int mt, nt;
-  tile_of(blockIdx.x, (g.M + BT - 1) / BT, (g.N + BT - 1) / BT, depth, mt, nt);
-  const int m0 = mt * BT, n0 = nt * BT;
-  const int kb = blockIdx.y * g.slice, ke = min(g.K, kb + g.slice);
-  f32x4 ra[QUADS], rb[QUADS];
-  // four neighbouring elements of an operand; those outside are zero (the contiguous extent is a multiple of 4)
-  auto fetch = [&](auto kc, const void* base, int64_t ld, int r0, int rows, int k0, f32x4 (&v)[QUADS]) {
+// The fp32 tiles: BT x BT outputs by two groups of four waves of (BT / 2)^2, each
+// group taking 16 of a stage's 32 k; two LDS buffers, the next stage's values
+// loaded into registers under the products.  An operand with k contiguous is
+// transposed on its way into LDS; its row pitch of BT + 2 spreads the eight
+// quads of a row over the banks.
+template <int BT_>
+struct TileF {
+  static constexpr int BT = BT_, BM = BT_, BN = BT_, BK = 32;
+  static constexpr int LDS = 2 * 2 * BK * (BT + 32) * 4;
+};
+
+template <bool KC, int BT>
+struct LoaderF {
+  static constexpr int BK = 32, QUADS = BT * BK / 4 / kThreads, PITCH = KC ? BT + 2 : BT + 32;
+  static_assert(QUADS >= 1, "a quad per thread");
+  f32x4 v[QUADS];
+  // four neighbouring elements each; those outside are zero (the contiguous extent is a multiple of 4)
+  __device__ __forceinline__ void fetch(const void* base, int64_t ld, int r0, int rows, int k0, int ke) {
 #pragma unroll
     for (int i = 0; i < QUADS; ++i) {
-      const int q = tid + 256 * i;
-      int r, k;
-      if constexpr (decltype(kc)::value) {
-        r = r0 + q / (BK / 4);
-        k = k0 + 4 * (q % (BK / 4));
-      } else {
-        k = k0 + q / (BT / 4);
-        r = r0 + 4 * (q % (BT / 4));
-      }
+      const int q = threadIdx.x + kThreads * i;
+      const int r = r0 + (KC ? q / (BK / 4) : 4 * (q % (BT / 4)));
+      const int k = k0 + (KC ? 4 * (q % (BK / 4)) : q / (BT / 4));
       const bool in = r < rows && k < ke;
-      const int64_t at = decltype(kc)::value ? r * ld + k : k * ld + r;
+      const int64_t at = KC ? r * ld + k : k * ld + r;
       v[i] = in ? *(const f32x4*)((const float*)base + at) : f32x4{0.f, 0.f, 0.f, 0.f};
     }
-  };
-  auto put = [&](auto kc, float* s, const f32x4 (&v)[QUADS]) {
+  }
+  __device__ __forceinline__ void put(float* s) const {
 #pragma unroll
     for (int i = 0; i < QUADS; ++i) {
-      const int q = tid + 256 * i;
-      if constexpr (decltype(kc)::value) {
+      const int q = threadIdx.x + kThreads * i;
+      if (KC) {
         const int r = q / (BK / 4), k = 4 * (q % (BK / 4));
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[(k + j) * PITCH + r] = v[i][j];
@@ -450,9 +457,24 @@ __global__ __launch_bounds__(256) void linear_f32_kernel(LinearProduct g, int de
         *(f32x4*)(s + (q / (BT / 4)) * PITCH + 4 * (q % (BT / 4))) = v[i];
       }
     }
-  };
-  using A = std::integral_constant<bool, AKC>;
-  using B = std::integral_constant<bool, BKC>;
+  }
+};
+
+template <bool AKC, bool BKC, typename C, bool TAIL>
+__device__ __forceinline__ void tile_product_f32(const LinearProduct& g, int tile, int slice, unsigned char* s_dyn) {
+  constexpr int BT = C::BT, BK = C::BK, NB = BT / 64;  // 32 x 32 blocks per wave side
+  using LA = LoaderF<AKC, BT>;
+  using LB = LoaderF<BKC, BT>;
+  constexpr int BUF = BK * (BT + 32);  // floats of one operand's buffer
+  float* s_f = reinterpret_cast<float*>(s_dyn);
+  const int tid = threadIdx.x, w = (tid >> 6) & 3, kg = tid >> 8, l = tid & 63, l32 = l & 31, hk = l >> 5;
+  const int wm = w & 1, wn = w >> 1;
+  int mt, nt;
+  tile_of(tile, (g.M + BT - 1) / BT, (g.N + BT - 1) / BT, 8, mt, nt);
+  const int m0 = mt * BT, n0 = nt * BT;
+  const int kb = slice * g.slice, ke = min(g.K, kb + g.slice);
+  LA la;
+  LB lb;
   f32x16 acc[NB][NB];
 #pragma unroll
   for (int i = 0; i < NB; ++i)
@@ -460,37 +482,59 @@ __global__ __launch_bounds__(256) void linear_f32_kernel(LinearProduct g, int de
     for (int j = 0; j < NB; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  fetch(A{}, g.a, g.lda, m0, g.M, kb, ra);
-  fetch(B{}, g.b, g.ldb, n0, g.N, kb, rb);
-  for (int k0 = kb; k0 < ke; k0 += BK) {
-    put(A{}, s_a, ra);
-    put(B{}, s_b, rb);
-    __syncthreads();
+  la.fetch(g.a, g.lda, m0, g.M, kb, ke);
+  lb.fetch(g.b, g.ldb, n0, g.N, kb, ke);
+  int turn = 0;
+  for (int k0 = kb; k0 < ke; k0 += BK, turn ^= 1) {
+    float* s_a = s_f + turn * 2 * BUF;
+    float* s_b = s_a + BUF;
+    la.put(s_a);
+    lb.put(s_b);
+    __syncthreads();  // the other buffer is free as well: every wave is past its products
     if (k0 + BK < ke) {
-      fetch(A{}, g.a, g.lda, m0, g.M, k0 + BK, ra);
-      fetch(B{}, g.b, g.ldb, n0, g.N, k0 + BK, rb);
+      la.fetch(g.a, g.lda, m0, g.M, k0 + BK, ke);
+      lb.fetch(g.b, g.ldb, n0, g.N, k0 + BK, ke);
     }
 #pragma unroll
-    for (int k = 0; k < BK; k += 2) {
+    for (int k = 0; k < BK / 2; k += 2) {
       float fa[NB], fb[NB];
+      const int kk = kg * (BK / 2) + k + hk;
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
-        fa[i] = s_a[(k + hk) * PITCH + 32 * (NB * wm + i) + l32];
-        fb[i] = s_b[(k + hk) * PITCH + 32 * (NB * wn + i) + l32];
+        fa[i] = s_a[kk * LA::PITCH + 32 * (NB * wm + i) + l32];
+        fb[i] = s_b[kk * LB::PITCH + 32 * (NB * wn + i) + l32];
       }
 #pragma unroll
       for (int j = 0; j < NB; ++j)
 #pragma unroll
         for (int i = 0; i < NB; ++i) acc[i][j] = mfma32_f32(fb[j], fa[i], acc[i][j]);
     }
-    __syncthreads();
   }
-  // lane pairs l, l + 32 hold the two halves of eight neighbouring columns of one
-  // row: they swap quads so that each holds whole runs
+  // The second group's sums reach the first through LDS.  There, lane pairs l, l + 32 hold the
+  // two halves of eight neighbouring columns of one row: they swap quads so that each holds whole runs.
+  static_assert(4 * 64 * NB * NB * 16 * 4 <= C::LDS, "the second group's sums");
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < NB; ++i)
 #pragma unroll
     for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        f32x4* at = (f32x4*)(s_f + (((i * NB + j) * 4 + q) * 256 + w * 64 + l) * 4);
+        if (kg == 1) *at = f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+      }
+  __syncthreads();
+  if (kg == 1) return;
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x4 o = *(const f32x4*)(s_f + (((i * NB + j) * 4 + q) * 256 + w * 64 + l) * 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += o[e];
+      }
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const int m = m0 + 32 * (NB * wm + i) + l32;
@@ -500,13 +544,64 @@ __global__ __launch_bounds__(256) void linear_f32_kernel(LinearProduct g, int de
         for (int e = 0; e < 4; ++e) {
           // quads 2 p (columns + 0..7) and 2 p + 1 (columns + 8..15): lane half 0 keeps the first run, half 1 the second
           const float mine0 = acc[i][j][8 * p + e], mine1 = acc[i][j][8 * p + 4 + e];
-          const float give = hk ? mine0 : mine1;
-          const float got = __shfl_xor(give, 32, kWave);
+          const float got = __shfl_xor(hk ? mine0 : mine1, 32, kWave);
           v[e] = hk ? got : mine0;
           v[4 + e] = hk ? mine1 : got;
         }
-        if (m < g.M && n < g.N) leave8<float>(g, blockIdx.y, m, n, v);
+        if (m < g.M && n < g.N) leave8<float>(g, slice, m, n, v);
       }
+    }
+}
+
+template <typename T, bool AKC, bool BKC, typename C, bool TAIL>
+__device__ __forceinline__ void any_product(const LinearProduct& g, int item, unsigned char* s_dyn) {
+  const int tiles = ((g.M + C::BM - 1) / C::BM) * ((g.N + C::BN - 1) / C::BN);
+  if constexpr (std::is_same<T, float>::value)
+    tile_product_f32<AKC, BKC, C, TAIL>(g, item % tiles, item / tiles, s_dyn);
+  else
+    tile_product<AKC, BKC, C, TAIL>(g, item % tiles, item / tiles, s_dyn);
+}
+
+// One workgroup per tile and slice: x W.
+template <typename T, typename C, bool TAIL>
+__global__ __launch_bounds__(kThreads, 2) void linear_fwd_kernel(LinearProduct g) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char s_dyn[];
+  any_product<T, true, false, C, TAIL>(g, blockIdx.x, s_dyn);
+}
+
+// The backward's products in one launch, so that one's workgroups fill the CUs
+// that the other leaves idle: `nw` workgroups of x^T dz, `nx` of dz W^T (the longer ones first), and behind them
+// the sums of dbias' partial rows.
+struct ColumnSum {
+  const float* part;
+  int n, cols;
+  void* out;
+};
+
+template <typename T>
+__device__ __forceinline__ void column_sum(const ColumnSum& c, int block, float* s) {
+  const int w = threadIdx.x >> 6, l = threadIdx.x & 63, col = block * 64 + l;
+  float v = 0.0f;
+  if (col < c.cols)
+    for (int p = w; p < c.n; p += kThreads / 64) v += c.part[(size_t)p * c.cols + col];
+  s[w * 64 + l] = v;
+  __syncthreads();
+  if (w != 0 || col >= c.cols) return;
+  v = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kThreads / 64; ++i) v += s[i * 64 + l];
+  store1((T*)c.out + col, v);
+}
+
+template <typename T, typename CX, typename CW, bool TAIL>
+__global__ __launch_bounds__(kThreads, 2) void linear_bwd_kernel(LinearProduct gx, LinearProduct gw, ColumnSum sum, int nx,
+                                                                 int nw, int x_first) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char s_dyn[];
+  int b = blockIdx.x;
+  if (b >= nx + nw) return column_sum<T>(sum, b - nx - nw, reinterpret_cast<float*>(s_dyn));
+  const bool is_x = x_first ? b < nx : b >= nw;
+  if (is_x) any_product<T, true, true, CX, TAIL>(gx, x_first ? b : b - nw, s_dyn);
+  else any_product<T, false, false, CW, TAIL>(gw, x_first ? b - nx : b, s_dyn);
 }
 
 // dz, dmul and the column sums of dz.  Workgroup = 32 runs of eight columns x 8
@@ -554,29 +649,147 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(int rows, int O, int act
   part[(size_t)blockIdx.y * O + col] = v;
 }
 
-// out[c] = sum_p part[p][c], p ascending within each of four waves, then the waves.
-template <typename T>
-__global__ __launch_bounds__(256) void linear_dbias_kernel(int n, int O, const float* __restrict__ part, T* out) {
-  __shared__ float s[4][64];
-  const int w = threadIdx.x >> 6, l = threadIdx.x & 63, c = blockIdx.x * 64 + l;
-  float v = 0.0f;
-  if (c < O)
-    for (int p = w; p < n; p += 4) v += part[(size_t)p * O + c];
-  s[w][l] = v;
-  __syncthreads();
-  if (w == 0 && c < O) store1(out + c, s[0][l] + s[1][l] + s[2][l] + s[3][l]);
-}
-
 // Row slots of linear_dz_kernel: about 1024 workgroups, eight rows each at least.
 int dz_slots(int T, int O) {
   const int cols = (O + 255) / 256;
   return std::max(1, std::min((T + 7) / 8, 1024 / std::min(cols, 1024)));
 }
+size_t dbias_bytes(int T, int O) { return ((size_t)dz_slots(T, O) * O * sizeof(float) + 15) / 16 * 16; }
 
 // ---- launchers -------------------------------------------------------------------
 
+// The workgroup tiles, largest first, and what a pass of them over the chip's
+// 256 CUs takes: `step` us per 64 k (`step_few` when at most 160 workgroups
+// run), `round` us for a tile's prologue and epilogue.  Measured on one MI355X with
+// grids of 128, 256 and 512 workgroups and reductions of 512, 2048 and 4096
+// (all three operand layouts within 8 %).  A larger tile moves fewer bytes
+// through LDS per product (at 256 workgroups: 256 x 256 1.32 PFLOP/s,
+// 256 x 128 1.14, 128 x 128 1.01, 128 x 64 0.84, 64 x 64 0.61) but leaves CUs
+// idle where the outputs are few: 4099 x 768 over 2048 takes 49 us on 256 x 256,
+// 30 on 256 x 128, 20.9 on 128 x 128, 25.8 on 128 x 64 tiles.
+enum { kTile256x256 = 0, kTile256x128, kTile128x128, kTile128x64, kTile64x64, kTiles };
+using Tile0 = Tile<256, 256, 8, 2, 1, 2>;
+using Tile1 = Tile<256, 128, 8, 4, 1, 3>;
+using Tile2 = Tile<128, 128, 4, 2, 2, 2>;
+using Tile3 = Tile<128, 64, 4, 2, 2, 3>;
+using Tile4 = Tile<64, 64, 4, 2, 2, 4>;
+enum { kTileF128 = 0, kTileF64, kTilesF };
+struct TileCost {
+  int bm, bn;
+  double step, step_few, round;
+};
+constexpr TileCost kCost[kTiles] = {{256, 256, 1.62, 1.13, 8.5},
+                                    {256, 128, 0.94, 0.74, 4.5},
+                                    {128, 128, 0.53, 0.47, 2.6},
+                                    {128, 64, 0.33, 0.27, 2.0},
+                                    {64, 64, 0.22, 0.19, 1.0}};
+constexpr TileCost kCostF[kTilesF] = {{128, 128, 4.0, 4.0, 3.0}, {64, 64, 1.4, 1.2, 2.0}};  // fp32, per 64 k
+
+constexpr int kCus = 256, kFew = 160;
+constexpr double kLaunchUs = 3.5;           // one more kernel behind another
+constexpr double kSliceBytesPerUs = 4.0e6;  // partials written and read again
+
+const TileCost& cost_of(int tile, int esize) { return esize == 2 ? kCost[tile] : kCostF[tile]; }
+
+// How a product is cut: its workgroup tile and the slices of its reduction.
+struct Cut {
+  int tile, slices, slice;  // k per slice
+  int64_t groups;           // workgroups
+  double each;              // us of one workgroup
+  double after;             // us of adding the slices
+};
+
+Cut cut_of(int M, int N, int K, int esize, int tile, int want, bool few) {
+  constexpr int kGrain = 128;  // slices are whole stages
+  const TileCost& t = cost_of(tile, esize);
+  Cut c{};
+  c.tile = tile;
+  c.slice = (int)((((int64_t)K + want - 1) / want + kGrain - 1) / kGrain * kGrain);
+  c.slices = (K + c.slice - 1) / c.slice;
+  c.groups = (int64_t)((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn) * c.slices;
+  c.each = (double)((std::min(K, c.slice) + 63) / 64) * (few ? t.step_few : t.step) + t.round;
+  c.after = c.slices > 1 ? (double)c.slices * M * N * 8.0 / kSliceBytesPerUs : 0.0;
+  return c;
+}
+
+// Cuts worth a look: splitting a reduction pays where few tiles meet a long one
+// (2048 x 768 outputs over 4099 rows: 56 us on 128 x 128 tiles, 31 us in two
+// slices with the sum behind them).
+template <typename Fn>
+void each_cut(int M, int N, int K, int esize, int tile, bool few, Fn&& f) {
+  for (int want : {1, 2, 3, 4, 6, 8, 12, 16}) {
+    const Cut c = cut_of(M, N, K, esize, tile, want, few);
+    if (want > 1 && (c.slices == 1 || c.groups > 2 * kCus)) return;
+    f(c);
+  }
+}
+
+// The forward's cut of least estimated time: full passes over the CUs, then the rest.
+Cut plan_fwd(int M, int N, int K, int esize) {
+  Cut best{};
+  double best_us = 0.0;
+  for (int tile = 0; tile < (esize == 2 ? (int)kTiles : (int)kTilesF); ++tile)
+    each_cut(M, N, K, esize, tile, false, [&](const Cut& c) {
+      const int64_t rest = c.groups % kCus;
+      double us = kLaunchUs + (double)(c.groups / kCus) * c.each + (c.slices > 1 ? kLaunchUs + c.after : 0.0);
+      if (rest > 0) us += rest > kFew ? c.each : cut_of(M, N, K, esize, tile, c.slices, true).each;
+      if (best.slices == 0 || us < best_us) {
+        best = c;
+        best_us = us;
+      }
+    });
+  return best;
+}
+
+// The backward's cuts: dx and dw share a launch (Pairs: which tiles meet), so
+// what counts is their joint work over the CUs, and the longest workgroup.
+struct Plan2 {
+  int pair;
+  Cut x, w;
+};
+struct Pair {
+  int x, w;
+};
+constexpr Pair kPairs[] = {{kTile256x256, kTile256x256}, {kTile256x256, kTile256x128}, {kTile256x128, kTile256x256},
+                           {kTile256x128, kTile256x128}, {kTile128x128, kTile128x128}, {kTile128x64, kTile128x64},
+                           {kTile64x64, kTile64x64}};
+constexpr Pair kPairsF[] = {{kTileF128, kTileF128}, {kTileF64, kTileF64}};
+
+Plan2 plan_bwd(int T, int I, int O, int esize, bool dx, bool dw) {
+  Plan2 best{};
+  double best_us = -1.0;
+  const int pairs = esize == 2 ? (int)std::size(kPairs) : (int)std::size(kPairsF);
+  for (int p = 0; p < pairs; ++p) {
+    const Pair tiles = esize == 2 ? kPairs[p] : kPairsF[p];
+    auto weigh = [&](const Cut* x, const Cut* w) {
+      const int64_t gx = x ? x->groups : 0, gw = w ? w->groups : 0;
+      const double ex = x ? x->each : 0.0, ew = w ? w->each : 0.0;
+      double us = std::max({((double)gx * ex + (double)gw * ew) / kCus, ex, ew});
+      if (gx + gw > kCus) us += 0.5 * std::min(gx ? ex : ew, gw ? ew : ex);  // the last ones end unevenly
+      const double after = (x ? x->after : 0.0) + (w ? w->after : 0.0);
+      if (after > 0.0) us += kLaunchUs + after;
+      if (best_us < 0.0 || us < best_us) {
+        best_us = us;
+        best = Plan2{p, x ? *x : Cut{}, w ? *w : Cut{}};
+      }
+    };
+    auto with_w = [&](const Cut* x) {
+      if (!dw) return weigh(x, nullptr);
+      each_cut(I, O, T, esize, tiles.w, false, [&](const Cut& w) { weigh(x, &w); });
+    };
+    if (!dx) with_w(nullptr);
+    else each_cut(T, I, O, esize, tiles.x, false, [&](const Cut& x) { with_w(&x); });
+  }
+  return best;
+}
+
+size_t slice_bytes(int M, int N, const Cut& c) {
+  return c.slices > 1 ? ((size_t)c.slices * M * N * sizeof(float) + 15) / 16 * 16 : 0;
+}
+
 template <typename T>
 hipError_t add_slices(const LinearProduct& g, hipStream_t stream) {
+  if (g.part == nullptr) return hipSuccess;
   const int slices = (g.K + g.slice - 1) / g.slice;
   const int64_t runs = (int64_t)g.M * (g.N / 8);
   MOE_LAUNCH((linear_slices_kernel<T>), dim3((unsigned)std::min<int64_t>((runs + 255) / 256, 4096)), dim3(256), 0,
@@ -584,115 +797,64 @@ hipError_t add_slices(const LinearProduct& g, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// The workgroup tiles, largest first, and what a pass of them over the chip's
-// 256 CUs takes: `step` us per 64 k (`step_few` when at most 160 workgroups run), `round` us for its prologue
-// and epilogue.  Measured on one MI355X with grids of 128, 256 and 512
-// workgroups and reductions of 512, 2048 and 4096 (all three operand layouts
-// within 8 %).  A larger tile moves fewer bytes through LDS per product (at 256
-// workgroups: 256 x 256 1.32 PFLOP/s, 256 x 128 1.14, 128 x 128 1.01, 128 x 64 0.84, 64 x 64 0.61) but
-// leaves CUs idle where the outputs are few: 4099 x 768 over 2048 takes 49 us
-// on 256 x 256, 30 on 256 x 128, 20.9 on 128 x 128, 25.8 on 128 x 64 tiles.
-struct TileCost {
-  int bm, bn;
-  double step, step_few, round;
-};
-enum { kTile256x256 = 0, kTile256x128, kTile128x128, kTile128x64, kTile64x64, kTilesBf16 };
-constexpr TileCost kCostBf16[kTilesBf16] = {
-    {256, 256, 1.62, 1.13, 8.5}, {256, 128, 0.94, 0.74, 4.5}, {128, 128, 0.53, 0.47, 2.6},
-    {128, 64, 0.33, 0.27, 2.0},  {64, 64, 0.22, 0.19, 1.0}};
-// fp32: the same per 16 k
-enum { kTileF128 = 0, kTileF64, kTilesF32 };
-constexpr TileCost kCostF32[kTilesF32] = {{128, 128, 1.10, 1.10, 4.0}, {64, 64, 0.35, 0.30, 2.0}};
-
-constexpr double kLaunchUs = 3.5;              // one more kernel behind another
-constexpr double kSliceBytesPerUs = 4.0e6;     // partials written and read again
-
-// What runs a product: the tile, and the slices of its reduction.
-struct Plan {
-  int tile;
-  int slices;
-  int slice;  // k per slice
-};
-
-// The plan of least estimated time.  Splitting the reduction pays where few
-// tiles meet a long reduction: 2048 x 768 outputs over 4099 rows take 56 us on
-// 128 x 128 tiles, 31 us in two slices with the sum behind them.
-Plan plan_of(int M, int N, int K, int esize) {
-  constexpr int kCus = 256, kFew = 160;
-  const bool bf16 = esize == 2;
-  const int stage = bf16 ? 64 : 16, grain = bf16 ? 128 : 16;
-  Plan best{};
-  double best_us = 0.0;
-  for (int c = 0; c < (bf16 ? (int)kTilesBf16 : (int)kTilesF32); ++c) {
-    const TileCost& t = bf16 ? kCostBf16[c] : kCostF32[c];
-    const int64_t tiles = (int64_t)((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
-    for (int want : {1, 2, 3, 4, 6, 8, 12, 16}) {
-      const int slice = ((K + want - 1) / want + grain - 1) / grain * grain;
-      const int slices = (K + slice - 1) / slice;
-      if (want > 1 && (slices == 1 || tiles * want > 2 * kCus)) break;
-      const int64_t groups = tiles * slices, rest = groups % kCus;
-      const double steps = (double)((std::min(K, slice) + stage - 1) / stage);
-      double us = kLaunchUs + (double)(groups / kCus) * (steps * t.step + t.round);
-      if (rest > 0) us += steps * (rest > kFew ? t.step : t.step_few) + t.round;
-      if (slices > 1) us += kLaunchUs + (double)slices * M * N * 8.0 / kSliceBytesPerUs;
-      if (best.slices == 0 || us < best_us) {
-        best = Plan{c, slices, slice};
-        best_us = us;
-      }
-    }
-  }
-  return best;
+// Whether stages of C reach past the product's edges and must be masked: every
+// stage of every slice is whole where this is false (one that ran past the
+// reduction's end would read past the operands).
+template <bool AKC, bool BKC, typename C>
+bool has_tail(const LinearProduct& g) {
+  return g.K % (64 * C::KG) != 0 || g.slice % (64 * C::KG) != 0 || (!BKC && g.N % C::BN != 0) ||
+         (!AKC && g.M % C::BM != 0);
 }
 
-size_t plan_bytes(int M, int N, int K, int esize) {
-  const Plan p = plan_of(M, N, K, esize);
-  return p.slices > 1 ? (size_t)p.slices * M * N * sizeof(float) : 0;
-}
-
-template <bool AKC, bool BKC, int BM, int BN, int NW, int WM, int KG, int STAGES, bool TAIL>
-hipError_t launch_tiles(const LinearProduct& g, int slices, hipStream_t stream) {
-  constexpr size_t lds = (size_t)STAGES * KG * (BM + BN) * 64 * 2;
-  auto kern = linear_tile_kernel<AKC, BKC, BM, BN, NW, WM, KG, STAGES, TAIL>;
+template <typename T, typename C, bool TAIL>
+hipError_t run_fwd(const LinearProduct& g, int64_t groups, hipStream_t stream) {
+  auto kern = linear_fwd_kernel<T, C, TAIL>;
   static PerDeviceOnce once;
-  hipError_t err = allow_dynamic_lds(once, (const void*)kern, lds);
+  hipError_t err = allow_dynamic_lds(once, (const void*)kern, C::LDS);
   if (err != hipSuccess) return err;
-  const int64_t tiles = (int64_t)((g.M + BM - 1) / BM) * ((g.N + BN - 1) / BN);
-  MOE_LAUNCH(kern, dim3((unsigned)tiles, slices), dim3(64 * NW * KG), lds, stream, g, 1024 / BM);
+  MOE_LAUNCH(kern, dim3((unsigned)groups), dim3(kThreads), C::LDS, stream, g);
   return hipGetLastError();
 }
 
-template <bool AKC, bool BKC, int BM, int BN, int NW, int WM, int KG, int STAGES>
-hipError_t launch_bf16(const LinearProduct& g, int slices, hipStream_t stream) {
-  // whole stages, in every slice: nothing to mask (a stage that ran past the reduction's end would read past the operands)
-  const bool tail = g.K % (64 * KG) != 0 || (slices > 1 && g.slice % (64 * KG) != 0) || (!BKC && g.N % BN != 0) || (!AKC && g.M % BM != 0);
-  return tail ? launch_tiles<AKC, BKC, BM, BN, NW, WM, KG, STAGES, true>(g, slices, stream)
-              : launch_tiles<AKC, BKC, BM, BN, NW, WM, KG, STAGES, false>(g, slices, stream);
-}
-
-// AKC, BKC: which operands have k contiguous.
-template <typename T, bool AKC, bool BKC>
-hipError_t product(LinearProduct g, float* ws, hipStream_t stream) {
-  const Plan p = plan_of(g.M, g.N, g.K, sizeof(T));
-  g.slice = p.slice;
-  g.part = p.slices > 1 ? ws : nullptr;
+template <typename T>
+hipError_t linear_fwd_typed(LinearProduct g, float* ws, hipStream_t stream) {
+  const Cut c = plan_fwd(g.M, g.N, g.K, sizeof(T));
+  g.slice = c.slice;
+  g.part = c.slices > 1 ? ws : nullptr;
   hipError_t err;
   if constexpr (std::is_same<T, float>::value) {
-    const int bt = kCostF32[p.tile].bm;
-    const dim3 grid((unsigned)((int64_t)((g.M + bt - 1) / bt) * ((g.N + bt - 1) / bt)), p.slices);
-    if (p.tile == kTileF128) MOE_LAUNCH((linear_f32_kernel<AKC, BKC, 128>), grid, dim3(256), 0, stream, g, 8);
-    else MOE_LAUNCH((linear_f32_kernel<AKC, BKC, 64>), grid, dim3(256), 0, stream, g, 8);
-    err = hipGetLastError();
+    err = c.tile == kTileF128 ? run_fwd<T, TileF<128>, true>(g, c.groups, stream)
+                              : run_fwd<T, TileF<64>, true>(g, c.groups, stream);
   } else {
-    switch (p.tile) {
-      case kTile256x256: err = launch_bf16<AKC, BKC, 256, 256, 8, 2, 1, 2>(g, p.slices, stream); break;
-      case kTile256x128: err = launch_bf16<AKC, BKC, 256, 128, 8, 4, 1, 3>(g, p.slices, stream); break;
-      case kTile128x128: err = launch_bf16<AKC, BKC, 128, 128, 4, 2, 2, 2>(g, p.slices, stream); break;
-      case kTile128x64: err = launch_bf16<AKC, BKC, 128, 64, 4, 2, 2, 3>(g, p.slices, stream); break;
-      default: err = launch_bf16<AKC, BKC, 64, 64, 4, 2, 2, 4>(g, p.slices, stream); break;
+    auto run = [&](auto tile) {
+      using C = decltype(tile);
+      return has_tail<true, false, C>(g) ? run_fwd<T, C, true>(g, c.groups, stream)
+                                         : run_fwd<T, C, false>(g, c.groups, stream);
+    };
+    switch (c.tile) {
+      case kTile256x256: err = run(Tile0{}); break;
+      case kTile256x128: err = run(Tile1{}); break;
+      case kTile128x128: err = run(Tile2{}); break;
+      case kTile128x64: err = run(Tile3{}); break;
+      default: err = run(Tile4{}); break;
     }
   }
-  if (err != hipSuccess || p.slices == 1) return err;
+  if (err != hipSuccess) return err;
   return add_slices<T>(g, stream);
+}
+
+template <typename T, typename CX, typename CW, bool TAIL>
+hipError_t run_bwd(const LinearProduct& gx, const LinearProduct& gw, const ColumnSum& sum, const Plan2& p,
+                   hipStream_t stream) {
+  constexpr size_t lds = std::max(CX::LDS, CW::LDS);
+  auto kern = linear_bwd_kernel<T, CX, CW, TAIL>;
+  static PerDeviceOnce once;
+  hipError_t err = allow_dynamic_lds(once, (const void*)kern, lds);
+  if (err != hipSuccess) return err;
+  const int64_t sums = sum.out != nullptr ? (sum.cols + 63) / 64 : 0;
+  MOE_LAUNCH(kern, dim3((unsigned)(p.x.groups + p.w.groups + sums)), dim3(kThreads), lds, stream, gx, gw, sum,
+             (int)p.x.groups, (int)p.w.groups, p.x.each > p.w.each ? 1 : 0);
+  return hipGetLastError();
 }
 
 template <typename T>
@@ -700,46 +862,65 @@ hipError_t linear_bwd_typed(const LinearArgs& g, const void* z, const void* mul,
                             const void* dx_add, void* dx, void* dw, void* dbias, void* dmul, float* ws,
                             hipStream_t stream) {
   const bool plain = g.act == kActNone && mul == nullptr;
-  const int T_ = g.T, I = g.I, O = g.O;
+  const int T_ = g.T, I = g.I, O = g.O, slots = dz_slots(T_, O);
   if (!plain || dbias != nullptr) {
-    const int slots = dz_slots(T_, O);
     MOE_LAUNCH((linear_dz_kernel<T>), dim3((O + 255) / 256, slots), dim3(256), 0, stream, T_, O, g.act,
                plain ? nullptr : (const T*)z, (const T*)mul, (const T*)dy, (T*)dz, (T*)dmul,
                dbias != nullptr ? ws : nullptr);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    if (dbias != nullptr) {
-      MOE_LAUNCH((linear_dbias_kernel<T>), dim3((O + 63) / 64), dim3(256), 0, stream, slots, O, (const float*)ws,
-                 (T*)dbias);
-      if ((err = hipGetLastError()) != hipSuccess) return err;
+  }
+  if (dx == nullptr && dw == nullptr && dbias == nullptr) return hipSuccess;
+  const void* d = plain ? dy : dz;
+  const Plan2 p = plan_bwd(T_, I, O, sizeof(T), dx != nullptr, dw != nullptr);
+  LinearProduct gx{T_, I, O, d, O, g.w, O, kActNone, nullptr, nullptr, dx_add, nullptr, dx, p.x.slice, nullptr};
+  LinearProduct gw{I, O, T_, g.x, I, d, O, kActNone, nullptr, nullptr, nullptr, nullptr, dw, p.w.slice, nullptr};
+  const ColumnSum sum{ws, slots, O, dbias};
+  char* at = (char*)ws + dbias_bytes(T_, O);
+  if (p.x.slices > 1) gx.part = (float*)at;
+  at += slice_bytes(T_, I, p.x);
+  if (p.w.slices > 1) gw.part = (float*)at;
+  hipError_t err;
+  if constexpr (std::is_same<T, float>::value) {
+    err = p.pair == 0 ? run_bwd<T, TileF<128>, TileF<128>, true>(gx, gw, sum, p, stream)
+                      : run_bwd<T, TileF<64>, TileF<64>, true>(gx, gw, sum, p, stream);
+  } else {
+    auto run = [&](auto tx, auto tw) {
+      using CX = decltype(tx);
+      using CW = decltype(tw);
+      const bool tail = (dx != nullptr && has_tail<true, true, CX>(gx)) || (dw != nullptr && has_tail<false, false, CW>(gw));
+      return tail ? run_bwd<T, CX, CW, true>(gx, gw, sum, p, stream) : run_bwd<T, CX, CW, false>(gx, gw, sum, p, stream);
+    };
+    switch (p.pair) {
+      case 0: err = run(Tile0{}, Tile0{}); break;
+      case 1: err = run(Tile0{}, Tile1{}); break;
+      case 2: err = run(Tile1{}, Tile0{}); break;
+      case 3: err = run(Tile1{}, Tile1{}); break;
+      case 4: err = run(Tile2{}, Tile2{}); break;
+      case 5: err = run(Tile3{}, Tile3{}); break;
+      default: err = run(Tile4{}, Tile4{}); break;
     }
   }
-  const void* d = plain ? dy : dz;
-  if (dx != nullptr) {
-    LinearProduct p{T_, I, O, d, O, g.w, O, kActNone, nullptr, nullptr, dx_add, nullptr, dx, 0, nullptr};
-    hipError_t err = product<T, true, true>(p, ws, stream);
-    if (err != hipSuccess) return err;
-  }
-  if (dw != nullptr) {
-    LinearProduct p{I, O, T_, g.x, I, d, O, kActNone, nullptr, nullptr, nullptr, nullptr, dw, 0, nullptr};
-    return product<T, false, false>(p, ws, stream);
-  }
-  return hipSuccess;
+  if (err != hipSuccess || (err = add_slices<T>(gx, stream)) != hipSuccess) return err;
+  return add_slices<T>(gw, stream);
 }
 
 }  // namespace
 
-// The partials of one launch at a time: a backward's column sums, then each product's slices.
+// The partials: the forward's slices, or the backward's column sums and both products' slices.
 size_t linear_workspace_bytes(int T, int I, int O, int esize) {
-  return std::max({(size_t)dz_slots(T, O) * O * sizeof(float), plan_bytes(T, O, I, esize), plan_bytes(T, I, O, esize),
-                   plan_bytes(I, O, T, esize)});
+  size_t need = slice_bytes(T, O, plan_fwd(T, O, I, esize));
+  for (int want = 0; want < 4; ++want) {  // any of dx and dw
+    const Plan2 p = plan_bwd(T, I, O, esize, want & 1, want & 2);
+    need = std::max(need, dbias_bytes(T, O) + slice_bytes(T, I, p.x) + slice_bytes(I, O, p.w));
+  }
+  return need;
 }
 
 hipError_t launch_linear_fwd(const LinearArgs& g, int esize, const void* bias, const void* mul, const void* residual,
                              void* z, void* y, void* ws, hipStream_t stream) {
   const LinearProduct p{g.T, g.O, g.I, g.x, g.I, g.w, g.O, g.act, bias, mul, residual, z, y, 0, nullptr};
-  return esize == 4 ? product<float, true, false>(p, (float*)ws, stream)
-                    : product<uint16_t, true, false>(p, (float*)ws, stream);
+  return esize == 4 ? linear_fwd_typed<float>(p, (float*)ws, stream) : linear_fwd_typed<uint16_t>(p, (float*)ws, stream);
 }
 
 hipError_t launch_linear_bwd(const LinearArgs& g, int esize, const void* z, const void* mul, const void* dy, void* dz,
