@@ -41,49 +41,72 @@ __device__ __forceinline__ float normal_cdf(float z) {
   return z > 0.0f ? 1.0f - tail : tail;
 }
 
-// act(z); NaN stays NaN.
-__device__ __forceinline__ float act_value(int act, float z) {
+// v = act(v) for eight values; NaN stays NaN.  One branch per run, not per value.
+__device__ __forceinline__ void act8(int act, float (&v)[8]) {
   switch (act) {
-    case kActRelu: return z < 0.0f ? 0.0f : z;
-    case kActGelu: return z * normal_cdf(z);
-    case kActGeluTanh: return z * logistic(2.0f * kTanhA * (z + kTanhB * z * z * z));  // (1 + tanh u) / 2 = logistic(2 u)
-    case kActSilu: return z * logistic(z);
-    default: return z;
+    case kActRelu:
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = v[j] < 0.0f ? 0.0f : v[j];
+      return;
+    case kActGelu:
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= normal_cdf(v[j]);
+      return;
+    case kActGeluTanh:  // (1 + tanh u) / 2 = logistic(2 u)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= logistic(2.0f * kTanhA * (v[j] + kTanhB * v[j] * v[j] * v[j]));
+      return;
+    case kActSilu:
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= logistic(v[j]);
+      return;
+    default: return;
   }
 }
 
-// act(z) and act'(z).  The slopes are 0 or 1 to fp32 precision beyond |z| = 30
-// (SILU: 100), where their formulas would form 0 * inf.
-__device__ __forceinline__ void act_both(int act, float z, float& value, float& slope) {
+__device__ __forceinline__ float clamped(float z, float most) { return z > most ? most : (z < -most ? -most : z); }
+
+// value = act(z) and slope = act'(z) for eight values.  The slopes are 0 or 1 to
+// fp32 precision beyond |z| = 30 (SILU: 100), where their formulas would form 0 * inf.
+__device__ __forceinline__ void act8_both(int act, const float (&z)[8], float (&value)[8], float (&slope)[8]) {
   switch (act) {
     case kActRelu:
-      value = z < 0.0f ? 0.0f : z;
-      slope = z > 0.0f ? 1.0f : 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        value[j] = z[j] < 0.0f ? 0.0f : z[j];
+        slope[j] = z[j] > 0.0f ? 1.0f : 0.0f;
+      }
       return;
-    case kActGelu: {
-      const float c = z > 30.0f ? 30.0f : (z < -30.0f ? -30.0f : z);
-      const float phi = normal_cdf(c);
-      value = z * phi;
-      slope = phi + c * 0.3989422804014327f * quick_exp(-0.5f * c * c);
+    case kActGelu:
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float c = clamped(z[j], 30.0f), phi = normal_cdf(c);
+        value[j] = z[j] * phi;
+        slope[j] = phi + c * 0.3989422804014327f * quick_exp(-0.5f * c * c);
+      }
       return;
-    }
-    case kActGeluTanh: {
-      const float c = z > 30.0f ? 30.0f : (z < -30.0f ? -30.0f : z);
-      const float s = logistic(2.0f * kTanhA * (c + kTanhB * c * c * c));
-      value = z * s;
-      slope = s + c * s * (1.0f - s) * 2.0f * kTanhA * (1.0f + 3.0f * kTanhB * c * c);
+    case kActGeluTanh:
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float c = clamped(z[j], 30.0f), s = logistic(2.0f * kTanhA * (c + kTanhB * c * c * c));
+        value[j] = z[j] * s;
+        slope[j] = s + c * s * (1.0f - s) * 2.0f * kTanhA * (1.0f + 3.0f * kTanhB * c * c);
+      }
       return;
-    }
-    case kActSilu: {
-      const float c = z > 100.0f ? 100.0f : (z < -100.0f ? -100.0f : z);
-      const float s = logistic(c);
-      value = z * s;
-      slope = s * (1.0f + c * (1.0f - s));
+    case kActSilu:
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float c = clamped(z[j], 100.0f), s = logistic(c);
+        value[j] = z[j] * s;
+        slope[j] = s * (1.0f + c * (1.0f - s));
+      }
       return;
-    }
     default:
-      value = z;
-      slope = 1.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        value[j] = z[j];
+        slope[j] = 1.0f;
+      }
   }
 }
 
@@ -114,10 +137,7 @@ __device__ __forceinline__ void finish8(const LinearProduct& g, int64_t m, int n
     for (int j = 0; j < 8; ++j) v[j] += u[j];
   }
   if (g.z != nullptr) store8((T*)g.z + at, v);
-  if (g.act != kActNone) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = act_value(g.act, v[j]);
-  }
+  act8(g.act, v);
   if (g.mul != nullptr) {
     load8((const T*)g.mul + at, u);
 #pragma unroll
@@ -418,8 +438,8 @@ __device__ __forceinline__ f32x16 mfma32_f32(float first, float second, f32x16 a
 }
 
 // The fp32 tiles: BT x BT outputs by two groups of four waves of (BT / 2)^2, each
-// group taking 16 of a stage's 32 k; two LDS buffers, the next stage's values
-// loaded into registers under the products.  An operand with k contiguous is
+// group taking 16 of a stage's 32 k; two LDS buffers, the next stage stored and the one
+// behind it loaded into registers under the products.  An operand with k contiguous is
 // transposed on its way into LDS; its row pitch of BT + 2 spreads the eight
 // quads of a row over the banks.
 template <int BT_>
@@ -432,17 +452,29 @@ template <bool KC, int BT>
 struct LoaderF {
   static constexpr int BK = 32, QUADS = BT * BK / 4 / kThreads, PITCH = KC ? BT + 2 : BT + 32;
   static_assert(QUADS >= 1, "a quad per thread");
+  const float* src[QUADS];
+  int k[QUADS];
+  int64_t step;
   f32x4 v[QUADS];
-  // four neighbouring elements each; those outside are zero (the contiguous extent is a multiple of 4)
-  __device__ __forceinline__ void fetch(const void* base, int64_t ld, int r0, int rows, int k0, int ke) {
+  __device__ __forceinline__ void init(const void* base, int64_t ld, int r0, int rows, int k0) {
+    step = KC ? BK : BK * ld;
 #pragma unroll
     for (int i = 0; i < QUADS; ++i) {
       const int q = threadIdx.x + kThreads * i;
       const int r = r0 + (KC ? q / (BK / 4) : 4 * (q % (BT / 4)));
-      const int k = k0 + (KC ? 4 * (q % (BK / 4)) : q / (BT / 4));
-      const bool in = r < rows && k < ke;
-      const int64_t at = KC ? r * ld + k : k * ld + r;
-      v[i] = in ? *(const f32x4*)((const float*)base + at) : f32x4{0.f, 0.f, 0.f, 0.f};
+      k[i] = k0 + (KC ? 4 * (q % (BK / 4)) : q / (BT / 4));
+      src[i] = (const float*)base + (KC ? r * ld + k[i] : k[i] * ld + r);
+      if (r >= rows) k[i] = 0x40000000;  // never inside
+    }
+  }
+  // Four neighbouring elements each of the next stage, zeros for those outside
+  // (the contiguous extent is a multiple of 4).
+  __device__ __forceinline__ void fetch(int ke) {
+#pragma unroll
+    for (int i = 0; i < QUADS; ++i) {
+      v[i] = *(const f32x4*)(k[i] < ke ? src[i] : reinterpret_cast<const float*>(kZeroChunk));
+      src[i] += step;
+      k[i] += BK;
     }
   }
   __device__ __forceinline__ void put(float* s) const {
@@ -482,75 +514,92 @@ __device__ __forceinline__ void tile_product_f32(const LinearProduct& g, int til
     for (int j = 0; j < NB; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  la.fetch(g.a, g.lda, m0, g.M, kb, ke);
-  lb.fetch(g.b, g.ldb, n0, g.N, kb, ke);
+  la.init(g.a, g.lda, m0, g.M, kb);
+  lb.init(g.b, g.ldb, n0, g.N, kb);
+  auto fetch = [&] {
+    la.fetch(ke);
+    lb.fetch(ke);
+  };
+  auto put = [&](int turn) {
+    la.put(s_f + turn * 2 * BUF);
+    lb.put(s_f + turn * 2 * BUF + BUF);
+  };
+  fetch();
+  put(0);
+  fetch();
+  __syncthreads();
   int turn = 0;
   for (int k0 = kb; k0 < ke; k0 += BK, turn ^= 1) {
-    float* s_a = s_f + turn * 2 * BUF;
-    float* s_b = s_a + BUF;
-    la.put(s_a);
-    lb.put(s_b);
-    __syncthreads();  // the other buffer is free as well: every wave is past its products
-    if (k0 + BK < ke) {
-      la.fetch(g.a, g.lda, m0, g.M, k0 + BK, ke);
-      lb.fetch(g.b, g.ldb, n0, g.N, k0 + BK, ke);
-    }
-#pragma unroll
-    for (int k = 0; k < BK / 2; k += 2) {
-      float fa[NB], fb[NB];
-      const int kk = kg * (BK / 2) + k + hk;
+    const float* s_a = s_f + turn * 2 * BUF;
+    const float* s_b = s_a + BUF;
+    // fragments one step ahead of the products
+    float fa[2][NB], fb[2][NB];
+    auto read = [&](int step) {
+      const int kk = kg * (BK / 2) + 2 * step + hk;
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
-        fa[i] = s_a[kk * LA::PITCH + 32 * (NB * wm + i) + l32];
-        fb[i] = s_b[kk * LB::PITCH + 32 * (NB * wn + i) + l32];
+        fa[step & 1][i] = s_a[kk * LA::PITCH + 32 * (NB * wm + i) + l32];
+        fb[step & 1][i] = s_b[kk * LB::PITCH + 32 * (NB * wn + i) + l32];
       }
+    };
+    auto products = [&](int step) {
+      if (step + 1 < BK / 4) read(step + 1);
 #pragma unroll
       for (int j = 0; j < NB; ++j)
 #pragma unroll
-        for (int i = 0; i < NB; ++i) acc[i][j] = mfma32_f32(fb[j], fa[i], acc[i][j]);
+        for (int i = 0; i < NB; ++i) acc[i][j] = mfma32_f32(fb[step & 1][j], fa[step & 1][i], acc[i][j]);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);            // one product
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);            // the next step's reads
+      __builtin_amdgcn_sched_group_barrier(0x008, NB * NB - 1, 0);  // the other products
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    // Under the products: the next stage into the other buffer (every wave has been
+    // past its products there since the last barrier), and the one behind it into
+    // registers.  The two groups, which share the SIMDs, do so at different times:
+    // together they left the matrix pipes idle for a quarter of the stage.
+    auto advance = [&] {
+      if (k0 + BK < ke) {
+        put(turn ^ 1);
+        fetch();
+      }
+    };
+    read(0);
+#pragma unroll
+    for (int step = 0; step < BK / 4; ++step) {
+      products(step);
+      if (step == 1 && kg == 0) advance();
+      if (step == BK / 4 - 3 && kg == 1) advance();
     }
+    __syncthreads();
   }
-  // The second group's sums reach the first through LDS.  There, lane pairs l, l + 32 hold the
-  // two halves of eight neighbouring columns of one row: they swap quads so that each holds whole runs.
-  static_assert(4 * 64 * NB * NB * 16 * 4 <= C::LDS, "the second group's sums");
-  __syncthreads();
+  // The tile leaves through LDS ([row][BT], 16-byte chunk c of row r at c ^ (r & 15)), the groups' sums added there.
+  static_assert(BT * BT * 4 <= C::LDS, "staging");
 #pragma unroll
-  for (int i = 0; i < NB; ++i)
+  for (int k2 = 0; k2 < 2; ++k2) {
+    if (kg == k2) {
 #pragma unroll
-    for (int j = 0; j < NB; ++j)
+      for (int i = 0; i < NB; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        f32x4* at = (f32x4*)(s_f + (((i * NB + j) * 4 + q) * 256 + w * 64 + l) * 4);
-        if (kg == 1) *at = f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-      }
-  __syncthreads();
-  if (kg == 1) return;
+        for (int j = 0; j < NB; ++j)
 #pragma unroll
-  for (int i = 0; i < NB; ++i)
-#pragma unroll
-    for (int j = 0; j < NB; ++j) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const f32x4 o = *(const f32x4*)(s_f + (((i * NB + j) * 4 + q) * 256 + w * 64 + l) * 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += o[e];
-      }
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int m = m0 + 32 * (NB * wm + i) + l32;
-        const int n = n0 + 32 * (NB * wn + j) + 16 * p + 8 * hk;
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // quads 2 p (columns + 0..7) and 2 p + 1 (columns + 8..15): lane half 0 keeps the first run, half 1 the second
-          const float mine0 = acc[i][j][8 * p + e], mine1 = acc[i][j][8 * p + 4 + e];
-          const float got = __shfl_xor(hk ? mine0 : mine1, 32, kWave);
-          v[e] = hk ? got : mine0;
-          v[4 + e] = hk ? mine1 : got;
-        }
-        if (m < g.M && n < g.N) leave8<float>(g, slice, m, n, v);
-      }
+          for (int q = 0; q < 4; ++q) {
+            const int row = 32 * (NB * wm + i) + l32, col = 32 * (NB * wn + j) + 8 * q + 4 * hk;
+            f32x4* at = (f32x4*)(s_f + row * BT + 4 * ((col >> 2) ^ (row & 15)));
+            f32x4 v = f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+            if (k2 > 0) v += *at;
+            *at = v;
+          }
     }
+    __syncthreads();
+  }
+  for (int it = tid; it < BT * BT / 8; it += kThreads) {
+    const int row = it / (BT / 8), c8 = it % (BT / 8), m = m0 + row, n = n0 + 8 * c8;
+    if (m >= g.M || n >= g.N) continue;
+    const f32x4 lo = *(const f32x4*)(s_f + row * BT + 4 * ((2 * c8) ^ (row & 15)));
+    const f32x4 hi = *(const f32x4*)(s_f + row * BT + 4 * ((2 * c8 + 1) ^ (row & 15)));
+    float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    leave8<float>(g, slice, m, n, v);
+  }
 }
 
 template <typename T, bool AKC, bool BKC, typename C, bool TAIL>
@@ -620,17 +669,21 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(int rows, int O, int act
       float d[8];
       load8(dy + at, d);
       if (z != nullptr) {
-        float zv[8], mv[8], dm[8];
+        float zv[8], value[8], slope[8];
         load8(z + at, zv);
-        if (mul != nullptr) load8(mul + at, mv);
+        act8_both(act, zv, value, slope);
+        if (mul != nullptr) {
+          float mv[8];
+          load8(mul + at, mv);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float value, slope;
-          act_both(act, zv[j], value, slope);
-          dm[j] = d[j] * value;
-          d[j] = (mul != nullptr ? d[j] * mv[j] : d[j]) * slope;
+          for (int j = 0; j < 8; ++j) {
+            value[j] *= d[j];
+            d[j] *= mv[j];
+          }
+          store8(dmul + at, value);
         }
-        if (mul != nullptr) store8(dmul + at, dm);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] *= slope[j];
         store8(dz + at, d);
       }
 #pragma unroll
