@@ -355,6 +355,7 @@ int check_norm(const char* fn, int T, int H, int dtype) {
 
 int check_linear(const char* fn, int T, int I, int O, int dtype, int act) {
   REQUIRE(T >= 1, MOE_ERR_INVALID_ARGUMENT, "%s: T=%d must be >= 1", fn, T);
+  REQUIRE(T <= moe::kLinearMaxRows, MOE_ERR_UNSUPPORTED, "%s: T=%d exceeds %d", fn, T, moe::kLinearMaxRows);
   int rc = check_dtype(fn, dtype);
   if (rc || (rc = check_row_width(fn, "I", I)) || (rc = check_row_width(fn, "O", O))) return rc;
   REQUIRE(I <= moe::kLinearMaxWidth && O <= moe::kLinearMaxWidth, MOE_ERR_UNSUPPORTED, "%s: I=%d or O=%d exceeds %d",
@@ -981,7 +982,7 @@ int moe_layernorm_bwd(int T, int H, int dtype, const void* x, const void* gamma,
 }
 
 size_t moe_linear_workspace_bytes(int T, int I, int O, int dtype) {
-  if (T < 1 || I < 1 || O < 1 || I > moe::kLinearMaxWidth || O > moe::kLinearMaxWidth || esize_of(dtype) == 0) return 0;
+  if (T < 1 || T > moe::kLinearMaxRows || I < 1 || O < 1 || I > moe::kLinearMaxWidth || O > moe::kLinearMaxWidth || esize_of(dtype) == 0) return 0;
   return moe::linear_workspace_bytes(T, I, O, esize_of(dtype));
 }
 

@@ -229,7 +229,7 @@ hipError_t launch_layernorm_bwd(int T, int H, int esize, const void* x, const vo
                                 const float* rstd, const void* dy, const void* dx_add, void* dx, void* dgamma,
                                 void* dbeta, void* ws, hipStream_t stream);
 
-constexpr int kLinearMaxWidth = 1 << 20;
+constexpr int kLinearMaxWidth = 1 << 20, kLinearMaxRows = 1 << 30;
 // Dense product of T rows, I inputs, O outputs: x [T, I], w [I, O].
 struct LinearArgs {
   int T, I, O;

@@ -731,12 +731,12 @@ struct TileCost {
   int bm, bn;
   double step, step_few, round;
 };
-constexpr TileCost kCost[kTiles] = {{256, 256, 1.62, 1.13, 8.5},
-                                    {256, 128, 0.94, 0.74, 4.5},
-                                    {128, 128, 0.53, 0.47, 2.6},
-                                    {128, 64, 0.33, 0.27, 2.0},
-                                    {64, 64, 0.22, 0.19, 1.0}};
-constexpr TileCost kCostF[kTilesF] = {{128, 128, 4.0, 4.0, 3.0}, {64, 64, 1.4, 1.2, 2.0}};  // fp32, per 64 k
+constexpr TileCost kCost[kTiles] = {{256, 256, 1.62, 1.18, 9.0},
+                                    {256, 128, 0.94, 0.74, 5.0},
+                                    {128, 128, 0.55, 0.47, 2.7},
+                                    {128, 64, 0.35, 0.29, 2.1},
+                                    {64, 64, 0.24, 0.20, 1.3}};
+constexpr TileCost kCostF[kTilesF] = {{128, 128, 4.1, 4.05, 5.0}, {64, 64, 1.23, 1.22, 1.2}};  // fp32, per 64 k
 
 constexpr int kCus = 256, kFew = 160;
 constexpr double kLaunchUs = 3.5;           // one more kernel behind another
@@ -769,11 +769,13 @@ Cut cut_of(int M, int N, int K, int esize, int tile, int want, bool few) {
 // (2048 x 768 outputs over 4099 rows: 56 us on 128 x 128 tiles, 31 us in two
 // slices with the sum behind them).
 template <typename Fn>
-void each_cut(int M, int N, int K, int esize, int tile, bool few, Fn&& f) {
+void each_cut(int M, int N, int K, int esize, int tile, Fn&& f) {
+  int last = 0;
   for (int want : {1, 2, 3, 4, 6, 8, 12, 16}) {
-    const Cut c = cut_of(M, N, K, esize, tile, want, few);
-    if (want > 1 && (c.slices == 1 || c.groups > 2 * kCus)) return;
-    f(c);
+    const Cut c = cut_of(M, N, K, esize, tile, want, false);
+    if (want > 1 && c.groups > 2 * kCus) return;
+    if (c.slices != last) f(c);
+    last = c.slices;
   }
 }
 
@@ -782,7 +784,7 @@ Cut plan_fwd(int M, int N, int K, int esize) {
   Cut best{};
   double best_us = 0.0;
   for (int tile = 0; tile < (esize == 2 ? (int)kTiles : (int)kTilesF); ++tile)
-    each_cut(M, N, K, esize, tile, false, [&](const Cut& c) {
+    each_cut(M, N, K, esize, tile, [&](const Cut& c) {
       const int64_t rest = c.groups % kCus;
       double us = kLaunchUs + (double)(c.groups / kCus) * c.each + (c.slices > 1 ? kLaunchUs + c.after : 0.0);
       if (rest > 0) us += rest > kFew ? c.each : cut_of(M, N, K, esize, tile, c.slices, true).each;
@@ -828,12 +830,35 @@ Plan2 plan_bwd(int T, int I, int O, int esize, bool dx, bool dw) {
     };
     auto with_w = [&](const Cut* x) {
       if (!dw) return weigh(x, nullptr);
-      each_cut(I, O, T, esize, tiles.w, false, [&](const Cut& w) { weigh(x, &w); });
+      each_cut(I, O, T, esize, tiles.w, [&](const Cut& w) { weigh(x, &w); });
     };
     if (!dx) with_w(nullptr);
-    else each_cut(T, I, O, esize, tiles.x, false, [&](const Cut& x) { with_w(&x); });
+    else each_cut(T, I, O, esize, tiles.x, [&](const Cut& x) { with_w(&x); });
   }
   return best;
+}
+
+// The last plans of this thread by their sizes: a training or decoding loop asks
+// for the same few shapes, and a search costs a few us of the host's time.
+template <typename P, typename Fn>
+const P& remembered(int T, int I, int O, int kind, Fn&& search) {
+  struct Entry {
+    int T, I, O, kind;
+    P plan;
+  };
+  thread_local Entry entries[64] = {};
+  const uint32_t h = ((uint32_t)T * 0x9e3779b1u) ^ ((uint32_t)I * 0x85ebca77u) ^ ((uint32_t)O * 0xc2b2ae3du) ^
+                     ((uint32_t)kind * 0x27d4eb2fu);
+  Entry& e = entries[(h >> 16) & 63];
+  if (e.T != T || e.I != I || e.O != O || e.kind != kind) e = Entry{T, I, O, kind, search()};
+  return e.plan;
+}
+const Cut& fwd_cut(int T, int I, int O, int esize) {
+  return remembered<Cut>(T, I, O, esize, [&] { return plan_fwd(T, O, I, esize); });
+}
+const Plan2& bwd_cuts(int T, int I, int O, int esize, bool dx, bool dw) {
+  return remembered<Plan2>(T, I, O, esize + (dx ? 8 : 0) + (dw ? 16 : 0),
+                           [&] { return plan_bwd(T, I, O, esize, dx, dw); });
 }
 
 size_t slice_bytes(int M, int N, const Cut& c) {
@@ -871,7 +896,7 @@ hipError_t run_fwd(const LinearProduct& g, int64_t groups, hipStream_t stream) {
 
 template <typename T>
 hipError_t linear_fwd_typed(LinearProduct g, float* ws, hipStream_t stream) {
-  const Cut c = plan_fwd(g.M, g.N, g.K, sizeof(T));
+  const Cut& c = fwd_cut(g.M, g.K, g.N, sizeof(T));
   g.slice = c.slice;
   g.part = c.slices > 1 ? ws : nullptr;
   hipError_t err;
@@ -925,7 +950,7 @@ hipError_t linear_bwd_typed(const LinearArgs& g, const void* z, const void* mul,
   }
   if (dx == nullptr && dw == nullptr && dbias == nullptr) return hipSuccess;
   const void* d = plain ? dy : dz;
-  const Plan2 p = plan_bwd(T_, I, O, sizeof(T), dx != nullptr, dw != nullptr);
+  const Plan2& p = bwd_cuts(T_, I, O, sizeof(T), dx != nullptr, dw != nullptr);
   LinearProduct gx{T_, I, O, d, O, g.w, O, kActNone, nullptr, nullptr, dx_add, nullptr, dx, p.x.slice, nullptr};
   LinearProduct gw{I, O, T_, g.x, I, d, O, kActNone, nullptr, nullptr, nullptr, nullptr, dw, p.w.slice, nullptr};
   const ColumnSum sum{ws, slots, O, dbias};
@@ -960,14 +985,17 @@ hipError_t linear_bwd_typed(const LinearArgs& g, const void* z, const void* mul,
 
 }  // namespace
 
-// The partials: the forward's slices, or the backward's column sums and both products' slices.
+// The partials of any call with these sizes: the forward's slices, or the
+// backward's column sums and both products' slices (either product may be left out).
 size_t linear_workspace_bytes(int T, int I, int O, int esize) {
-  size_t need = slice_bytes(T, O, plan_fwd(T, O, I, esize));
-  for (int want = 0; want < 4; ++want) {  // any of dx and dw
-    const Plan2 p = plan_bwd(T, I, O, esize, want & 1, want & 2);
-    need = std::max(need, dbias_bytes(T, O) + slice_bytes(T, I, p.x) + slice_bytes(I, O, p.w));
-  }
-  return need;
+  return remembered<size_t>(T, I, O, esize + 32, [&] {
+    size_t need = slice_bytes(T, O, fwd_cut(T, I, O, esize));
+    for (int want = 0; want < 4; ++want) {
+      const Plan2& p = bwd_cuts(T, I, O, esize, want & 1, want & 2);
+      need = std::max(need, dbias_bytes(T, O) + slice_bytes(T, I, p.x) + slice_bytes(I, O, p.w));
+    }
+    return need;
+  });
 }
 
 hipError_t launch_linear_fwd(const LinearArgs& g, int esize, const void* bias, const void* mul, const void* residual,

@@ -113,6 +113,9 @@ int moe_abi_version(void);
  *   moe_router_bwd_dlogits                  2, plus 1 when its dW_r reduction is split
  *   moe_route_scored, moe_route_scored_bwd, moe_layernorm_fwd  1
  *   moe_layernorm_bwd                       2
+ *   moe_linear_fwd                          1, plus 1 when its reduction is split
+ *   moe_linear_bwd                          1 for dz or dbias (none without an activation, gate
+ *                                           and dbias), 1 for the products, plus 1 for each that is split
  * These counts are what a HIP graph of a layer step captures. */
 int64_t moe_launch_count(void);
 
@@ -593,7 +596,7 @@ size_t moe_linear_workspace_bytes(int T, int I, int O, int dtype);
  * backward), y [T, O] (device, out).  y may be mul or residual; z_save and y
  * overlap nothing else.  With act = SILU and mul = x W_up this is a gated expert's hidden row; with residual =
  * the routed experts' sum a shared expert's output joins it.
- * I and O multiples of 8, at most 2^20, pointers 16-byte aligned, workspace of at least moe_linear_workspace_bytes (may
+ * I and O multiples of 8, at most 2^20, T at most 2^30, pointers 16-byte aligned, workspace of at least moe_linear_workspace_bytes (may
  * be NULL when that is 0).  Calls that may overlap need a workspace each. */
 int moe_linear_fwd(int T, int I, int O, int dtype, int act, const void* x, const void* w, const void* bias,
                    const void* mul, const void* residual, void* z_save, void* y, void* workspace,
