@@ -158,12 +158,16 @@ __device__ __forceinline__ void leave8(const LinearProduct& g, int slice, int64_
   else finish8<T>(g, m, n, v);
 }
 
-// Adds the slices of a split reduction in order, then the epilogue.
+// Adds the slices of split reductions in order, then the epilogue: `first`
+// workgroups for one product, the others for a second one.
 template <typename T>
-__global__ __launch_bounds__(256) void linear_slices_kernel(LinearProduct g, int slices) {
-  const int runs = g.N / 8;
+__global__ __launch_bounds__(256) void linear_slices_kernel(LinearProduct g0, LinearProduct g1, int first) {
+  const bool second = (int)blockIdx.x >= first;
+  const LinearProduct& g = second ? g1 : g0;
+  const int groups = second ? gridDim.x - first : first, group = second ? blockIdx.x - first : blockIdx.x;
+  const int runs = g.N / 8, slices = (g.K + g.slice - 1) / g.slice;
   const int64_t total = (int64_t)g.M * runs, MN = (int64_t)g.M * g.N;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+  for (int64_t i = (int64_t)group * 256 + threadIdx.x; i < total; i += (int64_t)groups * 256) {
     float v[8], u[8];
     load8(g.part + 8 * i, v);
     for (int s = 1; s < slices; ++s) {
@@ -865,13 +869,16 @@ size_t slice_bytes(int M, int N, const Cut& c) {
   return c.slices > 1 ? ((size_t)c.slices * M * N * sizeof(float) + 15) / 16 * 16 : 0;
 }
 
+// The sums of up to two split products (those with partials) in one launch.
 template <typename T>
-hipError_t add_slices(const LinearProduct& g, hipStream_t stream) {
-  if (g.part == nullptr) return hipSuccess;
-  const int slices = (g.K + g.slice - 1) / g.slice;
-  const int64_t runs = (int64_t)g.M * (g.N / 8);
-  MOE_LAUNCH((linear_slices_kernel<T>), dim3((unsigned)std::min<int64_t>((runs + 255) / 256, 4096)), dim3(256), 0,
-             stream, g, slices);
+hipError_t add_slices(const LinearProduct& a, const LinearProduct& b, hipStream_t stream) {
+  auto groups = [](const LinearProduct& g) {
+    const int64_t runs = (int64_t)g.M * (g.N / 8);
+    return g.part == nullptr ? 0 : (int)std::min<int64_t>((runs + 255) / 256, 2048);
+  };
+  const int ga = groups(a), gb = groups(b);
+  if (ga + gb == 0) return hipSuccess;
+  MOE_LAUNCH((linear_slices_kernel<T>), dim3(ga + gb), dim3(256), 0, stream, a, b, ga);
   return hipGetLastError();
 }
 
@@ -918,7 +925,7 @@ hipError_t linear_fwd_typed(LinearProduct g, float* ws, hipStream_t stream) {
     }
   }
   if (err != hipSuccess) return err;
-  return add_slices<T>(g, stream);
+  return add_slices<T>(g, LinearProduct{}, stream);
 }
 
 template <typename T, typename CX, typename CW, bool TAIL>
@@ -979,8 +986,8 @@ hipError_t linear_bwd_typed(const LinearArgs& g, const void* z, const void* mul,
       default: err = run(Tile4{}, Tile4{}); break;
     }
   }
-  if (err != hipSuccess || (err = add_slices<T>(gx, stream)) != hipSuccess) return err;
-  return add_slices<T>(gw, stream);
+  if (err != hipSuccess) return err;
+  return add_slices<T>(gx, gw, stream);
 }
 
 }  // namespace

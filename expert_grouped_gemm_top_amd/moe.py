@@ -490,7 +490,7 @@ def _addr(t, name, shape, dtype, dev):
     if t is None:
         return None
     try:
-        if t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.device.index == dev:
+        if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
@@ -501,23 +501,24 @@ def _addr(t, name, shape, dtype, dev):
 
 
 def _need(t, name, shape, dtype, dev):
-    if t is None:
+    p = _addr(t, name, shape, dtype, dev)
+    if p is None:
         raise MoeError(f"{name} is required")
-    return _addr(t, name, shape, dtype, dev)
+    return p
 
 
 def _space(workspace, dev):
     """Address and bytes of a workspace."""
     if workspace is None:
         return None, 0
-    return _addr(workspace, "workspace", workspace.shape, workspace.dtype, dev), workspace.nbytes
+    return _addr(workspace, "workspace", workspace.shape, workspace.dtype, dev), workspace.nbytes  # any shape and type
 
 
 def _device(t, name):
     """The current device, for a call whose first argument is `t`."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise MoeError(f"{name} must be a GPU tensor")
-    return torch.cuda.current_device()
+    return torch._C._cuda_getDevice()
 
 
 def _queue(stream, dev):

@@ -115,7 +115,7 @@ int moe_abi_version(void);
  *   moe_layernorm_bwd                       2
  *   moe_linear_fwd                          1, plus 1 when its reduction is split
  *   moe_linear_bwd                          1 for dz or dbias (none without an activation, gate
- *                                           and dbias), 1 for the products, plus 1 for each that is split
+ *                                           and dbias), 1 for the products, plus 1 when either is split
  * These counts are what a HIP graph of a layer step captures. */
 int64_t moe_launch_count(void);
 

@@ -203,6 +203,10 @@ def test_calls_on_another_device_are_refused():
         @property
         def device(self):
             return torch.device("cuda", torch.cuda.current_device() + 1)
+
+        def get_device(self):
+            return torch.cuda.current_device() + 1
+
     x = torch.zeros(4, 64, device="cuda")
     with pytest.raises(moe.MoeError, match="current device"):
         moe.moe_layernorm_fwd(x.as_subclass(Elsewhere), x[0].clone(), None, torch.empty_like(x))
