@@ -863,6 +863,10 @@ int moe_route_scored(int T, int E, int k, int score, int n_groups, int top_group
   NONNULL(logits);
   NONNULL(topk_idx);
   NONNULL(topk_w);
+  const int64_t sel = (int64_t)T * k * 4;
+  const Span sl{"logits", logits, (int64_t)T * E * 4}, sb{"bias", bias, (int64_t)E * 4};
+  const Span si{"topk_idx", topk_idx, sel}, sw{"topk_w", topk_w, sel};
+  if ((rc = check_output(fn, si, {sl, sb, sw}, false)) || (rc = check_output(fn, sw, {sl, sb}, false))) return rc;
   hipStream_t s = as_stream(stream);
   return hip_status(timed(MOE_K_ROUTE_SCORED, s,
                           [&] {

@@ -253,7 +253,7 @@ struct Norm {
   static hipError_t fwd(int T_, int H, float eps, const void* x, const void* gamma, const void* beta, void* y,
                         float* mean, float* rstd, hipStream_t stream) {
     constexpr int RPW = kWaves / WPR;
-    MOE_LAUNCH((layernorm_fwd_kernel<T, WPR, NC>), dim3((T_ + RPW - 1) / RPW), dim3(64 * kWaves), 0, stream, T_, H,
+    MOE_LAUNCH((layernorm_fwd_kernel<T, WPR, NC>), dim3((unsigned)(((int64_t)T_ + RPW - 1) / RPW)), dim3(64 * kWaves), 0, stream, T_, H,
                eps, (const T*)x, (const T*)gamma, (const T*)beta, (T*)y, mean, rstd, past_caches(T_, H, sizeof(T)));
     return hipGetLastError();
   }

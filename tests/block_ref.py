@@ -105,6 +105,40 @@ def route(l, bias, k, score, groups=1, top_groups=1, group_top=1, renorm=True, s
     return idx.astype(np.int32), weights(l, idx, score, renorm, scale)
 
 
+def undecided(l, bias, k, score, groups=1, top_groups=1, group_top=1):
+    """Tokens whose choice 64-bit arithmetic does not define: two different sums (a choice score s + b, or the
+    worth of a group) next to the border that are equal as real numbers, or as good as.  A sum of up to four
+    terms below 2 is off by at most 4 ulp, 2^-50, and either side may round the other way: 2^-48 apart decides.
+    Sums of the same logits and biases are equal on both sides and go by index."""
+    l = np.asarray(l, np.float64)
+    T, E = l.shape
+    b = np.zeros(E) if bias is None else np.asarray(bias, np.float64)
+    c = np.where(l == -INF, -INF, scores(l, score) + b)
+    out = np.zeros(T, bool)
+    if bias is None and (groups == 1 or group_top == 1):
+        return out
+    near = 2.0 ** -48
+    for t in range(T):
+        order = _ranked(c[t:t + 1])[0]
+        if groups > 1:
+            size = E // groups
+            best = [sorted(range(g * size, (g + 1) * size), key=lambda e: -c[t, e])[:group_top] for g in range(groups)]
+            worth = np.array([sum(c[t, e] for e in m if c[t, e] > -INF) if c[t, m[0]] > -INF else -INF for m in best])
+            by = np.argsort(-worth, kind="stable")
+            edge = by[top_groups - 1]
+            for g in by:  # any group as good as the last kept one, but from other terms
+                same = [(l[t, e], b[e]) for e in best[g]] == [(l[t, e], b[e]) for e in best[edge]]
+                if g != edge and abs(worth[g] - worth[edge]) <= near and not same:
+                    out[t] = True
+            kept = set(by[:top_groups])
+            order = [e for e in order if e // size in kept]
+        if bias is not None:
+            for i, j in zip(order[:k], order[1:k + 1]):
+                if abs(c[t, i] - c[t, j]) <= near and (l[t, i], b[i]) != (l[t, j], b[j]):
+                    out[t] = True
+    return out
+
+
 def weights(l, idx, score, renorm, scale):
     """Of the selected experts, from log scores: ratios that do not underflow."""
     l = np.asarray(l, np.float64)

@@ -43,7 +43,8 @@ def test_route_scored(lib):
         ({5: 9}, 1, "top_groups"), ({6: 0}, 1, "group_top"), ({6: 3}, 1, "group_top"),
         ({1: 8, 2: 1, 4: 8, 5: 1, 6: 2}, 1, "group size 1"), ({1: 32, 5: 1, 2: 5}, 1, "4 experts of 1"),
         ({8: float("nan")}, 1, "scale"), ({8: float("inf")}, 1, "scale"),
-        ({9: NULL}, 1, "logits"), ({11: NULL}, 1, "topk_idx"), ({12: NULL}, 1, "topk_w")])
+        ({9: NULL}, 1, "logits"), ({11: NULL}, 1, "topk_idx"), ({12: NULL}, 1, "topk_w"), ({11: P(0)}, 1, "topk_idx overlaps logits"),
+        ({12: P(1)}, 1, "topk_w overlaps bias"), ({12: ctypes.c_void_p(P(2).value + 4)}, 1, "topk_idx overlaps topk_w")])
 
 
 def test_route_scored_bwd(lib):
@@ -87,7 +88,7 @@ def test_linear_fwd(lib):
     ws = lib.moe_linear_workspace_bytes(64, 256, 128, 1)
     ok = [64, 256, 128, 1, 4] + [P(i) for i in range(8)] + [ws, NULL]
     refuses(lib, lib.moe_linear_fwd, ok, [
-        ({0: 0}, 1, "T=0"), ({1: 20}, 2, "I=20"), ({2: 0}, 1, "O=0"), ({2: 36}, 2, "O=36"), ({1: (1 << 20) + 8}, 2, "exceeds"),
+        ({0: 0}, 1, "T=0"), ({0: (1 << 30) + 1}, 2, "T=1073741825"), ({1: 20}, 2, "I=20"), ({2: 0}, 1, "O=0"), ({2: 36}, 2, "O=36"), ({1: (1 << 20) + 8}, 2, "exceeds"),
         ({3: 4}, 1, "dtype"), ({4: 5}, 1, "activation"), ({4: -1}, 1, "activation"), ({5: NULL}, 1, "x must"), ({6: NULL}, 1, "w must"),
         ({11: NULL}, 1, "y must"), ({5: ctypes.c_void_p(34)}, 1, "aligned"), ({11: P(0)}, 1, "y overlaps x"),
         ({11: P(1)}, 1, "y overlaps w"), ({11: P(5)}, 1, "y overlaps z_save"), ({10: P(4)}, 1, "z_save overlaps residual"),

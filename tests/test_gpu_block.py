@@ -124,6 +124,28 @@ def test_block_on_another_stream():
         assert torch.equal(t, ref[n]), n
 
 
+def test_two_blocks_at_once():
+    """Two steps on two streams, each with its own buffers, interleaved call by call."""
+    steps = []
+    for seed in (23, 40):
+        B, p, new = make(seed=seed)
+        steps.append((B, p, new(), new()))
+    ref = []
+    for B, p, x, dy in steps:
+        step(B, p, x, dy)
+        torch.cuda.synchronize()
+        ref.append({n: t.clone() for n, t in outputs(B).items()})
+    streams = [torch.cuda.Stream() for _ in steps]
+    for _ in range(3):
+        for s, (B, p, x, dy) in zip(streams, steps):
+            s.wait_stream(torch.cuda.current_stream())
+            step(B, p, x, dy, s)
+    torch.cuda.synchronize()
+    for r, (B, *_) in zip(ref, steps):
+        for n, t in outputs(B).items():
+            assert torch.equal(t, r[n]), n
+
+
 def test_block_in_a_captured_graph():
     """Replays with new inputs are the eager step bit for bit, with eager steps between them, and two graphs
     that share a workspace, replayed in turn."""
@@ -193,8 +215,39 @@ def test_launch_counts():
     assert counted(moe.moe_route_scored_bwd, f(T, E), idx, f(T, k), f(T, E)) == 1
     assert counted(moe.moe_layernorm_fwd, b(T, H), b(H), None, b(T, H)) == 1
     ws = f(1 << 24, dt=torch.uint8)
+    w, y = b(H, O), b(T, O)
+    assert counted(moe.moe_linear_fwd, b(T, H), w, None, y, workspace=ws) == 1
+    assert counted(moe.moe_linear_bwd, b(T, H), w, y, None, b(T, H), b(H, O), workspace=ws) == 1
+    assert counted(moe.moe_linear_bwd, b(T, H), w, y, None, b(T, H), b(H, O), b(O), workspace=ws) == 2
+    assert counted(moe.moe_linear_bwd, b(T, H), w, y, b(T, O), b(T, H), b(H, O), b(O), 4, y, workspace=ws) == 2
+    # one row tile and a long reduction: split, so its slices are added
+    assert counted(moe.moe_linear_fwd, b(8, 8192), b(8192, 64), None, b(8, 64), workspace=ws) == 2
     assert counted(moe.moe_layernorm_bwd, b(T, H), b(H), f(T), f(T), b(T, H), b(T, H), b(H), b(H), ws) == 2
     torch.cuda.synchronize()
+
+
+def test_profiling_hook_times_the_new_phases():
+    import ctypes
+    L = moe.lib()
+    L.moe_profile_kernel.argtypes = [ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p]
+    B, p, new = make()
+    x, dy = new(), new()
+    step(B, p, x, dy)
+    torch.cuda.synchronize()
+    ref = {n: t.clone() for n, t in outputs(B).items()}
+    events = {}
+    for kind in (12, 13, 14, 15):  # MOE_K_ROUTE_SCORED, LAYERNORM, LINEAR_FWD, LINEAR_BWD
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record(), b.record()
+        events[kind] = (a, b)
+        assert L.moe_profile_kernel(kind, ctypes.c_void_p(a.cuda_event), ctypes.c_void_p(b.cuda_event)) == 0
+    assert L.moe_profile_kernel(16, None, None) == 1
+    step(B, p, x, dy)
+    torch.cuda.synchronize()
+    for kind, (a, b) in events.items():
+        assert 0.0 < a.elapsed_time(b) < 50.0, kind
+    for n, t in outputs(B).items():
+        assert torch.equal(t, ref[n]), n
 
 
 def test_calls_on_another_device_are_refused():

@@ -146,3 +146,29 @@ def test_rows_behind_the_last_are_left():
     moe.moe_layernorm_fwd(x[:9], gamma, None, y[:9])
     torch.cuda.synchronize()
     assert (y[9:] == 7.0).all() and (y[:9] == 0.0).all()
+
+
+def test_rows_past_32_bits():
+    """More than 2^31 elements: the last rows forward and backward, and dgamma over all."""
+    T, H = (1 << 31) // 4096 + 700, 4096
+    note(f"norm T={T} H={H}")
+    v = inputs(300, H, "bf16", 11)
+    x, dy = torch.ones(T, H, dtype=torch.bfloat16, device="cuda"), torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    x[-300:], dy[-300:] = R.dev(v["x"], "bf16"), R.dev(v["dy"], "bf16")
+    y, mean, rstd = torch.empty_like(x), torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    gamma, beta = R.dev(v["gamma"], "bf16"), R.dev(v["beta"], "bf16")
+    moe.moe_layernorm_fwd(x, gamma, beta, y, mean, rstd)
+    dga, dbe = torch.empty_like(gamma), torch.empty_like(gamma)
+    ws = torch.empty(moe.moe_layernorm_workspace_bytes(T, H), dtype=torch.uint8, device="cuda")
+    last = R.host(y[-300:])
+    moe.moe_layernorm_bwd(x, gamma, mean, rstd, dy, y, dga, dbe, ws)
+    torch.cuda.synchronize()
+    ry, rm, rr = R.norm(v["x"], v["gamma"], v["beta"], 1e-5)
+    # half a bf16 step and what check_forward counts for fp32, here at most 200 half steps of values below 30
+    R.within("y", last, ry, 2.0 ** -8 * np.abs(ry) + 200 * 30 * STEP)
+    rx, rg, rb = R.norm_bwd(v["x"], v["gamma"], rm, rr, v["dy"])
+    R.within("dx", R.host(y[-300:]), rx, 2.0 ** -8 * np.abs(rx) + 400 * 30 * STEP)
+    assert (y[:-300] == 0).all()
+    # the other rows add exact zeros; sums of 300 terms below 30
+    R.within("dgamma", R.host(dga), rg, 2.0 ** -8 * np.abs(rg) + 320 * 300 * 5 * STEP)
+    R.within("dbeta", R.host(dbe), rb, 2.0 ** -8 * np.abs(rb) + 320 * 300 * 5 * STEP)

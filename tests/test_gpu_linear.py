@@ -70,7 +70,7 @@ def test_forward(T, I, O, dtype):  # noqa: E741
 LARGE = [  # every workgroup tile with and without masked edges, split reductions, more workgroups than CUs
     (4096, 2048, 4096, "bf16"), (4090, 2040, 4088, "bf16"), (2500, 1024, 2048, "bf16"), (4099, 2048, 768, "bf16"),
     (700, 1032, 1000, "bf16"), (40, 4096, 512, "bf16"), (9, 4104, 4096, "bf16"), (1500, 520, 1032, "f32"),
-    (70, 3080, 136, "f32"),
+    (70, 3080, 136, "f32"), (3, 65536, 64, "bf16"), (2, 20000, 40, "f32"),
 ]
 
 
@@ -209,3 +209,46 @@ def test_nan_stays_in_its_row():
         torch.cuda.synchronize()
         bad = torch.isnan(y).cpu().numpy()
         assert bad[7].all() and not np.delete(bad, 7, axis=0).any()
+
+
+def test_rows_past_32_bits():
+    """More than 2^31 outputs and inputs: the last rows of each."""
+    T, I, O = (1 << 31) // 2048 + 300, 2048, 64  # noqa: E741
+    for T, I, O in ((T, I, O), (T, O, I)):  # noqa: E741
+        note(f"linear T={T} I={I} O={O}")
+        v = inputs(300, I, O, "bf16", 12)
+        bf = dict(dtype=torch.bfloat16, device="cuda")
+        x, dy, z = torch.zeros(T, I, **bf), torch.zeros(T, O, **bf), torch.zeros(T, O, **bf)
+        x[-300:], dy[-300:], z[-300:] = R.dev(v["x"], "bf16"), R.dev(v["dy"], "bf16"), R.dev(v["z"], "bf16")
+        w, b = R.dev(v["w"], "bf16"), R.dev(v["b"], "bf16")
+        y = torch.empty(T, O, **bf)
+        ws = torch.empty(max(16, moe.moe_linear_workspace_bytes(T, I, O, torch.bfloat16)), dtype=torch.uint8, device="cuda")
+        moe.moe_linear_fwd(x, w, b, y, R.SILU, workspace=ws)
+        torch.cuda.synchronize()
+        ry, _ = R.linear(v["x"], v["w"], v["b"], R.SILU)
+        size = np.abs(v["x"]) @ np.abs(v["w"]) + np.abs(v["b"])
+        R.within("y", R.host(y[-300:]), ry, 2.0 ** -8 * np.abs(ry) + 1.2 * (I + 40) * 2.0 ** -23 * size)
+        first = R.act(R.SILU, v["b"])  # rows of zeros
+        R.within("y of zeros", R.host(y[:5]), np.tile(first, (5, 1)), 2.0 ** -8 * np.abs(first) + 1e-6)
+        dx, dw = torch.empty(T, I, **bf), torch.empty_like(w)
+        moe.moe_linear_bwd(x, w, dy, y, dx, dw, None, R.SILU, z, workspace=ws)
+        torch.cuda.synchronize()
+        rz, _ = R.linear_dz(v["z"], None, v["dy"], R.SILU)
+        slip = 2.0 ** -8 * np.abs(rz) + 40 * 2.0 ** -24 * np.abs(v["dy"]) * (1 + np.abs(v["z"]))
+        ref, size = rz @ v["w"].T, np.abs(rz) @ np.abs(v["w"].T)
+        R.within("dx", R.host(dx[-300:]), ref, 2.0 ** -8 * np.abs(ref) + (O + 2) * 2.0 ** -23 * size + 1.01 * slip @ np.abs(v["w"].T))
+        ref, size = v["x"].T @ rz, np.abs(v["x"].T) @ np.abs(rz)
+        R.within("dw", R.host(dw), ref, 2.0 ** -8 * np.abs(ref) + 302 * 2.0 ** -23 * size + 1.01 * np.abs(v["x"].T) @ slip)
+        assert (dx[:-300] == 0).all()
+
+
+def test_rows_behind_the_last_are_left():
+    v = inputs(40, 72, 136, "bf16", 13)
+    t = {n: R.dev(v[n], "bf16") for n in ("x", "w", "b", "dy")}
+    y = torch.full((60, 136), 7.0, dtype=torch.bfloat16, device="cuda")
+    dx = torch.full((60, 72), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws, need = workspace(40, 72, 136, "bf16")
+    moe.moe_linear_fwd(t["x"], t["w"], t["b"], y[:40], workspace=ws[:need])
+    moe.moe_linear_bwd(t["x"], t["w"], t["dy"], None, dx[:40], None, workspace=ws[:need])
+    torch.cuda.synchronize()
+    assert (y[40:] == 7.0).all() and (dx[40:] == 7.0).all()
