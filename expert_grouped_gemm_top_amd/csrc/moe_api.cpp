@@ -360,6 +360,8 @@ int check_linear(const char* fn, int T, int I, int O, int dtype, int act) {
   if (rc || (rc = check_row_width(fn, "I", I)) || (rc = check_row_width(fn, "O", O))) return rc;
   REQUIRE(I <= moe::kLinearMaxWidth && O <= moe::kLinearMaxWidth, MOE_ERR_UNSUPPORTED, "%s: I=%d or O=%d exceeds %d",
           fn, I, O, moe::kLinearMaxWidth);
+  REQUIRE((int64_t)T * std::max(I, O) < ((int64_t)1 << 40), MOE_ERR_UNSUPPORTED, "%s: T=%d rows of %d are too large", fn,
+          T, std::max(I, O));
   REQUIRE(act >= MOE_ACT_NONE && act <= MOE_ACT_SILU, MOE_ERR_INVALID_ARGUMENT, "%s: unknown activation %d", fn, act);
   return MOE_OK;
 }
@@ -986,7 +988,9 @@ int moe_layernorm_bwd(int T, int H, int dtype, const void* x, const void* gamma,
 }
 
 size_t moe_linear_workspace_bytes(int T, int I, int O, int dtype) {
-  if (T < 1 || T > moe::kLinearMaxRows || I < 1 || O < 1 || I > moe::kLinearMaxWidth || O > moe::kLinearMaxWidth || esize_of(dtype) == 0) return 0;
+  if (T < 1 || T > moe::kLinearMaxRows || I < 1 || O < 1 || I > moe::kLinearMaxWidth || O > moe::kLinearMaxWidth ||
+      (int64_t)T * std::max(I, O) >= ((int64_t)1 << 40) || esize_of(dtype) == 0)
+    return 0;
   return moe::linear_workspace_bytes(T, I, O, esize_of(dtype));
 }
 

@@ -4,13 +4,19 @@
 //   z = x W + bias,  y = act(z) [* mul] [+ residual]
 //   dz = dy [* mul] act'(z),  dmul = dy act(z),
 //   dx = dz W^T [+ dx_add],  dW = x^T dz,  dbias = sum_t dz
+//
+// The products run on the matrix cores from LDS tiles: bf16 on 32x32x16, fp32 on
+// 32x32x2.  Sums are fp32 throughout.  The backward rounds dz to the element
+// type once, as the operand of both products and a tensor the caller keeps:
+// that adds an error as large as the outputs' own rounding (2^-9 of dx and dW
+// in the root mean square); dbias sums the unrounded values.
 #include <algorithm>
-#include <iterator>
 #include <type_traits>
 
 #include "moe_common.h"
 #include "moe_launch.h"
 #include "moe_lds32.h"
+#include "moe_linear_plan.h"
 #include "moe_rows.h"
 
 namespace moe {
@@ -623,8 +629,11 @@ __global__ __launch_bounds__(kThreads, 2) void linear_fwd_kernel(LinearProduct g
 }
 
 // The backward's products in one launch, so that one's workgroups fill the CUs
-// that the other leaves idle: `nw` workgroups of x^T dz, `nx` of dz W^T (the longer ones first), and behind them
-// the sums of dbias' partial rows.
+// that the other leaves idle: `nw` workgroups of x^T dz, `nx` of dz W^T (the
+// longer ones first), and behind them the sums of dbias' partial rows.  Both
+// products at 4099 x 2048 x 768: 46 us, in launches of their own 30 + 33; at
+// 128 x 2048 x 768 10.3 us, 9.6 + 9.6; at 8192 x 4096 x 1408 203-210 us
+// (0.90-0.93 PFLOP/s; 171 us on operands of zeros, so the chip's power bounds it).
 struct ColumnSum {
   const float* part;
   int n, cols;
@@ -636,6 +645,7 @@ __device__ __forceinline__ void column_sum(const ColumnSum& c, int block, float*
   const int w = threadIdx.x >> 6, l = threadIdx.x & 63, col = block * 64 + l;
   float v = 0.0f;
   if (col < c.cols)
+#pragma unroll 8
     for (int p = w; p < c.n; p += kThreads / 64) v += c.part[(size_t)p * c.cols + col];
   s[w * 64 + l] = v;
   __syncthreads();
@@ -647,8 +657,8 @@ __device__ __forceinline__ void column_sum(const ColumnSum& c, int block, float*
 }
 
 template <typename T, typename CX, typename CW, bool TAIL>
-__global__ __launch_bounds__(kThreads, 2) void linear_bwd_kernel(LinearProduct gx, LinearProduct gw, ColumnSum sum, int nx,
-                                                                 int nw, int x_first) {
+__global__ __launch_bounds__(kThreads, 2) void linear_bwd_kernel(LinearProduct gx, LinearProduct gw, ColumnSum sum,
+                                                                 int nx, int nw, int x_first) {
   extern __shared__ __attribute__((aligned(16))) unsigned char s_dyn[];
   int b = blockIdx.x;
   if (b >= nx + nw) return column_sum<T>(sum, b - nx - nw, reinterpret_cast<float*>(s_dyn));
@@ -657,7 +667,8 @@ __global__ __launch_bounds__(kThreads, 2) void linear_bwd_kernel(LinearProduct g
   else any_product<T, false, false, CW, TAIL>(gw, x_first ? b - nx : b, s_dyn);
 }
 
-// dz, dmul and the column sums of dz.  Workgroup = 32 runs of eight columns x 8
+// dz, dmul and the column sums of dz.  HBM-bound: 25 us at 8192 x 1408 with a
+// gate (three tensors read, two written, 4.6 TB/s).  Workgroup = 32 runs of eight columns x 8
 // rows at a time, blockIdx.y strides over the rows; each thread keeps its
 // columns' sums, the eight of a column meet in LDS and leave one partial row.
 template <typename T>
@@ -715,132 +726,12 @@ size_t dbias_bytes(int T, int O) { return ((size_t)dz_slots(T, O) * O * sizeof(f
 
 // ---- launchers -------------------------------------------------------------------
 
-// The workgroup tiles, largest first, and what a pass of them over the chip's
-// 256 CUs takes: `step` us per 64 k (`step_few` when at most 160 workgroups
-// run), `round` us for a tile's prologue and epilogue.  Measured on one MI355X with
-// grids of 128, 256 and 512 workgroups and reductions of 512, 2048 and 4096
-// (all three operand layouts within 8 %).  A larger tile moves fewer bytes
-// through LDS per product (at 256 workgroups: 256 x 256 1.32 PFLOP/s,
-// 256 x 128 1.14, 128 x 128 1.01, 128 x 64 0.84, 64 x 64 0.61) but leaves CUs
-// idle where the outputs are few: 4099 x 768 over 2048 takes 49 us on 256 x 256,
-// 30 on 256 x 128, 20.9 on 128 x 128, 25.8 on 128 x 64 tiles.
-enum { kTile256x256 = 0, kTile256x128, kTile128x128, kTile128x64, kTile64x64, kTiles };
+// The tiles of moe_linear_plan.h.
 using Tile0 = Tile<256, 256, 8, 2, 1, 2>;
 using Tile1 = Tile<256, 128, 8, 4, 1, 3>;
 using Tile2 = Tile<128, 128, 4, 2, 2, 2>;
 using Tile3 = Tile<128, 64, 4, 2, 2, 3>;
 using Tile4 = Tile<64, 64, 4, 2, 2, 4>;
-enum { kTileF128 = 0, kTileF64, kTilesF };
-struct TileCost {
-  int bm, bn;
-  double step, step_few, round;
-};
-constexpr TileCost kCost[kTiles] = {{256, 256, 1.62, 1.18, 9.0},
-                                    {256, 128, 0.94, 0.74, 5.0},
-                                    {128, 128, 0.55, 0.47, 2.7},
-                                    {128, 64, 0.35, 0.29, 2.1},
-                                    {64, 64, 0.24, 0.20, 1.3}};
-constexpr TileCost kCostF[kTilesF] = {{128, 128, 4.1, 4.05, 5.0}, {64, 64, 1.23, 1.22, 1.2}};  // fp32, per 64 k
-
-constexpr int kCus = 256, kFew = 160;
-constexpr double kLaunchUs = 3.5;           // one more kernel behind another
-constexpr double kSliceBytesPerUs = 4.0e6;  // partials written and read again
-
-const TileCost& cost_of(int tile, int esize) { return esize == 2 ? kCost[tile] : kCostF[tile]; }
-
-// How a product is cut: its workgroup tile and the slices of its reduction.
-struct Cut {
-  int tile, slices, slice;  // k per slice
-  int64_t groups;           // workgroups
-  double each;              // us of one workgroup
-  double after;             // us of adding the slices
-};
-
-Cut cut_of(int M, int N, int K, int esize, int tile, int want, bool few) {
-  constexpr int kGrain = 128;  // slices are whole stages
-  const TileCost& t = cost_of(tile, esize);
-  Cut c{};
-  c.tile = tile;
-  c.slice = (int)((((int64_t)K + want - 1) / want + kGrain - 1) / kGrain * kGrain);
-  c.slices = (K + c.slice - 1) / c.slice;
-  c.groups = (int64_t)((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn) * c.slices;
-  c.each = (double)((std::min(K, c.slice) + 63) / 64) * (few ? t.step_few : t.step) + t.round;
-  c.after = c.slices > 1 ? (double)c.slices * M * N * 8.0 / kSliceBytesPerUs : 0.0;
-  return c;
-}
-
-// Cuts worth a look: splitting a reduction pays where few tiles meet a long one
-// (2048 x 768 outputs over 4099 rows: 56 us on 128 x 128 tiles, 31 us in two
-// slices with the sum behind them).
-template <typename Fn>
-void each_cut(int M, int N, int K, int esize, int tile, Fn&& f) {
-  int last = 0;
-  for (int want : {1, 2, 3, 4, 6, 8, 12, 16}) {
-    const Cut c = cut_of(M, N, K, esize, tile, want, false);
-    if (want > 1 && c.groups > 2 * kCus) return;
-    if (c.slices != last) f(c);
-    last = c.slices;
-  }
-}
-
-// The forward's cut of least estimated time: full passes over the CUs, then the rest.
-Cut plan_fwd(int M, int N, int K, int esize) {
-  Cut best{};
-  double best_us = 0.0;
-  for (int tile = 0; tile < (esize == 2 ? (int)kTiles : (int)kTilesF); ++tile)
-    each_cut(M, N, K, esize, tile, [&](const Cut& c) {
-      const int64_t rest = c.groups % kCus;
-      double us = kLaunchUs + (double)(c.groups / kCus) * c.each + (c.slices > 1 ? kLaunchUs + c.after : 0.0);
-      if (rest > 0) us += rest > kFew ? c.each : cut_of(M, N, K, esize, tile, c.slices, true).each;
-      if (best.slices == 0 || us < best_us) {
-        best = c;
-        best_us = us;
-      }
-    });
-  return best;
-}
-
-// The backward's cuts: dx and dw share a launch (Pairs: which tiles meet), so
-// what counts is their joint work over the CUs, and the longest workgroup.
-struct Plan2 {
-  int pair;
-  Cut x, w;
-};
-struct Pair {
-  int x, w;
-};
-constexpr Pair kPairs[] = {{kTile256x256, kTile256x256}, {kTile256x256, kTile256x128}, {kTile256x128, kTile256x256},
-                           {kTile256x128, kTile256x128}, {kTile128x128, kTile128x128}, {kTile128x64, kTile128x64},
-                           {kTile64x64, kTile64x64}};
-constexpr Pair kPairsF[] = {{kTileF128, kTileF128}, {kTileF64, kTileF64}};
-
-Plan2 plan_bwd(int T, int I, int O, int esize, bool dx, bool dw) {
-  Plan2 best{};
-  double best_us = -1.0;
-  const int pairs = esize == 2 ? (int)std::size(kPairs) : (int)std::size(kPairsF);
-  for (int p = 0; p < pairs; ++p) {
-    const Pair tiles = esize == 2 ? kPairs[p] : kPairsF[p];
-    auto weigh = [&](const Cut* x, const Cut* w) {
-      const int64_t gx = x ? x->groups : 0, gw = w ? w->groups : 0;
-      const double ex = x ? x->each : 0.0, ew = w ? w->each : 0.0;
-      double us = std::max({((double)gx * ex + (double)gw * ew) / kCus, ex, ew});
-      if (gx + gw > kCus) us += 0.5 * std::min(gx ? ex : ew, gw ? ew : ex);  // the last ones end unevenly
-      const double after = (x ? x->after : 0.0) + (w ? w->after : 0.0);
-      if (after > 0.0) us += kLaunchUs + after;
-      if (best_us < 0.0 || us < best_us) {
-        best_us = us;
-        best = Plan2{p, x ? *x : Cut{}, w ? *w : Cut{}};
-      }
-    };
-    auto with_w = [&](const Cut* x) {
-      if (!dw) return weigh(x, nullptr);
-      each_cut(I, O, T, esize, tiles.w, [&](const Cut& w) { weigh(x, &w); });
-    };
-    if (!dx) with_w(nullptr);
-    else each_cut(T, I, O, esize, tiles.x, [&](const Cut& x) { with_w(&x); });
-  }
-  return best;
-}
 
 // The last plans of this thread by their sizes: a training or decoding loop asks
 // for the same few shapes, and a search costs a few us of the host's time.
@@ -973,8 +864,10 @@ hipError_t linear_bwd_typed(const LinearArgs& g, const void* z, const void* mul,
     auto run = [&](auto tx, auto tw) {
       using CX = decltype(tx);
       using CW = decltype(tw);
-      const bool tail = (dx != nullptr && has_tail<true, true, CX>(gx)) || (dw != nullptr && has_tail<false, false, CW>(gw));
-      return tail ? run_bwd<T, CX, CW, true>(gx, gw, sum, p, stream) : run_bwd<T, CX, CW, false>(gx, gw, sum, p, stream);
+      const bool tail = (dx != nullptr && has_tail<true, true, CX>(gx)) ||
+                        (dw != nullptr && has_tail<false, false, CW>(gw));
+      return tail ? run_bwd<T, CX, CW, true>(gx, gw, sum, p, stream)
+                  : run_bwd<T, CX, CW, false>(gx, gw, sum, p, stream);
     };
     switch (p.pair) {
       case 0: err = run(Tile0{}, Tile0{}); break;
@@ -1008,7 +901,8 @@ size_t linear_workspace_bytes(int T, int I, int O, int esize) {
 hipError_t launch_linear_fwd(const LinearArgs& g, int esize, const void* bias, const void* mul, const void* residual,
                              void* z, void* y, void* ws, hipStream_t stream) {
   const LinearProduct p{g.T, g.O, g.I, g.x, g.I, g.w, g.O, g.act, bias, mul, residual, z, y, 0, nullptr};
-  return esize == 4 ? linear_fwd_typed<float>(p, (float*)ws, stream) : linear_fwd_typed<uint16_t>(p, (float*)ws, stream);
+  return esize == 4 ? linear_fwd_typed<float>(p, (float*)ws, stream)
+                    : linear_fwd_typed<uint16_t>(p, (float*)ws, stream);
 }
 
 hipError_t launch_linear_bwd(const LinearArgs& g, int esize, const void* z, const void* mul, const void* dy, void* dz,

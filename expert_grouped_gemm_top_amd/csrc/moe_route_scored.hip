@@ -253,6 +253,12 @@ __device__ __forceinline__ bool choose_exactly(const RouteArgs& g, const float* 
 // best are ordered by their 64-bit choice scores; where that does not settle
 // it, or a group is in doubt, or a value is not finite, the wave decides that
 // token over all experts in 64 bits (choose_exactly).  The choice is the exact one on every path.
+//
+// Measured at 16384 tokens: softmax over 128 experts 5.8 us, sigmoid with a bias
+// over 256 10.1 us, in 8 groups of which 4 are kept 13.3 us (everything in 64
+// bits, a wave per token: 149 us; the 17.8 MB alone would take 3.6 us).  Logits
+// with many equal values take the exact ways more often: 18 us on a grid of a
+// quarter.
 template <int V, bool FULL>
 __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs g) {
   __shared__ RouteLds<V> s;
@@ -510,7 +516,8 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs g) {
 // every lane writes whole runs of the token's dlogits once.  HBM-bound: the
 // output, and for plain softmax (DENSE, the only one whose gradient reaches
 // every expert) the logits.  QUAD: runs of four experts, every sixteenth run
-// of a lane; otherwise single experts.
+// of a lane; otherwise single experts.  16384 tokens, 128 experts: 6.2 us,
+// 2.9 TB/s (a wave per token that looked each of its experts up among the selected: 14.9 us).
 template <bool QUAD, bool DENSE>
 __global__ __launch_bounds__(256) void route_scored_bwd_kernel(int T, int E, int k, int score, int renorm, float scale,
                                                                const float* __restrict__ logits,
@@ -649,7 +656,8 @@ hipError_t launch_route_scored_bwd(int T, int E, int k, int score, bool renormal
     MOE_LAUNCH(kernel, grid, block, 0, stream, T, E, k, score, (int)renormalize, scale, logits, idx, dg, dlogits);
     return hipGetLastError();
   };
-  if (score == 0 && !renormalize) return quad ? run(route_scored_bwd_kernel<true, true>) : run(route_scored_bwd_kernel<false, true>);
+  if (score == 0 && !renormalize)
+    return quad ? run(route_scored_bwd_kernel<true, true>) : run(route_scored_bwd_kernel<false, true>);
   return quad ? run(route_scored_bwd_kernel<true, false>) : run(route_scored_bwd_kernel<false, false>);
 }
 

@@ -114,8 +114,9 @@ int moe_abi_version(void);
  *   moe_route_scored, moe_route_scored_bwd, moe_layernorm_fwd  1
  *   moe_layernorm_bwd                       2
  *   moe_linear_fwd                          1, plus 1 when its reduction is split
- *   moe_linear_bwd                          1 for dz or dbias (none without an activation, gate
- *                                           and dbias), 1 for the products, plus 1 when either is split
+ *   moe_linear_bwd                          1 for dz or dbias (0 without activation, gate and
+ *                                           dbias), 1 for the products and the sum of dbias,
+ *                                           plus 1 when a product is split
  * These counts are what a HIP graph of a layer step captures. */
 int64_t moe_launch_count(void);
 
@@ -520,8 +521,8 @@ typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_scor
  *    expert is worth -inf.  It is listed only when fewer than k experts are
  *    left, with weight 0.  A token whose selected scores are all zero has
  *    weights 0, not NaN.
- *  - A NaN choice score (or worth) ranks above every number, NaNs by lower index; a softmax
- *    token with a NaN or +inf logit has NaN scores throughout.
+ *  - A NaN choice score (or worth) ranks above every number, NaNs by lower
+ *    index; a softmax token with a NaN or +inf logit has NaN scores throughout.
  * Requires n_groups <= 16, n_groups dividing E, 1 <= top_groups <= n_groups,
  * group_top <= E / n_groups, k <= top_groups * E / n_groups, scale finite.
  * logits [T, E] fp32, bias [E] fp32 or NULL (device); topk_idx [T, k] int32,
@@ -554,10 +555,10 @@ int moe_router_bwd_dlogits(int T, int H, int E, int dtype, const void* x, const 
 
 /* Layer norm over rows of H:
  *   y = (x - mean) rstd gamma + beta, rstd = 1 / sqrt(var + eps)
- * with mean and (biased) variance in fp32, the variance from the differences to the mean.
- * x, y [T, H], gamma [H], beta [H] or NULL, of `dtype` (device); mean, rstd
- * [T] fp32 (device, out; both or neither may be NULL when no backward follows).  y may be x.  eps >= 0.
- * Pointers (but mean, rstd) 16-byte aligned.  H <= 16384. */
+ * with mean and (biased) variance in fp32, the variance from the differences
+ * to the mean.  x, y [T, H], gamma [H], beta [H] or NULL, of `dtype` (device);
+ * mean, rstd [T] fp32 (device, out; both NULL when no backward follows).  y
+ * may be x.  eps >= 0.  Pointers (but mean, rstd) 16-byte aligned.  H <= 16384. */
 int moe_layernorm_fwd(int T, int H, int dtype, float eps, const void* x, const void* gamma, const void* beta, void* y,
                       float* mean, float* rstd, void* stream);
 
@@ -568,10 +569,11 @@ size_t moe_layernorm_workspace_bytes(int T, int H);
 /* Its backward: with xh = (x - mean) rstd and g = dy gamma,
  *   dx = rstd (g - avg(g) - xh avg(g xh)) [+ dx_add],   averages over the row
  *   dgamma = sum_t dy xh,  dbeta = sum_t dy
- * Sums in fp32 in one fixed order.  dx_add [T, H] or NULL (the gradient that reaches x past the norm; it may
- * be dx); dx [T, H] (may be dy), dgamma [H], dbeta [H] or NULL of `dtype` (device, out);
- * workspace (device, 16-byte aligned) of at least moe_layernorm_workspace_bytes(T, H).
- * Calls that may overlap need a workspace each. */
+ * Sums in fp32 in one fixed order.  dx_add [T, H] or NULL (the gradient that
+ * reaches x past the norm; it may be dx); dx [T, H] (may be dy or x), dgamma
+ * [H], dbeta [H] or NULL of `dtype` (device, out); workspace (device, 16-byte
+ * aligned) of at least moe_layernorm_workspace_bytes(T, H).  Calls that may
+ * overlap in time need a workspace each. */
 int moe_layernorm_bwd(int T, int H, int dtype, const void* x, const void* gamma, const float* mean, const float* rstd,
                       const void* dy, const void* dx_add, void* dx, void* dgamma, void* dbeta, void* workspace,
                       size_t workspace_bytes, void* stream);
@@ -591,13 +593,15 @@ size_t moe_linear_workspace_bytes(int T, int I, int O, int dtype);
 
 /* Dense product with its epilogue:
  *   z = x W + bias,   y = act(z) [* mul] [+ residual]
- * all from the fp32 sums, y (and z_save) rounded once.  x [T, I], w [I, O], bias [O] or NULL, mul and
- * residual [T, O] or NULL of `dtype` (device); z_save [T, O] or NULL (z for the
- * backward), y [T, O] (device, out).  y may be mul or residual; z_save and y
- * overlap nothing else.  With act = SILU and mul = x W_up this is a gated expert's hidden row; with residual =
- * the routed experts' sum a shared expert's output joins it.
- * I and O multiples of 8, at most 2^20, T at most 2^30, pointers 16-byte aligned, workspace of at least moe_linear_workspace_bytes (may
- * be NULL when that is 0).  Calls that may overlap need a workspace each. */
+ * all from the fp32 sums, y (and z_save) rounded once.  x [T, I], w [I, O],
+ * bias [O] or NULL, mul and residual [T, O] or NULL of `dtype` (device);
+ * z_save [T, O] or NULL (z for the backward), y [T, O] (device, out).  y may be
+ * mul or residual; z_save and y overlap nothing else.  With act = SILU and
+ * mul = x W_up this is a gated expert's hidden row; with residual = the routed
+ * experts' sum a shared expert's output joins it.
+ * I and O multiples of 8, at most 2^20, T at most 2^30, T I and T O below 2^40,
+ * pointers 16-byte aligned, workspace of at least moe_linear_workspace_bytes (may be NULL when
+ * that is 0).  Calls that may overlap in time need a workspace each. */
 int moe_linear_fwd(int T, int I, int O, int dtype, int act, const void* x, const void* w, const void* bias,
                    const void* mul, const void* residual, void* z_save, void* y, void* workspace,
                    size_t workspace_bytes, void* stream);
@@ -607,9 +611,10 @@ int moe_linear_fwd(int T, int I, int O, int dtype, int act, const void* x, const
  *   dx = dz W^T [+ dx_add],  dw = x^T dz,  dbias = sum_t dz
  * z: the forward's z_save, needed when act is not NONE or mul is given, else
  * ignored.  dz [T, O] (device, out; of `dtype`: the operand of both products,
- * so rounded to it; dbias sums the unrounded values) is needed in those cases too, and may be dy or z; without them dz is dy itself and
- * the argument is ignored.  relu'(0) = 0.  dmul [T, O] is written when mul is given (required then; it may be mul, z or dy).
- * dx_add [T, I] or NULL (may be dx).  dx and dw may each be NULL (not
+ * so rounded to it; dbias sums the unrounded values) is needed in those cases
+ * too, and may be dy or z; without them dz is dy itself and the argument is
+ * ignored.  relu'(0) = 0.  dmul [T, O] is written when mul is given (required
+ * then; it may be mul, z or dy).  dx_add [T, I] or NULL (may be dx).  dx and dw may each be NULL (not
  * wanted), dbias [O] too.  dx overlaps none of the inputs but dx_add. */
 int moe_linear_bwd(int T, int I, int O, int dtype, int act, const void* x, const void* w, const void* z,
                    const void* mul, const void* dy, void* dz, const void* dx_add, void* dx, void* dw, void* dbias,

@@ -88,7 +88,7 @@ def test_linear_fwd(lib):
     ws = lib.moe_linear_workspace_bytes(64, 256, 128, 1)
     ok = [64, 256, 128, 1, 4] + [P(i) for i in range(8)] + [ws, NULL]
     refuses(lib, lib.moe_linear_fwd, ok, [
-        ({0: 0}, 1, "T=0"), ({0: (1 << 30) + 1}, 2, "T=1073741825"), ({1: 20}, 2, "I=20"), ({2: 0}, 1, "O=0"), ({2: 36}, 2, "O=36"), ({1: (1 << 20) + 8}, 2, "exceeds"),
+        ({0: 0}, 1, "T=0"), ({0: (1 << 30) + 1}, 2, "T=1073741825"), ({0: 1 << 28, 1: 4096}, 2, "too large"), ({1: 20}, 2, "I=20"), ({2: 0}, 1, "O=0"), ({2: 36}, 2, "O=36"), ({1: (1 << 20) + 8}, 2, "exceeds"),
         ({3: 4}, 1, "dtype"), ({4: 5}, 1, "activation"), ({4: -1}, 1, "activation"), ({5: NULL}, 1, "x must"), ({6: NULL}, 1, "w must"),
         ({11: NULL}, 1, "y must"), ({5: ctypes.c_void_p(34)}, 1, "aligned"), ({11: P(0)}, 1, "y overlaps x"),
         ({11: P(1)}, 1, "y overlaps w"), ({11: P(5)}, 1, "y overlaps z_save"), ({10: P(4)}, 1, "z_save overlaps residual"),
