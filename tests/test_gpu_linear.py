@@ -79,7 +79,9 @@ def test_forward_large(T, I, O, dtype):  # noqa: E741
     check_forward(inputs(T, I, O, dtype, T + O), dtype, R.GELU_TANH, mul=True, residual=True)
 
 
-@pytest.mark.parametrize("T,I,O,dtype", LARGE + [(4088, 4090 // 8 * 8, 4080, "bf16"), (8192, 4096, 1408, "bf16"), (8195, 64, 72, "bf16")])
+@pytest.mark.parametrize("T,I,O,dtype", LARGE + [
+    (4088, 4088, 4080, "bf16"), (8192, 4096, 1408, "bf16"), (8195, 64, 72, "bf16"), (1536, 2048, 4096, "bf16"),
+    (1530, 2040, 4088, "bf16"), (1024, 2560, 1000, "bf16"), (1536, 4096, 1408, "bf16"), (1023, 1000, 2048, "bf16")])
 def test_backward_large(T, I, O, dtype):  # noqa: E741
     check_backward(inputs(T, I, O, dtype, T + O), dtype, R.SILU, mul=True, add=True)
 
