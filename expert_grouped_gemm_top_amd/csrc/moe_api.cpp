@@ -332,10 +332,12 @@ int check_output(const char* fn, const Span& out, std::initializer_list<Span> ot
   return MOE_OK;
 }
 
-int check_workspace(const char* fn, size_t need, const void* ws, size_t ws_bytes) {
+// A workspace of at least `need` bytes that shares no memory with `others`.
+int check_workspace(const char* fn, size_t need, const void* ws, size_t ws_bytes, std::initializer_list<Span> others) {
   REQUIRE(ws_bytes >= need, MOE_ERR_WORKSPACE_TOO_SMALL, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need);
   REQUIRE(need == 0 || ws != nullptr, MOE_ERR_INVALID_ARGUMENT, "%s: workspace must not be NULL", fn);
-  return check_aligned(fn, "workspace", ws);
+  int rc = check_aligned(fn, "workspace", ws);
+  return rc ? rc : check_output(fn, {"workspace", ws, (int64_t)need}, others, false);
 }
 
 int check_score(const char* fn, int score, float scale) {
@@ -939,7 +941,10 @@ int moe_layernorm_fwd(int T, int H, int dtype, float eps, const void* x, const v
       (rc = check_aligned(fn, "beta", beta)) || (rc = check_aligned(fn, "y", y)) ||
       (rc = check_output(fn, {"y", y, row}, {{"x", x, row}}, true)) ||
       (rc = check_output(fn, {"y", y, row},
-                         {{"gamma", gamma, col}, {"beta", beta, col}, {"mean", mean, 4ll * T}, {"rstd", rstd, 4ll * T}}, false)))
+                         {{"gamma", gamma, col}, {"beta", beta, col}, {"mean", mean, 4ll * T}, {"rstd", rstd, 4ll * T}}, false)) ||
+      (rc = check_output(fn, {"mean", mean, 4ll * T},
+                         {{"x", x, row}, {"gamma", gamma, col}, {"beta", beta, col}, {"rstd", rstd, 4ll * T}}, false)) ||
+      (rc = check_output(fn, {"rstd", rstd, 4ll * T}, {{"x", x, row}, {"gamma", gamma, col}, {"beta", beta, col}}, false)))
     return rc;
   hipStream_t s = as_stream(stream);
   return hip_status(
@@ -974,9 +979,10 @@ int moe_layernorm_bwd(int T, int H, int dtype, const void* x, const void* gamma,
       (rc = check_aligned(fn, "dy", dy)) || (rc = check_aligned(fn, "dx_add", dx_add)) ||
       (rc = check_aligned(fn, "dx", dx)) || (rc = check_output(fn, sdx, {sx, sdy, sadd}, true)) ||
       (rc = check_output(fn, sdx, {sgamma, smean, srstd, sdg, sdb}, false)) ||
-      (rc = check_output(fn, sdg, {sx, sgamma, sdy, sadd, sdb}, false)) ||
-      (rc = check_output(fn, sdb, {sx, sgamma, sdy, sadd}, false)) ||
-      (rc = check_workspace(fn, moe::layernorm_workspace_bytes(T, H), workspace, workspace_bytes)))
+      (rc = check_output(fn, sdg, {sx, sgamma, smean, srstd, sdy, sadd, sdb}, false)) ||
+      (rc = check_output(fn, sdb, {sx, sgamma, smean, srstd, sdy, sadd}, false)) ||
+      (rc = check_workspace(fn, moe::layernorm_workspace_bytes(T, H), workspace, workspace_bytes,
+                            {sx, sgamma, smean, srstd, sdy, sadd, sdx, sdg, sdb})))
     return rc;
   hipStream_t s = as_stream(stream);
   return hip_status(timed(MOE_K_LAYERNORM, s,
@@ -1012,7 +1018,8 @@ int moe_linear_fwd(int T, int I, int O, int dtype, int act, const void* x, const
       (rc = check_aligned(fn, "z_save", z_save)) || (rc = check_aligned(fn, "y", y)) ||
       (rc = check_output(fn, sy, {sm, sr}, true)) || (rc = check_output(fn, sy, {sx, sw, sb, sz}, false)) ||
       (rc = check_output(fn, sz, {sx, sw, sb, sm, sr}, false)) ||
-      (rc = check_workspace(fn, moe::linear_workspace_bytes(T, I, O, es), workspace, workspace_bytes)))
+      (rc = check_workspace(fn, moe::linear_workspace_bytes(T, I, O, es), workspace, workspace_bytes,
+                            {sx, sw, sb, sm, sr, sz, sy})))
     return rc;
   const moe::LinearArgs g{T, I, O, act, x, w};
   hipStream_t s = as_stream(stream);
@@ -1057,7 +1064,8 @@ int moe_linear_bwd(int T, int I, int O, int dtype, int act, const void* x, const
       (rc = check_output(fn, sdx, {sx, sw, sz, sm, sdy, sdz, sdw, sdb, sdm}, false)) ||
       (rc = check_output(fn, sdw, {sx, sw, sz, sm, sdy, sdz, sadd, sdb, sdm}, false)) ||
       (rc = check_output(fn, sdb, {sx, sw, sz, sm, sdy, sdz, sadd, sdm}, false)) ||
-      (rc = check_workspace(fn, moe::linear_workspace_bytes(T, I, O, es), workspace, workspace_bytes)))
+      (rc = check_workspace(fn, moe::linear_workspace_bytes(T, I, O, es), workspace, workspace_bytes,
+                            {sx, sw, sz, sm, sdy, sdz, sadd, sdx, sdw, sdb, sdm})))
     return rc;
   const moe::LinearArgs g{T, I, O, act, x, w};
   hipStream_t s = as_stream(stream);

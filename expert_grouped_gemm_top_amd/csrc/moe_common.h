@@ -117,6 +117,9 @@ __device__ __forceinline__ void build_tile_starts(const int32_t* __restrict__ of
   __syncthreads();
 }
 
+// Number of this workgroup in a wide_grid().
+__device__ __forceinline__ int group_id() { return (int)(blockIdx.y * gridDim.x + blockIdx.x); }
+
 // XCD-aware order.  Workgroups are dealt round-robin to the 8 XCDs, each with
 // its own L2.  Map workgroup `wg` of a launch segment to a work item so that
 // every XCD walks a contiguous range of the `real` items (neighbouring items

@@ -70,6 +70,15 @@ inline void launch_kernel(F kernel, dim3 grid, dim3 block, size_t shmem, hipStre
 }
 #define MOE_LAUNCH(...) ::moe::launch_kernel(__VA_ARGS__)
 
+// A grid of at least `groups` workgroups, numbered by group_id().  A launch may
+// have 2^32 threads along x at most, so many workgroups lie in rows of up to
+// 2^22 (whole multiples of the 8 XCDs); those past `groups` have nothing to do.
+inline dim3 wide_grid(int64_t groups) {
+  const int64_t rows = (groups + (1 << 22) - 1) >> 22;
+  const int64_t per_row = (groups + rows - 1) / rows;
+  return rows == 1 ? dim3((unsigned)groups) : dim3((unsigned)((per_row + 7) / 8 * 8), (unsigned)rows);
+}
+
 constexpr int kMaxExpertsHost = 256;  // expert ids fit in 8 bits
 enum RowGemmMode { kGemmGateUp = 0, kGemmDown = 1, kGemmDA = 2, kGemmDX = 3 };
 

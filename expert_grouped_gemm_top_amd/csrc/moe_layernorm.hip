@@ -51,7 +51,7 @@ __global__ __launch_bounds__(64 * kWaves) void layernorm_fwd_kernel(int rows, in
                                                                     bool stream) {
   __shared__ float s_sum[2][kWaves];
   const int w = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.x * (kWaves / WPR) + w / WPR;
+  const int64_t t = (int64_t)group_id() * (kWaves / WPR) + w / WPR;
   const bool live = t < rows;
   const int r0 = 8 * ((w % WPR) * 64 + (threadIdx.x & 63));  // first column of this lane's runs
   const T* xr = x + (live ? t : 0) * H;
@@ -261,7 +261,7 @@ struct Norm {
                         float* mean, float* rstd, hipStream_t stream) {
     constexpr int RPW = kWaves / WPR;
     const int64_t groups = ((int64_t)T_ + RPW - 1) / RPW;
-    MOE_LAUNCH((layernorm_fwd_kernel<T, WPR, NC>), dim3((unsigned)groups), dim3(64 * kWaves), 0, stream, T_, H, eps,
+    MOE_LAUNCH((layernorm_fwd_kernel<T, WPR, NC>), wide_grid(groups), dim3(64 * kWaves), 0, stream, T_, H, eps,
                (const T*)x, (const T*)gamma, (const T*)beta, (T*)y, mean, rstd, past_caches(T_, H, sizeof(T)));
     return hipGetLastError();
   }

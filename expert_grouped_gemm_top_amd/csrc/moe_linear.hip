@@ -615,6 +615,7 @@ __device__ __forceinline__ void tile_product_f32(const LinearProduct& g, int til
 template <typename T, bool AKC, bool BKC, typename C, bool TAIL>
 __device__ __forceinline__ void any_product(const LinearProduct& g, int item, unsigned char* s_dyn) {
   const int tiles = ((g.M + C::BM - 1) / C::BM) * ((g.N + C::BN - 1) / C::BN);
+  if (item / tiles * (int64_t)g.slice >= g.K) return;  // past the last slice: the grid may hold a few more
   if constexpr (std::is_same<T, float>::value)
     tile_product_f32<AKC, BKC, C, TAIL>(g, item % tiles, item / tiles, s_dyn);
   else
@@ -625,7 +626,7 @@ __device__ __forceinline__ void any_product(const LinearProduct& g, int item, un
 template <typename T, typename C, bool TAIL>
 __global__ __launch_bounds__(kThreads, 2) void linear_fwd_kernel(LinearProduct g) {
   extern __shared__ __attribute__((aligned(16))) unsigned char s_dyn[];
-  any_product<T, true, false, C, TAIL>(g, blockIdx.x, s_dyn);
+  any_product<T, true, false, C, TAIL>(g, group_id(), s_dyn);
 }
 
 // The backward's products in one launch, so that one's workgroups fill the CUs
@@ -643,6 +644,7 @@ struct ColumnSum {
 template <typename T>
 __device__ __forceinline__ void column_sum(const ColumnSum& c, int block, float* s) {
   const int w = threadIdx.x >> 6, l = threadIdx.x & 63, col = block * 64 + l;
+  if (c.out == nullptr) return;
   float v = 0.0f;
   if (col < c.cols)
 #pragma unroll 8
@@ -660,7 +662,7 @@ template <typename T, typename CX, typename CW, bool TAIL>
 __global__ __launch_bounds__(kThreads, 2) void linear_bwd_kernel(LinearProduct gx, LinearProduct gw, ColumnSum sum,
                                                                  int nx, int nw, int x_first) {
   extern __shared__ __attribute__((aligned(16))) unsigned char s_dyn[];
-  int b = blockIdx.x;
+  const int b = group_id();
   if (b >= nx + nw) return column_sum<T>(sum, b - nx - nw, reinterpret_cast<float*>(s_dyn));
   const bool is_x = x_first ? b < nx : b >= nw;
   if (is_x) any_product<T, true, true, CX, TAIL>(gx, x_first ? b : b - nw, s_dyn);
@@ -788,7 +790,7 @@ hipError_t run_fwd(const LinearProduct& g, int64_t groups, hipStream_t stream) {
   static PerDeviceOnce once;
   hipError_t err = allow_dynamic_lds(once, (const void*)kern, C::LDS);
   if (err != hipSuccess) return err;
-  MOE_LAUNCH(kern, dim3((unsigned)groups), dim3(kThreads), C::LDS, stream, g);
+  MOE_LAUNCH(kern, wide_grid(groups), dim3(kThreads), C::LDS, stream, g);
   return hipGetLastError();
 }
 
@@ -828,7 +830,7 @@ hipError_t run_bwd(const LinearProduct& gx, const LinearProduct& gw, const Colum
   hipError_t err = allow_dynamic_lds(once, (const void*)kern, lds);
   if (err != hipSuccess) return err;
   const int64_t sums = sum.out != nullptr ? (sum.cols + 63) / 64 : 0;
-  MOE_LAUNCH(kern, dim3((unsigned)(p.x.groups + p.w.groups + sums)), dim3(kThreads), lds, stream, gx, gw, sum,
+  MOE_LAUNCH(kern, wide_grid(p.x.groups + p.w.groups + sums), dim3(kThreads), lds, stream, gx, gw, sum,
              (int)p.x.groups, (int)p.w.groups, p.x.each > p.w.each ? 1 : 0);
   return hipGetLastError();
 }

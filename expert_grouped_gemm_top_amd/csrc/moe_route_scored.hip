@@ -264,7 +264,7 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs g) {
   __shared__ RouteLds<V> s;
   const float inf = __builtin_inff();
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, tok = lane >> 4, li = lane & 15;
-  const int64_t t = (int64_t)blockIdx.x * 16 + 4 * wv + tok;
+  const int64_t t = (int64_t)group_id() * 16 + 4 * wv + tok;
   const bool live = t < g.T;
   const float* lt = g.logits + (live ? t : g.T - 1) * g.E;
   const int E = FULL ? kRow * V : g.E, k = g.k, per_lane = FULL ? V : g.per_lane;
@@ -487,7 +487,7 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs g) {
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
       if (((open >> (kRow * q)) & 0xffffu) == 0) continue;
-      const int64_t tq = min((int64_t)blockIdx.x * 16 + 4 * wv + q, (int64_t)g.T - 1);
+      const int64_t tq = min((int64_t)group_id() * 16 + 4 * wv + q, (int64_t)g.T - 1);
       const bool none = choose_exactly(g, g.logits + tq * g.E, s.value[wv][q], s.sel[wv][q]);
       if (q == tok) poisoned = none;
     }
@@ -527,7 +527,7 @@ __global__ __launch_bounds__(256) void route_scored_bwd_kernel(int T, int E, int
   __shared__ __attribute__((aligned(16))) float s_d[4][4][kMaxExperts];
   const float inf = __builtin_inff();
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, tok = lane >> 4, li = lane & 15;
-  const int64_t row = (int64_t)blockIdx.x * 16 + 4 * wv + tok;
+  const int64_t row = (int64_t)group_id() * 16 + 4 * wv + tok;
   const bool live = row < T;
   const int64_t t = live ? row : T - 1;
   const float* lt = logits + t * E;
@@ -624,7 +624,7 @@ __global__ __launch_bounds__(256) void route_scored_bwd_kernel(int T, int E, int
 
 template <int V>
 hipError_t route_launch(const RouteArgs& g, bool aligned, hipStream_t stream) {
-  const dim3 grid((unsigned)(((int64_t)g.T + 15) / 16)), block(256);
+  const dim3 grid = wide_grid(((int64_t)g.T + 15) / 16), block(256);
   if (aligned && g.E == kRow * V) MOE_LAUNCH((route_scored_kernel<V, true>), grid, block, 0, stream, g);
   else MOE_LAUNCH((route_scored_kernel<V, false>), grid, block, 0, stream, g);
   return hipGetLastError();
@@ -650,7 +650,7 @@ hipError_t launch_route_scored(int T, int E, int k, int score, int n_groups, int
 
 hipError_t launch_route_scored_bwd(int T, int E, int k, int score, bool renormalize, float scale, const float* logits,
                                    const int32_t* idx, const float* dg, float* dlogits, hipStream_t stream) {
-  const dim3 grid((unsigned)(((int64_t)T + 15) / 16)), block(256);
+  const dim3 grid = wide_grid(((int64_t)T + 15) / 16), block(256);
   const bool quad = E % 4 == 0 && (((uintptr_t)logits | (uintptr_t)dlogits) & 15) == 0;
   auto run = [&](auto kernel) {
     MOE_LAUNCH(kernel, grid, block, 0, stream, T, E, k, score, (int)renormalize, scale, logits, idx, dg, dlogits);

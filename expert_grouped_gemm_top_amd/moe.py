@@ -479,6 +479,8 @@ def _rows(t, name):
     shape = t.shape
     if len(shape) != 2 or 0 in shape:
         raise MoeError(f"{name} must be a matrix with at least one element, got shape {tuple(shape)}")
+    if shape[0] > 0x7fffffff or shape[1] > 0x7fffffff:
+        raise MoeError(f"{name} has shape {tuple(shape)}, sizes end below 2^31")
     return shape
 
 
@@ -525,7 +527,11 @@ def _queue(stream, dev):
     """The hipStream_t of a call on device `dev`."""
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if not hasattr(stream, "cuda_stream"):
+        return int(stream)
+    if stream.device_index != dev:
+        raise MoeError(f"a stream of device cuda:{stream.device_index} in a call on the current device cuda:{dev}")
+    return stream.cuda_stream
 
 
 def moe_route_scored(logits, bias, topk_idx, topk_w, k: int, score: int = MOE_SCORE_SOFTMAX, n_groups: int = 1,

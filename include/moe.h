@@ -572,8 +572,9 @@ size_t moe_layernorm_workspace_bytes(int T, int H);
  * Sums in fp32 in one fixed order.  dx_add [T, H] or NULL (the gradient that
  * reaches x past the norm; it may be dx); dx [T, H] (may be dy or x), dgamma
  * [H], dbeta [H] or NULL of `dtype` (device, out); workspace (device, 16-byte
- * aligned) of at least moe_layernorm_workspace_bytes(T, H).  Calls that may
- * overlap in time need a workspace each. */
+ * aligned, apart from all other buffers) of at least
+ * moe_layernorm_workspace_bytes(T, H).  Calls that may overlap in time need a
+ * workspace each. */
 int moe_layernorm_bwd(int T, int H, int dtype, const void* x, const void* gamma, const float* mean, const float* rstd,
                       const void* dy, const void* dx_add, void* dx, void* dgamma, void* dbeta, void* workspace,
                       size_t workspace_bytes, void* stream);
@@ -600,8 +601,9 @@ size_t moe_linear_workspace_bytes(int T, int I, int O, int dtype);
  * mul = x W_up this is a gated expert's hidden row; with residual = the routed
  * experts' sum a shared expert's output joins it.
  * I and O multiples of 8, at most 2^20, T at most 2^30, T I and T O below 2^40,
- * pointers 16-byte aligned, workspace of at least moe_linear_workspace_bytes (may be NULL when
- * that is 0).  Calls that may overlap in time need a workspace each. */
+ * pointers 16-byte aligned, workspace (apart from all other buffers) of at
+ * least moe_linear_workspace_bytes (may be NULL when that is 0).  Calls that
+ * may overlap in time need a workspace each. */
 int moe_linear_fwd(int T, int I, int O, int dtype, int act, const void* x, const void* w, const void* bias,
                    const void* mul, const void* residual, void* z_save, void* y, void* workspace,
                    size_t workspace_bytes, void* stream);
@@ -614,8 +616,9 @@ int moe_linear_fwd(int T, int I, int O, int dtype, int act, const void* x, const
  * so rounded to it; dbias sums the unrounded values) is needed in those cases
  * too, and may be dy or z; without them dz is dy itself and the argument is
  * ignored.  relu'(0) = 0.  dmul [T, O] is written when mul is given (required
- * then; it may be mul, z or dy).  dx_add [T, I] or NULL (may be dx).  dx and dw may each be NULL (not
- * wanted), dbias [O] too.  dx overlaps none of the inputs but dx_add. */
+ * then; it may be mul, z or dy).  dx_add [T, I] or NULL (may be dx).  dx and dw
+ * may each be NULL (not wanted), dbias [O] too.  dx overlaps none of the inputs
+ * but dx_add. */
 int moe_linear_bwd(int T, int I, int O, int dtype, int act, const void* x, const void* w, const void* z,
                    const void* mul, const void* dy, void* dz, const void* dx_add, void* dx, void* dw, void* dbias,
                    void* dmul, void* workspace, size_t workspace_bytes, void* stream);

@@ -71,7 +71,8 @@ def test_layernorm(lib):
         ({3: -1.0}, 1, "eps"), ({3: float("nan")}, 1, "eps"), ({4: NULL}, 1, "x must"), ({5: NULL}, 1, "gamma"), ({7: NULL}, 1, "y must"),
         ({8: NULL}, 1, "mean and rstd"), ({4: ctypes.c_void_p(8)}, 1, "x must be 16-byte"),
         ({6: ctypes.c_void_p(P(2).value + 2)}, 1, "beta must be 16-byte"), ({7: ctypes.c_void_p(P(0).value + 16)}, 1, "y overlaps x"),
-        ({7: P(1)}, 1, "y overlaps gamma")])
+        ({7: P(1)}, 1, "y overlaps gamma"), ({8: P(0)}, 1, "mean overlaps x"), ({9: P(4)}, 1, "mean overlaps rstd"),
+        ({9: P(2)}, 1, "rstd overlaps beta")])
     ws = lib.moe_layernorm_workspace_bytes(64, 2048)
     assert 0 < ws <= 64 << 20 and lib.moe_layernorm_workspace_bytes(1 << 30, 16384) <= 64 << 20
     assert lib.moe_layernorm_workspace_bytes(0, 64) == 0
@@ -81,7 +82,8 @@ def test_layernorm(lib):
         ({7: NULL}, 1, "dy"), ({9: NULL}, 1, "dx must"), ({10: NULL}, 1, "dgamma"), ({13: ws - 1}, 3, "workspace"), ({12: NULL}, 1, "workspace"),
         ({12: ctypes.c_void_p(24)}, 1, "workspace must be 16-byte"), ({9: P(1)}, 1, "dx overlaps gamma"),
         ({9: ctypes.c_void_p(P(4).value + 32)}, 1, "dx overlaps dy"), ({10: P(0)}, 1, "dgamma overlaps x"),
-        ({10: P(8)}, 1, "dgamma overlaps dbeta")])
+        ({10: P(8)}, 1, "dgamma overlaps dbeta"), ({11: P(3)}, 1, "dbeta overlaps rstd"), ({12: P(6)}, 1, "workspace overlaps dx"),
+        ({12: ctypes.c_void_p(P(2).value + 64)}, 1, "workspace overlaps mean")])
 
 
 def test_linear_fwd(lib):
@@ -94,7 +96,8 @@ def test_linear_fwd(lib):
         ({11: P(1)}, 1, "y overlaps w"), ({11: P(5)}, 1, "y overlaps z_save"), ({10: P(4)}, 1, "z_save overlaps residual"),
         ({11: ctypes.c_void_p(P(4).value + 256)}, 1, "y overlaps residual")])
     if ws:
-        refuses(lib, lib.moe_linear_fwd, ok, [({13: ws - 1}, 3, "workspace"), ({12: NULL}, 1, "workspace")])
+        refuses(lib, lib.moe_linear_fwd, ok, [({13: ws - 1}, 3, "workspace"), ({12: NULL}, 1, "workspace"),
+                                              ({12: P(6)}, 1, "workspace overlaps y")])
 
 
 def test_linear_bwd(lib):
@@ -109,7 +112,7 @@ def test_linear_bwd(lib):
         ({mul: NULL}, 1, "mul and dmul"), ({dx: NULL}, 1, "dx_add without"), ({dz: ctypes.c_void_p(P(4).value + 16)}, 1, "dz overlaps dy"),
         ({dx: P(4)}, 1, "dx overlaps dy"), ({dx: P(5)}, 1, "dx overlaps dz"), ({dw: P(1)}, 1, "dw overlaps w"),
         ({dmul: P(5)}, 1, "dmul overlaps dz"), ({dbias: P(2)}, 1, "dbias overlaps z"), ({dx: ctypes.c_void_p(40)}, 1, "aligned"),
-        ({17: ws - 1}, 3, "workspace"), ({wsp: NULL}, 1, "workspace"),
+        ({17: ws - 1}, 3, "workspace"), ({wsp: NULL}, 1, "workspace"), ({wsp: P(5)}, 1, "workspace overlaps dz"),
         ({dx_add: NULL, dx: NULL, dw: NULL, dbias: NULL, mul: NULL, dmul: NULL}, 1, "no gradient"),
         ({4: 0, z: NULL, dz: NULL, mul: NULL, dmul: NULL, 17: 0}, 3, "workspace")])
 
@@ -131,3 +134,10 @@ def test_the_binding_refuses_before_the_library():
                  lambda: moe.moe_linear_bwd(a, a, a, None, a, a)):
         with pytest.raises(moe.MoeError):
             call()
+
+
+def test_sizes_that_an_int_cannot_hold():
+    from expert_grouped_gemm_top_amd import moe
+    for shape in ((2**32 + 8, 8), (8, 2**31)):
+        with pytest.raises(moe.MoeError, match="2\\^31"):
+            moe._rows(torch.empty(shape, device="meta"), "x")

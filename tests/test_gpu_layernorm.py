@@ -148,6 +148,23 @@ def test_rows_behind_the_last_are_left():
     assert (y[9:] == 7.0).all() and (y[:9] == 0.0).all()
 
 
+def test_more_rows_than_one_grid_row():
+    """2^26 narrow rows and some: more than 2^32 threads.  All rows but the last are zeros, whose norm is beta."""
+    T, H, n = (1 << 26) + 701, 8, 300
+    note(f"norm T={T} H={H}")
+    v = inputs(n, H, "bf16", 12)
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    x[-n:] = R.dev(v["x"], "bf16")
+    y, mean, rstd = torch.full_like(x, 7.0), torch.full((T,), 7.0, device="cuda"), torch.full((T,), 7.0, device="cuda")
+    gamma, beta = R.dev(v["gamma"], "bf16"), R.dev(v["beta"], "bf16")
+    moe.moe_layernorm_fwd(x, gamma, beta, y, mean, rstd)
+    torch.cuda.synchronize()
+    ry, _, _ = R.norm(v["x"], v["gamma"], v["beta"], 1e-5)
+    # as in test_rows_past_32_bits, with the values' own size (a row of 8 is at most sqrt(8) deviations from its mean)
+    R.within("y", R.host(y[-n:]), ry, 2.0 ** -8 * np.abs(ry) + 200 * 30 * STEP)
+    assert (y[:-n] == beta).all() and (mean[:-n] == 0).all() and (rstd[:-n] == rstd[0]).all()
+
+
 def test_rows_past_32_bits():
     """More than 2^31 elements: the last rows forward and backward, and dgamma over all."""
     T, H = (1 << 31) // 4096 + 700, 4096

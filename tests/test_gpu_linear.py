@@ -244,6 +244,32 @@ def test_rows_past_32_bits():
         assert (dx[:-300] == 0).all()
 
 
+def test_more_rows_than_one_grid_row():
+    """2^30 narrow rows: more than 2^32 threads.  Only the last 200 rows are not zero."""
+    T, I, O, n = 1 << 30, 8, 8, 200  # noqa: E741
+    note(f"linear T={T} I={I} O={O}")
+    v = inputs(n, I, O, "bf16", 15)
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    x, dy = torch.zeros(T, I, **bf), torch.zeros(T, O, **bf)
+    x[-n:], dy[-n:] = R.dev(v["x"], "bf16"), R.dev(v["dy"], "bf16")
+    w, b = R.dev(v["w"], "bf16"), R.dev(v["b"], "bf16")
+    ws = torch.empty(max(16, moe.moe_linear_workspace_bytes(T, I, O, torch.bfloat16)), dtype=torch.uint8, device="cuda")
+    y = torch.full((T, O), 7.0, **bf)
+    moe.moe_linear_fwd(x, w, b, y, workspace=ws)
+    torch.cuda.synchronize()
+    ref, size = v["x"] @ v["w"] + v["b"], np.abs(v["x"]) @ np.abs(v["w"]) + np.abs(v["b"])
+    R.within("y", R.host(y[-n:]), ref, 2.0 ** -8 * np.abs(ref) + (I + 2) * 2.0 ** -23 * size)
+    assert (y[:-n] == b).all()  # rows of zeros: the bias, which is in bf16
+    dw = torch.empty_like(w)
+    moe.moe_linear_bwd(x, w, dy, None, y, dw, workspace=ws)
+    torch.cuda.synchronize()
+    ref, size = v["dy"] @ v["w"].T, np.abs(v["dy"]) @ np.abs(v["w"].T)
+    R.within("dx", R.host(y[-n:]), ref, 2.0 ** -8 * np.abs(ref) + (O + 2) * 2.0 ** -23 * size)
+    assert (y[:-n] == 0).all()
+    ref, size = v["x"].T @ v["dy"], np.abs(v["x"].T) @ np.abs(v["dy"])
+    R.within("dw", R.host(dw), ref, 2.0 ** -8 * np.abs(ref) + (n + 2) * 2.0 ** -23 * size)
+
+
 def test_rows_behind_the_last_are_left():
     v = inputs(40, 72, 136, "bf16", 13)
     t = {n: R.dev(v[n], "bf16") for n in ("x", "w", "b", "dy")}

@@ -148,6 +148,26 @@ def test_route_rows_past_32_bits():
     assert not torch.isnan(d).any()
 
 
+def test_more_tokens_than_one_grid_row():
+    """2^28 tokens and some over two experts: more than 2^32 threads."""
+    T = (1 << 28) + 1001
+    note(f"route T={T} E=2")
+    l = torch.zeros(T, 2, device="cuda")
+    l[::3, 1] = 2.0
+    idx, w = torch.full((T, 1), -1, dtype=torch.int32, device="cuda"), torch.full((T, 1), 7.0, device="cuda")
+    moe.moe_route_scored(l, None, idx, w, 1, R.SIGMOID, renormalize=False)
+    torch.cuda.synchronize()
+    third = torch.arange(T, device="cuda") % 3 == 0
+    assert torch.equal(idx[:, 0] == 1, third) and ((idx == 0) | (idx == 1)).all()
+    two = 1.0 / (1.0 + np.exp(-2.0))  # the other tokens' score is 1 / 2
+    assert (w[third] - two).abs().max() <= 8 * 2.0 ** -24 and (w[~third] - 0.5).abs().max() <= 8 * 2.0 ** -24
+    d = torch.full((T, 2), 7.0, device="cuda")
+    moe.moe_route_scored_bwd(l, idx, w, d, R.SIGMOID, False)  # the weights as their own gradient
+    torch.cuda.synchronize()
+    assert (d[third, 1] - two * two * (1 - two)).abs().max() <= 16 * 2.0 ** -24 and (d[third, 0] == 0).all()
+    assert (d[~third, 0] - 0.125).abs().max() <= 16 * 2.0 ** -24 and (d[~third, 1] == 0).all()
+
+
 @pytest.mark.parametrize("score", [R.SOFTMAX, R.SIGMOID])
 def test_route_near_ties_are_decided_exactly(score):
     """Choice scores closer than fp32 resolves: biases that cancel the scores' differences down to ~1e-9, logits
