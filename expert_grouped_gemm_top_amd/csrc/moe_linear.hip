@@ -11,7 +11,6 @@
 // that adds an error as large as the outputs' own rounding (2^-9 of dx and dW
 // in the root mean square); dbias sums the unrounded values.
 #include <algorithm>
-#include <type_traits>
 
 #include "moe_common.h"
 #include "moe_launch.h"
@@ -196,113 +195,142 @@ __device__ __forceinline__ void tile_of(int wg, int mtiles, int ntiles, int dept
   nt = within / gm;
 }
 
-// ---- bf16 on the 32x32x16 matrix core ------------------------------------------
+// ---- one workgroup tile on the matrix cores ---------------------------------------
 
-// 16-byte chunk position in a [row][64 k] LDS tile (128-byte rows): 16 rows of
+// Both types lie alike in LDS: a stage is 128 bytes of k (64 bf16, 32 fp32), a
+// fragment 16 bytes per lane (8 bf16 or 4 fp32 k of one row), and a run of
+// products takes two fragments' k: one 32x32x16 bf16 product, or four 32x32x2
+// fp32 ones, the j-th over element j of both lanes' fragments.
+template <typename T>
+constexpr int kChunk = 16 / (int)sizeof(T);
+template <typename T>
+constexpr int kStageK = 128 / (int)sizeof(T);
+template <typename T>
+constexpr int kRunProducts = sizeof(T) == 2 ? 1 : 4;
+
+// The q-th product of a run.
+template <typename T>
+__device__ __forceinline__ f32x16 product32(u32x4 first, u32x4 second, int q, f32x16 acc) {
+  if constexpr (sizeof(T) == 2) return mfma32(first, second, acc);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(first[q]), __uint_as_float(second[q]), acc, 0, 0, 0);
+}
+
+// 16-byte chunk position in a [row][stage k] LDS tile (128-byte rows): 16 rows of
 // one fragment read fall in distinct bank groups.
 __device__ __forceinline__ int kc_key(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
 
-// k row of a [k][ROWS] LDS tile -> XOR on the 16-byte chunk index: the 4 k rows x
-// 4 chunks that half a wave's transpose read covers lie in distinct banks
-// (256-byte rows and longer: every row starts at the same bank; 128-byte rows: every other one).
-template <int ROWS>
+// k row of a [k][ROWS] LDS tile -> XOR on the 16-byte chunk index.  bf16: the 4 k
+// rows x 4 chunks that half a wave's transpose read covers lie in distinct banks
+// (256-byte rows and longer: every row starts at the same bank; 128-byte rows: every
+// other one).  fp32: the two k rows, 4 apart, of a wave's read.
+template <typename T, int ROWS>
 __device__ __forceinline__ int nc_key(int k) {
   static_assert(ROWS >= 64, "eight chunks at least");
+  if (sizeof(T) == 4) return 8 * ((k >> 2) & 1);
   return ROWS >= 128 ? 4 * (k & 3) : 4 * ((k >> 1) & 1);
 }
 
-// 32x32x16 operand fragment of rows row0 .. row0 + 31, k 16 sub .. + 15, from a
-// [k][ROWS] tile: in 16-lane group G, lane r points at k 8 (G >> 1) + 4 h +
-// (r >> 2) and rows 16 (G & 1) + 4 (r & 3) .. + 3, and receives 4 consecutive k of one
-// row (half of its 8).
-template <int ROWS>
+// Fragment of rows row0 .. row0 + 31, run `sub` of the stage's four, from a
+// [k][ROWS] tile.  bf16, k 16 sub .. + 15: in 16-lane group G, lane r points at k
+// 8 (G >> 1) + 4 h + (r >> 2) and rows 16 (G & 1) + 4 (r & 3) .. + 3, and receives 4
+// consecutive k of one row (half of its 8).  fp32, k 8 sub .. + 7: lane l reads k
+// 4 (l / 32) + j of row l % 32.
+template <typename T, int ROWS>
 __device__ __forceinline__ u32x4 nc_frag(const unsigned char* tile, int sub, int row0) {
   const int l = __lane_id(), G = l >> 4, r = l & 15;
+  if constexpr (sizeof(T) == 4) {
+    const int row = row0 + (l & 31), k = 8 * sub + 4 * (l >> 5);
+    const unsigned char* at = tile + k * (4 * ROWS) + 16 * ((row >> 2) ^ nc_key<T, ROWS>(k)) + 4 * (row & 3);
+    return u32x4{*(const uint32_t*)at, *(const uint32_t*)(at + 4 * ROWS), *(const uint32_t*)(at + 8 * ROWS),
+                 *(const uint32_t*)(at + 12 * ROWS)};
+  }
   const int row = row0 + 16 * (G & 1) + 4 * (r & 3);
   v4i16 part[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int k = 16 * sub + 8 * (G >> 1) + 4 * h + (r >> 2);
     part[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (lds_v4i16*)(tile + k * (2 * ROWS) + 16 * ((row >> 3) ^ nc_key<ROWS>(k)) + 2 * (row & 7)));
+        (lds_v4i16*)(tile + k * (2 * ROWS) + 16 * ((row >> 3) ^ nc_key<T, ROWS>(k)) + 2 * (row & 7)));
   }
   const u32x2 lo = __builtin_bit_cast(u32x2, part[0]), hi = __builtin_bit_cast(u32x2, part[1]);
   return u32x4{lo[0], lo[1], hi[0], hi[1]};
 }
 
-// One operand's stage: ROWS x BK elements by direct global->LDS loads, INS per
-// wave.  KC: LDS [row][BK]; otherwise LDS [BK][ROWS].  Chunks outside the
+// One operand's stage: ROWS x 128 bytes by direct global->LDS loads, INS per
+// wave.  KC: LDS [row][k]; otherwise LDS [k][ROWS].  Chunks outside the
 // operand come from zeros (TAIL; rows of a KC operand past its end re-read the
 // last row and reach only outputs that are not stored).
-template <bool KC, int ROWS, int BK, int NW, bool TAIL>
+template <typename T, bool KC, int ROWS, int NW, bool TAIL>
 struct Loader {
-  static constexpr int INS = ROWS * BK * 2 / 1024 / NW;
-  static_assert(ROWS * BK * 2 == INS * 1024 * NW, "whole loads");
-  const uint16_t* src[INS];
-  int k[INS];    // k of this lane's chunk within the stage
-  bool ok[INS];  // inside the operand's rows
-  int64_t step;  // elements per k
-  __device__ void init(const void* base, int64_t ld, int r0, int rows, int w, int l) {
-    step = KC ? 1 : ld;
+  static constexpr int INS = ROWS * 128 / 1024 / NW, CH = kChunk<T>, CHUNKS = ROWS / CH;
+  static_assert(ROWS * 128 == INS * 1024 * NW, "whole loads");
+  const T* src[INS];
+  uint32_t k[INS];  // TAIL: k of this lane's chunk, past any K for rows outside the operand
+  int64_t step;     // elements from one stage to the next
+  __device__ void init(const void* base, int64_t ld, int r0, int rows, int k0, int stage_k, int w, int l) {
+    step = KC ? stage_k : stage_k * ld;
 #pragma unroll
     for (int i = 0; i < INS; ++i) {
       if (KC) {
-        const int row = (512 / BK) * (INS * w + i) + l / (BK / 8);
-        const int chunk = kc_key(row, l % (BK / 8));
-        k[i] = 8 * chunk;
-        ok[i] = true;
-        src[i] = (const uint16_t*)base + (int64_t)min(r0 + row, rows - 1) * ld + 8 * chunk;
+        const int row = 8 * (INS * w + i) + l / 8;
+        k[i] = k0 + CH * kc_key(row, l % 8);
+        src[i] = (const T*)base + (int64_t)min(r0 + row, rows - 1) * ld + k[i];
       } else {
-        k[i] = (512 / ROWS) * (INS * w + i) + l / (ROWS / 8);
-        const int c = r0 + 8 * ((l % (ROWS / 8)) ^ nc_key<ROWS>(k[i]));
-        ok[i] = c < rows;
-        src[i] = (const uint16_t*)base + (int64_t)k[i] * ld + (ok[i] ? c : 0);
+        const int at = 64 * (INS * w + i) + l;  // chunk of the stage
+        const int c = r0 + CH * ((at % CHUNKS) ^ nc_key<T, ROWS>(at / CHUNKS));
+        k[i] = k0 + at / CHUNKS;
+        src[i] = (const T*)base + (int64_t)k[i] * ld + (c < rows ? c : 0);
+        if (c >= rows) k[i] = 0x80000000u;
       }
     }
   }
-  __device__ void issue(int k0, int K, unsigned char* tile, int w) const {
+  // The stages in turn.
+  __device__ void issue(int K, int stage_k, unsigned char* tile, int w) {
 #pragma unroll
     for (int i = 0; i < INS; ++i) {
-      const uint16_t* p = src[i] + k0 * step;
-      if (TAIL && (!ok[i] || k0 + k[i] >= K)) p = zero_chunk();
+      const T* p = src[i];
+      if (TAIL && k[i] >= (uint32_t)K) p = reinterpret_cast<const T*>(zero_chunk());
       g2lds(p, tile + 1024 * (INS * w + i));
+      src[i] += step;
+      if (TAIL) k[i] += stage_k;
     }
   }
 };
 
-template <bool KC, int ROWS, int BK>
+template <typename T, bool KC, int ROWS>
 __device__ __forceinline__ u32x4 tile_frag(const unsigned char* tile, int sub, int row0) {
   if (KC) {
     const int row = row0 + (__lane_id() & 31);
-    return *(const u32x4*)(tile + row * (2 * BK) + 16 * kc_key(row, 2 * sub + (__lane_id() >> 5)));
+    return *(const u32x4*)(tile + row * 128 + 16 * kc_key(row, 2 * sub + (__lane_id() >> 5)));
   } else {
-    return nc_frag<ROWS>(tile, sub, row0);
+    return nc_frag<T, ROWS>(tile, sub, row0);
   }
 }
 
 // A workgroup tile: BM x BN outputs by KG groups of NW waves, each group laid out
-// WM x (NW / WM) over the tile and taking every KG-th 64 k of the reduction
+// WM x (NW / WM) over the tile and taking every KG-th 128 bytes of the reduction
 // (the groups' sums are added at the end): two waves on a SIMD hide each other's
 // LDS reads and waits without a smaller wave tile.  STAGES LDS stages of KG x
-// 64 k.  All have eight waves, one workgroup per CU.
+// 128 bytes of k.  All have eight waves and mostly a CU's LDS to themselves.
 template <int BM_, int BN_, int NW_, int WM_, int KG_, int STAGES_>
 struct Tile {
   static constexpr int BM = BM_, BN = BN_, NW = NW_, WM = WM_, KG = KG_, STAGES = STAGES_;
-  static constexpr int LDS = STAGES * KG * (BM + BN) * 64 * 2;
+  static constexpr int LDS = STAGES * KG * (BM + BN) * 128;
   static_assert(NW * KG == 8 && LDS <= 160 * 1024, "eight waves, one CU's LDS");
 };
 constexpr int kThreads = 512;
 
 // Output tile `tile` of the product over slice `slice` of its reduction.  A stage
-// is waited for before the last 16 k of the one in front, so its first
+// is waited for before the last run of the one in front, so its first
 // fragments are read under those products, and its successor's loads go out in
 // two halves before the next two runs of products.
-template <bool AKC, bool BKC, typename C, bool TAIL>
+template <typename T, bool AKC, bool BKC, typename C, bool TAIL>
 __device__ __forceinline__ void tile_product(const LinearProduct& g, int tile, int slice, unsigned char* s_dyn) {
   constexpr int BM = C::BM, BN = C::BN, NW = C::NW, WM = C::WM, KG = C::KG, STAGES = C::STAGES;
-  constexpr int BK = 64, SUBS = BK / 16;
+  constexpr int BK = kStageK<T>, RUN = kRunProducts<T>;
   constexpr int TM = BM / WM, TN = BN / (NW / WM), MI = TM / 32, NJ = TN / 32;
-  constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, GROUP = A_BYTES + B_BYTES, STAGE = KG * GROUP;
+  constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, GROUP = A_BYTES + B_BYTES, STAGE = KG * GROUP;
   const int tid = threadIdx.x, l = tid & 63, l32 = l & 31, hk = l >> 5;
   const int kg = (tid >> 6) / NW, w = (tid >> 6) % NW;
   const int wm = w % WM, wn = w / WM;
@@ -311,15 +339,15 @@ __device__ __forceinline__ void tile_product(const LinearProduct& g, int tile, i
   const int m0 = mt * BM, n0 = nt * BN;
   const int kb = slice * g.slice, ke = min(g.K, kb + g.slice);
 
-  Loader<AKC, BM, BK, NW, TAIL> la;
-  Loader<BKC, BN, BK, NW, TAIL> lb;
-  la.init(g.a, g.lda, m0, g.M, w, l);
-  lb.init(g.b, g.ldb, n0, g.N, w, l);
-  constexpr int INS = Loader<AKC, BM, BK, NW, TAIL>::INS + Loader<BKC, BN, BK, NW, TAIL>::INS;  // loads of a stage
+  Loader<T, AKC, BM, NW, TAIL> la;
+  Loader<T, BKC, BN, NW, TAIL> lb;
+  la.init(g.a, g.lda, m0, g.M, kb + kg * BK, KG * BK, w, l);
+  lb.init(g.b, g.ldb, n0, g.N, kb + kg * BK, KG * BK, w, l);
+  constexpr int INS = Loader<T, AKC, BM, NW, TAIL>::INS + Loader<T, BKC, BN, NW, TAIL>::INS;  // loads of a stage
   // stage s lies in buffer s % STAGES; a group loads and reads its own part of it
   unsigned char* const mine = s_dyn + kg * GROUP;
-  auto issue_a = [&](int s, int buf) { la.issue(kb + (s * KG + kg) * BK, ke, mine + buf * STAGE, w); };
-  auto issue_b = [&](int s, int buf) { lb.issue(kb + (s * KG + kg) * BK, ke, mine + buf * STAGE + A_BYTES, w); };
+  auto issue_a = [&](int buf) { la.issue(ke, KG * BK, mine + buf * STAGE, w); };
+  auto issue_b = [&](int buf) { lb.issue(ke, KG * BK, mine + buf * STAGE + A_BYTES, w); };
 
   f32x16 acc[MI][NJ];
 #pragma unroll
@@ -335,17 +363,20 @@ __device__ __forceinline__ void tile_product(const LinearProduct& g, int tile, i
     __builtin_amdgcn_s_setprio(1);
     if (next_sub >= 0) {
 #pragma unroll
-      for (int i = 0; i < MI; ++i) nxt.a[i] = tile_frag<AKC, BM, BK>(st, next_sub, TM * wm + 32 * i);
+      for (int i = 0; i < MI; ++i) nxt.a[i] = tile_frag<T, AKC, BM>(st, next_sub, TM * wm + 32 * i);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) nxt.b[j] = tile_frag<BKC, BN, BK>(st + A_BYTES, next_sub, TN * wn + 32 * j);
+      for (int j = 0; j < NJ; ++j) nxt.b[j] = tile_frag<T, BKC, BN>(st + A_BYTES, next_sub, TN * wn + 32 * j);
     }
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
+    for (int q = 0; q < RUN; ++q)
 #pragma unroll
-      for (int i = 0; i < MI; ++i) acc[i][j] = mfma32(cur.b[j], cur.a[i], acc[i][j]);
-    constexpr int READS = ((AKC ? 1 : 2) * MI + (BKC ? 1 : 2) * NJ + MI * NJ - 1) / (MI * NJ);
+      for (int j = 0; j < NJ; ++j)
 #pragma unroll
-    for (int q = 0; q < MI * NJ; ++q) {
+        for (int i = 0; i < MI; ++i) acc[i][j] = product32<T>(cur.b[j], cur.a[i], q, acc[i][j]);
+    constexpr int ALL = MI * NJ * RUN, NCR = sizeof(T) == 2 ? 2 : 4;  // products; reads of an NC fragment
+    constexpr int READS = ((AKC ? 1 : NCR) * MI + (BKC ? 1 : NCR) * NJ + ALL - 1) / ALL;
+#pragma unroll
+    for (int q = 0; q < ALL; ++q) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);      // one product
       __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);  // its share of the LDS reads
     }
@@ -354,23 +385,22 @@ __device__ __forceinline__ void tile_product(const LinearProduct& g, int tile, i
   };
 
   const int steps = (ke - kb + KG * BK - 1) / (KG * BK);
-  static_assert(SUBS == 4, "four runs of products per stage");
   Frags f0, f1;
   for (int s = 0; s < STAGES - 1 && s < steps; ++s) {
-    issue_a(s, s);
-    issue_b(s, s);
+    issue_a(s);
+    issue_b(s);
   }
   if (steps >= STAGES - 1) wait_vmcnt<(STAGES - 2) * INS>();  // stage 0 has landed, later ones need not have
   else wait_vmcnt<0>();
   barrier_no_fence();
   if (steps > STAGES - 1) {
-    issue_a(STAGES - 1, STAGES - 1);
-    issue_b(STAGES - 1, STAGES - 1);
+    issue_a(STAGES - 1);
+    issue_b(STAGES - 1);
   }
 #pragma unroll
-  for (int i = 0; i < MI; ++i) f0.a[i] = tile_frag<AKC, BM, BK>(mine, 0, TM * wm + 32 * i);
+  for (int i = 0; i < MI; ++i) f0.a[i] = tile_frag<T, AKC, BM>(mine, 0, TM * wm + 32 * i);
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) f0.b[j] = tile_frag<BKC, BN, BK>(mine + A_BYTES, 0, TN * wn + 32 * j);
+  for (int j = 0; j < NJ; ++j) f0.b[j] = tile_frag<T, BKC, BN>(mine + A_BYTES, 0, TN * wn + 32 * j);
   products(f0, mine, 1, f1);
   products(f1, mine, 2, f0);
   products(f0, mine, 3, f1);
@@ -384,9 +414,9 @@ __device__ __forceinline__ void tile_product(const LinearProduct& g, int tile, i
     __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's reads of stage s - 1 are done
     barrier_no_fence();                   // ... and every wave's: its buffer can be loaded again
     const bool more = s + STAGES - 1 < steps;
-    if (more) issue_a(s + STAGES - 1, buf);
+    if (more) issue_a(buf);
     products(f1, st, 0, f0);
-    if (more) issue_b(s + STAGES - 1, buf);
+    if (more) issue_b(buf);
     products(f0, st, 1, f1);
     products(f1, st, 2, f0);
     products(f0, st, 3, f1);
@@ -433,182 +463,9 @@ __device__ __forceinline__ void tile_product(const LinearProduct& g, int tile, i
       const f32x4 lo = *(const f32x4*)(s_f + row * HC + 4 * ((2 * c8) ^ (row & 15)));
       const f32x4 hi = *(const f32x4*)(s_f + row * HC + 4 * ((2 * c8 + 1) ^ (row & 15)));
       float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      leave8<uint16_t>(g, slice, m, n, v);
+      leave8<T>(g, slice, m, n, v);
     }
     __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's reads of the staged rows are done
-  }
-}
-
-// ---- fp32 on the 32x32x2 matrix core ---------------------------------------------
-
-// D = first x second + D: lane l supplies row / column l % 32 of k = l / 32; the
-// registers of D lie as for mfma32.
-__device__ __forceinline__ f32x16 mfma32_f32(float first, float second, f32x16 acc) {
-  return __builtin_amdgcn_mfma_f32_32x32x2f32(first, second, acc, 0, 0, 0);
-}
-
-// The fp32 tiles: BT x BT outputs by two groups of four waves of (BT / 2)^2, each
-// group taking 16 of a stage's 32 k; two LDS buffers, the next stage stored and the one
-// behind it loaded into registers under the products.  An operand with k contiguous is
-// transposed on its way into LDS; its row pitch of BT + 2 spreads the eight
-// quads of a row over the banks.
-template <int BT_>
-struct TileF {
-  static constexpr int BT = BT_, BM = BT_, BN = BT_, BK = 32;
-  static constexpr int LDS = 2 * 2 * BK * (BT + 32) * 4;
-};
-
-template <bool KC, int BT>
-struct LoaderF {
-  static constexpr int BK = 32, QUADS = BT * BK / 4 / kThreads, PITCH = KC ? BT + 2 : BT + 32;
-  static_assert(QUADS >= 1, "a quad per thread");
-  const float* src[QUADS];
-  int k[QUADS];
-  int64_t step;
-  f32x4 v[QUADS];
-  __device__ __forceinline__ void init(const void* base, int64_t ld, int r0, int rows, int k0) {
-    step = KC ? BK : BK * ld;
-#pragma unroll
-    for (int i = 0; i < QUADS; ++i) {
-      const int q = threadIdx.x + kThreads * i;
-      const int r = r0 + (KC ? q / (BK / 4) : 4 * (q % (BT / 4)));
-      k[i] = k0 + (KC ? 4 * (q % (BK / 4)) : q / (BT / 4));
-      src[i] = (const float*)base + (KC ? r * ld + k[i] : k[i] * ld + r);
-      if (r >= rows) k[i] = 0x40000000;  // never inside
-    }
-  }
-  // Four neighbouring elements each of the next stage, zeros for those outside
-  // (the contiguous extent is a multiple of 4).
-  __device__ __forceinline__ void fetch(int ke) {
-#pragma unroll
-    for (int i = 0; i < QUADS; ++i) {
-      v[i] = *(const f32x4*)(k[i] < ke ? src[i] : reinterpret_cast<const float*>(kZeroChunk));
-      src[i] += step;
-      k[i] += BK;
-    }
-  }
-  __device__ __forceinline__ void put(float* s) const {
-#pragma unroll
-    for (int i = 0; i < QUADS; ++i) {
-      const int q = threadIdx.x + kThreads * i;
-      if (KC) {
-        const int r = q / (BK / 4), k = 4 * (q % (BK / 4));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[(k + j) * PITCH + r] = v[i][j];
-      } else {
-        *(f32x4*)(s + (q / (BT / 4)) * PITCH + 4 * (q % (BT / 4))) = v[i];
-      }
-    }
-  }
-};
-
-template <bool AKC, bool BKC, typename C, bool TAIL>
-__device__ __forceinline__ void tile_product_f32(const LinearProduct& g, int tile, int slice, unsigned char* s_dyn) {
-  constexpr int BT = C::BT, BK = C::BK, NB = BT / 64;  // 32 x 32 blocks per wave side
-  using LA = LoaderF<AKC, BT>;
-  using LB = LoaderF<BKC, BT>;
-  constexpr int BUF = BK * (BT + 32);  // floats of one operand's buffer
-  float* s_f = reinterpret_cast<float*>(s_dyn);
-  const int tid = threadIdx.x, w = (tid >> 6) & 3, kg = tid >> 8, l = tid & 63, l32 = l & 31, hk = l >> 5;
-  const int wm = w & 1, wn = w >> 1;
-  int mt, nt;
-  tile_of(tile, (g.M + BT - 1) / BT, (g.N + BT - 1) / BT, 8, mt, nt);
-  const int m0 = mt * BT, n0 = nt * BT;
-  const int kb = slice * g.slice, ke = min(g.K, kb + g.slice);
-  LA la;
-  LB lb;
-  f32x16 acc[NB][NB];
-#pragma unroll
-  for (int i = 0; i < NB; ++i)
-#pragma unroll
-    for (int j = 0; j < NB; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  la.init(g.a, g.lda, m0, g.M, kb);
-  lb.init(g.b, g.ldb, n0, g.N, kb);
-  auto fetch = [&] {
-    la.fetch(ke);
-    lb.fetch(ke);
-  };
-  auto put = [&](int turn) {
-    la.put(s_f + turn * 2 * BUF);
-    lb.put(s_f + turn * 2 * BUF + BUF);
-  };
-  fetch();
-  put(0);
-  fetch();
-  __syncthreads();
-  int turn = 0;
-  for (int k0 = kb; k0 < ke; k0 += BK, turn ^= 1) {
-    const float* s_a = s_f + turn * 2 * BUF;
-    const float* s_b = s_a + BUF;
-    // fragments one step ahead of the products
-    float fa[2][NB], fb[2][NB];
-    auto read = [&](int step) {
-      const int kk = kg * (BK / 2) + 2 * step + hk;
-#pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        fa[step & 1][i] = s_a[kk * LA::PITCH + 32 * (NB * wm + i) + l32];
-        fb[step & 1][i] = s_b[kk * LB::PITCH + 32 * (NB * wn + i) + l32];
-      }
-    };
-    auto products = [&](int step) {
-      if (step + 1 < BK / 4) read(step + 1);
-#pragma unroll
-      for (int j = 0; j < NB; ++j)
-#pragma unroll
-        for (int i = 0; i < NB; ++i) acc[i][j] = mfma32_f32(fb[step & 1][j], fa[step & 1][i], acc[i][j]);
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);            // one product
-      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);            // the next step's reads
-      __builtin_amdgcn_sched_group_barrier(0x008, NB * NB - 1, 0);  // the other products
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    // Under the products: the next stage into the other buffer (every wave has been
-    // past its products there since the last barrier), and the one behind it into
-    // registers.  The two groups, which share the SIMDs, do so at different times:
-    // together they left the matrix pipes idle for a quarter of the stage.
-    auto advance = [&] {
-      if (k0 + BK < ke) {
-        put(turn ^ 1);
-        fetch();
-      }
-    };
-    read(0);
-#pragma unroll
-    for (int step = 0; step < BK / 4; ++step) {
-      products(step);
-      if (step == 1 && kg == 0) advance();
-      if (step == BK / 4 - 3 && kg == 1) advance();
-    }
-    __syncthreads();
-  }
-  // The tile leaves through LDS ([row][BT], 16-byte chunk c of row r at c ^ (r & 15)), the groups' sums added there.
-  static_assert(BT * BT * 4 <= C::LDS, "staging");
-#pragma unroll
-  for (int k2 = 0; k2 < 2; ++k2) {
-    if (kg == k2) {
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-#pragma unroll
-        for (int j = 0; j < NB; ++j)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int row = 32 * (NB * wm + i) + l32, col = 32 * (NB * wn + j) + 8 * q + 4 * hk;
-            f32x4* at = (f32x4*)(s_f + row * BT + 4 * ((col >> 2) ^ (row & 15)));
-            f32x4 v = f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-            if (k2 > 0) v += *at;
-            *at = v;
-          }
-    }
-    __syncthreads();
-  }
-  for (int it = tid; it < BT * BT / 8; it += kThreads) {
-    const int row = it / (BT / 8), c8 = it % (BT / 8), m = m0 + row, n = n0 + 8 * c8;
-    if (m >= g.M || n >= g.N) continue;
-    const f32x4 lo = *(const f32x4*)(s_f + row * BT + 4 * ((2 * c8) ^ (row & 15)));
-    const f32x4 hi = *(const f32x4*)(s_f + row * BT + 4 * ((2 * c8 + 1) ^ (row & 15)));
-    float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-    leave8<float>(g, slice, m, n, v);
   }
 }
 
@@ -616,10 +473,7 @@ template <typename T, bool AKC, bool BKC, typename C, bool TAIL>
 __device__ __forceinline__ void any_product(const LinearProduct& g, int item, unsigned char* s_dyn) {
   const int tiles = ((g.M + C::BM - 1) / C::BM) * ((g.N + C::BN - 1) / C::BN);
   if (item / tiles * (int64_t)g.slice >= g.K) return;  // past the last slice: the grid may hold a few more
-  if constexpr (std::is_same<T, float>::value)
-    tile_product_f32<AKC, BKC, C, TAIL>(g, item % tiles, item / tiles, s_dyn);
-  else
-    tile_product<AKC, BKC, C, TAIL>(g, item % tiles, item / tiles, s_dyn);
+  tile_product<T, AKC, BKC, C, TAIL>(g, item % tiles, item / tiles, s_dyn);
 }
 
 // One workgroup per tile and slice: x W.
@@ -632,9 +486,9 @@ __global__ __launch_bounds__(kThreads, 2) void linear_fwd_kernel(LinearProduct g
 // The backward's products in one launch, so that one's workgroups fill the CUs
 // that the other leaves idle: `nw` workgroups of x^T dz, `nx` of dz W^T (the
 // longer ones first), and behind them the sums of dbias' partial rows.  Both
-// products at 4099 x 2048 x 768: 46 us, in launches of their own 30 + 33; at
-// 128 x 2048 x 768 10.3 us, 9.6 + 9.6; at 8192 x 4096 x 1408 203-210 us
-// (0.90-0.93 PFLOP/s; 171 us on operands of zeros, so the chip's power bounds it).
+// products at 4099 x 2048 x 768: 46 us, in launches of their own 30 + 30; at
+// 128 x 2048 x 768 8.1 us, 8.0 + 8.4; at 8192 x 4096 x 1408 198-209 us
+// (0.90-0.95 PFLOP/s; 167 us on operands of zeros, so the chip's power bounds it).
 struct ColumnSum {
   const float* part;
   int n, cols;
@@ -733,7 +587,11 @@ using Tile0 = Tile<256, 256, 8, 2, 1, 2>;
 using Tile1 = Tile<256, 128, 8, 4, 1, 3>;
 using Tile2 = Tile<128, 128, 4, 2, 2, 2>;
 using Tile3 = Tile<128, 64, 4, 2, 2, 3>;
-using Tile4 = Tile<64, 64, 4, 2, 2, 4>;
+// Four stages in flight for bf16; for fp32, whose stages take five times as long,
+// two, so that two workgroups share a CU and one's prologue and epilogue run
+// under the other's products (4330 x 1192 over 416: 65 -> 55 us).
+template <typename T>
+using Tile4 = Tile<64, 64, 4, 2, 2, sizeof(T) == 2 ? 4 : 2>;
 
 // The last plans of this thread by their sizes: a training or decoding loop asks
 // for the same few shapes, and a search costs a few us of the host's time.
@@ -778,9 +636,10 @@ hipError_t add_slices(const LinearProduct& a, const LinearProduct& b, hipStream_
 // Whether stages of C reach past the product's edges and must be masked: every
 // stage of every slice is whole where this is false (one that ran past the
 // reduction's end would read past the operands).
-template <bool AKC, bool BKC, typename C>
+template <typename T, bool AKC, bool BKC, typename C>
 bool has_tail(const LinearProduct& g) {
-  return g.K % (64 * C::KG) != 0 || g.slice % (64 * C::KG) != 0 || (!BKC && g.N % C::BN != 0) ||
+  constexpr int STAGE_K = kStageK<T> * C::KG;
+  return g.K % STAGE_K != 0 || g.slice % STAGE_K != 0 || (!BKC && g.N % C::BN != 0) ||
          (!AKC && g.M % C::BM != 0);
 }
 
@@ -799,24 +658,19 @@ hipError_t linear_fwd_typed(LinearProduct g, float* ws, hipStream_t stream) {
   const Cut& c = fwd_cut(g.M, g.K, g.N, sizeof(T));
   g.slice = c.slice;
   g.part = c.slices > 1 ? ws : nullptr;
-  hipError_t err;
-  if constexpr (std::is_same<T, float>::value) {
-    err = c.tile == kTileF128 ? run_fwd<T, TileF<128>, true>(g, c.groups, stream)
-                              : run_fwd<T, TileF<64>, true>(g, c.groups, stream);
-  } else {
-    auto run = [&](auto tile) {
-      using C = decltype(tile);
-      return has_tail<true, false, C>(g) ? run_fwd<T, C, true>(g, c.groups, stream)
-                                         : run_fwd<T, C, false>(g, c.groups, stream);
-    };
-    switch (c.tile) {
-      case kTile256x256: err = run(Tile0{}); break;
-      case kTile256x128: err = run(Tile1{}); break;
-      case kTile128x128: err = run(Tile2{}); break;
-      case kTile128x64: err = run(Tile3{}); break;
-      default: err = run(Tile4{}); break;
-    }
+  auto run = [&](auto tile) {
+    using C = decltype(tile);
+    return has_tail<T, true, false, C>(g) ? run_fwd<T, C, true>(g, c.groups, stream)
+                                          : run_fwd<T, C, false>(g, c.groups, stream);
+  };
+  hipError_t err = hipErrorUnknown;
+  if constexpr (sizeof(T) == 2) {
+    if (c.tile == kTile256x256) err = run(Tile0{});
+    if (c.tile == kTile256x128) err = run(Tile1{});
   }
+  if (c.tile == kTile128x128) err = run(Tile2{});
+  if (c.tile == kTile128x64) err = run(Tile3{});
+  if (c.tile == kTile64x64) err = run(Tile4<T>{});
   if (err != hipSuccess) return err;
   return add_slices<T>(g, LinearProduct{}, stream);
 }
@@ -858,29 +712,24 @@ hipError_t linear_bwd_typed(const LinearArgs& g, const void* z, const void* mul,
   if (p.x.slices > 1) gx.part = (float*)at;
   at += slice_bytes(T_, I, p.x);
   if (p.w.slices > 1) gw.part = (float*)at;
-  hipError_t err;
-  if constexpr (std::is_same<T, float>::value) {
-    err = p.pair == 0 ? run_bwd<T, TileF<128>, TileF<128>, true>(gx, gw, sum, p, stream)
-                      : run_bwd<T, TileF<64>, TileF<64>, true>(gx, gw, sum, p, stream);
-  } else {
-    auto run = [&](auto tx, auto tw) {
-      using CX = decltype(tx);
-      using CW = decltype(tw);
-      const bool tail = (dx != nullptr && has_tail<true, true, CX>(gx)) ||
-                        (dw != nullptr && has_tail<false, false, CW>(gw));
-      return tail ? run_bwd<T, CX, CW, true>(gx, gw, sum, p, stream)
-                  : run_bwd<T, CX, CW, false>(gx, gw, sum, p, stream);
-    };
-    switch (p.pair) {
-      case 0: err = run(Tile0{}, Tile0{}); break;
-      case 1: err = run(Tile0{}, Tile1{}); break;
-      case 2: err = run(Tile1{}, Tile0{}); break;
-      case 3: err = run(Tile1{}, Tile1{}); break;
-      case 4: err = run(Tile2{}, Tile2{}); break;
-      case 5: err = run(Tile3{}, Tile3{}); break;
-      default: err = run(Tile4{}, Tile4{}); break;
-    }
+  auto run = [&](auto tx, auto tw) {
+    using CX = decltype(tx);
+    using CW = decltype(tw);
+    const bool tail = (dx != nullptr && has_tail<T, true, true, CX>(gx)) ||
+                      (dw != nullptr && has_tail<T, false, false, CW>(gw));
+    return tail ? run_bwd<T, CX, CW, true>(gx, gw, sum, p, stream)
+                : run_bwd<T, CX, CW, false>(gx, gw, sum, p, stream);
+  };
+  hipError_t err = hipErrorUnknown;
+  if constexpr (sizeof(T) == 2) {
+    if (p.pair == 0) err = run(Tile0{}, Tile0{});
+    if (p.pair == 1) err = run(Tile0{}, Tile1{});
+    if (p.pair == 2) err = run(Tile1{}, Tile0{});
+    if (p.pair == 3) err = run(Tile1{}, Tile1{});
   }
+  if (p.pair == 4) err = run(Tile2{}, Tile2{});
+  if (p.pair == 5) err = run(Tile3{}, Tile3{});
+  if (p.pair == 6) err = run(Tile4<T>{}, Tile4<T>{});
   if (err != hipSuccess) return err;
   return add_slices<T>(gx, gw, stream);
 }

@@ -11,29 +11,33 @@
 namespace moe {
 
 // The workgroup tiles, largest first, and what a pass of them over the chip's
-// 256 CUs takes: `step` us per 64 k (`step_few` when at most 160 workgroups
+// 256 CUs takes: `step` us per 64 k (`step_few` when at most 128 workgroups
 // run), `round` us for a tile's prologue and epilogue.  Measured on one MI355X with
-// grids of 128, 256 and 512 workgroups and reductions of 512, 2048 and 4096
-// (all three operand layouts within 8 %).  A larger tile moves fewer bytes
-// through LDS per product (at 256 workgroups: 256 x 256 1.32 PFLOP/s,
-// 256 x 128 1.14, 128 x 128 1.01, 128 x 64 0.84, 64 x 64 0.61) but leaves CUs
-// idle where the outputs are few: 4099 x 768 over 2048 takes 49 us on 256 x 256,
-// 30 on 256 x 128, 20.9 on 128 x 128, 25.8 on 128 x 64 tiles.
+// grids of 128, 256 and 512 workgroups and reductions of 512 to 8192 (all three
+// operand layouts within 8 %), the small tiles' a little up where many of them run.  A larger tile moves fewer bytes
+// through LDS per product (at 256 workgroups: 256 x 256 1.31 PFLOP/s,
+// 256 x 128 1.13, 128 x 128 0.99, 128 x 64 0.75, 64 x 64 0.61) but leaves CUs
+// idle where the outputs are few: 4099 x 768 over 2048 takes 48 us on 256 x 256,
+// 30 on 256 x 128, 21 on 128 x 128, 27 on 128 x 64 tiles.
 enum { kTile256x256 = 0, kTile256x128, kTile128x128, kTile128x64, kTile64x64, kTiles };
-enum { kTileF128 = 0, kTileF64, kTilesF };
 struct TileCost {
   int bm, bn;
   double step, step_few, round;
 };
-constexpr TileCost kCost[kTiles] = {{256, 256, 1.62, 1.18, 9.0},
-                                    {256, 128, 0.94, 0.74, 5.0},
-                                    {128, 128, 0.55, 0.47, 2.7},
-                                    {128, 64, 0.35, 0.29, 2.1},
-                                    {64, 64, 0.24, 0.20, 1.3}};
-constexpr TileCost kCostF[kTilesF] = {{128, 128, 4.1, 4.05, 5.0}, {64, 64, 1.23, 1.22, 1.2}};  // fp32, per 64 k
+constexpr TileCost kCost[kTiles] = {{256, 256, 1.64, 1.12, 9.5},
+                                    {256, 128, 0.95, 0.70, 5.5},
+                                    {128, 128, 0.54, 0.43, 3.5},
+                                    {128, 64, 0.37, 0.29, 2.5},
+                                    {64, 64, 0.26, 0.20, 2.0}};
+// fp32, which takes the last three (256 workgroups: 138, 128, 120 TFLOP/s).
+constexpr TileCost kCostF[kTiles] = {{},
+                                     {},
+                                     {128, 128, 3.9, 3.9, 6.5},
+                                     {128, 64, 2.1, 2.1, 4.0},
+                                     {64, 64, 1.12, 1.12, 1.2}};
 
-constexpr int kCus = 256, kFew = 160;
-constexpr double kLaunchUs = 3.5;           // one more kernel behind another
+constexpr int kCus = 256;
+constexpr double kLaunchUs = 4.5;           // one more kernel behind another
 constexpr double kSliceBytesPerUs = 6.5e6;  // partials written and read again
 
 inline const TileCost& cost_of(int tile, int esize) { return esize == 2 ? kCost[tile] : kCostF[tile]; }
@@ -46,7 +50,13 @@ struct Cut {
   double after;             // us of adding the slices
 };
 
-inline Cut cut_of(int M, int N, int K, int esize, int tile, int want, bool few) {
+// us of a pass of `groups` workgroups (at most 256) over reductions of k.
+inline double pass_us(const TileCost& t, int k, int64_t groups) {
+  const double full = std::min(std::max((double)(groups - 128) / 128.0, 0.0), 1.0);
+  return (double)((k + 63) / 64) * (t.step_few + full * (t.step - t.step_few)) + t.round;
+}
+
+inline Cut cut_of(int M, int N, int K, int esize, int tile, int want) {
   constexpr int kGrain = 128;  // slices are whole stages
   const TileCost& t = cost_of(tile, esize);
   Cut c{};
@@ -54,19 +64,19 @@ inline Cut cut_of(int M, int N, int K, int esize, int tile, int want, bool few) 
   c.slice = (int)((((int64_t)K + want - 1) / want + kGrain - 1) / kGrain * kGrain);
   c.slices = (K + c.slice - 1) / c.slice;
   c.groups = (int64_t)((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn) * c.slices;
-  c.each = (double)((std::min(K, c.slice) + 63) / 64) * (few ? t.step_few : t.step) + t.round;
+  c.each = pass_us(t, std::min(K, c.slice), kCus);
   c.after = c.slices > 1 ? (double)c.slices * M * N * 8.0 / kSliceBytesPerUs : 0.0;
   return c;
 }
 
 // Cuts worth a look: splitting a reduction pays where few tiles meet a long one
-// (2048 x 768 outputs over 4099 rows: 56 us on 128 x 128 tiles, 31 us in two
+// (2048 x 768 outputs over 4099 rows: 38 us on 128 x 128 tiles, 30 us in two
 // slices with the sum behind them).
 template <typename Fn>
 void each_cut(int M, int N, int K, int esize, int tile, Fn&& f) {
   int last = 0;
   for (int want : {1, 2, 3, 4, 6, 8, 12, 16}) {
-    const Cut c = cut_of(M, N, K, esize, tile, want, false);
+    const Cut c = cut_of(M, N, K, esize, tile, want);
     if (want > 1 && c.groups > 2 * kCus) return;
     if (c.slices != last) f(c);
     last = c.slices;
@@ -77,11 +87,11 @@ void each_cut(int M, int N, int K, int esize, int tile, Fn&& f) {
 inline Cut plan_fwd(int M, int N, int K, int esize) {
   Cut best{};
   double best_us = 0.0;
-  for (int tile = 0; tile < (esize == 2 ? (int)kTiles : (int)kTilesF); ++tile)
+  for (int tile = esize == 2 ? 0 : (int)kTile128x128; tile < kTiles; ++tile)
     each_cut(M, N, K, esize, tile, [&](const Cut& c) {
       const int64_t rest = c.groups % kCus;
       double us = kLaunchUs + (double)(c.groups / kCus) * c.each + (c.slices > 1 ? kLaunchUs + c.after : 0.0);
-      if (rest > 0) us += rest > kFew ? c.each : cut_of(M, N, K, esize, tile, c.slices, true).each;
+      if (rest > 0) us += pass_us(cost_of(tile, esize), std::min(K, c.slice), rest);
       if (best.slices == 0 || us < best_us) {
         best = c;
         best_us = us;
@@ -102,17 +112,18 @@ struct Pair {
 constexpr Pair kPairs[] = {{kTile256x256, kTile256x256}, {kTile256x256, kTile256x128}, {kTile256x128, kTile256x256},
                            {kTile256x128, kTile256x128}, {kTile128x128, kTile128x128}, {kTile128x64, kTile128x64},
                            {kTile64x64, kTile64x64}};
-constexpr Pair kPairsF[] = {{kTileF128, kTileF128}, {kTileF64, kTileF64}};
+constexpr int kPairsF = 4;  // fp32 takes those from here on
 
 inline Plan2 plan_bwd(int T, int I, int O, int esize, bool dx, bool dw) {
   Plan2 best{};
   double best_us = -1.0;
-  const int pairs = esize == 2 ? (int)std::size(kPairs) : (int)std::size(kPairsF);
-  for (int p = 0; p < pairs; ++p) {
-    const Pair tiles = esize == 2 ? kPairs[p] : kPairsF[p];
+  for (int p = esize == 2 ? 0 : kPairsF; p < (int)std::size(kPairs); ++p) {
+    const Pair tiles = kPairs[p];
     auto weigh = [&](const Cut* x, const Cut* w) {
       const int64_t gx = x ? x->groups : 0, gw = w ? w->groups : 0;
-      const double ex = x ? x->each : 0.0, ew = w ? w->each : 0.0;
+      const int64_t load = std::min<int64_t>(gx + gw, kCus);
+      const double ex = x ? pass_us(cost_of(tiles.x, esize), std::min(O, x->slice), load) : 0.0;
+      const double ew = w ? pass_us(cost_of(tiles.w, esize), std::min(T, w->slice), load) : 0.0;
       double us = std::max({((double)gx * ex + (double)gw * ew) / kCus, ex, ew});
       if (gx + gw > kCus) us += 0.5 * std::min(gx ? ex : ew, gw ? ew : ex);  // the last ones end unevenly
       const double after = (x ? x->after : 0.0) + (w ? w->after : 0.0);

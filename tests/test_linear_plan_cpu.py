@@ -35,7 +35,8 @@ int main() {
         const moe::Plan2 p = moe::plan_bwd(T, I, O, esize, want & 1, want & 2);
         if (want & 1) check(p.x, T, I, O, esize, "dx");
         if (want & 2) check(p.w, I, O, T, esize, "dw");
-        const moe::Pair pair = esize == 2 ? moe::kPairs[p.pair] : moe::kPairsF[p.pair];
+        const moe::Pair pair = moe::kPairs[p.pair];
+        if (esize == 4 && p.pair < moe::kPairsF) ++bad;
         if (((want & 1) && pair.x != p.x.tile) || ((want & 2) && pair.w != p.w.tile)) ++bad;
       }
     }
