@@ -223,13 +223,16 @@ __device__ __forceinline__ int kc_key(int row, int chunk) { return chunk ^ ((row
 // k row of a [k][ROWS] LDS tile -> XOR on the 16-byte chunk index.  bf16: the 4 k
 // rows x 4 chunks that half a wave's transpose read covers lie in distinct banks
 // (256-byte rows and longer: every row starts at the same bank; 128-byte rows: every
-// other one).  fp32: the two k rows, 4 apart, of a wave's read.
+// other one; 64-byte rows need no key).  fp32: the two k rows, 4 apart, of a wave's
+// read (128-byte rows, where a key cannot part them: their places, nc_place).
 template <typename T, int ROWS>
 __device__ __forceinline__ int nc_key(int k) {
-  static_assert(ROWS >= 64, "eight chunks at least");
+  if (ROWS == 32) return 0;
   if (sizeof(T) == 4) return 8 * ((k >> 2) & 1);
   return ROWS >= 128 ? 4 * (k & 3) : 4 * ((k >> 1) & 1);
 }
+template <typename T, int ROWS>
+__device__ __forceinline__ int nc_place(int k) { return ROWS == 32 && sizeof(T) == 4 ? k ^ ((k >> 2) & 1) : k; }
 
 // Fragment of rows row0 .. row0 + 31, run `sub` of the stage's four, from a
 // [k][ROWS] tile.  bf16, k 16 sub .. + 15: in 16-lane group G, lane r points at k
@@ -241,9 +244,11 @@ __device__ __forceinline__ u32x4 nc_frag(const unsigned char* tile, int sub, int
   const int l = __lane_id(), G = l >> 4, r = l & 15;
   if constexpr (sizeof(T) == 4) {
     const int row = row0 + (l & 31), k = 8 * sub + 4 * (l >> 5);
-    const unsigned char* at = tile + k * (4 * ROWS) + 16 * ((row >> 2) ^ nc_key<T, ROWS>(k)) + 4 * (row & 3);
-    return u32x4{*(const uint32_t*)at, *(const uint32_t*)(at + 4 * ROWS), *(const uint32_t*)(at + 8 * ROWS),
-                 *(const uint32_t*)(at + 12 * ROWS)};
+    const unsigned char* col = tile + 16 * ((row >> 2) ^ nc_key<T, ROWS>(k)) + 4 * (row & 3);
+    const unsigned char* even = col + nc_place<T, ROWS>(k) * (4 * ROWS);
+    const unsigned char* odd = col + nc_place<T, ROWS>(k + 1) * (4 * ROWS);
+    return u32x4{*(const uint32_t*)even, *(const uint32_t*)odd, *(const uint32_t*)(even + 8 * ROWS),
+                 *(const uint32_t*)(odd + 8 * ROWS)};
   }
   const int row = row0 + 16 * (G & 1) + 4 * (r & 3);
   v4i16 part[2];
@@ -278,8 +283,9 @@ struct Loader {
         src[i] = (const T*)base + (int64_t)min(r0 + row, rows - 1) * ld + k[i];
       } else {
         const int at = 64 * (INS * w + i) + l;  // chunk of the stage
-        const int c = r0 + CH * ((at % CHUNKS) ^ nc_key<T, ROWS>(at / CHUNKS));
-        k[i] = k0 + at / CHUNKS;
+        const int ks = nc_place<T, ROWS>(at / CHUNKS);  // its own inverse
+        const int c = r0 + CH * ((at % CHUNKS) ^ nc_key<T, ROWS>(ks));
+        k[i] = k0 + ks;
         src[i] = (const T*)base + (int64_t)k[i] * ld + (c < rows ? c : 0);
         if (c >= rows) k[i] = 0x80000000u;
       }
@@ -425,11 +431,13 @@ __device__ __forceinline__ void tile_product(const LinearProduct& g, int tile, i
   products(f1, mine, -1, f0);
 
   // The fp32 tile leaves through the idle stage buffers, HC columns at a time
-  // ([row][HC], 16-byte chunk c of row r at c ^ (r & 15)), so that the epilogue
+  // ([row][HC], 16-byte chunk c of row r at c ^ (r mod CH)), so that the epilogue
   // reads and writes runs of eight neighbouring outputs.  Register r of
   // acc[i][j] is row TM wm + 32 i + l32, column TN wn + 32 j + 8 (r / 4) + 4 hk + r % 4.
   constexpr int FIT = STAGES * STAGE / (BM * 4);
   constexpr int HC = FIT >= BN ? BN : (FIT >= 128 ? 128 : 64);
+  constexpr bool APART = FIT >= KG * BN;  // every group's sums in a place of their own
+  constexpr int CH = HC / 4 < 16 ? HC / 4 : 16;  // chunks that trade places
   static_assert(BM * HC * 4 <= STAGES * STAGE && HC % TN == 0 && BN % HC == 0, "staging");
   float* s_f = reinterpret_cast<float*>(s_dyn);
   __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's last fragment reads are done
@@ -437,8 +445,8 @@ __device__ __forceinline__ void tile_product(const LinearProduct& g, int tile, i
   for (int part = 0; part < BN / HC; ++part) {
     barrier_no_fence();  // every wave is done with the stage buffers / the previous part
 #pragma unroll
-    for (int k2 = 0; k2 < KG; ++k2) {  // the groups in turn: the first writes its sums, the others add theirs
-      if (kg == k2 && TN * wn / HC == part) {
+    for (int k2 = 0; k2 < (APART ? 1 : KG); ++k2) {  // else in turn: the first writes its sums, the others add theirs
+      if ((APART || kg == k2) && TN * wn / HC == part) {
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -446,7 +454,7 @@ __device__ __forceinline__ void tile_product(const LinearProduct& g, int tile, i
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const int row = TM * wm + 32 * i + l32, col = TN * wn - HC * part + 32 * j + 8 * q + 4 * hk;
-              f32x4* at = (f32x4*)(s_f + row * HC + 4 * ((col >> 2) ^ (row & 15)));
+              f32x4* at = (f32x4*)(s_f + ((APART ? kg * BM : 0) + row) * HC + 4 * ((col >> 2) ^ (row & (CH - 1))));
               f32x4 v = f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
               if (k2 > 0) v += *at;
               *at = v;
@@ -460,8 +468,15 @@ __device__ __forceinline__ void tile_product(const LinearProduct& g, int tile, i
       const int row = it / (HC / 8), c8 = it % (HC / 8);
       const int m = m0 + row, n = n0 + HC * part + 8 * c8;
       if (m >= g.M || n >= g.N) continue;  // N is a multiple of 8: a run is all in or all out
-      const f32x4 lo = *(const f32x4*)(s_f + row * HC + 4 * ((2 * c8) ^ (row & 15)));
-      const f32x4 hi = *(const f32x4*)(s_f + row * HC + 4 * ((2 * c8 + 1) ^ (row & 15)));
+      f32x4 lo, hi;
+#pragma unroll
+      for (int k2 = 0; k2 < (APART ? KG : 1); ++k2) {
+        const float* at = s_f + (k2 * BM + row) * HC;
+        const f32x4 l2 = *(const f32x4*)(at + 4 * ((2 * c8) ^ (row & (CH - 1))));
+        const f32x4 h2 = *(const f32x4*)(at + 4 * ((2 * c8 + 1) ^ (row & (CH - 1))));
+        lo = k2 == 0 ? l2 : lo + l2;
+        hi = k2 == 0 ? h2 : hi + h2;
+      }
       float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
       leave8<T>(g, slice, m, n, v);
     }
@@ -592,6 +607,11 @@ using Tile3 = Tile<128, 64, 4, 2, 2, 3>;
 // under the other's products (4330 x 1192 over 416: 65 -> 55 us).
 template <typename T>
 using Tile4 = Tile<64, 64, 4, 2, 2, sizeof(T) == 2 ? 4 : 2>;
+// For a few rows: eight waves over the reduction, so that 512 k (fp32: 256) of it are
+// on their way at once, and twice the CUs read the weights (bf16 in a captured
+// graph: 8 x 768 -> 2048 5.5 -> 4.7 us, 1 x 2048 -> 768 9.2 -> 5.5; fp32 8 x 768 ->
+// 2048 9.1 -> 7.3 us).
+using Tile5 = Tile<32, 32, 1, 1, 8, 2>;
 
 // The last plans of this thread by their sizes: a training or decoding loop asks
 // for the same few shapes, and a search costs a few us of the host's time.
@@ -671,6 +691,7 @@ hipError_t linear_fwd_typed(LinearProduct g, float* ws, hipStream_t stream) {
   if (c.tile == kTile128x128) err = run(Tile2{});
   if (c.tile == kTile128x64) err = run(Tile3{});
   if (c.tile == kTile64x64) err = run(Tile4<T>{});
+  if (c.tile == kTile32x32) err = run(Tile5{});
   if (err != hipSuccess) return err;
   return add_slices<T>(g, LinearProduct{}, stream);
 }
@@ -730,6 +751,7 @@ hipError_t linear_bwd_typed(const LinearArgs& g, const void* z, const void* mul,
   if (p.pair == 4) err = run(Tile2{}, Tile2{});
   if (p.pair == 5) err = run(Tile3{}, Tile3{});
   if (p.pair == 6) err = run(Tile4<T>{}, Tile4<T>{});
+  if (p.pair == 7) err = run(Tile5{}, Tile4<T>{});
   if (err != hipSuccess) return err;
   return add_slices<T>(gx, gw, stream);
 }

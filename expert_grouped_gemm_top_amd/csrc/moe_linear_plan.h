@@ -14,12 +14,14 @@ namespace moe {
 // 256 CUs takes: `step` us per 64 k (`step_few` when at most 128 workgroups
 // run), `round` us for a tile's prologue and epilogue.  Measured on one MI355X with
 // grids of 128, 256 and 512 workgroups and reductions of 512 to 8192 (all three
-// operand layouts within 8 %), the small tiles' a little up where many of them run.  A larger tile moves fewer bytes
+// operand layouts within 8 %), the small tiles' a little up where many of them
+// run.  A larger tile moves fewer bytes
 // through LDS per product (at 256 workgroups: 256 x 256 1.31 PFLOP/s,
 // 256 x 128 1.13, 128 x 128 0.99, 128 x 64 0.75, 64 x 64 0.61) but leaves CUs
 // idle where the outputs are few: 4099 x 768 over 2048 takes 48 us on 256 x 256,
-// 30 on 256 x 128, 21 on 128 x 128, 27 on 128 x 64 tiles.
-enum { kTile256x256 = 0, kTile256x128, kTile128x128, kTile128x64, kTile64x64, kTiles };
+// 30 on 256 x 128, 21 on 128 x 128, 27 on 128 x 64 tiles.  32 x 32 is for a few
+// rows, where the weights' way through as many CUs as there are is what counts.
+enum { kTile256x256 = 0, kTile256x128, kTile128x128, kTile128x64, kTile64x64, kTile32x32, kTiles };
 struct TileCost {
   int bm, bn;
   double step, step_few, round;
@@ -28,13 +30,15 @@ constexpr TileCost kCost[kTiles] = {{256, 256, 1.64, 1.12, 9.5},
                                     {256, 128, 0.95, 0.70, 5.5},
                                     {128, 128, 0.54, 0.43, 3.5},
                                     {128, 64, 0.37, 0.29, 2.5},
-                                    {64, 64, 0.26, 0.20, 2.0}};
-// fp32, which takes the last three (256 workgroups: 138, 128, 120 TFLOP/s).
+                                    {64, 64, 0.26, 0.20, 2.0},
+                                    {32, 32, 0.18, 0.14, 2.0}};
+// fp32, which takes the last four (256 workgroups: 138, 128, 120 and 95 TFLOP/s).
 constexpr TileCost kCostF[kTiles] = {{},
                                      {},
                                      {128, 128, 3.9, 3.9, 6.5},
                                      {128, 64, 2.1, 2.1, 4.0},
-                                     {64, 64, 1.12, 1.12, 1.2}};
+                                     {64, 64, 1.12, 1.12, 1.2},
+                                     {32, 32, 0.40, 0.31, 2.5}};
 
 constexpr int kCus = 256;
 constexpr double kLaunchUs = 4.5;           // one more kernel behind another
@@ -52,7 +56,8 @@ struct Cut {
 
 // us of a pass of `groups` workgroups (at most 256) over reductions of k.
 inline double pass_us(const TileCost& t, int k, int64_t groups) {
-  const double full = std::min(std::max((double)(groups - 128) / 128.0, 0.0), 1.0);
+  const double least = t.bm == 32 ? -0.5 : 0.0;  // the smallest tile's step falls on down to 64 workgroups
+  const double full = std::min(std::max((double)(groups - 128) / 128.0, least), 1.0);
   return (double)((k + 63) / 64) * (t.step_few + full * (t.step - t.step_few)) + t.round;
 }
 
@@ -111,7 +116,7 @@ struct Pair {
 };
 constexpr Pair kPairs[] = {{kTile256x256, kTile256x256}, {kTile256x256, kTile256x128}, {kTile256x128, kTile256x256},
                            {kTile256x128, kTile256x128}, {kTile128x128, kTile128x128}, {kTile128x64, kTile128x64},
-                           {kTile64x64, kTile64x64}};
+                           {kTile64x64, kTile64x64}, {kTile32x32, kTile64x64}};
 constexpr int kPairsF = 4;  // fp32 takes those from here on
 
 inline Plan2 plan_bwd(int T, int I, int O, int esize, bool dx, bool dw) {

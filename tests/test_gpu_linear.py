@@ -159,6 +159,18 @@ def test_backward(T, I, O, dtype):  # noqa: E741
     check_backward(v, dtype, R.SILU, bias=False, mul=True, add=True)
 
 
+@pytest.mark.parametrize("T,I,O", [
+    (1, 1024, 1024), (16, 1024, 1024), (33, 1536, 512), (7, 2472, 72), (31, 2000, 200), (5, 4096, 160), (40, 2048, 696),
+    (2, 1544, 96), (44, 4096, 64), (16, 512, 4096), (3, 72, 2560), (12, 256, 2048)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_few_rows(T, I, O, dtype):  # noqa: E741
+    """Decoding steps: whole and masked stages of the 32 x 32 tiles, one to several of them, split and not."""
+    v = inputs(T, I, O, dtype, T + O)
+    check_forward(v, dtype, R.SILU, mul=True, residual=True)
+    check_backward(v, dtype, R.SILU, mul=True, add=True)
+    check_backward(v, dtype, R.NONE, bias=False, want=("dx",))
+
+
 @pytest.mark.parametrize("act", range(5))
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_backward_epilogues(act, dtype):
