@@ -512,12 +512,23 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs g) {
 
 // The backward: sixteen lanes per token as in the forward.  Lanes j < k hold the
 // selected pairs' terms (an index listed twice: each holds the sum of its
-// terms, added in list order), which go through an LDS row of zeros so that
-// every lane writes whole runs of the token's dlogits once.  HBM-bound: the
-// output, and for plain softmax (DENSE, the only one whose gradient reaches
-// every expert) the logits.  QUAD: runs of four experts, every sixteenth run
-// of a lane; otherwise single experts.  16384 tokens, 128 experts: 6.2 us,
-// 2.9 TB/s (a wave per token that looked each of its experts up among the selected: 14.9 us).
+// terms), which go through an LDS row of zeros so that every lane writes whole
+// runs of the token's dlogits once.
+//
+// A confident router's gradient is a small difference: of 1 and a score, of g
+// and its mean over weights of which one is nearly 1.  None is formed from
+// rounded values that near each other: 1 - s of a sigmoid is 1 / (1 + exp(l)),
+// and as the weights sum to 1
+//   g_j - sum_i p_i g_i = sum_i p_i (g_j - g_i),
+// plain softmax alike over all experts, g = 0 where not selected:
+//   g_e - sum_i s_i g_i = sum_{i selected} s_i (g_e - g_i) + g_e sum_{i not selected} s_i.
+//
+// HBM-bound: the output, and for plain softmax (DENSE, the only one whose
+// gradient reaches every expert) the logits.  QUAD: runs of four experts, every
+// sixteenth run of a lane; otherwise single experts.  A call at 16384 tokens,
+// plain softmax: 128 experts 7.1 us, 256 8.6 us (with 1 - s and g - sum p g as
+// differences of rounded values 7.1 and 8.2 us, and no correct digit left
+// where a score is within 2^-24 of 1).
 template <bool QUAD, bool DENSE>
 __global__ __launch_bounds__(256) void route_scored_bwd_kernel(int T, int E, int k, int score, int renorm, float scale,
                                                                const float* __restrict__ logits,
@@ -575,31 +586,78 @@ __global__ __launch_bounds__(256) void route_scored_bwd_kernel(int T, int E, int
     sum = row_add(sum);
   }
   const bool avail = e_l >= 0 && a != -inf;
-  const float s = score == 0 ? 0.0f : 1.0f / (1.0f + expf(-a));
-  float d, sg = 0.0f;  // DENSE: sg = sum_i s_i g_i
-  if (renorm) {
-    const float p = renormalized(log_score(score, a), e_l >= 0, false);
-    const float pg = row_add(avail ? p * g : 0.0f);
-    d = scale * p * (g - pg) * (score == 0 ? 1.0f : 1.0f - s);
-  } else if (DENSE) {
-    const float se = avail ? expf(a - m) / sum : 0.0f;
-    sg = row_add(avail ? se * g : 0.0f);
-    d = scale * se * g;
-  } else {
-    d = scale * g * s * (1.0f - s);
-  }
-  if (!avail) d = 0.0f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int e = R * (li + kRow * i);
     if (QUAD) *(f32x4*)(d_row + e) = f32x4{0.f, 0.f, 0.f, 0.f};
     else d_row[e] = 0.0f;
   }
-  float total = 0.0f;
-  for (int j = 0; j < k; ++j) {
-    const int ej = __shfl(e_l, j, kRow);
-    const float dj = __shfl(d, j, kRow);
-    total += ej == e_l ? dj : 0.0f;
+  // sum_i p_i (g - g_i) over the token's lanes, from each lane's own p and g
+  auto spread = [&](float p, float g_own) {
+    float p_i = p, g_i = g_own, v = 0.0f;
+#pragma unroll
+    for (int i = 1; i < kRow; ++i) {
+      p_i = ror<1>(p_i);
+      g_i = ror<1>(g_i);
+      v += p_i * (g_own - g_i);
+    }
+    return v;
+  };
+  if (!avail) g = 0.0f;
+  float d, sg = 0.0f;  // DENSE: sg = sum_i s_i g_i
+  if (DENSE) {
+    // marks the selected experts, leaves l only to the others, and adds those
+    wave_lds_order();
+    if (e_l >= 0) d_row[e_l] = (float)(li + 1);
+    wave_lds_order();
+    float others = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = R * (li + kRow * i);
+      f32x4 mark;
+      if (QUAD) mark = *(const f32x4*)(d_row + e);
+      else mark[0] = d_row[e];
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        l[i][j] = mark[j] == 0.0f ? l[i][j] : 0.0f;
+        others += l[i][j];
+      }
+    }
+    others = row_add(others) / sum;
+    const float se = avail ? expf(a - m) / sum : 0.0f;
+    sg = row_add(se * g);
+    float g_e = g, listed = 1.0f;
+    if (__ballot(e_l >= 0 && d_row[max(e_l, 0)] != (float)(li + 1))) {
+      // an index listed twice: the sum of its g, its score shared out among the listings
+      float g_i = g;
+      int e_i = e_l;
+#pragma unroll 1
+      for (int i = 1; i < kRow; ++i) {
+        e_i = ror<1>(e_i);
+        g_i = ror<1>(g_i);
+        g_e += e_i == e_l ? g_i : 0.0f;
+        listed += e_i == e_l ? 1.0f : 0.0f;
+      }
+    }
+    d = scale * se * (spread(se / listed, g_e) + g_e * others);
+  } else {
+    const float s_not = score == 0 ? 1.0f : 1.0f / (1.0f + expf(a));  // 1 - s
+    if (renorm) {
+      const float p = renormalized(log_score(score, a), e_l >= 0, false);
+      d = scale * p * spread(p, g) * s_not;
+    } else {
+      d = scale * g * s_not / (1.0f + expf(-a));
+    }
+  }
+  if (!avail) d = 0.0f;
+  float total = d;
+  if (!DENSE) {
+    total = 0.0f;
+    for (int j = 0; j < k; ++j) {
+      const int ej = __shfl(e_l, j, kRow);
+      const float dj = __shfl(d, j, kRow);
+      total += ej == e_l ? dj : 0.0f;
+    }
   }
   wave_lds_order();
   if (e_l >= 0) d_row[e_l] = total;

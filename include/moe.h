@@ -540,7 +540,9 @@ int moe_route_scored(int T, int E, int k, int score, int n_groups, int top_group
  * and zero for the other experts of the first three.  Unavailable experts and
  * tokens whose selected scores are all zero get zeros.  The bias takes no
  * gradient (the selection does not pass one).  An index listed twice in a row
- * counts twice; one outside [0, E) is left out.
+ * counts twice; one outside [0, E) is left out.  The differences 1 - s_j and
+ * g_j - sum_i p_i g_i keep fp32's relative precision however near a score or a
+ * weight is to 1 (as long as they are normal fp32 numbers).
  * logits [T, E] fp32, topk_idx [T, k] int32, dg [T, k] fp32 (device);
  * dlogits [T, E] fp32 (device, out). */
 int moe_route_scored_bwd(int T, int E, int k, int score, int renormalize, float scale, const float* logits,
