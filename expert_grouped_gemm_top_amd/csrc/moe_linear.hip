@@ -27,17 +27,40 @@ enum Act { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu 
 constexpr float kTanhA = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kTanhB = 0.044715f;
 
-// exp(v) and 1 / (1 + exp(-v)) on the hardware's exp2 and reciprocal: relative
-// errors of at most (1.5 |v| + 2) 2^-24 and of that share of exp(-v) plus 2^-22
-// (the library's expf, erfcf and division took 7 of 28 us of a GELU product's
-// epilogue at 4099 x 768).
+// Logistic function and normal distribution of an activation, by the element type.
+// bf16: on the hardware's exp2 and reciprocal, exp(v) within (1.5 |v| + 2) 2^-24
+// of itself, and the distribution within 1.5e-7 (5e-5 of itself at -3, 2^-9
+// from -5.2 on, where it is below 1e-7): the library's expf, erfcf and division
+// took 7 of 28 us of a GELU product's epilogue at 4099 x 768.  fp32: those,
+// whose errors are a few 2^-24 of the result in the tails too; they cost its
+// products 0.2 to 0.7 us (4096 x 512 -> 1024 with GELU and a gate 45.5 us).
 __device__ __forceinline__ float quick_exp(float v) { return __builtin_amdgcn_exp2f(v * 1.44269504f); }
-__device__ __forceinline__ float logistic(float v) { return __builtin_amdgcn_rcpf(1.0f + quick_exp(-v)); }
+template <typename T>
+__device__ __forceinline__ float exp_of(float v) {
+  return sizeof(T) == 4 ? expf(v) : quick_exp(v);
+}
 
-// Phi(z), the normal distribution: erfc(|z| / sqrt 2) / 2 by formula 7.1.26 of
-// Abramowitz and Stegun, erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + p x),
-// |error| <= 1.5e-7, mirrored for z > 0.
+// s = 1 / (1 + exp(-v)), and `rest` = 1 - s.
+struct Logistic {
+  float s, rest;
+};
+template <typename T>
+__device__ __forceinline__ Logistic logistic(float v) {
+  if constexpr (sizeof(T) == 2) {
+    const float s = __builtin_amdgcn_rcpf(1.0f + quick_exp(-v));
+    return {s, 1.0f - s};
+  } else {
+    const float e = expf(-fabsf(v)), near = 1.0f / (1.0f + e), far = e / (1.0f + e);
+    return v >= 0.0f ? Logistic{near, far} : Logistic{far, near};
+  }
+}
+
+// Phi(z), the normal distribution: erfc(-z / sqrt 2) / 2.  bf16: by formula
+// 7.1.26 of Abramowitz and Stegun, erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2),
+// t = 1 / (1 + p x), |error| <= 1.5e-7, mirrored for z > 0.
+template <typename T>
 __device__ __forceinline__ float normal_cdf(float z) {
+  if constexpr (sizeof(T) == 4) return 0.5f * erfcf(-z * 0.70710678f);
   const float x = fabsf(z) * 0.70710678f;
   const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * x);
   const float poly =
@@ -46,7 +69,8 @@ __device__ __forceinline__ float normal_cdf(float z) {
   return z > 0.0f ? 1.0f - tail : tail;
 }
 
-// v = act(v) for eight values; NaN stays NaN.  One branch per run, not per value.
+// v = act(v) for eight values of an output of type T; NaN stays NaN.  One branch per run, not per value.
+template <typename T>
 __device__ __forceinline__ void act8(int act, float (&v)[8]) {
   switch (act) {
     case kActRelu:
@@ -55,15 +79,15 @@ __device__ __forceinline__ void act8(int act, float (&v)[8]) {
       return;
     case kActGelu:
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= normal_cdf(v[j]);
+      for (int j = 0; j < 8; ++j) v[j] *= normal_cdf<T>(v[j]);
       return;
     case kActGeluTanh:  // (1 + tanh u) / 2 = logistic(2 u)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= logistic(2.0f * kTanhA * (v[j] + kTanhB * v[j] * v[j] * v[j]));
+      for (int j = 0; j < 8; ++j) v[j] *= logistic<T>(2.0f * kTanhA * (v[j] + kTanhB * v[j] * v[j] * v[j])).s;
       return;
     case kActSilu:
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= logistic(v[j]);
+      for (int j = 0; j < 8; ++j) v[j] *= logistic<T>(v[j]).s;
       return;
     default: return;
   }
@@ -73,6 +97,7 @@ __device__ __forceinline__ float clamped(float z, float most) { return z > most 
 
 // value = act(z) and slope = act'(z) for eight values.  The slopes are 0 or 1 to
 // fp32 precision beyond |z| = 30 (SILU: 100), where their formulas would form 0 * inf.
+template <typename T>
 __device__ __forceinline__ void act8_both(int act, const float (&z)[8], float (&value)[8], float (&slope)[8]) {
   switch (act) {
     case kActRelu:
@@ -85,25 +110,27 @@ __device__ __forceinline__ void act8_both(int act, const float (&z)[8], float (&
     case kActGelu:
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float c = clamped(z[j], 30.0f), phi = normal_cdf(c);
+        const float c = clamped(z[j], 30.0f), phi = normal_cdf<T>(c);
         value[j] = z[j] * phi;
-        slope[j] = phi + c * 0.3989422804014327f * quick_exp(-0.5f * c * c);
+        slope[j] = phi + c * 0.3989422804014327f * exp_of<T>(-0.5f * c * c);
       }
       return;
     case kActGeluTanh:
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float c = clamped(z[j], 30.0f), s = logistic(2.0f * kTanhA * (c + kTanhB * c * c * c));
-        value[j] = z[j] * s;
-        slope[j] = s + c * s * (1.0f - s) * 2.0f * kTanhA * (1.0f + 3.0f * kTanhB * c * c);
+        const float c = clamped(z[j], 30.0f);
+        const Logistic u = logistic<T>(2.0f * kTanhA * (c + kTanhB * c * c * c));
+        value[j] = z[j] * u.s;
+        slope[j] = u.s + c * u.s * u.rest * 2.0f * kTanhA * (1.0f + 3.0f * kTanhB * c * c);
       }
       return;
     case kActSilu:
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float c = clamped(z[j], 100.0f), s = logistic(c);
-        value[j] = z[j] * s;
-        slope[j] = s * (1.0f + c * (1.0f - s));
+        const float c = clamped(z[j], 100.0f);
+        const Logistic u = logistic<T>(c);
+        value[j] = z[j] * u.s;
+        slope[j] = u.s * (1.0f + c * u.rest);
       }
       return;
     default:
@@ -142,7 +169,7 @@ __device__ __forceinline__ void finish8(const LinearProduct& g, int64_t m, int n
     for (int j = 0; j < 8; ++j) v[j] += u[j];
   }
   if (g.z != nullptr) store8((T*)g.z + at, v);
-  act8(g.act, v);
+  act8<T>(g.act, v);
   if (g.mul != nullptr) {
     load8((const T*)g.mul + at, u);
 #pragma unroll
@@ -557,7 +584,7 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(int rows, int O, int act
       if (z != nullptr) {
         float zv[8], value[8], slope[8];
         load8(z + at, zv);
-        act8_both(act, zv, value, slope);
+        act8_both<T>(act, zv, value, slope);
         if (mul != nullptr) {
           float mv[8];
           load8(mul + at, mv);
