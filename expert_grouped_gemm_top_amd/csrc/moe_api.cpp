@@ -1013,13 +1013,15 @@ int moe_linear_fwd(int T, int I, int O, int dtype, int act, const void* x, const
   const int64_t in = (int64_t)T * I * es, out = (int64_t)T * O * es;
   const Span sx{"x", x, in}, sw{"w", w, (int64_t)I * O * es}, sb{"bias", bias, (int64_t)O * es};
   const Span sm{"mul", mul, out}, sr{"residual", residual, out}, sz{"z_save", z_save, out}, sy{"y", y, out};
+  // an unsplit reduction leaves nothing in a workspace, so none need be given
+  const bool without = workspace == nullptr && workspace_bytes == 0 && !moe::linear_fwd_splits(T, I, O, es);
+  const size_t need = without ? 0 : moe::linear_workspace_bytes(T, I, O, es);
   if ((rc = check_aligned(fn, "x", x)) || (rc = check_aligned(fn, "w", w)) || (rc = check_aligned(fn, "bias", bias)) ||
       (rc = check_aligned(fn, "mul", mul)) || (rc = check_aligned(fn, "residual", residual)) ||
       (rc = check_aligned(fn, "z_save", z_save)) || (rc = check_aligned(fn, "y", y)) ||
       (rc = check_output(fn, sy, {sm, sr}, true)) || (rc = check_output(fn, sy, {sx, sw, sb, sz}, false)) ||
       (rc = check_output(fn, sz, {sx, sw, sb, sm, sr}, false)) ||
-      (rc = check_workspace(fn, moe::linear_workspace_bytes(T, I, O, es), workspace, workspace_bytes,
-                            {sx, sw, sb, sm, sr, sz, sy})))
+      (rc = check_workspace(fn, need, workspace, workspace_bytes, {sx, sw, sb, sm, sr, sz, sy})))
     return rc;
   const moe::LinearArgs g{T, I, O, act, x, w};
   hipStream_t s = as_stream(stream);

@@ -247,6 +247,7 @@ struct LinearArgs {
   const void* w;
 };
 size_t linear_workspace_bytes(int T, int I, int O, int esize);
+bool linear_fwd_splits(int T, int I, int O, int esize);  // whether the forward uses its workspace
 hipError_t launch_linear_fwd(const LinearArgs& g, int esize, const void* bias, const void* mul, const void* residual,
                              void* z, void* y, void* ws, hipStream_t stream);
 hipError_t launch_linear_bwd(const LinearArgs& g, int esize, const void* z, const void* mul, const void* dy, void* dz,

@@ -798,6 +798,8 @@ size_t linear_workspace_bytes(int T, int I, int O, int esize) {
   });
 }
 
+bool linear_fwd_splits(int T, int I, int O, int esize) { return fwd_cut(T, I, O, esize).slices > 1; }
+
 hipError_t launch_linear_fwd(const LinearArgs& g, int esize, const void* bias, const void* mul, const void* residual,
                              void* z, void* y, void* ws, hipStream_t stream) {
   const LinearProduct p{g.T, g.O, g.I, g.x, g.I, g.w, g.O, g.act, bias, mul, residual, z, y, 0, nullptr};

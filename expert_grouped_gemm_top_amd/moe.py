@@ -602,13 +602,14 @@ def moe_layernorm_bwd(x, gamma, mean, rstd, dy, dx, dgamma, dbeta, workspace, dx
 
 
 def moe_linear_workspace_bytes(T: int, I: int, O: int, dtype) -> int:  # noqa: E741
+    """Bytes for moe_linear_fwd and moe_linear_bwd of these sizes (fewer rows may need more)."""
     return int(lib().moe_linear_workspace_bytes(T, I, O, MOE_F32 if dtype == torch.float32 else MOE_BF16))
 
 
 def moe_linear_fwd(x, w, bias, y, act: int = MOE_ACT_NONE, mul=None, residual=None, z_save=None, workspace=None,
                    stream=None):
     """y = act(x w + bias) [* mul] [+ residual]; z_save keeps x w + bias for the
-    backward.  y may be mul or residual."""
+    backward.  y may be mul or residual.  workspace None: only where the reduction is not split."""
     dev = _device(x, "x")
     T, I = _rows(x, "x")  # noqa: E741
     O = _rows(w, "w")[1]  # noqa: E741

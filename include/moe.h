@@ -589,9 +589,11 @@ typedef enum moe_act {
   MOE_ACT_SILU = 4
 } moe_act;
 
-/* Workspace (device bytes) that moe_linear_fwd and moe_linear_bwd need for T
- * rows, I inputs and O outputs: fp32 partial sums of split reductions (0 when none
- * is split).  Host-only. */
+/* Workspace (device bytes) of moe_linear_fwd and moe_linear_bwd for T rows, I
+ * inputs and O outputs: fp32 partial sums of dbias and of split reductions, enough
+ * for either call whatever it is asked for (0 only for sizes that are refused).
+ * Fewer rows may need more, as they are split further: a buffer for several T
+ * holds the largest of their sizes.  Host-only. */
 size_t moe_linear_workspace_bytes(int T, int I, int O, int dtype);
 
 /* Dense product with its epilogue:
@@ -608,7 +610,9 @@ size_t moe_linear_workspace_bytes(int T, int I, int O, int dtype);
  * experts' sum a shared expert's output joins it.
  * I and O multiples of 8, at most 2^20, T at most 2^30, T I and T O below 2^40,
  * pointers 16-byte aligned, workspace (apart from all other buffers) of at
- * least moe_linear_workspace_bytes (may be NULL when that is 0).  Calls that
+ * least moe_linear_workspace_bytes.  A forward whose reduction is not split (any
+ * with I <= 128, and most of more than a few rows) uses none: it takes NULL with
+ * 0 bytes, one that is split answers MOE_ERR_WORKSPACE_TOO_SMALL.  Calls that
  * may overlap in time need a workspace each. */
 int moe_linear_fwd(int T, int I, int O, int dtype, int act, const void* x, const void* w, const void* bias,
                    const void* mul, const void* residual, void* z_save, void* y, void* workspace,
