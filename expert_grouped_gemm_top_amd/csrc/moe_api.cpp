@@ -311,14 +311,14 @@ int check_aligned(const char* fn, const char* name, const void* p) {
   return MOE_OK;
 }
 
-// A buffer of a call: NULL ones overlap nothing.
+// A buffer of a call: NULL and empty ones overlap nothing.
 struct Span {
   const char* name;
   const void* p;
   int64_t bytes;
 };
 bool overlap(const Span& a, const Span& b) {
-  if (a.p == nullptr || b.p == nullptr) return false;
+  if (a.p == nullptr || b.p == nullptr || a.bytes == 0 || b.bytes == 0) return false;
   const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
   return x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
 }
@@ -914,11 +914,18 @@ int moe_router_bwd_dlogits(int T, int H, int E, int dtype, const void* x, const 
   NONNULL(dlogits);
   NONNULL(dw_r);
   NONNULL(dx);
-  if ((rc = check_router_workspace(fn, T, H, E, workspace, workspace_bytes))) return rc;
+  const int es = esize_of(dtype);
+  const int64_t row = (int64_t)T * H * es, wide = (int64_t)H * E * es;
+  const Span sx{"x", x, row}, sw{"w_r", w_r, wide}, sl{"dlogits", dlogits, (int64_t)T * E * 4};
+  const Span sdw{"dw_r", dw_r, wide}, sdx{"dx", dx, row};
+  // x is read by the first product alone, so dx, which the second one writes, may lie on it
+  if ((rc = check_output(fn, sdw, {sx, sw, sl, sdx}, false)) || (rc = check_output(fn, sdx, {sw, sl}, false)) ||
+      (rc = check_workspace(fn, moe::router_workspace_bytes(T, H, E), workspace, workspace_bytes, {sx, sw, sl, sdw, sdx})))
+    return rc;
   hipStream_t s = as_stream(stream);
   return hip_status(timed(MOE_K_ROUTER_DW, s,
                           [&] {
-                            return moe::launch_router_bwd_dlogits(T, H, E, esize_of(dtype), x, w_r, dlogits, dw_r, dx,
+                            return moe::launch_router_bwd_dlogits(T, H, E, es, x, w_r, dlogits, dw_r, dx,
                                                                   dx_accumulate != 0, workspace, s);
                           }),
                     fn);

@@ -550,7 +550,9 @@ int moe_route_scored_bwd(int T, int E, int k, int score, int renormalize, float 
 
 /* The two products of moe_router_bwd for a logits' gradient that is given
  * (from moe_route_scored_bwd, or any other): dw_r = x^T dlogits and dx (+)=
- * dlogits W_r^T.  Arguments as there; dlogits [T, E] fp32 is read. */
+ * dlogits W_r^T.  Arguments as there; dlogits [T, E] fp32 is read.  dw_r, dx and
+ * the workspace share no memory with each other or the inputs, but dx may lie on
+ * x, which is read before it is written. */
 int moe_router_bwd_dlogits(int T, int H, int E, int dtype, const void* x, const void* w_r, const float* dlogits,
                            void* dw_r, void* dx, int dx_accumulate, void* workspace, size_t workspace_bytes,
                            void* stream);
