@@ -463,33 +463,28 @@ __device__ __forceinline__ void tile_product(const LinearProduct& g, int tile, i
   // acc[i][j] is row TM wm + 32 i + l32, column TN wn + 32 j + 8 (r / 4) + 4 hk + r % 4.
   constexpr int FIT = STAGES * STAGE / (BM * 4);
   constexpr int HC = FIT >= BN ? BN : (FIT >= 128 ? 128 : 64);
-  constexpr bool APART = FIT >= KG * BN;  // every group's sums in a place of their own
   constexpr int CH = HC / 4 < 16 ? HC / 4 : 16;  // chunks that trade places
   static_assert(BM * HC * 4 <= STAGES * STAGE && HC % TN == 0 && BN % HC == 0, "staging");
+  static_assert(KG == 1 || FIT >= KG * BN, "every group's sums in a place of their own");
   float* s_f = reinterpret_cast<float*>(s_dyn);
   __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's last fragment reads are done
 #pragma unroll
   for (int part = 0; part < BN / HC; ++part) {
     barrier_no_fence();  // every wave is done with the stage buffers / the previous part
+    if (TN * wn / HC == part) {
 #pragma unroll
-    for (int k2 = 0; k2 < (APART ? 1 : KG); ++k2) {  // else in turn: the first writes its sums, the others add theirs
-      if ((APART || kg == k2) && TN * wn / HC == part) {
+      for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
-          for (int j = 0; j < NJ; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int row = TM * wm + 32 * i + l32, col = TN * wn - HC * part + 32 * j + 8 * q + 4 * hk;
-              f32x4* at = (f32x4*)(s_f + ((APART ? kg * BM : 0) + row) * HC + 4 * ((col >> 2) ^ (row & (CH - 1))));
-              f32x4 v = f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-              if (k2 > 0) v += *at;
-              *at = v;
-            }
-      }
-      __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the staged values are written
-      barrier_no_fence();
+          for (int q = 0; q < 4; ++q) {
+            const int row = TM * wm + 32 * i + l32, col = TN * wn - HC * part + 32 * j + 8 * q + 4 * hk;
+            *(f32x4*)(s_f + (kg * BM + row) * HC + 4 * ((col >> 2) ^ (row & (CH - 1)))) =
+                f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+          }
     }
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the staged values are written
+    barrier_no_fence();
 #pragma unroll 2
     for (int it = tid; it < BM * HC / 8; it += 64 * NW * KG) {
       const int row = it / (HC / 8), c8 = it % (HC / 8);
@@ -497,7 +492,7 @@ __device__ __forceinline__ void tile_product(const LinearProduct& g, int tile, i
       if (m >= g.M || n >= g.N) continue;  // N is a multiple of 8: a run is all in or all out
       f32x4 lo, hi;
 #pragma unroll
-      for (int k2 = 0; k2 < (APART ? KG : 1); ++k2) {
+      for (int k2 = 0; k2 < KG; ++k2) {
         const float* at = s_f + (k2 * BM + row) * HC;
         const f32x4 l2 = *(const f32x4*)(at + 4 * ((2 * c8) ^ (row & (CH - 1))));
         const f32x4 h2 = *(const f32x4*)(at + 4 * ((2 * c8 + 1) ^ (row & (CH - 1))));
