@@ -154,7 +154,7 @@ struct LinearProduct {
   int act;
   const void *bias, *mul, *residual;
   void *z, *out;
-  int slice;    // k per slice of a split reduction, a multiple of the kernels' stage depth (>= K: not split)
+  int slice;    // k per slice of a split reduction, a multiple of 128 (>= K: not split)
   float* part;  // split: fp32 partials [slices][M][N]
 };
 

@@ -62,7 +62,10 @@ inline double pass_us(const TileCost& t, int k, int64_t groups) {
 }
 
 inline Cut cut_of(int M, int N, int K, int esize, int tile, int want) {
-  constexpr int kGrain = 128;  // slices are whole stages
+  // Whole stages of all tiles but the smallest, whose eight reduction groups take
+  // 512 k (fp32: 256) to a stage: a slice may end inside one of its stages, the
+  // rest of which is masked, and the estimate counts the k that are there.
+  constexpr int kGrain = 128;
   const TileCost& t = cost_of(tile, esize);
   Cut c{};
   c.tile = tile;

@@ -1,6 +1,5 @@
 // moe_rows.h -- device helpers of the row-wise kernels: runs of eight
-// neighbouring elements of an fp32 or bf16 row as fp32 values, and sums of
-// per-workgroup column partials.
+// neighbouring elements of an fp32 or bf16 row as fp32 values.
 #pragma once
 
 #include "moe_common.h"
