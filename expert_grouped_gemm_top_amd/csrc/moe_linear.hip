@@ -28,13 +28,12 @@ constexpr float kTanhA = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kTanhB = 0.044715f;
 
 // Logistic function and normal distribution of an activation, by the element type.
-// bf16: on the hardware's exp2 and reciprocal, exp(v) within (1.5 |v| + 2) 2^-24
-// of itself, and the distribution within 1.5e-7 (5e-5 of itself at -3, 2^-9
-// from -5.2 on, where it is below 1e-7): the library's expf, erfcf and division
-// took 7 of 28 us of a GELU product's epilogue at 4099 x 768.  fp32: those,
-// whose errors are a few 2^-24 of the result in the tails too; they cost its
-// products 0.2 to 0.7 us (4096 x 512 -> 1024 with GELU and a gate 45.5 us).
-__device__ __forceinline__ float quick_exp(float v) { return __builtin_amdgcn_exp2f(v * 1.44269504f); }
+// bf16: on the hardware's exp2 (quick_exp) and reciprocal, the distribution
+// within 1.5e-7 (5e-5 of itself at -3, 2^-9 from -5.2 on, where it is below
+// 1e-7): the library's expf, erfcf and division took 7 of 28 us of a GELU
+// product's epilogue at 4099 x 768.  fp32: those, whose errors are a few 2^-24
+// of the result in the tails too; they cost its products 0.2 to 0.7 us
+// (4096 x 512 -> 1024 with GELU and a gate 45.5 us).
 template <typename T>
 __device__ __forceinline__ float exp_of(float v) {
   return sizeof(T) == 4 ? expf(v) : quick_exp(v);

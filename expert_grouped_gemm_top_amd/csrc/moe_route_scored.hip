@@ -107,9 +107,6 @@ __device__ __forceinline__ void sort_down(uint32_t (&v)[N]) {
           }
 }
 
-// exp(v) on the hardware's exp2: off by at most (1.5 |v| + 2) 2^-24 of the result.
-__device__ __forceinline__ float quick_exp(float v) { return __builtin_amdgcn_exp2f(v * 1.44269504f); }
-
 template <int V>
 struct RouteLds {
   uint64_t value[4][4][kRow * V];  // wave, token of the wave, expert
