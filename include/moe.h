@@ -542,7 +542,9 @@ int moe_route_scored(int T, int E, int k, int score, int n_groups, int top_group
  * gradient (the selection does not pass one).  An index listed twice in a row
  * counts twice; one outside [0, E) is left out.  The differences 1 - s_j and
  * g_j - sum_i p_i g_i keep fp32's relative precision however near a score or a
- * weight is to 1 (as long as they are normal fp32 numbers).
+ * weight is to 1 (as long as they are normal fp32 numbers).  All forms but plain
+ * softmax read the selected logits only: a NaN among the others, which makes a
+ * softmax token's weights NaN, does not reach a renormalised gradient.
  * logits [T, E] fp32, topk_idx [T, k] int32, dg [T, k] fp32 (device);
  * dlogits [T, E] fp32 (device, out). */
 int moe_route_scored_bwd(int T, int E, int k, int score, int renormalize, float scale, const float* logits,

@@ -154,3 +154,30 @@ def test_a_confident_expert_listed_twice(renorm):
                 size = size + s * (extra * (1 - s) + (s * extra).sum(1, keepdims=True) * (extra == 0))
         n = steps(x, k, score, renorm) + 4
         R.within("dlogits", R.host(d), ref, 1.01 * n * HALF * size + 32 * 2.0 ** -126)
+
+
+@pytest.mark.parametrize("score,renorm", [(R.SOFTMAX, True), (R.SIGMOID, True), (R.SIGMOID, False)])
+def test_logits_that_are_not_selected_are_not_read(score, renorm):
+    """NaN and infinities among them leave the gradient as it is; at a selected one they reach that token."""
+    rng = np.random.default_rng(5)
+    T, E, k = 20, 48, 4
+    l = np.float32(rng.standard_normal((T, E)))
+    idx = np.argsort(rng.random((T, E)), axis=1)[:, :k]
+    g = np.float32(rng.standard_normal((T, k)))
+    check(l.astype(np.float64), idx, g, score, renorm, 1.0)
+    spoilt = l.copy()
+    for t in range(T):
+        spoilt[t, np.setdiff1d(np.arange(E), idx[t])[:3]] = np.nan, np.inf, -np.inf
+    spoilt[7, idx[7, 2]] = np.nan
+    out = []
+    for v in (l, spoilt):
+        d = torch.full((T, E), 7.0, device="cuda")
+        moe.moe_route_scored_bwd(torch.from_numpy(v).cuda(), torch.from_numpy(np.int32(idx)).cuda(),
+                                 torch.from_numpy(g).cuda(), d, score, renorm, 1.0)
+        torch.cuda.synchronize()
+        out.append(R.host(d))
+    others = np.arange(T) != 7
+    assert np.array_equal(out[0][others], out[1][others])
+    bad = np.isnan(out[1][7])
+    assert bad[idx[7, 2]] and (bad[idx[7]].all() if renorm else bad.sum() == 1)
+    assert not out[1][7, np.setdiff1d(np.arange(E), idx[7])].any()
