@@ -523,8 +523,9 @@ __global__ __launch_bounds__(kThreads, 2) void linear_fwd_kernel(LinearProduct g
 // that the other leaves idle: `nw` workgroups of x^T dz, `nx` of dz W^T (the
 // longer ones first), and behind them the sums of dbias' partial rows.  Both
 // products at 4099 x 2048 x 768: 46 us, in launches of their own 30 + 30; at
-// 128 x 2048 x 768 8.1 us, 8.0 + 8.4; at 8192 x 4096 x 1408 198-209 us
-// (0.90-0.95 PFLOP/s; 167 us on operands of zeros, so the chip's power bounds it).
+// 128 x 2048 x 768 8.1 us, 8.0 + 8.4; at 8192 x 4096 x 1408 220 us (0.86
+// PFLOP/s), on operands of zeros 194 us: a ninth of it goes with the power that
+// the values' switching draws.
 struct ColumnSum {
   const float* part;
   int n, cols;
