@@ -94,8 +94,9 @@ __device__ __forceinline__ void act8(int act, float (&v)[8]) {
 
 __device__ __forceinline__ float clamped(float z, float most) { return z > most ? most : (z < -most ? -most : z); }
 
-// value = act(z) and slope = act'(z) for eight values.  The slopes are 0 or 1 to
-// fp32 precision beyond |z| = 30 (SILU: 100), where their formulas would form 0 * inf.
+// value = act(z) and slope = act'(z) for eight values.  Slopes, and the factor of z
+// in the values, are 0 or 1 in fp32 beyond |z| = 30 (SILU: 110, exp(-110) is below
+// the smallest subnormal), where the slopes' formulas would form 0 * inf.
 template <typename T>
 __device__ __forceinline__ void act8_both(int act, const float (&z)[8], float (&value)[8], float (&slope)[8]) {
   switch (act) {
@@ -126,7 +127,7 @@ __device__ __forceinline__ void act8_both(int act, const float (&z)[8], float (&
     case kActSilu:
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float c = clamped(z[j], 100.0f);
+        const float c = clamped(z[j], 110.0f);
         const Logistic u = logistic<T>(c);
         value[j] = z[j] * u.s;
         slope[j] = u.s * (1.0f + c * u.rest);

@@ -106,3 +106,28 @@ def test_slopes_and_values_of_the_backward(act):
     for t in range(2):
         R.within("dmul", R.host(dm)[t], ref, 1.01 * n * HALF * np.abs(ref) + small)
         R.within("dz", R.host(dz)[t], slo, 1.01 * bound + small * (1 + z * z))
+
+
+@pytest.mark.parametrize("act", range(1, 5))
+def test_far_out(act):
+    """Pre-activations from 200 in size to the largest: values z and 0, slopes 1 and 0, to the last bit (what is
+    left of them is below exp(-200), far below the smallest fp32 number, also times the largest)."""
+    note(f"fp32 activation {act} far out")
+    top = float(np.finfo(np.float32).max)
+    z = np.array([v * s for v in (200.0, 1e4, 1e15, 1e30, 3e38, top, 1e38, 250.0) for s in (1, -1)])
+    z = np.float32(z).astype(np.float64)
+    n = len(z)
+    ws = torch.empty(moe.moe_linear_workspace_bytes(2, 8, n, torch.float32), dtype=torch.uint8, device="cuda")
+    x, w = np.zeros((2, 8)), np.zeros((8, n))
+    x[:, 0], w[0] = 1.0, z
+    y = torch.full((2, n), 7.0, device="cuda")
+    moe.moe_linear_fwd(R.dev(x, "f32"), R.dev(w, "f32"), None, y, act, workspace=ws)
+    one = torch.ones(2, n, device="cuda")
+    dz, dm = torch.full_like(one, 7.0), torch.full_like(one, 7.0)
+    moe.moe_linear_bwd(torch.zeros(2, 8, device="cuda"), torch.zeros(8, n, device="cuda"), one, dz, None, None, act=act,
+                       z=R.dev(np.tile(z, (2, 1)), "f32"), mul=one, dmul=dm, workspace=ws)
+    torch.cuda.synchronize()
+    for t in range(2):
+        assert np.array_equal(R.host(y)[t], np.maximum(z, 0)), "y"
+        assert np.array_equal(R.host(dm)[t], np.maximum(z, 0)), "dmul"
+        assert np.array_equal(R.host(dz)[t], (z > 0) * 1.0), "dz"
