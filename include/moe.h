@@ -614,10 +614,10 @@ size_t moe_linear_workspace_bytes(int T, int I, int O, int dtype);
  * experts' sum a shared expert's output joins it.
  * I and O multiples of 8, at most 2^20, T at most 2^30, T I and T O below 2^40,
  * pointers 16-byte aligned, workspace (apart from all other buffers) of at
- * least moe_linear_workspace_bytes.  A forward whose reduction is not split (any
- * with I <= 128, and most of more than a few rows) uses none: it takes NULL with
- * 0 bytes, one that is split answers MOE_ERR_WORKSPACE_TOO_SMALL.  Calls that
- * may overlap in time need a workspace each. */
+ * least moe_linear_workspace_bytes.  A forward whose reduction is not split
+ * (never with I <= 128; else by T and O) uses none: it takes NULL with 0 bytes,
+ * one that is split answers MOE_ERR_WORKSPACE_TOO_SMALL.  Calls that may overlap
+ * in time need a workspace each. */
 int moe_linear_fwd(int T, int I, int O, int dtype, int act, const void* x, const void* w, const void* bias,
                    const void* mul, const void* residual, void* z_save, void* y, void* workspace,
                    size_t workspace_bytes, void* stream);
