@@ -10,7 +10,9 @@
 #include <cstdio>
 #include <cstring>
 #include <initializer_list>
+#include <new>
 #include <string>
+#include <vector>
 
 #include "moe.h"
 #include "moe_launch.h"
@@ -368,6 +370,30 @@ int check_linear(const char* fn, int T, int I, int O, int dtype, int act) {
   return MOE_OK;
 }
 
+int check_balance(const char* fn, int T, int E, int k, int n_seq, int score, float alpha, const int32_t* seq_offsets) {
+  int rc = check_routing_dims(fn, T, E, k);
+  if (rc || (rc = check_score(fn, score, 1.0f))) return rc;
+  REQUIRE(std::isfinite(alpha), MOE_ERR_INVALID_ARGUMENT, "%s: alpha must be finite", fn);
+  REQUIRE(n_seq >= 1, MOE_ERR_INVALID_ARGUMENT, "%s: n_seq=%d must be >= 1", fn, n_seq);
+  REQUIRE(n_seq <= moe::kBalanceMaxSeqs, MOE_ERR_UNSUPPORTED, "%s: n_seq=%d exceeds %d", fn, n_seq,
+          moe::kBalanceMaxSeqs);
+  REQUIRE(seq_offsets != nullptr || n_seq == 1, MOE_ERR_INVALID_ARGUMENT, "%s: %d sequences without seq_offsets", fn,
+          n_seq);
+  return MOE_OK;
+}
+
+// No two of the spans share memory.
+int check_apart(const char* fn, std::vector<Span>& spans) {
+  std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return (uintptr_t)a.p < (uintptr_t)b.p; });
+  const Span* last = nullptr;
+  for (const Span& b : spans) {
+    if (b.p == nullptr || b.bytes == 0) continue;
+    if (last != nullptr) REQUIRE(!overlap(*last, b), MOE_ERR_INVALID_ARGUMENT, "%s: %s overlaps %s", fn, last->name, b.name);
+    last = &b;
+  }
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -391,7 +417,8 @@ int64_t moe_launch_count(void) { return moe::g_launches; }
 
 int moe_profile_kernel(int kernel, void* start_event, void* stop_event) {
   const char* fn = "moe_profile_kernel";
-  REQUIRE(kernel >= 0 && kernel < MOE_K_COUNT, MOE_ERR_INVALID_ARGUMENT, "%s: unknown kernel %d", fn, kernel);
+  REQUIRE(kernel >= 0 && kernel < MOE_K_COUNT && kernel != 16, MOE_ERR_INVALID_ARGUMENT, "%s: unknown kernel %d", fn,
+          kernel);
   REQUIRE((start_event == nullptr) == (stop_event == nullptr), MOE_ERR_INVALID_ARGUMENT,
           "%s: give both events or neither", fn);
   g_armed[kernel].start = reinterpret_cast<hipEvent_t>(start_event);
@@ -1084,6 +1111,167 @@ int moe_linear_bwd(int T, int I, int O, int dtype, int act, const void* x, const
                                                           workspace, s);
                           }),
                     fn);
+}
+
+size_t moe_balance_loss_workspace_bytes(int T, int E, int n_seq) {
+  if (T < 1 || E < 1 || E > moe::kMaxExpertsHost || n_seq < 1 || n_seq > moe::kBalanceMaxSeqs) return 0;
+  return moe::balance_workspace_bytes(T, E, n_seq);
+}
+
+int moe_balance_loss_fwd(int T, int E, int k, int n_seq, int score, float alpha, const float* logits,
+                         const int32_t* topk_idx, const int32_t* seq_offsets, int32_t* counts, float* mean_p,
+                         float* loss, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_balance_loss_fwd";
+  int rc = check_balance(fn, T, E, k, n_seq, score, alpha, seq_offsets);
+  if (rc) return rc;
+  NONNULL(logits);
+  NONNULL(topk_idx);
+  NONNULL(counts);
+  NONNULL(mean_p);
+  NONNULL(loss);
+  const int64_t per_seq = (int64_t)n_seq * E * 4;
+  const Span sl{"logits", logits, (int64_t)T * E * 4}, si{"topk_idx", topk_idx, (int64_t)T * k * 4};
+  const Span so{"seq_offsets", seq_offsets, ((int64_t)n_seq + 1) * 4}, sc{"counts", counts, per_seq};
+  const Span sp{"mean_p", mean_p, per_seq}, ss{"loss", loss, 4};
+  if ((rc = check_output(fn, sc, {sl, si, so, sp, ss}, false)) || (rc = check_output(fn, sp, {sl, si, so, ss}, false)) ||
+      (rc = check_output(fn, ss, {sl, si, so}, false)) ||
+      (rc = check_workspace(fn, moe::balance_workspace_bytes(T, E, n_seq), workspace, workspace_bytes,
+                            {sl, si, so, sc, sp, ss})))
+    return rc;
+  const moe::BalanceArgs g{T, E, k, n_seq, score, alpha, logits, topk_idx, seq_offsets};
+  hipStream_t s = as_stream(stream);
+  return hip_status(
+      timed(MOE_K_BALANCE, s, [&] { return moe::launch_balance_fwd(g, counts, mean_p, loss, workspace, s); }), fn);
+}
+
+int moe_balance_loss_bwd(int T, int E, int k, int n_seq, int score, float alpha, const float* logits,
+                         const int32_t* counts, const int32_t* seq_offsets, const float* dloss, const float* dl_add,
+                         float* dlogits, void* stream) {
+  const char* fn = "moe_balance_loss_bwd";
+  int rc = check_balance(fn, T, E, k, n_seq, score, alpha, seq_offsets);
+  if (rc) return rc;
+  NONNULL(logits);
+  NONNULL(counts);
+  NONNULL(dlogits);
+  const int64_t row = (int64_t)T * E * 4;
+  const Span out{"dlogits", dlogits, row};
+  if ((rc = check_output(fn, out, {{"dl_add", dl_add, row}}, true)) ||
+      (rc = check_output(fn, out,
+                         {{"logits", logits, row}, {"counts", counts, (int64_t)n_seq * E * 4},
+                          {"seq_offsets", seq_offsets, ((int64_t)n_seq + 1) * 4}, {"dloss", dloss, 4}},
+                         false)))
+    return rc;
+  const moe::BalanceArgs g{T, E, k, n_seq, score, alpha, logits, nullptr, seq_offsets};
+  hipStream_t s = as_stream(stream);
+  return hip_status(
+      timed(MOE_K_BALANCE, s, [&] { return moe::launch_balance_bwd(g, counts, dloss, dl_add, dlogits, s); }), fn);
+}
+
+size_t moe_adamw_plan_bytes(int n) {
+  if (n < 1 || n > moe::kAdamwMaxTensors) return 0;
+  return moe::adamw_plan_bytes(n);
+}
+
+int moe_adamw_plan(int n, const moe_adamw_tensor* tensors, int dtype, int state_bits, void* plan, size_t plan_bytes) {
+  const char* fn = "moe_adamw_plan";
+  REQUIRE(n >= 1, MOE_ERR_INVALID_ARGUMENT, "%s: n=%d must be >= 1", fn, n);
+  REQUIRE(n <= moe::kAdamwMaxTensors, MOE_ERR_UNSUPPORTED, "%s: n=%d exceeds %d", fn, n, moe::kAdamwMaxTensors);
+  int rc = check_dtype(fn, dtype);
+  if (rc) return rc;
+  REQUIRE(state_bits == 8 || state_bits == 32, MOE_ERR_INVALID_ARGUMENT, "%s: state_bits=%d is neither 8 nor 32", fn,
+          state_bits);
+  NONNULL(tensors);
+  NONNULL(plan);
+  REQUIRE(plan_bytes >= moe::adamw_plan_bytes(n), MOE_ERR_WORKSPACE_TOO_SMALL, "%s: plan of %zu bytes, %zu needed", fn,
+          plan_bytes, moe::adamw_plan_bytes(n));
+  const int es = esize_of(dtype);
+  const bool small = state_bits == 8;
+  try {
+    std::vector<Span> spans;
+    std::vector<moe::AdamwEntry> entries;
+    int64_t blocks = 0;
+    bool master = false, any = false;
+    for (int i = 0; i < n; ++i) {
+      const moe_adamw_tensor& t = tensors[i];
+      REQUIRE(t.numel >= 0, MOE_ERR_INVALID_ARGUMENT, "%s: tensor %d has %lld elements", fn, i, (long long)t.numel);
+      REQUIRE(t.numel < (int64_t)1 << 40, MOE_ERR_UNSUPPORTED, "%s: tensor %d has %lld elements", fn, i,
+              (long long)t.numel);
+      REQUIRE(std::isfinite(t.weight_decay) && t.weight_decay >= 0.0, MOE_ERR_INVALID_ARGUMENT,
+              "%s: tensor %d: weight_decay must be finite and not negative", fn, i);
+      const int64_t n_blocks = (t.numel + moe::kAdamwBlock - 1) / moe::kAdamwBlock;
+      blocks += n_blocks;
+      entries.push_back({t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.master, t.numel, 0, t.weight_decay});
+      if (t.numel == 0) continue;
+      REQUIRE(t.param != nullptr && t.grad != nullptr && t.m != nullptr && t.v != nullptr, MOE_ERR_INVALID_ARGUMENT,
+              "%s: tensor %d: param, grad, m and v must not be NULL", fn, i);
+      REQUIRE((t.m_scale != nullptr) == small && (t.v_scale != nullptr) == small, MOE_ERR_INVALID_ARGUMENT,
+              "%s: tensor %d: m_scale and v_scale are given with 8-bit moments, and only then", fn, i);
+      REQUIRE(!any || master == (t.master != nullptr), MOE_ERR_INVALID_ARGUMENT,
+              "%s: tensor %d: all tensors of a plan have a master, or none", fn, i);
+      REQUIRE(t.master == nullptr || dtype == MOE_BF16, MOE_ERR_INVALID_ARGUMENT,
+              "%s: tensor %d: a master beside an fp32 param", fn, i);
+      master = t.master != nullptr;
+      any = true;
+      const int64_t state = t.numel * (small ? 1 : 4);
+      const Span own[] = {{"param", t.param, t.numel * es}, {"grad", t.grad, t.numel * es},
+                          {"m", t.m, state}, {"v", t.v, state}, {"master", t.master, t.numel * 4}};
+      for (const Span& b : own) {
+        if ((rc = check_aligned(fn, b.name, b.p))) return rc;
+        spans.push_back(b);
+      }
+      for (const Span& b : {Span{"m_scale", t.m_scale, n_blocks * 4}, Span{"v_scale", t.v_scale, n_blocks * 4}}) {
+        REQUIRE(((uintptr_t)b.p & 3) == 0, MOE_ERR_INVALID_ARGUMENT, "%s: %s must be 4-byte aligned", fn, b.name);
+        spans.push_back(b);
+      }
+    }
+    REQUIRE(blocks < (int64_t)1 << 40, MOE_ERR_UNSUPPORTED, "%s: too many elements", fn);
+    if ((rc = check_apart(fn, spans))) return rc;
+    moe::adamw_make_plan(n, entries.data(), es, small, master, plan);
+  } catch (const std::bad_alloc&) {
+    return fail(MOE_ERR_INVALID_ARGUMENT, "%s: out of host memory", fn);
+  }
+  return MOE_OK;
+}
+
+int moe_adamw_step(const void* plan, const void* plan_device, int32_t* counter, const float* lr, double beta1,
+                   double beta2, double eps, const float* grad_scale, uint32_t seed, void* stream) {
+  const char* fn = "moe_adamw_step";
+  NONNULL(plan);
+  NONNULL(plan_device);
+  NONNULL(counter);
+  NONNULL(lr);
+  REQUIRE(moe::adamw_is_plan(plan), MOE_ERR_INVALID_ARGUMENT, "%s: plan is not one of moe_adamw_plan's", fn);
+  int rc = check_aligned(fn, "plan_device", plan_device);
+  if (rc) return rc;
+  REQUIRE(beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0, MOE_ERR_INVALID_ARGUMENT,
+          "%s: beta1 and beta2 must be in [0, 1)", fn);
+  REQUIRE(eps >= 0.0 && std::isfinite(eps), MOE_ERR_INVALID_ARGUMENT, "%s: eps must be finite and not negative", fn);
+  const moe::AdamwStep a{counter, lr, grad_scale, beta1, beta2, eps, seed};
+  hipStream_t s = as_stream(stream);
+  return hip_status(timed(MOE_K_ADAMW, s, [&] { return moe::launch_adamw(plan, plan_device, a, s); }), fn);
+}
+
+int moe_adamw_moments(int64_t numel, const uint8_t* m, const uint8_t* v, const float* m_scale, const float* v_scale,
+                      float* m_out, float* v_out, void* stream) {
+  const char* fn = "moe_adamw_moments";
+  REQUIRE(numel >= 1, MOE_ERR_INVALID_ARGUMENT, "%s: numel=%lld must be >= 1", fn, (long long)numel);
+  REQUIRE(numel < (int64_t)1 << 40, MOE_ERR_UNSUPPORTED, "%s: numel=%lld is too large", fn, (long long)numel);
+  NONNULL(m);
+  NONNULL(v);
+  NONNULL(m_scale);
+  NONNULL(v_scale);
+  NONNULL(m_out);
+  NONNULL(v_out);
+  const int64_t scales = (numel + moe::kAdamwBlock - 1) / moe::kAdamwBlock * 4;
+  const Span sm{"m", m, numel}, sv{"v", v, numel}, sms{"m_scale", m_scale, scales}, svs{"v_scale", v_scale, scales};
+  const Span smo{"m_out", m_out, numel * 4}, svo{"v_out", v_out, numel * 4};
+  int rc;
+  if ((rc = check_aligned(fn, "m", m)) || (rc = check_aligned(fn, "v", v)) || (rc = check_aligned(fn, "m_out", m_out)) ||
+      (rc = check_aligned(fn, "v_out", v_out)) || (rc = check_output(fn, smo, {sm, sv, sms, svs, svo}, false)) ||
+      (rc = check_output(fn, svo, {sm, sv, sms, svs}, false)))
+    return rc;
+  hipStream_t s = as_stream(stream);
+  return hip_status(moe::launch_adamw_moments(numel, m, v, m_scale, v_scale, m_out, v_out, s), fn);
 }
 
 }  // extern "C"

@@ -254,6 +254,46 @@ hipError_t launch_linear_bwd(const LinearArgs& g, int esize, const void* z, cons
                              const void* dx_add, void* dx, void* dw, void* dbias, void* dmul, void* ws,
                              hipStream_t stream);
 
+// The balance loss over the sequences [offsets[s], offsets[s + 1]) of a batch (NULL: one, all T tokens).
+struct BalanceArgs {
+  int T, E, k, n_seq;
+  int score;  // 0 softmax, 1 sigmoid
+  float alpha;
+  const float* logits;
+  const int32_t* idx;
+  const int32_t* offsets;
+};
+constexpr int kBalanceMaxSeqs = 65535;
+size_t balance_workspace_bytes(int T, int E, int n_seq);
+hipError_t launch_balance_fwd(const BalanceArgs& g, int32_t* counts, float* mean_p, float* loss, void* ws,
+                              hipStream_t stream);
+hipError_t launch_balance_bwd(const BalanceArgs& g, const int32_t* counts, const float* dloss, const float* dl_add,
+                              float* dlogits, hipStream_t stream);
+
+constexpr int kAdamwBlock = 256;   // elements that share a scale of 8-bit moments
+constexpr int kAdamwChunk = 2048;  // elements of one pass of a workgroup
+constexpr int kAdamwMaxTensors = 1 << 20;
+struct AdamwEntry {
+  void* param;
+  const void* grad;
+  void *m, *v;
+  float *m_scale, *v_scale, *master;
+  int64_t numel, first;  // first: blocks of the tensors in front
+  double decay;
+};
+struct AdamwStep {
+  int32_t* counter;
+  const float *lr, *grad_scale;
+  double beta1, beta2, eps;
+  uint32_t seed;
+};
+size_t adamw_plan_bytes(int n);
+void adamw_make_plan(int n, const AdamwEntry* entries, int esize, bool small, bool master, void* plan);
+bool adamw_is_plan(const void* plan);
+hipError_t launch_adamw_moments(int64_t numel, const uint8_t* m, const uint8_t* v, const float* m_scale,
+                                const float* v_scale, float* m_out, float* v_out, hipStream_t stream);
+hipError_t launch_adamw(const void* plan, const void* plan_device, const AdamwStep& a, hipStream_t stream);
+
 hipError_t launch_fill_i32(int32_t* a, int64_t n, int32_t v, hipStream_t stream);
 hipError_t launch_compact(int64_t N, int E, int cap, const int32_t* counts, const int32_t* offsets, const int32_t* perm,
                           const float* score, int32_t* kept_counts, int32_t* kept_offsets, int32_t* kept_perm,

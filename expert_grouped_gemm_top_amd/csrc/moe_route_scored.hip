@@ -6,13 +6,13 @@
 //   idx = the k largest c (ties: lower index),  w = scale s_j [/ sum s_i].
 #include "moe_common.h"
 #include "moe_launch.h"
+#include "moe_rows.h"
 
 namespace moe {
 
 namespace {
 
 constexpr int kMaxGroups = 16;
-constexpr int kRow = 16;  // lanes per token: a DPP row
 
 struct RouteArgs {
   int T, E, k;
@@ -27,31 +27,6 @@ struct RouteArgs {
   int per_lane;  // experts per lane, neighbours: ceil(E / 16)
   int on_lanes;  // every group is a whole number of lanes
 };
-
-template <int N>
-__device__ __forceinline__ int ror(int v) { return __builtin_amdgcn_update_dpp(0, v, 0x120 + N, 0xf, 0xf, false); }
-template <int N>
-__device__ __forceinline__ float ror(float v) { return __int_as_float(ror<N>(__float_as_int(v))); }
-
-// Over the 16 lanes of a token; every lane gets the same bits.
-__device__ __forceinline__ float row_max(float v) {
-  v = fmaxf(v, ror<8>(v));
-  v = fmaxf(v, ror<4>(v));
-  v = fmaxf(v, ror<2>(v));
-  return fmaxf(v, ror<1>(v));
-}
-__device__ __forceinline__ float row_add(float v) {
-  v += ror<8>(v);
-  v += ror<4>(v);
-  v += ror<2>(v);
-  return v + ror<1>(v);
-}
-__device__ __forceinline__ uint32_t row_max(uint32_t v) {
-  v = max(v, (uint32_t)ror<8>((int)v));
-  v = max(v, (uint32_t)ror<4>((int)v));
-  v = max(v, (uint32_t)ror<2>((int)v));
-  return max(v, (uint32_t)ror<1>((int)v));
-}
 
 // Key whose order as an unsigned number is the order of a 64-bit value: -0
 // equals +0, every NaN is the largest key, and no value has key 0.

@@ -1,5 +1,6 @@
 // moe_rows.h -- device helpers of the row-wise kernels: runs of eight
-// neighbouring elements of an fp32 or bf16 row as fp32 values.
+// neighbouring elements of an fp32 or bf16 row as fp32 values, and reductions
+// over the 16 lanes that share a token.
 #pragma once
 
 #include "moe_common.h"
@@ -61,7 +62,36 @@ struct Raw8<uint16_t> {
   __device__ __forceinline__ void load(const uint16_t* p) { v = *(const u32x4*)p; }
   __device__ __forceinline__ float get(int j) const { return (j & 1) ? bf_hi(v[j >> 1]) : bf_lo(v[j >> 1]); }
 };
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ float load1(const uint16_t* p) { return bf2f(*p); }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = (uint16_t)f2bf(v); }
+
+constexpr int kRow = 16;  // lanes per token: a DPP row
+
+template <int N>
+__device__ __forceinline__ int ror(int v) { return __builtin_amdgcn_update_dpp(0, v, 0x120 + N, 0xf, 0xf, false); }
+template <int N>
+__device__ __forceinline__ float ror(float v) { return __int_as_float(ror<N>(__float_as_int(v))); }
+
+// Over the 16 lanes of a token; every lane gets the same bits.
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, ror<8>(v));
+  v = fmaxf(v, ror<4>(v));
+  v = fmaxf(v, ror<2>(v));
+  return fmaxf(v, ror<1>(v));
+}
+__device__ __forceinline__ float row_add(float v) {
+  v += ror<8>(v);
+  v += ror<4>(v);
+  v += ror<2>(v);
+  return v + ror<1>(v);
+}
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+  v = max(v, (uint32_t)ror<8>((int)v));
+  v = max(v, (uint32_t)ror<4>((int)v));
+  v = max(v, (uint32_t)ror<2>((int)v));
+  return max(v, (uint32_t)ror<1>((int)v));
+}
 
 }  // namespace moe

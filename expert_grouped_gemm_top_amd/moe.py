@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import typing
 
 import torch
 
@@ -68,6 +69,13 @@ _SIGS = {
     "moe_linear_workspace_bytes": ([_i] * 4, _sz),
     "moe_linear_fwd": ([_i] * 5 + [_vp] * 8 + [_sz, _vp], _i),
     "moe_linear_bwd": ([_i] * 5 + [_vp] * 12 + [_sz, _vp], _i),
+    "moe_balance_loss_workspace_bytes": ([_i] * 3, _sz),
+    "moe_balance_loss_fwd": ([_i] * 5 + [_f] + [_vp] * 7 + [_sz, _vp], _i),
+    "moe_balance_loss_bwd": ([_i] * 5 + [_f] + [_vp] * 7, _i),
+    "moe_adamw_plan_bytes": ([_i], _sz),
+    "moe_adamw_plan": ([_i, _vp, _i, _i, _vp, _sz], _i),
+    "moe_adamw_moments": ([_i64] + [_vp] * 7, _i),
+    "moe_adamw_step": ([_vp] * 4 + [_d] * 3 + [_vp, ctypes.c_uint32, _vp], _i),
 }
 
 
@@ -636,3 +644,111 @@ def moe_linear_bwd(x, w, dy, dz, dx, dw, dbias=None, act: int = MOE_ACT_NONE, z=
         _addr(mul, "mul", out, d, dev), _need(dy, "dy", out, d, dev), _addr(dz, "dz", out, d, dev),
         _addr(dx_add, "dx_add", into, d, dev), _addr(dx, "dx", into, d, dev), _addr(dw, "dw", (I, O), d, dev),
         _addr(dbias, "dbias", (O,), d, dev), _addr(dmul, "dmul", out, d, dev), ws, ws_bytes, _queue(stream, dev)))
+
+
+# ---- from the block's output to the next step's weights -----------------------------
+
+def moe_balance_loss_workspace_bytes(T: int, E: int, n_seq: int = 1) -> int:
+    return int(lib().moe_balance_loss_workspace_bytes(T, E, n_seq))
+
+
+def moe_balance_loss_fwd(logits, topk_idx, counts, mean_p, loss, workspace=None, score: int = MOE_SCORE_SOFTMAX,
+                         alpha: float = 1.0, seq_offsets=None, stream=None):
+    """counts and mean_p [n_seq, E] and loss [1] of the routers' balance loss;
+    seq_offsets [n_seq + 1] int32, None: one sequence of all rows."""
+    dev = _device(logits, "logits")
+    T, E = _rows(logits, "logits")
+    k = _rows(topk_idx, "topk_idx")[1]
+    S = _rows(counts, "counts")[0]
+    ws, ws_bytes = _space(workspace, dev)
+    _check(lib().moe_balance_loss_fwd(
+        T, E, k, S, score, alpha, _need(logits, "logits", (T, E), F32, dev), _need(topk_idx, "topk_idx", (T, k), I32, dev),
+        _addr(seq_offsets, "seq_offsets", (S + 1,), I32, dev), _need(counts, "counts", (S, E), I32, dev),
+        _need(mean_p, "mean_p", (S, E), F32, dev), _need(loss, "loss", (1,), F32, dev), ws, ws_bytes, _queue(stream, dev)))
+
+
+def moe_balance_loss_bwd(logits, counts, dlogits, k: int, score: int = MOE_SCORE_SOFTMAX, alpha: float = 1.0,
+                         seq_offsets=None, dloss=None, dl_add=None, stream=None):
+    """dlogits of the balance loss times dloss [1] (None: 1) [+ dl_add, which may be dlogits]."""
+    dev = _device(logits, "logits")
+    T, E = rows = _rows(logits, "logits")
+    S = _rows(counts, "counts")[0]
+    _check(lib().moe_balance_loss_bwd(
+        T, E, k, S, score, alpha, _need(logits, "logits", rows, F32, dev), _need(counts, "counts", (S, E), I32, dev),
+        _addr(seq_offsets, "seq_offsets", (S + 1,), I32, dev), _addr(dloss, "dloss", (1,), F32, dev),
+        _addr(dl_add, "dl_add", rows, F32, dev), _need(dlogits, "dlogits", rows, F32, dev), _queue(stream, dev)))
+
+
+class AdamWTensor(typing.NamedTuple):
+    """One tensor of an AdamW step: param and grad (fp32 or bf16), the moments m and
+    v (fp32, or uint8 codes with their scales of one fp32 for each 256 elements),
+    an fp32 master of a bf16 param, and the weight decay.  Any shapes, contiguous."""
+    param: torch.Tensor
+    grad: torch.Tensor
+    m: torch.Tensor
+    v: torch.Tensor
+    m_scale: torch.Tensor | None = None
+    v_scale: torch.Tensor | None = None
+    master: torch.Tensor | None = None
+    weight_decay: float = 0.0
+
+
+class _AdamWEntry(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("param", "grad", "m", "v", "m_scale", "v_scale", "master")] + [("numel", _i64), ("weight_decay", _d)]
+
+
+class AdamWPlan:
+    """A step's tensors (AdamWTensor each) laid out once for moe_adamw_step, on the
+    host and on the current device.  Holds the tensors; they must stay where they are."""
+
+    def __init__(self, tensors):
+        self.tensors = tensors = [AdamWTensor(*t) for t in tensors]
+        if not tensors:
+            raise MoeError("a plan needs a tensor")
+        self.device_index = dev = _device(tensors[0].param, "param")
+        d, small = tensors[0].param.dtype, tensors[0].m.dtype == torch.uint8
+        dt, state = _dt(tensors[0].param), torch.uint8 if small else F32
+        entries = (_AdamWEntry * len(tensors))()
+        for e, t in zip(entries, tensors):
+            n = t.param.numel()
+            if (t.m_scale is None or t.v_scale is None) == small:
+                raise MoeError("m_scale and v_scale are given with 8-bit moments, and only then")
+            for name, dtype, numel in (("param", d, n), ("grad", d, n), ("m", state, n), ("v", state, n),
+                                       ("m_scale", F32, -(-n // 256)), ("v_scale", F32, -(-n // 256)), ("master", F32, n)):
+                x = getattr(t, name)
+                p = _ptr(x, name, dtype, allow_none=name in ("m_scale", "v_scale", "master"))
+                if x is not None and x.numel() != numel:
+                    raise MoeError(f"{name} holds {x.numel()} elements, needs {numel}")
+                if x is not None and x.get_device() != dev:
+                    raise MoeError(f"{name} is on {x.device} in a plan on the current device cuda:{dev}")
+                setattr(e, name, p)
+            e.numel, e.weight_decay = n, t.weight_decay
+        size = int(lib().moe_adamw_plan_bytes(len(tensors)))
+        if size == 0:
+            raise MoeError(f"a plan of {len(tensors)} tensors is too large")
+        self.host = torch.zeros(size, dtype=torch.uint8)
+        _check(lib().moe_adamw_plan(len(tensors), entries, dt, 8 if small else 32, self.host.data_ptr(), size))
+        self.on_device = self.host.to(torch.device("cuda", dev))
+
+
+def moe_adamw_step(plan: AdamWPlan, counter, lr, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+                   grad_scale=None, seed: int = 0, stream=None):
+    """One step over the plan's tensors; counter [2] int32 counts the steps (zeros
+    before the first), lr [1] and grad_scale [1] fp32 (None: 1) on the device."""
+    dev = _device(counter, "counter")
+    if plan.device_index != dev:
+        raise MoeError(f"a plan of device cuda:{plan.device_index} in a call on the current device cuda:{dev}")
+    _check(lib().moe_adamw_step(
+        plan.host.data_ptr(), plan.on_device.data_ptr(), _need(counter, "counter", (2,), I32, dev),
+        _need(lr, "lr", (1,), F32, dev), beta1, beta2, eps, _addr(grad_scale, "grad_scale", (1,), F32, dev),
+        seed & 0xffffffff, _queue(stream, dev)))
+
+
+def moe_adamw_moments(m, v, m_scale, v_scale, m_out, v_out, stream=None):
+    """The moments that 8-bit codes stand for, in fp32 tensors of the codes' shape."""
+    dev = _device(m, "m")
+    n, blocks = m.numel(), (-(-m.numel() // 256),)
+    _check(lib().moe_adamw_moments(
+        n, _need(m, "m", m.shape, torch.uint8, dev), _need(v, "v", m.shape, torch.uint8, dev),
+        _need(m_scale, "m_scale", blocks, F32, dev), _need(v_scale, "v_scale", blocks, F32, dev),
+        _need(m_out, "m_out", m.shape, F32, dev), _need(v_out, "v_out", m.shape, F32, dev), _queue(stream, dev)))

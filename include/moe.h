@@ -38,6 +38,13 @@
  *   moe_linear_fwd, moe_linear_bwd          a dense product with bias, activation,
  *                           gate and residual in its epilogue (shared experts)
  *
+ * From the block's output to the next step's weights:
+ *
+ *   moe_balance_loss_fwd, moe_balance_loss_bwd  the routers' balance loss, counts
+ *                           per expert, and the logits' gradient
+ *   moe_adamw_plan, moe_adamw_step, moe_adamw_moments  AdamW over many tensors at
+ *                           once, moments of 32 or 8 bits, and those read back
+ *
  * Conventions for every call:
  *  - Pointers marked (device) are device pointers owned by the caller; the
  *    library allocates no memory and keeps no pointer after a call returns
@@ -114,6 +121,9 @@ int moe_abi_version(void);
  *   moe_route_scored, moe_route_scored_bwd, moe_layernorm_fwd  1
  *   moe_layernorm_bwd                       2
  *   moe_linear_fwd                          1, plus 1 when its reduction is split
+ *   moe_balance_loss_fwd                    1 for one sequence of T <= 256, else 2
+ *   moe_balance_loss_bwd, moe_adamw_step,
+ *   moe_adamw_moments                       1
  *   moe_linear_bwd                          1 for dz or dbias (0 without activation, gate and
  *                                           dbias), 1 for the products and the sum of dbias,
  *                                           plus 1 when a product is split
@@ -138,7 +148,10 @@ typedef enum moe_kernel {
   MOE_K_LAYERNORM = 13,    /* moe_layernorm_fwd, moe_layernorm_bwd */
   MOE_K_LINEAR_FWD = 14,   /* moe_linear_fwd */
   MOE_K_LINEAR_BWD = 15,   /* moe_linear_bwd */
-  MOE_K_COUNT = 16
+  /* 16 names no kernel */
+  MOE_K_BALANCE = 17,      /* moe_balance_loss_fwd, moe_balance_loss_bwd */
+  MOE_K_ADAMW = 18,        /* moe_adamw_step */
+  MOE_K_COUNT = 19
 } moe_kernel;
 
 /* Profiling hook.  Arms a one-shot request on the calling thread: the next
@@ -636,6 +649,97 @@ int moe_linear_fwd(int T, int I, int O, int dtype, int act, const void* x, const
 int moe_linear_bwd(int T, int I, int O, int dtype, int act, const void* x, const void* w, const void* z,
                    const void* mul, const void* dy, void* dz, const void* dx_add, void* dx, void* dw, void* dbias,
                    void* dmul, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- from the block's output to the next step's weights ----------------------- */
+
+/* Workspace (device bytes) of moe_balance_loss_fwd: the workgroups' partial sums
+ * (0 where one workgroup does it all).  Host-only. */
+size_t moe_balance_loss_workspace_bytes(int T, int E, int n_seq);
+
+/* The routers' balance loss.  Row t's shares p_te are the softmax over all E
+ * logits, or the sigmoids divided by their sum; sequence s holds the rows
+ * [seq_offsets[s], seq_offsets[s + 1]) (seq_offsets NULL: n_seq = 1, all T rows),
+ * n_s of them, N in all sequences:
+ *   counts[s, e] = how often topk_idx lists e in sequence s
+ *   mean_p[s, e] = sum_{t in s} p_te / n_s
+ *   loss = alpha E / (k N) sum_s sum_e counts[s, e] mean_p[s, e]
+ * that is alpha for perfect balance, each sequence by its tokens.  Rows in no
+ * sequence (padding) count nowhere; an empty sequence has counts and means 0; an
+ * index outside [0, E) is left out.  An expert whose logit is -inf has share 0,
+ * a row of such experts shares 0 throughout; a NaN makes its row's shares NaN.
+ * logits [T, E] fp32, topk_idx [T, k], seq_offsets [n_seq + 1] int32 (device, not
+ * descending; what lies outside [0, T] is cut off); counts [n_seq, E] int32,
+ * mean_p [n_seq, E] and loss [1] fp32 (device, out).  n_seq <= 65535.  Calls that
+ * may overlap in time need a workspace each. */
+int moe_balance_loss_fwd(int T, int E, int k, int n_seq, int score, float alpha, const float* logits,
+                         const int32_t* topk_idx, const int32_t* seq_offsets, int32_t* counts, float* mean_p,
+                         float* loss, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Its gradient, the counts held fixed (they are piecewise constant):
+ *   dl_te = dloss alpha E / (k N n_s) p_te (c_se - sum_j p_tj c_sj)   [softmax]
+ *           the same times 1 - sigmoid(l_te)                          [sigmoid]
+ *   dlogits = dl [+ dl_add]
+ * and dl = 0 for rows in no sequence.  The difference keeps fp32's precision
+ * however near a share is to 1.  dloss [1] fp32 (device) or NULL for 1; dl_add
+ * [T, E] or NULL (e.g. moe_route_scored_bwd's dlogits; it may be dlogits, whose
+ * rows outside the sequences then stay untouched); dlogits [T, E] fp32 (device,
+ * out), for moe_router_bwd_dlogits. */
+int moe_balance_loss_bwd(int T, int E, int k, int n_seq, int score, float alpha, const float* logits,
+                         const int32_t* counts, const int32_t* seq_offsets, const float* dloss, const float* dl_add,
+                         float* dlogits, void* stream);
+
+/* One tensor of an AdamW step (device pointers, 16-byte aligned, scales 4-byte). */
+typedef struct moe_adamw_tensor {
+  void* param;        /* of the plan's dtype; read and written */
+  const void* grad;   /* of the plan's dtype */
+  void *m, *v;        /* fp32, or codes of 8 bits */
+  float *m_scale, *v_scale; /* 8 bits: one for each 256 elements, ceil(numel / 256); else NULL */
+  float* master;      /* fp32 copy of a bf16 param that the step works on, or NULL */
+  int64_t numel;      /* may be 0 */
+  double weight_decay;
+} moe_adamw_tensor;
+
+/* Size of a plan for n tensors.  Host-only. */
+size_t moe_adamw_plan_bytes(int n);
+
+/* Lays out a step over n tensors in `plan` (host memory of plan_bytes); the caller
+ * keeps it and a copy of it on the device for moe_adamw_step, as long as the
+ * tensors stay where they are.  All tensors of a plan have the same dtype and
+ * state_bits (32 or 8), and all have a master or none; no two buffers share
+ * memory.  New 8-bit moments are zeros throughout (codes and scales).  Host-only. */
+int moe_adamw_plan(int n, const moe_adamw_tensor* tensors, int dtype, int state_bits, void* plan, size_t plan_bytes);
+
+/* An AdamW step over the plan's tensors, with t = counter[0] + 1:
+ *   g = grad_scale grad,  m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * p is the master where there is one (param then holds it rounded to nearest),
+ * else param.  counter [2] int32 (device; zeros before the first step) counts the
+ * steps in counter[0], so that a captured step moves on with each replay; lr [1]
+ * and grad_scale [1] (NULL: 1) fp32 (device) may change from step to step.
+ * Rounded up or down by a hash of step, seed and the element's place, up with the
+ * probability of what is left over: bf16 params without a master, and the codes
+ * of 8-bit moments.  Element i of a tensor has place 256 b + i, b the number of
+ * blocks of 256 begun by the tensors in front of it; with
+ *   mix(x): x = (x ^ x >> 16) 0x85ebca77; x = (x ^ x >> 15) 0xc2b2ae3d; x ^ x >> 16
+ *   r = mix(place ^ mix(mix(t) + seed))      (32 bits; places below 2^32)
+ * a param goes up for the share ((r 0x9e3779b1) >> 16) / 2^16 of a bf16 step, m's
+ * code for (r % 2^16 + 1/3) / 2^16 of its step, v's for (r >> 16 + 1/3) / 2^16.
+ * Codes of 8 bits, times the block's scale, the smallest power of two that keeps
+ * its largest value (as fp32) within 448 for m and 1.75 for v, from 2^-126 to
+ * 2^127: m in E4M3; v without a sign, c = (8 + c % 8) 2^(c / 8 - 34) for c = 1 to
+ * 254, 0 for 0, and what is not zero has at least code 1.  Codes are decided in 64
+ * bits; what is not finite has a NaN code (0x7f, 255).
+ * 0 <= beta1, beta2 < 1, eps >= 0.  Steps that may overlap in time share no
+ * tensors and no counter. */
+int moe_adamw_step(const void* plan, const void* plan_device, int32_t* counter, const float* lr, double beta1,
+                   double beta2, double eps, const float* grad_scale, uint32_t seed, void* stream);
+
+/* The moments that 8-bit codes stand for, as fp32 (a checkpoint's, or to go on with
+ * 32 bits): m_out[i] = m's value times m_scale[i / 256], v_out alike, NaN for the
+ * NaN codes.  All of numel elements (device; codes and outputs 16-byte aligned;
+ * outputs on none of the inputs). */
+int moe_adamw_moments(int64_t numel, const uint8_t* m, const uint8_t* v, const float* m_scale, const float* v_scale,
+                      float* m_out, float* v_out, void* stream);
 
 #ifdef __cplusplus
 }
