@@ -208,7 +208,12 @@ def _own(s):
             cut("v_scale", at, n, BLOCK), cut("master", at, n), decay) for (at, n), decay in zip(s["parts"], s["decay"])])
     moe.moe_adamw_step(s["plan"], s["counter"], s["lr"], beta1=BETA1, beta2=BETA2, eps=ADAM_EPS, grad_scale=s["grad_scale"],
                        seed=SEED)
-    return _adamw_outputs(s)
+    if c["bits"] == 32:
+        return _adamw_outputs(s)
+    if "moments" not in s:
+        s["moments"] = [torch.empty(s["m"].shape, device=dev) for _ in range(2)]
+    moe.moe_adamw_moments(s["m"], s["v"], s["m_scale"], s["v_scale"], *s["moments"])
+    return [s["param"]] + ([s["master"]] if c["master"] else []) + s["moments"]
 
 
 def _adamw_outputs(s):
