@@ -382,6 +382,18 @@ int check_balance(const char* fn, int T, int E, int k, int n_seq, int score, flo
   return MOE_OK;
 }
 
+int check_vocab(const char* fn, int T, int H, int V, int vocab, int dtype) {
+  REQUIRE(T >= 1, MOE_ERR_INVALID_ARGUMENT, "%s: T=%d must be >= 1", fn, T);
+  REQUIRE(T <= moe::kVocabMaxRows, MOE_ERR_UNSUPPORTED, "%s: T=%d exceeds %d", fn, T, moe::kVocabMaxRows);
+  int rc = check_dtype(fn, dtype);
+  if (rc || (rc = check_row_width(fn, "H", H)) || (rc = check_row_width(fn, "V", V))) return rc;
+  REQUIRE(H <= moe::kLinearMaxWidth && V <= moe::kLinearMaxWidth, MOE_ERR_UNSUPPORTED, "%s: H=%d or V=%d exceeds %d", fn,
+          H, V, moe::kLinearMaxWidth);
+  REQUIRE((int64_t)T * H < ((int64_t)1 << 40), MOE_ERR_UNSUPPORTED, "%s: T=%d rows of %d are too large", fn, T, H);
+  REQUIRE(vocab >= 1 && vocab <= V, MOE_ERR_INVALID_ARGUMENT, "%s: vocab=%d is not in 1..%d", fn, vocab, V);
+  return MOE_OK;
+}
+
 // No two of the spans share memory.
 int check_apart(const char* fn, std::vector<Span>& spans) {
   std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return (uintptr_t)a.p < (uintptr_t)b.p; });
@@ -1272,6 +1284,73 @@ int moe_adamw_moments(int64_t numel, const uint8_t* m, const uint8_t* v, const f
     return rc;
   hipStream_t s = as_stream(stream);
   return hip_status(moe::launch_adamw_moments(numel, m, v, m_scale, v_scale, m_out, v_out, s), fn);
+}
+
+size_t moe_vocab_loss_workspace_bytes(int T, int H, int V, int dtype) {
+  if (T < 1 || T > moe::kVocabMaxRows || H < 1 || V < 1 || H > moe::kLinearMaxWidth || V > moe::kLinearMaxWidth ||
+      (int64_t)T * H >= ((int64_t)1 << 40) || esize_of(dtype) == 0)
+    return 0;
+  return moe::vocab_workspace_bytes(T, H, V, esize_of(dtype));
+}
+
+int moe_vocab_loss_fwd(int T, int H, int V, int vocab, int dtype, const void* x, const void* w, const int32_t* target,
+                       float* loss, float* lse, float* mean, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_vocab_loss_fwd";
+  int rc = check_vocab(fn, T, H, V, vocab, dtype);
+  if (rc) return rc;
+  NONNULL(x);
+  NONNULL(w);
+  NONNULL(target);
+  NONNULL(loss);
+  NONNULL(lse);
+  NONNULL(mean);
+  const int es = esize_of(dtype);
+  const int64_t row = (int64_t)T * 4;
+  const Span sx{"x", x, (int64_t)T * H * es}, sw{"w", w, (int64_t)H * V * es}, st{"target", target, row};
+  const Span sl{"loss", loss, row}, ss{"lse", lse, row}, sm{"mean", mean, 8};
+  if ((rc = check_aligned(fn, "x", x)) || (rc = check_aligned(fn, "w", w)) ||
+      (rc = check_output(fn, sl, {sx, sw, st, ss, sm}, false)) || (rc = check_output(fn, ss, {sx, sw, st, sm}, false)) ||
+      (rc = check_output(fn, sm, {sx, sw, st}, false)) ||
+      (rc = check_workspace(fn, moe::vocab_workspace_bytes(T, H, V, es), workspace, workspace_bytes,
+                            {sx, sw, st, sl, ss, sm})))
+    return rc;
+  const moe::VocabArgs g{T, H, V, vocab, x, w, target};
+  hipStream_t s = as_stream(stream);
+  return hip_status(
+      timed(MOE_K_VOCAB_FWD, s, [&] { return moe::launch_vocab_fwd(g, es, loss, lse, mean, workspace, s); }), fn);
+}
+
+int moe_vocab_loss_bwd(int T, int H, int V, int vocab, int dtype, const void* x, const void* w, const int32_t* target,
+                       const float* loss, const float* lse, const float* mean, const float* dloss, float scale, void* dx,
+                       void* dw, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_vocab_loss_bwd";
+  int rc = check_vocab(fn, T, H, V, vocab, dtype);
+  if (rc) return rc;
+  REQUIRE(std::isfinite(scale), MOE_ERR_INVALID_ARGUMENT, "%s: scale must be finite", fn);
+  NONNULL(x);
+  NONNULL(w);
+  NONNULL(target);
+  NONNULL(loss);
+  NONNULL(lse);
+  REQUIRE(mean != nullptr || dloss != nullptr, MOE_ERR_INVALID_ARGUMENT, "%s: mean or dloss must be given", fn);
+  REQUIRE(dx != nullptr || dw != nullptr, MOE_ERR_INVALID_ARGUMENT, "%s: no gradient is wanted", fn);
+  const int es = esize_of(dtype);
+  const int64_t row = (int64_t)T * 4, in = (int64_t)T * H * es, wide = (int64_t)H * V * es;
+  const Span sx{"x", x, in}, sw{"w", w, wide}, st{"target", target, row}, sl{"loss", loss, row}, ss{"lse", lse, row};
+  const Span sm{"mean", mean, 8}, sd{"dloss", dloss, row}, sdx{"dx", dx, in}, sdw{"dw", dw, wide};
+  for (const Span& b : {sx, sw, sdx, sdw})
+    if ((rc = check_aligned(fn, b.name, b.p))) return rc;
+  if ((rc = check_output(fn, sdx, {sx, sw, st, sl, ss, sm, sd, sdw}, false)) ||
+      (rc = check_output(fn, sdw, {sx, sw, st, sl, ss, sm, sd}, false)) ||
+      (rc = check_workspace(fn, moe::vocab_workspace_bytes(T, H, V, es), workspace, workspace_bytes,
+                            {sx, sw, st, sl, ss, sm, sd, sdx, sdw})))
+    return rc;
+  const moe::VocabArgs g{T, H, V, vocab, x, w, target};
+  hipStream_t s = as_stream(stream);
+  return hip_status(
+      timed(MOE_K_VOCAB_BWD, s,
+            [&] { return moe::launch_vocab_bwd(g, es, loss, lse, mean, dloss, scale, dx, dw, workspace, s); }),
+      fn);
 }
 
 }  // extern "C"

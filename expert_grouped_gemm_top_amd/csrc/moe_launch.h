@@ -270,6 +270,19 @@ hipError_t launch_balance_fwd(const BalanceArgs& g, int32_t* counts, float* mean
 hipError_t launch_balance_bwd(const BalanceArgs& g, const int32_t* counts, const float* dloss, const float* dl_add,
                               float* dlogits, hipStream_t stream);
 
+constexpr int kVocabMaxRows = 1 << 24;
+// Cross entropy of T rows x [T, H] against w [H, V], the classes its first `vocab` columns.
+struct VocabArgs {
+  int T, H, V, vocab;
+  const void *x, *w;
+  const int32_t* target;
+};
+size_t vocab_workspace_bytes(int T, int H, int V, int esize);
+hipError_t launch_vocab_fwd(const VocabArgs& g, int esize, float* loss, float* lse, float* mean, void* ws,
+                            hipStream_t stream);
+hipError_t launch_vocab_bwd(const VocabArgs& g, int esize, const float* loss, const float* lse, const float* mean,
+                            const float* dloss, float scale, void* dx, void* dw, void* ws, hipStream_t stream);
+
 constexpr int kAdamwBlock = 256;   // elements that share a scale of 8-bit moments
 constexpr int kAdamwChunk = 2048;  // elements of one pass of a workgroup
 constexpr int kAdamwMaxTensors = 1 << 20;

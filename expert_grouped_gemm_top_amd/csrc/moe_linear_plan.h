@@ -122,11 +122,12 @@ constexpr Pair kPairs[] = {{kTile256x256, kTile256x256}, {kTile256x256, kTile256
                            {kTile64x64, kTile64x64}, {kTile32x32, kTile64x64}};
 constexpr int kPairsF = 4;  // fp32 takes those from here on
 
-inline Plan2 plan_bwd(int T, int I, int O, int esize, bool dx, bool dw) {
+inline Plan2 plan_bwd(int T, int I, int O, int esize, bool dx, bool dw, bool split_w = true) {
   Plan2 best{};
   double best_us = -1.0;
   for (int p = esize == 2 ? 0 : kPairsF; p < (int)std::size(kPairs); ++p) {
     const Pair tiles = kPairs[p];
+    Cut w_whole{};
     auto weigh = [&](const Cut* x, const Cut* w) {
       const int64_t gx = x ? x->groups : 0, gw = w ? w->groups : 0;
       const int64_t load = std::min<int64_t>(gx + gw, kCus);
@@ -143,7 +144,8 @@ inline Plan2 plan_bwd(int T, int I, int O, int esize, bool dx, bool dw) {
     };
     auto with_w = [&](const Cut* x) {
       if (!dw) return weigh(x, nullptr);
-      each_cut(I, O, T, esize, tiles.w, [&](const Cut& w) { weigh(x, &w); });
+      if (split_w) each_cut(I, O, T, esize, tiles.w, [&](const Cut& w) { weigh(x, &w); });
+      else weigh(x, &(w_whole = cut_of(I, O, T, esize, tiles.w, 1)));
     };
     if (!dx) with_w(nullptr);
     else each_cut(T, I, O, esize, tiles.x, [&](const Cut& x) { with_w(&x); });

@@ -1,0 +1,633 @@
+// moe_vocab.hip -- softmax cross entropy over a vocabulary, without keeping the
+// logits, and its gradients.
+//
+//   l_tv = x_t W_v,  loss_t = log sum_v exp(l_tv) - l_ty,  y = target[t]
+//   dz_tv = w_t (p_tv - [v = y]),  p = exp(l - lse)
+//   dx = c dz W^T,  dW = c x^T dz
+//
+// Tokens that are not counted are left out of every product: the first kernel
+// lists the others.  The forward's tiles of logits leave one maximum and sum of
+// exponentials per row and run of columns.  The backward goes over the vocabulary
+// in pieces: a piece's logits again, from them its dz, then both gradients' products
+// with it.
+//
+// The target's column is kept apart: with rest = sum_{v != y} exp(l_v - l_y),
+// loss = log(1 + rest), and its dz is expm1(-loss), both with all their digits where
+// a confident token's p is next to 1.
+//
+// dz is rounded to the element type, as the operand of both products.  It is held
+// without the common factor c, so that the targets' entries, mostly just above -1,
+// lose little by it; the others' errors go in all directions (bf16, 8192 tokens over
+// 65536 x 4096: dx 1.7e-3, dW 1.9e-3 of their norms off, 1.7e-3 of both by their own
+// rounding).
+#include <algorithm>
+
+#include "moe_common.h"
+#include "moe_launch.h"
+#include "moe_linear_plan.h"
+#include "moe_rows.h"
+#include "moe_tile.h"
+
+namespace moe {
+
+namespace {
+
+// What the first kernel leaves: the counted tokens in order, and by their places in that list what the others read.
+struct Listed {
+  int32_t* head;  // [0] their number, [1] a ticket, set to 0
+  int32_t* rows;  // [n] token
+  int32_t* place; // [T] place of a token, -1 where not counted
+  int32_t* y;     // [n] target
+  float* lse;     // [n] backward: as the forward left them
+  float* loss;
+  float* w;       // [n] backward: the token's weight
+};
+
+// The tokens with a target in [0, vocab), in order, by one workgroup.  loss_out and lse_out (forward) become 0 for the others.
+constexpr int kListRun = 8;
+__global__ __launch_bounds__(1024) void vocab_list_kernel(int T, int vocab, const int32_t* __restrict__ target, Listed out,
+                                                          float* loss_out, float* lse_out, const float* loss,
+                                                          const float* lse, const float* dloss) {
+  __shared__ int s_wave[16];
+  const int tid = threadIdx.x, w = tid >> 6;
+  int before = 0;
+  for (int64_t base = 0; base < T; base += 1024 * kListRun) {
+    const int64_t first = base + (int64_t)tid * kListRun;
+    int y[kListRun], mine = 0;
+#pragma unroll
+    for (int j = 0; j < kListRun; ++j) {
+      y[j] = first + j < T ? target[first + j] : -1;
+      if (y[j] < 0 || y[j] >= vocab) y[j] = -1;
+      mine += y[j] >= 0;
+    }
+    const int upto = wave_inclusive_scan(mine);
+    __syncthreads();
+    if ((tid & 63) == 63) s_wave[w] = upto;
+    __syncthreads();
+    int at = before + upto - mine;
+    for (int i = 0; i < 16; ++i) {
+      at += i < w ? s_wave[i] : 0;
+      before += s_wave[i];
+    }
+#pragma unroll
+    for (int j = 0; j < kListRun; ++j) {
+      const int64_t t = first + j;
+      if (t >= T) break;
+      out.place[t] = y[j] >= 0 ? at : -1;
+      if (y[j] < 0) {
+        if (loss_out != nullptr) loss_out[t] = lse_out[t] = 0.0f;
+        continue;
+      }
+      out.rows[at] = (int)t;
+      out.y[at] = y[j];
+      if (loss_out == nullptr) {
+        out.loss[at] = loss[t];
+        out.lse[at] = lse[t];
+        out.w[at] = dloss != nullptr ? dloss[t] : 1.0f;
+      }
+      ++at;
+    }
+  }
+  if (tid == 0) {
+    out.head[0] = before;
+    out.head[1] = 0;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ float exp_of(float v) {
+  return sizeof(T) == 4 ? expf(v) : quick_exp(v);
+}
+
+// ---- the forward ----------------------------------------------------------------
+
+// A row's maximum over a run of columns, its target's left out, and the sum of exponentials above it.
+struct Run {
+  float top, sum;
+};
+
+template <typename T>
+struct LossOut {
+  int n, vocab, pitch;
+  const int32_t* y;
+  float* own;  // [n] the targets' logits
+  Run* runs;   // [run][pitch rows]
+  __device__ __forceinline__ bool skip(int, int) const { return false; }
+  template <typename Lanes>
+  __device__ __forceinline__ void operator()(int64_t m, int n0, float (&v)[8], Lanes) const {
+    const int at = (m < n ? y[m] : -1) - n0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (at == j) own[m] = v[j];
+      if (at == j || n0 + j >= vocab) v[j] = -__builtin_inff();
+    }
+    float top = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
+#pragma unroll
+    for (int o = Lanes::value / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, kWave));
+    const float base = top == -__builtin_inff() ? 0.0f : top;
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += exp_of<T>(v[j] - base);
+#pragma unroll
+    for (int o = Lanes::value / 2; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, kWave);
+    constexpr int COLS = 8 * Lanes::value;
+    if (n0 % COLS == 0 && m < n && n0 < vocab) runs[(int64_t)(n0 / COLS) * pitch + m] = Run{top, sum};
+  }
+};
+
+template <typename T>
+struct LogitsArgs {
+  TileSource g;  // M: the batch's tokens; b from the piece's first column on
+  int K;
+  Listed list;
+};
+
+// Tile of the counted tokens' rows; false past the last.
+template <typename C>
+__device__ __forceinline__ bool row_tile(int item, int n, int N, int& mt, int& nt) {
+  const int mtiles = (n + C::BM - 1) / C::BM, ntiles = (N + C::BN - 1) / C::BN;
+  if (item >= mtiles * ntiles) return false;
+  tile_of(item, mtiles, ntiles, 1024 / C::BM, mt, nt);
+  return true;
+}
+
+template <typename T, typename C, bool TAIL>
+__global__ __launch_bounds__(kTileThreads, 2) void vocab_loss_kernel(LogitsArgs<T> a, int vocab, int pitch, float* own,
+                                                                     Run* runs) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char s_dyn[];
+  TileSource g = a.g;
+  g.M = a.list.head[0];
+  int mt, nt;
+  if (!row_tile<C>(group_id(), g.M, g.N, mt, nt)) return;
+  tile_product<T, true, false, C, TAIL>(g, mt, nt, 0, a.K, s_dyn, LossOut<T>{g.M, vocab, pitch, a.list.y, own, runs});
+}
+
+// Joins the runs of 16 rows per workgroup, 16 threads each; the last workgroup adds up the mean.
+struct JoinArgs {
+  int n_runs, pitch;
+  const Run* runs;
+  const float* own;
+  Listed list;
+  double* part;  // a sum of losses of each workgroup
+  float *loss, *lse, *mean;
+};
+__global__ __launch_bounds__(256) void vocab_join_kernel(JoinArgs a) {
+  __shared__ float s_top[16][17], s_sum[16][17];
+  __shared__ double s_loss[16];
+  __shared__ bool s_last;
+  const int tid = threadIdx.x, r = tid & 15, q = tid >> 4, n = a.list.head[0];
+  const int row = blockIdx.x * 16 + r;
+  const int groups = max(1, (n + 15) / 16);
+  if ((int)blockIdx.x >= groups) return;
+  float top = -__builtin_inff(), sum = 0.0f;
+  if (row < n)
+#pragma unroll 4
+    for (int i = q; i < a.n_runs; i += 16) {
+      const Run p = a.runs[(int64_t)i * a.pitch + row];
+      const float t = fmaxf(top, p.top);
+      const float base = t == -__builtin_inff() ? 0.0f : t;
+      sum = sum * expf(top - base) + p.sum * expf(p.top - base);
+      top = t;
+    }
+  s_top[q][r] = top;
+  s_sum[q][r] = sum;
+  __syncthreads();
+  if (tid < 16) {
+    double l = 0.0;
+    if (row < n) {
+      for (int i = 1; i < 16; ++i) {
+        const float t = fmaxf(top, s_top[i][r]);
+        const float base = t == -__builtin_inff() ? 0.0f : t;
+        sum = sum * expf(top - base) + s_sum[i][r] * expf(s_top[i][r] - base);
+        top = t;
+      }
+      const float own = a.own[row], d = top + logf(sum) - own;  // log of the others' sum over the target's
+      const float loss = fmaxf(d, 0.0f) + log1pf(expf(-fabsf(d)));
+      const int t = a.list.rows[row];
+      a.loss[t] = loss;
+      a.lse[t] = own + loss;
+      l = (double)loss;
+    }
+    s_loss[tid] = l;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    double l = 0.0;
+    for (int i = 0; i < 16; ++i) l += s_loss[i];
+    __hip_atomic_store(a.part + blockIdx.x, l, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    s_last = __hip_atomic_fetch_add(a.list.head + 1, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == groups - 1;
+  }
+  __syncthreads();
+  if (!s_last || tid >= 64) return;
+  double l = 0.0;
+  for (int i = tid; i < groups; i += 64) l += __hip_atomic_load(a.part + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) l += __shfl_xor(l, o, kWave);
+  if (tid == 0) {
+    a.mean[0] = n > 0 ? (float)(l / n) : 0.0f;
+    a.mean[1] = n > 0 ? (float)(1.0 / n) : 0.0f;
+  }
+}
+
+// ---- the backward ---------------------------------------------------------------
+
+template <typename T>
+struct GradOut {
+  int n, first, vocab;  // the piece's first column
+  int pitch;
+  Listed list;
+  T* dz;
+  __device__ __forceinline__ bool skip(int, int) const { return false; }
+  template <typename Lanes>
+  __device__ __forceinline__ void operator()(int64_t m, int n0, float (&v)[8], Lanes) const {
+    if (m >= n) return;
+    const float lse = list.lse[m], w = list.w[m];
+    const int at = list.y[m] - first - n0, end = vocab - first - n0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < end ? w * exp_of<T>(v[j] - lse) : 0.0f;
+    if (at >= 0 && at < 8) {
+      const float own = w * expm1f(-list.loss[m]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = j == at ? own : v[j];
+    }
+    store8(dz + m * pitch + n0, v);
+  }
+};
+
+template <typename T, typename C, bool TAIL>
+__global__ __launch_bounds__(kTileThreads, 2) void vocab_dz_kernel(LogitsArgs<T> a, int first, int vocab, int pitch,
+                                                                   T* dz) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char s_dyn[];
+  TileSource g = a.g;
+  g.M = a.list.head[0];
+  int mt, nt;
+  if (!row_tile<C>(group_id(), g.M, g.N, mt, nt)) return;
+  tile_product<T, true, false, C, TAIL>(g, mt, nt, 0, a.K, s_dyn, GradOut<T>{g.M, first, vocab, pitch, a.list, dz});
+}
+
+// The listed tokens' rows of x, one behind the other, for dW, which sums over them.
+template <typename T>
+__global__ __launch_bounds__(256) void vocab_gather_kernel(int H, const T* __restrict__ x, Listed list, T* __restrict__ out) {
+  const int n = list.head[0];
+  for (int64_t r = blockIdx.x; r < n; r += gridDim.x) {
+    const u32x4* src = (const u32x4*)(x + (int64_t)list.rows[r] * H);
+    u32x4* dst = (u32x4*)(out + r * H);
+    for (int i = threadIdx.x; i < H * (int)sizeof(T) / 16; i += 256) dst[i] = src[i];
+  }
+}
+
+// Sums of dx over the pieces, [slice][pitch rows][H].
+struct DxOut {
+  int n, H, pitch, slice;
+  bool add;
+  float* sums;
+  __device__ __forceinline__ bool skip(int m, int h) const { return m >= n || h >= H; }
+  template <typename Lanes>
+  __device__ __forceinline__ void operator()(int64_t m, int h, float (&v)[8], Lanes) const {
+    float* at = sums + ((int64_t)slice * pitch + m) * H + h;
+    if (add) {
+      float u[8];
+      load8(at, u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += u[j];
+    }
+    store8(at, v);
+  }
+};
+
+template <typename T>
+struct DwOut {
+  int H, N;
+  int64_t ld;
+  float c;
+  T* dw;
+  __device__ __forceinline__ bool skip(int h, int n) const { return h >= H || n >= N; }
+  template <typename Lanes>
+  __device__ __forceinline__ void operator()(int64_t h, int n, float (&v)[8], Lanes) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= c;
+    store8(dw + h * ld + n, v);
+  }
+};
+
+// The factor that dz was held without.
+struct Factor {
+  float scale;
+  const float* per_mean;  // {mean, 1 / n}; NULL where tokens are weighted one by one
+  __device__ __forceinline__ float get() const { return per_mean != nullptr ? scale * per_mean[1] : scale; }
+};
+
+struct GradArgs {
+  TileSource gx, gw;    // dz W^T (M: the batch's tokens) and x^T dz
+  int Kx, slice, pitch; // the piece's columns, those of a slice, rows of dz and of a slice's sums
+  Listed list;
+  int add;              // not the first piece
+  float* sums;
+  Factor c;
+  void* dw;
+  int64_t ldw;
+  int64_t nx, nw;       // workgroups of each product
+  int x_first;
+};
+
+// Both gradients' products with one piece of dz, in one launch as in linear_bwd_kernel.  dW sums over as many
+// tokens as are counted: its last stage is masked.
+template <typename T, typename CX, typename CW, bool TAIL>
+__global__ __launch_bounds__(kTileThreads, 2) void vocab_grads_kernel(GradArgs a) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char s_dyn[];
+  const int64_t b = group_id();
+  const int n = a.list.head[0];
+  const bool is_x = a.x_first ? b < a.nx : b >= a.nw;
+  if (is_x) {
+    TileSource g = a.gx;
+    g.M = n;
+    const int mtiles = (n + CX::BM - 1) / CX::BM, ntiles = (g.N + CX::BN - 1) / CX::BN, tiles = mtiles * ntiles;
+    const int item = (int)(a.x_first ? b : b - a.nw);
+    if (tiles == 0) return;
+    const int s = item / tiles, kb = s * a.slice;
+    if (s * (int64_t)a.slice >= a.Kx) return;
+    int mt, nt;
+    tile_of(item % tiles, mtiles, ntiles, 1024 / CX::BM, mt, nt);
+    tile_product<T, true, true, CX, TAIL>(g, mt, nt, kb, min(a.Kx, kb + a.slice), s_dyn,
+                                           DxOut{n, g.N, a.pitch, s, a.add != 0, a.sums});
+  } else {
+    const TileSource& g = a.gw;
+    const int mtiles = (g.M + CW::BM - 1) / CW::BM, ntiles = (g.N + CW::BN - 1) / CW::BN;
+    const int item = (int)(a.x_first ? b - a.nx : b);
+    if (item >= mtiles * ntiles) return;
+    int mt, nt;
+    tile_of(item, mtiles, ntiles, 1024 / CW::BM, mt, nt);
+    tile_product<T, false, false, CW, true>(g, mt, nt, 0, n, s_dyn, DwOut<T>{g.M, g.N, a.ldw, a.c.get(), (T*)a.dw});
+  }
+}
+
+// dx of every token from the slices' sums; zeros where not counted.
+template <typename T>
+__global__ __launch_bounds__(256) void vocab_dx_kernel(int T_, int H, int slices, int pitch, Listed list,
+                                                       const float* __restrict__ sums, Factor f, T* __restrict__ dx) {
+  const float c = f.get();
+  const int runs = H / 8;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)T_ * runs; i += (int64_t)gridDim.x * 256) {
+    const int64_t t = i / runs;
+    const int h = 8 * (int)(i % runs), place = list.place[t];
+    float v[8] = {};
+    if (place >= 0) {
+      for (int s = 0; s < slices; ++s) {
+        float u[8];
+        load8(sums + ((int64_t)s * pitch + place) * H + h, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = s == 0 ? u[j] : v[j] + u[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= c;
+    }
+    store8(dx + t * H + h, v);
+  }
+}
+
+// ---- plans and launchers -----------------------------------------------------------
+
+int rounded_up(int64_t v, int to) { return (int)((v + to - 1) / to * to); }
+
+template <typename T, typename Fn>
+hipError_t with_tile(int tile, Fn&& run) {
+  if constexpr (sizeof(T) == 2) {
+    if (tile == kTile256x256) return run(Tile0{});
+    if (tile == kTile256x128) return run(Tile1{});
+  }
+  if (tile == kTile128x128) return run(Tile2{});
+  if (tile == kTile128x64) return run(Tile3{});
+  if (tile == kTile64x64) return run(Tile4<T>{});
+  return run(Tile5{});
+}
+
+struct VocabPlan {
+  int logits;       // tile of the logits' products
+  int piece;        // columns of a piece of the backward, a multiple of 256
+  int pitch;        // rows of dz: T in whole tiles
+  Plan2 grads;
+};
+
+// The columns of a piece: dz of some 64 Mi elements, so that it is read again from the last-level cache.
+constexpr int64_t kPieceElements = 64 << 20;
+
+VocabPlan vocab_plan(int T, int H, int V, int esize, bool dx, bool dw) {
+  VocabPlan p{};
+  p.pitch = rounded_up(T, 256);
+  const int64_t cols = std::max<int64_t>(kPieceElements / p.pitch / 256 * 256, 1024);
+  p.piece = (int)std::min<int64_t>(cols, rounded_up(V, 256));
+  double best = -1.0;
+  for (int tile = esize == 2 ? 0 : (int)kTile128x128; tile < kTiles; ++tile) {
+    const Cut c = cut_of(T, dx || dw ? p.piece : V, H, esize, tile, 1);
+    const int64_t rest = c.groups % kCus;
+    double us = (double)(c.groups / kCus) * c.each;
+    if (rest > 0) us += pass_us(cost_of(tile, esize), H, rest);
+    if (best < 0.0 || us < best) {
+      best = us;
+      p.logits = tile;
+    }
+  }
+  if (dx || dw) p.grads = plan_bwd(T, H, p.piece, esize, dx, dw, false);
+  return p;
+}
+
+// The columns of a run that a tile of the forward leaves.
+template <typename T>
+int run_cols(int tile) {
+  int cols = 0;
+  (void)with_tile<T>(tile, [&](auto t) {
+    cols = decltype(t)::OUT_COLS;
+    return hipSuccess;
+  });
+  return cols;
+}
+
+struct Space {
+  Listed list;
+  double* part;
+  float* own;
+  Run* runs;
+  void *x, *dz;
+  float* sums;
+  size_t bytes;
+};
+
+// A workspace's parts: the list, then the forward's runs or the backward's piece.
+Space vocab_space(void* ws, int T, int H, int V, int esize, const VocabPlan& p, bool bwd) {
+  Space s{};
+  char* at = (char*)ws;
+  auto take = [&](size_t bytes) {
+    char* here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  const size_t row = (size_t)T * 4;
+  s.list.head = (int32_t*)take(256);
+  s.list.rows = (int32_t*)take(row);
+  s.list.place = (int32_t*)take(row);
+  s.list.y = (int32_t*)take(row);
+  if (!bwd) {
+    s.part = (double*)take(((size_t)T + 15) / 16 * 8);
+    s.own = (float*)take(row);
+    const int cols = esize == 4 ? run_cols<float>(p.logits) : run_cols<uint16_t>(p.logits);
+    s.runs = (Run*)take((size_t)((V + cols - 1) / cols) * p.pitch * sizeof(Run));
+  } else {
+    s.list.lse = (float*)take(row);
+    s.list.loss = (float*)take(row);
+    s.list.w = (float*)take(row);
+    s.x = take((size_t)p.pitch * H * esize);
+    s.dz = take((size_t)p.pitch * p.piece * esize);
+    s.sums = (float*)take((size_t)std::max(1, p.grads.x.slices) * p.pitch * H * 4);
+  }
+  s.bytes = (size_t)(at - (char*)ws);
+  return s;
+}
+
+template <typename Kern, typename... Args>
+hipError_t run_tiles(Kern kern, size_t lds, int64_t groups, hipStream_t stream, PerDeviceOnce& once, Args... args) {
+  hipError_t err = allow_dynamic_lds(once, (const void*)kern, lds);
+  if (err != hipSuccess) return err;
+  MOE_LAUNCH(kern, wide_grid(groups), dim3(kTileThreads), lds, stream, args...);
+  return hipGetLastError();
+}
+
+template <typename C>
+int64_t tiles_of(int M, int N) {
+  return (int64_t)((M + C::BM - 1) / C::BM) * ((N + C::BN - 1) / C::BN);
+}
+
+template <typename T, typename C, bool TAIL>
+hipError_t run_loss(const LogitsArgs<T>& a, int vocab, int pitch, float* own, Run* runs, hipStream_t stream) {
+  static PerDeviceOnce once;
+  return run_tiles(vocab_loss_kernel<T, C, TAIL>, C::LDS, tiles_of<C>(a.g.M, a.g.N), stream, once, a, vocab, pitch, own,
+                   runs);
+}
+
+template <typename T, typename C, bool TAIL>
+hipError_t run_dz(const LogitsArgs<T>& a, int first, int vocab, int pitch, T* dz, hipStream_t stream) {
+  static PerDeviceOnce once;
+  return run_tiles(vocab_dz_kernel<T, C, TAIL>, C::LDS, tiles_of<C>(a.g.M, a.g.N), stream, once, a, first, vocab, pitch,
+                   dz);
+}
+
+template <typename T, typename CX, typename CW, bool TAIL>
+hipError_t run_grads(const GradArgs& a, hipStream_t stream) {
+  static PerDeviceOnce once;
+  return run_tiles(vocab_grads_kernel<T, CX, CW, TAIL>, std::max(CX::LDS, CW::LDS), a.nx + a.nw, stream, once, a);
+}
+
+template <typename T>
+hipError_t vocab_fwd_typed(const VocabArgs& g, float* loss, float* lse, float* mean, void* ws, hipStream_t stream) {
+  const VocabPlan p = vocab_plan(g.T, g.H, g.V, sizeof(T), false, false);
+  const Space s = vocab_space(ws, g.T, g.H, g.V, sizeof(T), p, false);
+  MOE_LAUNCH(vocab_list_kernel, dim3(1), dim3(1024), 0, stream, g.T, g.vocab, g.target, s.list, loss, lse, nullptr, nullptr,
+             nullptr);
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  // columns past the vocabulary's end need no product
+  const int cols = std::min(g.V, rounded_up(g.vocab, 8));
+  const LogitsArgs<T> a{{g.T, cols, g.x, g.H, g.w, g.V, s.list.rows}, g.H, s.list};
+  err = with_tile<T>(p.logits, [&](auto tile) {
+    using C = decltype(tile);
+    const bool tail = g.H % (kStageK<T> * C::KG) != 0;
+    return tail ? run_loss<T, C, true>(a, g.vocab, p.pitch, s.own, s.runs, stream)
+                : run_loss<T, C, false>(a, g.vocab, p.pitch, s.own, s.runs, stream);
+  });
+  if (err != hipSuccess) return err;
+  const int run = run_cols<T>(p.logits);
+  const JoinArgs j{(cols + run - 1) / run, p.pitch, s.runs, s.own, s.list, s.part, loss, lse, mean};
+  MOE_LAUNCH(vocab_join_kernel, dim3((g.T + 15) / 16), dim3(256), 0, stream, j);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t vocab_bwd_typed(const VocabArgs& g, const float* loss, const float* lse, const float* mean, const float* dloss,
+                           float scale, void* dx, void* dw, void* ws, hipStream_t stream) {
+  const VocabPlan p = vocab_plan(g.T, g.H, g.V, sizeof(T), dx != nullptr, dw != nullptr);
+  const Space s = vocab_space(ws, g.T, g.H, g.V, sizeof(T), p, true);
+  MOE_LAUNCH(vocab_list_kernel, dim3(1), dim3(1024), 0, stream, g.T, g.vocab, g.target, s.list, nullptr, nullptr, loss, lse,
+             dloss);
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  if (dw != nullptr) {
+    MOE_LAUNCH(vocab_gather_kernel<T>, dim3(std::min(g.T, 2048)), dim3(256), 0, stream, g.H, (const T*)g.x, s.list, (T*)s.x);
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+  }
+  const Factor c{scale, dloss != nullptr ? nullptr : mean};
+  T* dz = (T*)s.dz;
+  for (int first = 0; first < g.V; first += p.piece) {
+    const int cols = std::min(p.piece, g.V - first);
+    const T* w = (const T*)g.w + first;
+    LogitsArgs<T> a{{g.T, cols, g.x, g.H, w, g.V, s.list.rows}, g.H, s.list};
+    err = with_tile<T>(p.logits, [&](auto tile) {
+      using C = decltype(tile);
+      const bool tail = g.H % (kStageK<T> * C::KG) != 0;
+      return tail ? run_dz<T, C, true>(a, first, g.vocab, p.piece, dz, stream)
+                  : run_dz<T, C, false>(a, first, g.vocab, p.piece, dz, stream);
+    });
+    if (err != hipSuccess) return err;
+    GradArgs b{};
+    b.gx = TileSource{g.T, g.H, dz, p.piece, w, g.V, nullptr};
+    b.gw = TileSource{g.H, dw != nullptr ? cols : 0, s.x, g.H, dz, p.piece, nullptr};
+    b.Kx = dx != nullptr ? cols : 0;
+    b.slice = p.grads.x.slice;
+    b.pitch = p.pitch;
+    b.list = s.list;
+    b.add = first > 0;
+    b.sums = s.sums;
+    b.c = c;
+    b.dw = dw != nullptr ? (T*)dw + first : nullptr;
+    b.ldw = g.V;
+    b.x_first = p.grads.x.each > p.grads.w.each;
+    auto run = [&](auto tx, auto tw) {
+      using CX = decltype(tx);
+      using CW = decltype(tw);
+      b.nx = dx != nullptr ? tiles_of<CX>(g.T, g.H) * ((cols + b.slice - 1) / b.slice) : 0;
+      b.nw = dw != nullptr ? tiles_of<CW>(g.H, cols) : 0;
+      constexpr int SX = kStageK<T> * CX::KG;
+      const bool tail_x = cols % SX != 0 || b.slice % SX != 0;
+      return tail_x ? run_grads<T, CX, CW, true>(b, stream) : run_grads<T, CX, CW, false>(b, stream);
+    };
+    const int pair = p.grads.pair;
+    err = hipErrorUnknown;
+    if constexpr (sizeof(T) == 2) {
+      if (pair == 0) err = run(Tile0{}, Tile0{});
+      if (pair == 1) err = run(Tile0{}, Tile1{});
+      if (pair == 2) err = run(Tile1{}, Tile0{});
+      if (pair == 3) err = run(Tile1{}, Tile1{});
+    }
+    if (pair == 4) err = run(Tile2{}, Tile2{});
+    if (pair == 5) err = run(Tile3{}, Tile3{});
+    if (pair == 6) err = run(Tile4<T>{}, Tile4<T>{});
+    if (pair == 7) err = run(Tile5{}, Tile4<T>{});
+    if (err != hipSuccess) return err;
+  }
+  if (dx == nullptr) return hipSuccess;
+  const int64_t runs = (int64_t)g.T * (g.H / 8);
+  MOE_LAUNCH(vocab_dx_kernel<T>, dim3((unsigned)std::min<int64_t>((runs + 255) / 256, 8192)), dim3(256), 0, stream, g.T, g.H,
+             (std::min(p.piece, g.V) + p.grads.x.slice - 1) / p.grads.x.slice, p.pitch, s.list, s.sums, c, (T*)dx);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t vocab_workspace_bytes(int T, int H, int V, int esize) {
+  size_t need = vocab_space(nullptr, T, H, V, esize, vocab_plan(T, H, V, esize, false, false), false).bytes;
+  for (int want = 1; want < 4; ++want)
+    need = std::max(need, vocab_space(nullptr, T, H, V, esize, vocab_plan(T, H, V, esize, want & 1, want & 2), true).bytes);
+  return need;
+}
+
+hipError_t launch_vocab_fwd(const VocabArgs& g, int esize, float* loss, float* lse, float* mean, void* ws,
+                            hipStream_t stream) {
+  return esize == 4 ? vocab_fwd_typed<float>(g, loss, lse, mean, ws, stream)
+                    : vocab_fwd_typed<uint16_t>(g, loss, lse, mean, ws, stream);
+}
+
+hipError_t launch_vocab_bwd(const VocabArgs& g, int esize, const float* loss, const float* lse, const float* mean,
+                            const float* dloss, float scale, void* dx, void* dw, void* ws, hipStream_t stream) {
+  return esize == 4 ? vocab_bwd_typed<float>(g, loss, lse, mean, dloss, scale, dx, dw, ws, stream)
+                    : vocab_bwd_typed<uint16_t>(g, loss, lse, mean, dloss, scale, dx, dw, ws, stream);
+}
+
+}  // namespace moe

@@ -72,6 +72,9 @@ _SIGS = {
     "moe_balance_loss_workspace_bytes": ([_i] * 3, _sz),
     "moe_balance_loss_fwd": ([_i] * 5 + [_f] + [_vp] * 7 + [_sz, _vp], _i),
     "moe_balance_loss_bwd": ([_i] * 5 + [_f] + [_vp] * 7, _i),
+    "moe_vocab_loss_workspace_bytes": ([_i] * 4, _sz),
+    "moe_vocab_loss_fwd": ([_i] * 5 + [_vp] * 7 + [_sz, _vp], _i),
+    "moe_vocab_loss_bwd": ([_i] * 5 + [_vp] * 7 + [_f] + [_vp] * 3 + [_sz, _vp], _i),
     "moe_adamw_plan_bytes": ([_i], _sz),
     "moe_adamw_plan": ([_i, _vp, _i, _i, _vp, _sz], _i),
     "moe_adamw_moments": ([_i64] + [_vp] * 7, _i),
@@ -677,6 +680,40 @@ def moe_balance_loss_bwd(logits, counts, dlogits, k: int, score: int = MOE_SCORE
         T, E, k, S, score, alpha, _need(logits, "logits", rows, F32, dev), _need(counts, "counts", (S, E), I32, dev),
         _addr(seq_offsets, "seq_offsets", (S + 1,), I32, dev), _addr(dloss, "dloss", (1,), F32, dev),
         _addr(dl_add, "dl_add", rows, F32, dev), _need(dlogits, "dlogits", rows, F32, dev), _queue(stream, dev)))
+
+
+def moe_vocab_loss_workspace_bytes(T: int, H: int, V: int, dtype) -> int:
+    return int(lib().moe_vocab_loss_workspace_bytes(T, H, V, MOE_F32 if dtype == torch.float32 else MOE_BF16))
+
+
+def moe_vocab_loss_fwd(x, w, target, loss, lse, mean, workspace, vocab: int | None = None, stream=None):
+    """loss and lse [T] of the logits x w over the first `vocab` columns (None: all),
+    mean = {mean loss, 1 / counted tokens}; targets outside [0, vocab) are not counted."""
+    dev = _device(x, "x")
+    T, H = rows = _rows(x, "x")
+    V = _rows(w, "w")[1]
+    d, each = x.dtype, (T,)
+    ws, ws_bytes = _space(workspace, dev)
+    _check(lib().moe_vocab_loss_fwd(
+        T, H, V, V if vocab is None else vocab, _dt(x), _need(x, "x", rows, d, dev), _need(w, "w", (H, V), d, dev),
+        _need(target, "target", each, I32, dev), _need(loss, "loss", each, F32, dev), _need(lse, "lse", each, F32, dev),
+        _need(mean, "mean", (2,), F32, dev), ws, ws_bytes, _queue(stream, dev)))
+
+
+def moe_vocab_loss_bwd(x, w, target, loss, lse, mean, dx, dw, workspace, dloss=None, scale: float = 1.0,
+                       vocab: int | None = None, stream=None):
+    """dx and dw (either may be None) of scale times the mean loss, or of scale times
+    the sum of dloss [T] loss (mean may then be None)."""
+    dev = _device(x, "x")
+    T, H = rows = _rows(x, "x")
+    V = _rows(w, "w")[1]
+    d, each = x.dtype, (T,)
+    ws, ws_bytes = _space(workspace, dev)
+    _check(lib().moe_vocab_loss_bwd(
+        T, H, V, V if vocab is None else vocab, _dt(x), _need(x, "x", rows, d, dev), _need(w, "w", (H, V), d, dev),
+        _need(target, "target", each, I32, dev), _need(loss, "loss", each, F32, dev), _need(lse, "lse", each, F32, dev),
+        _addr(mean, "mean", (2,), F32, dev), _addr(dloss, "dloss", each, F32, dev), scale, _addr(dx, "dx", rows, d, dev),
+        _addr(dw, "dw", (H, V), d, dev), ws, ws_bytes, _queue(stream, dev)))
 
 
 class AdamWTensor(typing.NamedTuple):

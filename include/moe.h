@@ -42,6 +42,8 @@
  *
  *   moe_balance_loss_fwd, moe_balance_loss_bwd  the routers' balance loss, counts
  *                           per expert, and the logits' gradient
+ *   moe_vocab_loss_fwd, moe_vocab_loss_bwd  softmax cross entropy over a vocabulary
+ *                           without keeping the logits, and its gradients
  *   moe_adamw_plan, moe_adamw_step, moe_adamw_moments  AdamW over many tensors at
  *                           once, moments of 32 or 8 bits, and those read back
  *
@@ -122,6 +124,8 @@ int moe_abi_version(void);
  *   moe_layernorm_bwd                       2
  *   moe_linear_fwd                          1, plus 1 when its reduction is split
  *   moe_balance_loss_fwd                    1 for one sequence of T <= 256, else 2
+ *   moe_vocab_loss_fwd                      3
+ *   moe_vocab_loss_bwd                      1, plus 1 for dw, 2 for each piece of the vocabulary, 1 for dx
  *   moe_balance_loss_bwd, moe_adamw_step,
  *   moe_adamw_moments                       1
  *   moe_linear_bwd                          1 for dz or dbias (0 without activation, gate and
@@ -151,7 +155,9 @@ typedef enum moe_kernel {
   /* 16 names no kernel */
   MOE_K_BALANCE = 17,      /* moe_balance_loss_fwd, moe_balance_loss_bwd */
   MOE_K_ADAMW = 18,        /* moe_adamw_step */
-  MOE_K_COUNT = 19
+  MOE_K_VOCAB_FWD = 19,    /* moe_vocab_loss_fwd */
+  MOE_K_VOCAB_BWD = 20,    /* moe_vocab_loss_bwd */
+  MOE_K_COUNT = 21
 } moe_kernel;
 
 /* Profiling hook.  Arms a one-shot request on the calling thread: the next
@@ -687,6 +693,43 @@ int moe_balance_loss_fwd(int T, int E, int k, int n_seq, int score, float alpha,
 int moe_balance_loss_bwd(int T, int E, int k, int n_seq, int score, float alpha, const float* logits,
                          const int32_t* counts, const int32_t* seq_offsets, const float* dloss, const float* dl_add,
                          float* dlogits, void* stream);
+
+/* Workspace (device bytes) of moe_vocab_loss_fwd and moe_vocab_loss_bwd: the list of
+ * counted tokens, and the forward's row statistics (8 bytes for each token and run
+ * of 32 to 128 columns) or the backward's piece of dz (some 64 Mi elements), its
+ * rows of x and the fp32 sums of dx.  Host-only. */
+size_t moe_vocab_loss_workspace_bytes(int T, int H, int V, int dtype);
+
+/* Softmax cross entropy of the logits x W over the classes 0 .. vocab - 1, which are
+ * computed in tiles and not kept:
+ *   lse[t] = log sum_v exp(x_t W_v),  loss[t] = lse[t] - x_t W_target[t]
+ *   mean = {sum_t loss[t] / n, 1 / n}
+ * over the n tokens that are counted, those whose target is in [0, vocab); the
+ * others' loss and lse are 0, and their rows of x are not read (mean is {0, 0}
+ * where none is counted).  Sums in fp32; loss keeps its relative precision where
+ * the target's probability is next to 1.  x [T, H], w [H, V] of `dtype`, target
+ * [T] int32 (device); loss, lse [T] and mean [2] fp32 (device, out).  H and V
+ * multiples of 8, at most 2^20, 1 <= vocab <= V (columns from vocab on are padding:
+ * no classes, finite values), T at most 2^24, T H below 2^40; x, w 16-byte
+ * aligned; workspace (apart from all other buffers) of at least
+ * moe_vocab_loss_workspace_bytes.  Calls that may overlap in time need a workspace
+ * each. */
+int moe_vocab_loss_fwd(int T, int H, int V, int vocab, int dtype, const void* x, const void* w, const int32_t* target,
+                       float* loss, float* lse, float* mean, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Its gradients, of scale * mean[0] (dloss NULL) or of scale * sum_t dloss[t]
+ * loss[t], in pieces of the vocabulary whose logits are computed again:
+ *   dz_tv = w_t (exp(x_t W_v - lse[t]) - [v = target[t]]),  w_t = 1 or dloss[t]
+ *   dx = c dz W^T,  dw = c x^T dz,                          c = scale / n or scale
+ * dz is rounded to `dtype` as the operand of both products; sums in fp32 over all
+ * pieces, dx and dw rounded once.  Rows of tokens that are not counted, and padding
+ * columns, get zeros.  loss, lse: as the forward left them; mean [2] as well (not
+ * read with dloss, else needed); dloss [T] fp32 (device) or NULL.  dx [T, H] and
+ * dw [H, V] of `dtype` (device, out), either may be NULL (a frozen head); 16-byte
+ * aligned.  The rest as for the forward. */
+int moe_vocab_loss_bwd(int T, int H, int V, int vocab, int dtype, const void* x, const void* w, const int32_t* target,
+                       const float* loss, const float* lse, const float* mean, const float* dloss, float scale, void* dx,
+                       void* dw, void* workspace, size_t workspace_bytes, void* stream);
 
 /* One tensor of an AdamW step (device pointers, 16-byte aligned, scales 4-byte). */
 typedef struct moe_adamw_tensor {

@@ -65,6 +65,42 @@ def balance_bwd(l, counts, k, offsets, score, alpha, dloss):
     return dl, size
 
 
+# ---- vocabulary loss ---------------------------------------------------------------
+
+
+def vocab(x, w, y, n_classes, dloss=None, scale=1.0):
+    """loss, lse, mean, dx and dw in 64 bits, and what the gradients' errors are counted by: the sums of their terms'
+    sizes.  Rows that are not counted are not looked at."""
+    T, V = len(y), w.shape[1]
+    rows = np.flatnonzero((y >= 0) & (y < n_classes))
+    n = len(rows)
+    loss, lse, dx, dw = np.zeros(T), np.zeros(T), np.zeros(x.shape), np.zeros(w.shape)
+    sx, sw = np.zeros(x.shape), np.zeros(w.shape)
+    l = x[rows] @ w[:, :n_classes]
+    own = l[np.arange(n), y[rows]]
+    with np.errstate(all="ignore"):
+        others = l.copy()
+        others[np.arange(n), y[rows]] = -INF
+        top = np.maximum(others.max(1), -1e300) if n else np.zeros(0)
+        d = top + np.log(np.exp(others - top[:, None]).sum(1)) - own
+        loss[rows] = np.logaddexp(0.0, d)
+    lse[rows] = own + loss[rows]
+    p = np.exp(l - lse[rows][:, None])
+    p[np.arange(n), y[rows]] = np.expm1(-loss[rows])
+    c = scale * (1.0 / max(n, 1) if dloss is None else 1.0)
+    p = p * (1.0 if dloss is None else dloss[rows][:, None]) * c
+    dx[rows] = p @ w[:, :n_classes].T
+    dw[:, :n_classes] = x[rows].T @ p
+    sx[rows] = np.abs(p) @ np.abs(w[:, :n_classes]).T
+    sw[:, :n_classes] = np.abs(x[rows]).T @ np.abs(p)
+    mean = np.array([loss.sum() / n, 1.0 / n]) if n else np.zeros(2)
+    # the size of a logit's terms, row by row: what rounding its sum is counted by
+    size = np.zeros(T)
+    if n:
+        size[rows] = (np.abs(x[rows]) @ np.abs(w[:, :n_classes])).max(1)
+    return dict(loss=loss, lse=lse, mean=mean, dx=dx, dw=dw, sx=sx, sw=sw, size=size, n=n)
+
+
 # ---- AdamW -----------------------------------------------------------------------
 
 
