@@ -42,54 +42,69 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
 // Blocks of 256 elements share a power-of-two scale.  m: E4M3 (bias 7, largest
 // 448).  v, which has no sign and twice the range: 5 bits of exponent, 3 of
 // mantissa, code c = (8 + c % 8) 2^(c / 8 - 34), 0 zero, 254 the largest, 1.75.
-// Both keep NaN (0x7f, 255) for elements that are not finite.  A root of v that
-// was rounded to zero would divide by eps alone: what is not zero stays so.
+// Both keep NaN (0x7f, 255) for elements that are not finite (where v is not, m is
+// not: g^2 does not leave the range of 64 bits).  A root of v that was rounded to
+// zero would divide by eps alone: what is not zero stays so.
 //
 // m and v are formed in 64 bits, so that the code and the scale of every element
 // are those of the formula: in 32 bits one in some millions would fall on the
 // other side of a border, and differ by a whole code.
 constexpr int kMaxM = 126, kMaxV = 254;
 
-__device__ __forceinline__ float value_m(uint32_t code) { return __builtin_amdgcn_cvt_f32_fp8((int)code, 0); }
-__device__ __forceinline__ float value_v(uint32_t code) {
-  if (code == 255) return __builtin_nanf("");
-  return code == 0 ? 0.0f : __uint_as_float((code + ((127 - 31) << 3)) << 20);
+// The value of byte j of four codes of m, j a constant.
+__device__ __forceinline__ float value_m(uint32_t codes, int j) {
+  switch (j) {
+    case 0: return __builtin_amdgcn_cvt_f32_fp8((int)codes, 0);
+    case 1: return __builtin_amdgcn_cvt_f32_fp8((int)codes, 1);
+    case 2: return __builtin_amdgcn_cvt_f32_fp8((int)codes, 2);
+    default: return __builtin_amdgcn_cvt_f32_fp8((int)codes, 3);
+  }
+}
+// The value of a code of v, whose bits are a double's but for the bias.  (255 need not read as NaN in a step: m's code
+// says so too.)
+__device__ __forceinline__ double value_v(uint32_t code) {
+  return __hiloint2double(code == 0 ? 0 : (int)((code + ((1023 - 31) << 3)) << 17), 0);
 }
 
 // 2^e as a double.
 __device__ __forceinline__ double pow2(int e) { return __hiloint2double((e + 1023) << 20, 0); }
 
-// Exponent of the smallest power of two s with top <= 1.75 2^up s: 448 = 1.75 2^8.
-__device__ __forceinline__ int scale_exponent(float top, int up) {
-  const uint32_t bits = __float_as_uint(top);
+// Exponent of the smallest power of two s with top <= 1.75 2^up s: 448 = 1.75 2^8.  By top's bits as fp32 (infinity,
+// from a value past fp32's range, counts as the largest there).
+__device__ __forceinline__ int scale_exponent(uint32_t bits, int up) {
   const int e = (int)(bits >> 23) - 127 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0) - up;
   return min(max(e, -126), 127);  // subnormal tops lie below the first
 }
 
-// The size of a finite value as fp32, for the scale.
-__device__ __forceinline__ float size_of(double a) {
-  const float f = fabsf((float)a);
-  return a - a == 0.0 ? fminf(f, 3.402823466e38f) : 0.0f;
-}
+// Sign aside, the upper word of a double: 0x7ff00000 and more where it is not finite.
+__device__ __forceinline__ uint32_t upper(double a) { return (uint32_t)__double2hiint(a) & 0x7fffffffu; }
+__device__ __forceinline__ bool finite(double a) { return upper(a) < 0x7ff00000u; }
 
-// Codes of a >= 0 by their exponent and three bits of mantissa, from 2^least on in
-// steps of an eighth of the binade, below in those of that binade (codes from -8
-// on).  Rounded up for the share (h + 1/3) / 2^16 of what is left over (the third
-// keeps the border off values that short binary codes and gradients add up to).
-__device__ __forceinline__ int eighths(double a, int least, uint32_t h) {
-  const bool small = a < pow2(least);
-  const uint64_t b = (uint64_t)__double_as_longlong(small ? a + pow2(least) : a) + (((uint64_t)h << 33) + 0xaaaaaaaau);
-  return (int)(b >> 49) - ((1023 + least) << 3) - (small ? 8 : 0);
+// Exponent and three bits of mantissa of the double (hi, lo), rounded up by an
+// addition below them, 49 bits of h and a third: for the share (h + 1/3) / 2^16 of
+// what is left over (the third keeps the border off values that short binary codes
+// and gradients add up to).  Taken less e binades.  The lower words only carry.
+__device__ __forceinline__ int eighths(int hi, uint32_t lo, uint32_t h, int e) {
+  return (hi + (int)(h << 1) - (e << 20) + (lo > 0x55555555u ? 1 : 0)) >> 17;
 }
-__device__ __forceinline__ uint32_t code_m(double a, uint32_t h) {
-  if (a - a != 0.0) return 0x7f;
-  const int c = min(eighths(fabs(a), -6, h) + 8, kMaxM);  // 2^-6 has code 8
-  return (uint32_t)c | (a < 0.0 ? 0x80u : 0u);
+// The code of m's size at the scale 2^e, where that is 8 (2^-6) or more.
+__device__ __forceinline__ int size_code_m(double m, int e, uint32_t h) {
+  return eighths((int)upper(m), (uint32_t)__double2loint(m), h, e) - ((1022 - 6) << 3);
 }
-__device__ __forceinline__ uint32_t code_v(double a, uint32_t h) {
-  if (a - a != 0.0) return 255;
-  if (a == 0.0) return 0;
-  return (uint32_t)min(max(eighths(a, -31, h), 1), kMaxV);
+// The same below: steps stay as large as there.  2^-6 is added, and its eight codes come off.
+__device__ __forceinline__ int low_code_m(double m, int e, uint32_t h) {
+  const double a = fma(fabs(m), pow2(-e), 0x1p-6);
+  return eighths(__double2hiint(a), (uint32_t)__double2loint(a), h, 0) - ((1023 - 6) << 3);
+}
+__device__ __forceinline__ uint32_t code_m(double m, int size_code) {
+  const uint32_t c = (uint32_t)min(size_code, kMaxM) | (((uint32_t)__double2hiint(m) >> 24) & 0x80u);
+  return finite(m) ? c : 0x7fu;
+}
+// The code of v at the scale 2^e.
+__device__ __forceinline__ uint32_t code_v(double v, int e, uint32_t h) {
+  const int hi = __double2hiint(v);
+  const int c = eighths(hi, (uint32_t)__double2loint(v), h, e) - ((1023 - 31) << 3);
+  return v == 0.0 ? 0u : (uint32_t)min(max(c, 1), kMaxV);
 }
 
 // ---- the step ----------------------------------------------------------------------
@@ -107,6 +122,90 @@ struct AdamwArgs {
   uint32_t seed;
 };
 
+// Loads and stores of device memory through a pointer that was itself read from there (for the compiler it might point
+// into LDS or scratch).
+template <typename V>
+__device__ __forceinline__ V get(const void* p) {
+  return *(const __attribute__((address_space(1))) V*)p;
+}
+template <typename V>
+__device__ __forceinline__ void put(void* p, V v) {
+  *(__attribute__((address_space(1))) V*)p = v;
+}
+
+// Eight neighbouring elements, of which `live` are there (FULL: all).
+template <bool FULL>
+__device__ __forceinline__ void get8(const float* p, int live, float (&v)[8]) {
+  if (FULL || live == 8) {
+    const f32x4 lo = get<f32x4>(p), hi = get<f32x4>(p + 4);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < 4 ? lo[j] : hi[j - 4];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < live ? get<float>(p + j) : 0.0f;
+  }
+}
+template <bool FULL>
+__device__ __forceinline__ void get8(const uint16_t* p, int live, float (&v)[8]) {
+  if (FULL || live == 8) {
+    const u32x4 q = get<u32x4>(p);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (j & 1) ? bf_hi(q[j >> 1]) : bf_lo(q[j >> 1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < live ? bf2f(get<uint16_t>(p + j)) : 0.0f;
+  }
+}
+template <bool FULL>
+__device__ __forceinline__ u32x2 get_codes(const void* p, int live) {
+  if (FULL || live == 8) return get<u32x2>(p);
+  u32x2 q = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) q[j >> 2] |= (j < live ? (uint32_t)get<uint8_t>((const uint8_t*)p + j) : 0u) << (8 * (j & 3));
+  return q;
+}
+template <bool FULL>
+__device__ __forceinline__ void put8(float* p, int live, const float (&v)[8]) {
+  if (FULL || live == 8) {
+    put(p, f32x4{v[0], v[1], v[2], v[3]});
+    put(p + 4, f32x4{v[4], v[5], v[6], v[7]});
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < live) put(p + j, v[j]);
+  }
+}
+// bf16 values by their bits.
+template <bool FULL>
+__device__ __forceinline__ void put_bits(uint16_t* p, int live, const uint32_t (&q)[8]) {
+  if (FULL || live == 8) {
+    put(p, u32x4{q[0] | q[1] << 16, q[2] | q[3] << 16, q[4] | q[5] << 16, q[6] | q[7] << 16});
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < live) put(p + j, (uint16_t)q[j]);
+  }
+}
+template <bool FULL>
+__device__ __forceinline__ void put_codes(void* p, int live, u32x2 q) {
+  if (FULL || live == 8) return put(p, q);
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < live) put((uint8_t*)p + j, (uint8_t)(q[j >> 2] >> (8 * (j & 3))));
+}
+
+// A value that all lanes hold, in scalar registers.
+template <typename V>
+__device__ __forceinline__ V uniform(V v) {
+  static_assert(sizeof(V) % 4 == 0, "whole words");
+  uint32_t w[sizeof(V) / 4];
+  __builtin_memcpy(w, &v, sizeof(V));
+#pragma unroll
+  for (size_t i = 0; i < sizeof(V) / 4; ++i) w[i] = __builtin_amdgcn_readfirstlane(w[i]);
+  __builtin_memcpy(&v, w, sizeof(V));
+  return v;
+}
+
 // What all elements share.
 struct Shared {
   double gs;
@@ -114,19 +213,116 @@ struct Shared {
   uint32_t key;
 };
 
+// Root and reciprocal by the hardware's, each within 2^-23 of its value (a subnormal v's root is below 1e-19 and any
+// eps of use).
 __device__ __forceinline__ float updated(float p, float keep, float m, float v, const Shared& sh, float eps) {
-  return p * keep - sh.step1 * (m / (sqrtf(v) * sh.inv_root2 + eps));
+  return p * keep - sh.step1 * (m * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v) * sh.inv_root2 + eps));
 }
 
 // bf16 of p, rounded by 16 of the hash's bits.
 __device__ __forceinline__ uint32_t dithered(float p, uint32_t r) {
   const uint32_t bits = __float_as_uint(p);
-  if ((bits & 0x7f800000u) == 0x7f800000u) return f2bf(p);
-  return (bits + ((r * 0x9e3779b1u) >> 16)) >> 16;
+  const uint32_t up = (bits + ((r * 0x9e3779b1u) >> 16)) >> 16;  // infinities stay: nothing is below their 16 bits
+  return p != p ? 0x7fc0u : up;
+}
+
+// One pass over a chunk: eight elements a thread, from element `at` of tensor e on.
+template <typename T, bool MASTER, bool SMALL, bool FULL>
+__device__ __forceinline__ void adamw_pass(const AdamwArgs& g, const Shared& sh, const AdamwEntry& e, int64_t at) {
+  const int live = FULL ? 8 : (int)min((int64_t)8, max((int64_t)0, e.numel - at));
+  const float keep = (float)(1.0 - (double)sh.lr * e.decay);
+  float p[8], gr[8];
+  get8<FULL>((const T*)e.grad + at, live, gr);
+  if constexpr (MASTER) get8<FULL>(e.master + at, live, p);
+  else get8<FULL>((const T*)e.param + at, live, p);
+  uint32_t r[8];
+  if (SMALL || (!MASTER && sizeof(T) == 2)) {
+    const uint64_t place = (uint64_t)e.first * kAdamwBlock + (uint64_t)at;
+    uint32_t key = sh.key;
+    if (place >> 32) key ^= mix32((uint32_t)(place >> 32));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = mix32(((uint32_t)place ^ key) ^ j);  // places of runs are multiples of 8
+  }
+  if constexpr (!SMALL) {
+    const float b1 = (float)g.beta1, a1 = (float)(1.0 - g.beta1), b2 = (float)g.beta2, a2 = (float)(1.0 - g.beta2);
+    const float gs = (float)sh.gs;
+    float m[8], v[8];
+    float *mp = (float*)e.m + at, *vp = (float*)e.v + at;
+    get8<FULL>(mp, live, m);
+    get8<FULL>(vp, live, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float gj = gr[j] * gs;
+      m[j] = b1 * m[j] + a1 * gj;
+      v[j] = b2 * v[j] + a2 * gj * gj;
+      p[j] = updated(p[j], keep, m[j], v[j], sh, g.eps);
+    }
+    put8<FULL>(mp, live, m);
+    put8<FULL>(vp, live, v);
+  } else {
+    uint8_t *mp = (uint8_t*)e.m + at, *vp = (uint8_t*)e.v + at;
+    const int64_t block = at / kAdamwBlock;
+    const u32x2 mc = get_codes<FULL>(mp, live), vc = get_codes<FULL>(vp, live);
+    // scales are powers of two: their products with the betas are exact
+    const double bm = live > 0 ? g.beta1 * (double)get<float>(e.m_scale + block) : 0.0;
+    const double bv = live > 0 ? g.beta2 * (double)get<float>(e.v_scale + block) : 0.0;
+    const double am = (1.0 - g.beta1) * sh.gs, av = (1.0 - g.beta2) * sh.gs * sh.gs;
+    double m[8], v[8];
+    uint32_t top_m = 0, top_v = 0;  // as fp32 bits: the order of what is not negative
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const double gj = (double)gr[j];
+      m[j] = fma(gj, am, (double)value_m(mc[j >> 2], j & 3) * bm);
+      v[j] = fma(gj * gj, av, value_v((vc[j >> 2] >> (8 * (j & 3))) & 255) * bv);
+      const float mf = (float)m[j], vf = (float)v[j];
+      p[j] = updated(p[j], keep, mf, vf, sh, g.eps);
+      const bool ok = finite(m[j]);
+      top_m = max(top_m, ok ? __float_as_uint(mf) & 0x7fffffffu : 0u);
+      top_v = max(top_v, ok ? __float_as_uint(vf) : 0u);
+    }
+    top_m = row_max(top_m);  // the 32 lanes of a block
+    top_v = row_max(top_v);
+    top_m = max(top_m, (uint32_t)__shfl_xor((int)top_m, 16, kWave));
+    top_v = max(top_v, (uint32_t)__shfl_xor((int)top_v, 16, kWave));
+    const int em = scale_exponent(top_m, 8), ev = scale_exponent(top_v, 0);
+    int c[8];
+    bool low = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      c[j] = size_code_m(m[j], em, r[j] & 0xffffu);
+      low |= c[j] < 8;
+    }
+    if (__ballot(low)) {  // few waves: 2^-14.8 of the block's largest
+#pragma unroll
+      for (int j = 0; j < 8; ++j) c[j] = c[j] < 8 ? low_code_m(m[j], em, r[j] & 0xffffu) : c[j];
+    }
+    u32x2 mq = {0, 0}, vq = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      mq[j >> 2] |= code_m(m[j], c[j]) << (8 * (j & 3));
+      const uint32_t cv = code_v(v[j], ev, r[j] >> 16);
+      vq[j >> 2] |= (finite(m[j]) ? cv : 255u) << (8 * (j & 3));
+    }
+    put_codes<FULL>(mp, live, mq);
+    put_codes<FULL>(vp, live, vq);
+    if ((threadIdx.x & 31) == 0 && live > 0) {
+      put(e.m_scale + block, (float)pow2(em));
+      put(e.v_scale + block, (float)pow2(ev));
+    }
+  }
+  if constexpr (sizeof(T) == 4) {
+    put8<FULL>((float*)e.param + at, live, p);
+  } else {
+    uint32_t q[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = MASTER ? f2bf(p[j]) : dithered(p[j], r[j]);
+    if constexpr (MASTER) put8<FULL>(e.master + at, live, p);
+    put_bits<FULL>((uint16_t*)e.param + at, live, q);
+  }
 }
 
 template <typename T, bool MASTER, bool SMALL>
-__global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs g) {
+__global__ __launch_bounds__(256, SMALL ? 4 : 1) void adamw_kernel(AdamwArgs g) {
   __shared__ Shared s_sh;
   const int tid = threadIdx.x;
   if (tid == 0) {
@@ -139,9 +335,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs g) {
     s_sh.key = mix32(mix32((uint32_t)t) + g.seed);
   }
   __syncthreads();
-  const Shared sh = s_sh;
-  const float b1 = (float)g.beta1, a1 = (float)(1.0 - g.beta1), b2 = (float)g.beta2, a2 = (float)(1.0 - g.beta2);
-  const float gs = (float)sh.gs;
+  const Shared sh = uniform(s_sh);
   int i = 0;
   int64_t from = 0, to = 0;  // chunks of tensor i
   AdamwEntry e{};
@@ -154,136 +348,11 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs g) {
       }
       from = g.starts[i];
       to = g.starts[i + 1];
-      e = g.entries[i];
+      e = uniform(g.entries[i]);
     }
-    const int64_t at = (chunk - from) * kAdamwChunk + 8 * tid;  // of this thread's eight elements
-    const int live = (int)min((int64_t)8, max((int64_t)0, e.numel - at));
-    const float keep = (float)(1.0 - (double)sh.lr * e.decay);
-    const uint64_t place = (uint64_t)e.first * kAdamwBlock + (uint64_t)at;
-    float p[8], gr[8];
-    T* param = (T*)e.param + at;
-    const T* grad = (const T*)e.grad + at;
-    if (live == 8) {
-      load8(grad, gr);
-      if (MASTER) load8(e.master + at, p);
-      else load8(param, p);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        gr[j] = j < live ? load1(grad + j) : 0.0f;
-        p[j] = j < live ? (MASTER ? e.master[at + j] : load1(param + j)) : 0.0f;
-      }
-    }
-    uint32_t r[8];
-    if (SMALL || (!MASTER && sizeof(T) == 2)) {
-      const uint32_t key = sh.key ^ mix32((uint32_t)(place >> 32)) * (uint32_t)((place >> 32) != 0);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) r[j] = mix32(((uint32_t)place + j) ^ key);
-    }
-    if (!SMALL) {
-      float m[8], v[8];
-      float *mp = (float*)e.m + at, *vp = (float*)e.v + at;
-      if (live == 8) {
-        load8(mp, m);
-        load8(vp, v);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          m[j] = j < live ? mp[j] : 0.0f;
-          v[j] = j < live ? vp[j] : 0.0f;
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float gj = gr[j] * gs;
-        m[j] = b1 * m[j] + a1 * gj;
-        v[j] = b2 * v[j] + a2 * gj * gj;
-        p[j] = updated(p[j], keep, m[j], v[j], sh, g.eps);
-      }
-      if (live == 8) {
-        store8(mp, m);
-        store8(vp, v);
-      } else {
-        for (int j = 0; j < live; ++j) {
-          mp[j] = m[j];
-          vp[j] = v[j];
-        }
-      }
-    } else {
-      uint8_t *mp = (uint8_t*)e.m + at, *vp = (uint8_t*)e.v + at;
-      uint32_t mc[2] = {}, vc[2] = {};
-      if (live == 8) {
-        const u32x2 a = *(const u32x2*)mp, b = *(const u32x2*)vp;
-        mc[0] = a[0], mc[1] = a[1], vc[0] = b[0], vc[1] = b[1];
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          mc[j >> 2] |= (j < live ? (uint32_t)mp[j] : 0u) << (8 * (j & 3));
-          vc[j >> 2] |= (j < live ? (uint32_t)vp[j] : 0u) << (8 * (j & 3));
-        }
-      }
-      const int64_t block = at / kAdamwBlock;
-      const double ms = live > 0 ? (double)e.m_scale[block] : 0.0, vs = live > 0 ? (double)e.v_scale[block] : 0.0;
-      double m[8], v[8];
-      float top_m = 0.0f, top_v = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const double gj = (double)gr[j] * sh.gs;
-        m[j] = g.beta1 * ((double)value_m((mc[j >> 2] >> (8 * (j & 3))) & 255) * ms) + (1.0 - g.beta1) * gj;
-        v[j] = g.beta2 * ((double)value_v((vc[j >> 2] >> (8 * (j & 3))) & 255) * vs) + (1.0 - g.beta2) * gj * gj;
-        p[j] = updated(p[j], keep, (float)m[j], (float)v[j], sh, g.eps);
-        top_m = fmaxf(top_m, size_of(m[j]));
-        top_v = fmaxf(top_v, size_of(v[j]));
-      }
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) {  // the 32 lanes of a block
-        top_m = fmaxf(top_m, __shfl_xor(top_m, o, kWave));
-        top_v = fmaxf(top_v, __shfl_xor(top_v, o, kWave));
-      }
-      const int em = scale_exponent(top_m, 8), ev = scale_exponent(top_v, 0);
-      const double im = pow2(-em), iv = pow2(-ev);
-      mc[0] = mc[1] = vc[0] = vc[1] = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        mc[j >> 2] |= code_m(m[j] * im, r[j] & 0xffffu) << (8 * (j & 3));
-        vc[j >> 2] |= code_v(v[j] * iv, r[j] >> 16) << (8 * (j & 3));
-      }
-      if (live == 8) {
-        *(u32x2*)mp = u32x2{mc[0], mc[1]};
-        *(u32x2*)vp = u32x2{vc[0], vc[1]};
-      } else {
-        for (int j = 0; j < live; ++j) {
-          mp[j] = (uint8_t)(mc[j >> 2] >> (8 * (j & 3)));
-          vp[j] = (uint8_t)(vc[j >> 2] >> (8 * (j & 3)));
-        }
-      }
-      if ((tid & 31) == 0 && live > 0) {
-        e.m_scale[block] = (float)pow2(em);
-        e.v_scale[block] = (float)pow2(ev);
-      }
-    }
-    if (MASTER) {
-      if (live == 8) {
-        store8(e.master + at, p);
-        store8(param, p);
-      } else {
-        for (int j = 0; j < live; ++j) {
-          e.master[at + j] = p[j];
-          store1(param + j, p[j]);
-        }
-      }
-    } else if constexpr (sizeof(T) == 2) {
-      uint32_t q[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) q[j] = dithered(p[j], r[j]);
-      if (live == 8) *(u32x4*)param = u32x4{q[0] | q[1] << 16, q[2] | q[3] << 16, q[4] | q[5] << 16, q[6] | q[7] << 16};
-      else
-        for (int j = 0; j < live; ++j) param[j] = (T)q[j];
-    } else {
-      if (live == 8) store8(param, p);
-      else
-        for (int j = 0; j < live; ++j) store1(param + j, p[j]);
-    }
+    const int64_t first = (chunk - from) * kAdamwChunk;
+    if (first + kAdamwChunk <= e.numel) adamw_pass<T, MASTER, SMALL, true>(g, sh, e, first + 8 * tid);
+    else adamw_pass<T, MASTER, SMALL, false>(g, sh, e, first + 8 * tid);
   }
   // The last workgroup to get here counts the step: every one has read the counter.
   if (tid == 0 && (uint32_t)atomicAdd((uint32_t*)g.counter + 1, 1u) == gridDim.x - 1) {
@@ -298,26 +367,20 @@ __global__ __launch_bounds__(256) void adamw_moments_kernel(int64_t numel, const
                                                             const float* __restrict__ m_scale,
                                                             const float* __restrict__ v_scale, float* __restrict__ m_out,
                                                             float* __restrict__ v_out) {
-  for (int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; at < numel; at += (int64_t)gridDim.x * 2048) {
-    const double ms = (double)m_scale[at / kAdamwBlock], vs = (double)v_scale[at / kAdamwBlock];
-    const int live = (int)min((int64_t)8, numel - at);
-    float a[8], b[8];
-    if (live == 8) {
-      const u32x2 mc = *(const u32x2*)(m + at), vc = *(const u32x2*)(v + at);
+  const int64_t at = ((int64_t)group_id() * 256 + threadIdx.x) * 8;
+  if (at >= numel) return;
+  const double ms = (double)m_scale[at / kAdamwBlock], vs = (double)v_scale[at / kAdamwBlock];
+  const int live = (int)min((int64_t)8, numel - at);
+  const u32x2 mc = get_codes<false>(m + at, live), vc = get_codes<false>(v + at, live);
+  float a[8], b[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        a[j] = (float)((double)value_m((mc[j >> 2] >> (8 * (j & 3))) & 255) * ms);
-        b[j] = (float)((double)value_v((vc[j >> 2] >> (8 * (j & 3))) & 255) * vs);
-      }
-      store8(m_out + at, a);
-      store8(v_out + at, b);
-    } else {
-      for (int j = 0; j < live; ++j) {
-        m_out[at + j] = (float)((double)value_m(m[at + j]) * ms);
-        v_out[at + j] = (float)((double)value_v(v[at + j]) * vs);
-      }
-    }
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t c = (vc[j >> 2] >> (8 * (j & 3))) & 255;
+    a[j] = (float)((double)value_m(mc[j >> 2], j & 3) * ms);
+    b[j] = c == 255 ? __builtin_nanf("") : (float)(value_v(c) * vs);
   }
+  put8<false>(m_out + at, live, a);
+  put8<false>(v_out + at, live, b);
 }
 
 struct Plan {
@@ -374,7 +437,10 @@ hipError_t launch_adamw(const void* plan, const void* plan_device, const AdamwSt
   g.log_beta2 = a.beta2 > 0.0 ? log(a.beta2) : -__builtin_inf();
   g.eps = (float)a.eps;
   g.seed = a.seed;
-  const dim3 grid((unsigned)std::max<int64_t>(1, std::min<int64_t>(h.chunks, 2048))), block(256);
+  // 32-bit moments are bound by HBM, best with one workgroup on a CU (151M weights with masters: 256 workgroups 808 us,
+  // 512 835, 2048 859); the codes' arithmetic wants every SIMD full (256 workgroups 660 us, 1024 395, 2048 375).
+  const int64_t most = h.small ? 2048 : 256;
+  const dim3 grid((unsigned)std::max<int64_t>(1, std::min(h.chunks, most))), block(256);
   auto run = [&](auto kernel) {
     MOE_LAUNCH(kernel, grid, block, 0, stream, g);
     return hipGetLastError();
@@ -387,8 +453,7 @@ hipError_t launch_adamw(const void* plan, const void* plan_device, const AdamwSt
 
 hipError_t launch_adamw_moments(int64_t numel, const uint8_t* m, const uint8_t* v, const float* m_scale,
                                 const float* v_scale, float* m_out, float* v_out, hipStream_t stream) {
-  const dim3 grid((unsigned)std::min<int64_t>((numel + 2047) / 2048, 8192));
-  MOE_LAUNCH(adamw_moments_kernel, grid, dim3(256), 0, stream, numel, m, v, m_scale, v_scale, m_out, v_out);
+  MOE_LAUNCH(adamw_moments_kernel, wide_grid((numel + 2047) / 2048), dim3(256), 0, stream, numel, m, v, m_scale, v_scale, m_out, v_out);
   return hipGetLastError();
 }
 
