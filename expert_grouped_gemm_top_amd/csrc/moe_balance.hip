@@ -35,11 +35,12 @@ __device__ __forceinline__ double loss_factor(const BalanceArgs& g) {
   return N > 0 ? (double)g.alpha * g.E / ((double)g.k * N) : 0.0;
 }
 
-// One token's logits over its 16 lanes: runs of R experts (four where rows
-// are 16-byte aligned), every sixteenth run of a lane; -inf past the last.
-template <bool QUAD>
+// One token's logits over its 16 lanes: N runs of R experts a lane (four where rows
+// are 16-byte aligned), every sixteenth run; -inf past the last.
+template <int R_, int N_>
 struct Token {
-  static constexpr int R = QUAD ? 4 : 1, N = kMaxExperts / (kRow * R);
+  static constexpr int R = R_, N = N_;
+  static constexpr bool QUAD = R == 4;
   float v[N][R];
   static __device__ __forceinline__ int expert(int i, int li) { return R * (li + kRow * i); }
   __device__ __forceinline__ void load(const float* __restrict__ l, int E, int li) {
@@ -68,13 +69,13 @@ struct Token {
   __device__ __forceinline__ void to_shares(int score, float top) {
     float m = score == 0 ? top : fminf(top, 0.0f);
     if (m == -__builtin_inff()) m = 0.0f;
-    const float em = score == 0 ? 0.0f : expf(m);
+    const float em = score == 0 ? 0.0f : quick_exp(m);
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
       for (int j = 0; j < R; ++j) {
-        v[i][j] = score == 0 ? expf(v[i][j] - m) : __builtin_amdgcn_rcpf(expf(m - v[i][j]) + em);
+        v[i][j] = score == 0 ? quick_exp(v[i][j] - m) : __builtin_amdgcn_rcpf(quick_exp(m - v[i][j]) + em);
         sum += v[i][j];
       }
     sum = row_add(sum);
@@ -99,28 +100,37 @@ __device__ __forceinline__ double group_sum(double v, double* s) {
   return v;
 }
 
-// Partial sums of `splits` workgroups per sequence, and what the last kernel joins.
+// Partial sums of the workgroups, `most` at most for a sequence, and what the last kernel joins.
 struct BalanceParts {
-  float* p;       // [n_seq][splits][E]
-  int32_t* c;     // [n_seq][splits][E]
+  int most;
+  float* p;       // [n_seq][most][E]
+  int32_t* c;     // [n_seq][most][E]
   double* loss;   // a term of each workgroup of the second kernel
   uint32_t* done; // how many of them have ended, set to 0 by the first kernel
 };
 
-// Workgroup (j, s): rows j of `splits` parts of sequence s.  ONE: it is the only
-// workgroup, and writes the results itself.
-template <bool QUAD, bool ONE, int NT>
-__global__ __launch_bounds__(NT) void balance_rows_kernel(BalanceArgs g, BalanceParts part, int32_t* __restrict__ counts,
-                                                          float* __restrict__ mean_p, float* __restrict__ loss) {
-  using Tok = Token<QUAD>;
+constexpr int kRowThreads = 1024, kRowsAtOnce = kRowThreads / kRow;
+// Rows of a workgroup for a sequence of n: as many as it takes at once, or what `most` workgroups must take.
+__device__ __forceinline__ int rows_each(int n, int most) {
+  return max(kRowsAtOnce, ((n + most - 1) / most + kRowsAtOnce - 1) / kRowsAtOnce * kRowsAtOnce);
+}
+
+// Workgroup (j, s): the j-th run of sequence s' rows.  ONE: it is the only workgroup, and writes the results itself.
+template <typename Tok, bool ONE>
+__global__ __launch_bounds__(kRowThreads) void balance_rows_kernel(BalanceArgs g, BalanceParts part,
+                                                                   int32_t* __restrict__ counts,
+                                                                   float* __restrict__ mean_p, float* __restrict__ loss) {
+  constexpr int NT = kRowThreads;
   __shared__ float s_p[NT / 64][kMaxExperts];
   __shared__ int s_c[kMaxExperts];
   __shared__ double s_sum[NT / 64];
-  const int tid = threadIdx.x, li = tid & 15, splits = gridDim.x, s = blockIdx.y;
+  const int tid = threadIdx.x, li = tid & 15, s = blockIdx.y;
   const Rows rows = rows_of(g.offsets, s, g.T);
-  const int64_t n = rows.end - rows.begin;
-  const int begin = rows.begin + (int)(n * blockIdx.x / splits), end = rows.begin + (int)(n * (blockIdx.x + 1) / splits);
+  const int n = rows.end - rows.begin;
   if (!ONE && blockIdx.x == 0 && s == 0 && tid == 0) *part.done = 0;
+  const int64_t each = ONE ? n : rows_each(n, part.most), begin = rows.begin + each * blockIdx.x;
+  const int64_t end = min(begin + each, (int64_t)rows.end);
+  if (!ONE && begin >= end) return;
   for (int e = tid; e < kMaxExperts; e += NT) s_c[e] = 0;
   __syncthreads();
   float acc[Tok::N][Tok::R] = {};
@@ -158,7 +168,7 @@ __global__ __launch_bounds__(NT) void balance_rows_kernel(BalanceArgs g, Balance
       mean_p[tid] = mean;
       term = (double)s_c[tid] * mean;
     } else {
-      const size_t at = ((size_t)s * splits + blockIdx.x) * g.E + tid;
+      const size_t at = ((size_t)s * part.most + blockIdx.x) * g.E + tid;
       part.p[at] = v;
       part.c[at] = s_c[tid];
     }
@@ -170,9 +180,8 @@ __global__ __launch_bounds__(NT) void balance_rows_kernel(BalanceArgs g, Balance
 
 // Workgroup (j, s) joins the parts of sequence s for 32 experts; the last one to end adds all terms in order.
 constexpr int kJoinCols = 32;
-__global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs g, BalanceParts part, int splits,
-                                                            int32_t* __restrict__ counts, float* __restrict__ mean_p,
-                                                            float* __restrict__ loss) {
+__global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs g, BalanceParts part, int32_t* __restrict__ counts,
+                                                            float* __restrict__ mean_p, float* __restrict__ loss) {
   __shared__ float s_p[32][kJoinCols];
   __shared__ int s_c[32][kJoinCols];
   __shared__ double s_sum[16];
@@ -183,9 +192,10 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs g, Balan
   float p = 0.0f;
   int c = 0;
   if (e < g.E) {
-    const size_t first = (size_t)s * splits * g.E + e;
+    const int each = rows_each(n, part.most), runs = (n + each - 1) / each;
+    const size_t first = (size_t)s * part.most * g.E + e;
 #pragma unroll 8
-    for (int i = q; i < splits; i += 32) {
+    for (int i = q; i < runs; i += 32) {
       p += part.p[first + (size_t)i * g.E];
       c += part.c[first + (size_t)i * g.E];
     }
@@ -225,11 +235,10 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs g, Balan
 // The gradient.  c_e - sum_j p_j c_j is formed from differences to the likeliest
 // expert's count, d_j = c_j - c_top: of a confident token's top expert it is
 // -sum_{j != top} p_j d_j, without the difference of two large numbers.
-template <bool QUAD>
+template <typename Tok>
 __global__ __launch_bounds__(256) void balance_bwd_kernel(BalanceArgs g, const int32_t* __restrict__ counts,
                                                           const float* __restrict__ dloss, const float* dl_add,
                                                           float* dlogits) {
-  using Tok = Token<QUAD>;
   const int li = threadIdx.x & 15, S = g.offsets == nullptr ? 1 : g.n_seq;
   const float factor = (float)(loss_factor(g) * (dloss != nullptr ? (double)*dloss : 1.0));
   int s = -1;
@@ -267,7 +276,7 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(BalanceArgs g, const i
 #pragma unroll
         for (int j = 0; j < Tok::R; ++j) {
           if (tok.v[i][j] == top) c_top = max(c_top, (uint32_t)c[i][j]);
-          rest[i][j] = g.score == 0 ? 1.0f : __builtin_amdgcn_rcpf(1.0f + expf(tok.v[i][j]));
+          rest[i][j] = g.score == 0 ? 1.0f : __builtin_amdgcn_rcpf(1.0f + quick_exp(tok.v[i][j]));
         }
       c_top = row_max(c_top);
       tok.to_shares(g.score, top);
@@ -290,7 +299,7 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(BalanceArgs g, const i
       const int e = Tok::expert(i, li);
       if (e >= g.E) continue;
       const int64_t at = t * g.E + e;
-      if (QUAD) {
+      if (Tok::QUAD) {
         f32x4 v = {d[i][0], d[i][1 % Tok::R], d[i][2 % Tok::R], d[i][3 % Tok::R]};
         if (dl_add != nullptr) v += *(const f32x4*)(dl_add + at);
         *(f32x4*)(dlogits + at) = v;
@@ -301,10 +310,10 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(BalanceArgs g, const i
   }
 }
 
-constexpr int kRowThreads = 1024;  // 64 rows at once
-// Workgroups per sequence: 64 rows each at an even split, 1024 in all.
-int balance_splits(int T, int n_seq) {
-  return std::max(1, std::min((int)(((int64_t)T + 63) / 64), 1024) / n_seq);
+// Workgroups that a sequence may have: 1024 in all.  Those past its rows end at once, so ragged sequences are shared
+// out nearly as evenly as equal ones (16384 tokens in 8 of them, both kernels: 1024 workgroups 14.8 us, 2048 16.5).
+int balance_most(int T, int n_seq) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>(((int64_t)T + kRowsAtOnce - 1) / kRowsAtOnce, 1024 / n_seq));
 }
 constexpr int kOneGroupRows = 256;  // up to here one workgroup does it all
 int join_groups(int E) { return (E + kJoinCols - 1) / kJoinCols; }
@@ -312,9 +321,10 @@ int join_groups(int E) { return (E + kJoinCols - 1) / kJoinCols; }
 bool balance_alone(int T, int n_seq) { return n_seq == 1 && T <= kOneGroupRows; }
 
 BalanceParts balance_parts(int T, int E, int n_seq, void* ws, size_t* bytes) {
-  const size_t n = (size_t)n_seq * balance_splits(T, n_seq) * E * 4;
   char* at = (char*)ws;
   BalanceParts p;
+  p.most = balance_most(T, n_seq);
+  const size_t n = (size_t)n_seq * p.most * E * 4;
   p.loss = (double*)at;
   at += (size_t)n_seq * join_groups(E) * sizeof(double);
   p.done = (uint32_t*)at;
@@ -336,41 +346,44 @@ size_t balance_workspace_bytes(int T, int E, int n_seq) {
   return bytes;
 }
 
+// Runs f for the runs of experts that E and the rows' alignment ask for.
+template <typename Fn>
+static hipError_t with_token(int E, bool aligned, Fn&& f) {
+  if (!aligned || E % 4 != 0) return f(Token<1, 16>{});
+  if (E <= 64) return f(Token<4, 1>{});
+  if (E <= 128) return f(Token<4, 2>{});
+  return f(Token<4, 4>{});
+}
+
 hipError_t launch_balance_fwd(const BalanceArgs& g, int32_t* counts, float* mean_p, float* loss, void* ws,
                               hipStream_t stream) {
-  const bool quad = g.E % 4 == 0 && ((uintptr_t)g.logits & 15) == 0;
-  if (balance_alone(g.T, g.n_seq)) {
-    if (quad)
-      MOE_LAUNCH((balance_rows_kernel<true, true, kRowThreads>), dim3(1), dim3(kRowThreads), 0, stream, g, BalanceParts{}, counts, mean_p,
-                 loss);
-    else
-      MOE_LAUNCH((balance_rows_kernel<false, true, kRowThreads>), dim3(1), dim3(kRowThreads), 0, stream, g, BalanceParts{}, counts,
-                 mean_p, loss);
-    return hipGetLastError();
-  }
+  const bool aligned = ((uintptr_t)g.logits & 15) == 0;
+  if (balance_alone(g.T, g.n_seq))
+    return with_token(g.E, aligned, [&](auto tok) {
+      MOE_LAUNCH((balance_rows_kernel<decltype(tok), true>), dim3(1), dim3(kRowThreads), 0, stream, g, BalanceParts{},
+                 counts, mean_p, loss);
+      return hipGetLastError();
+    });
   size_t bytes;
   const BalanceParts part = balance_parts(g.T, g.E, g.n_seq, ws, &bytes);
-  const int splits = balance_splits(g.T, g.n_seq);
-  if (quad)
-    MOE_LAUNCH((balance_rows_kernel<true, false, kRowThreads>), dim3(splits, g.n_seq), dim3(kRowThreads), 0, stream, g, part, counts,
-               mean_p, loss);
-  else
-    MOE_LAUNCH((balance_rows_kernel<false, false, kRowThreads>), dim3(splits, g.n_seq), dim3(kRowThreads), 0, stream, g, part, counts,
-               mean_p, loss);
-  hipError_t err = hipGetLastError();
+  hipError_t err = with_token(g.E, aligned, [&](auto tok) {
+    MOE_LAUNCH((balance_rows_kernel<decltype(tok), false>), dim3(part.most, g.n_seq), dim3(kRowThreads), 0, stream, g, part,
+               counts, mean_p, loss);
+    return hipGetLastError();
+  });
   if (err != hipSuccess) return err;
-  MOE_LAUNCH(balance_join_kernel, dim3(join_groups(g.E), g.n_seq), dim3(1024), 0, stream, g, part, splits, counts, mean_p, loss);
+  MOE_LAUNCH(balance_join_kernel, dim3(join_groups(g.E), g.n_seq), dim3(1024), 0, stream, g, part, counts, mean_p, loss);
   return hipGetLastError();
 }
 
 hipError_t launch_balance_bwd(const BalanceArgs& g, const int32_t* counts, const float* dloss, const float* dl_add,
                               float* dlogits, hipStream_t stream) {
-  const bool quad =
-      g.E % 4 == 0 && (((uintptr_t)g.logits | (uintptr_t)dl_add | (uintptr_t)dlogits) & 15) == 0;
+  const bool aligned = (((uintptr_t)g.logits | (uintptr_t)dl_add | (uintptr_t)dlogits) & 15) == 0;
   const dim3 grid((unsigned)std::min<int64_t>(((int64_t)g.T + 15) / 16, 1 << 14)), block(256);
-  if (quad) MOE_LAUNCH(balance_bwd_kernel<true>, grid, block, 0, stream, g, counts, dloss, dl_add, dlogits);
-  else MOE_LAUNCH(balance_bwd_kernel<false>, grid, block, 0, stream, g, counts, dloss, dl_add, dlogits);
-  return hipGetLastError();
+  return with_token(g.E, aligned, [&](auto tok) {
+    MOE_LAUNCH(balance_bwd_kernel<decltype(tok)>, grid, block, 0, stream, g, counts, dloss, dl_add, dlogits);
+    return hipGetLastError();
+  });
 }
 
 }  // namespace moe

@@ -180,6 +180,8 @@ __device__ __forceinline__ void finish8(const LinearProduct& g, int64_t m, int n
 // Eight outputs of a tile: to the slice's partials or through the epilogue.
 template <typename T>
 struct Leave {
+  template <typename C>
+  static constexpr bool kWhole = false;
   const LinearProduct& g;
   int slice;
   // N is a multiple of 8: a run is all in or all out

@@ -171,6 +171,37 @@ struct Tile {
 };
 constexpr int kTileThreads = 512;
 
+// A tile's sums as bf16 rows: make(row, col, v) turns four neighbouring sums (row and
+// column of the tile) into the values to store, put(row, col, q) stores eight of
+// them.  They change places in LDS, [row][BN] with 16-byte chunk c of row r at
+// c ^ (r mod 16), so that whole 16-byte lanes of contiguous row runs leave.
+template <typename C, int MI, int NJ, typename Make, typename Put>
+__device__ __forceinline__ void leave_bf16(f32x16 (&acc)[MI][NJ], unsigned char* s_dyn, Make&& make, Put&& put) {
+  constexpr int BM = C::BM, BN = C::BN, CH = BN / 8, KEY = CH < 16 ? CH - 1 : 15;
+  static_assert(C::KG == 1 && BM * BN * 2 <= C::LDS, "staging");
+  const int tid = threadIdx.x, l32 = tid & 31, hk = (tid >> 5) & 1, w = tid >> 6;
+  const int row0 = BM / C::WM * (w % C::WM) + l32, col0 = BN / (C::NW / C::WM) * (w / C::WM) + 4 * hk;
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int row = row0 + 32 * i, col = col0 + 32 * j + 8 * q;
+        float v[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        make(i, row, col, v);
+        *(u32x2*)(s_dyn + row * (2 * BN) + 16 * ((col >> 3) ^ (row & KEY)) + 2 * (col & 7)) =
+            u32x2{pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3])};
+      }
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the staged values are written
+  barrier_no_fence();
+#pragma unroll 4
+  for (int it = tid; it < BM * CH; it += 64 * C::NW) {
+    const int row = it / CH, c = it % CH;
+    put(row, 8 * c, *(const u32x4*)(s_dyn + row * (2 * BN) + 16 * (c ^ (row & KEY))));
+  }
+}
+
 // The tiles of moe_linear_plan.h.
 using Tile0 = Tile<256, 256, 8, 2, 1, 2>;
 using Tile1 = Tile<256, 128, 8, 4, 1, 3>;
@@ -191,7 +222,10 @@ using Tile5 = Tile<32, 32, 1, 1, 8, 2>;
 // is waited for before the last run of the one in front, so its first
 // fragments are read under those products, and its successor's loads go out in
 // two halves before the next two runs of products.
-// `out` gets the outputs: out.skip(m, n) says that a run is not wanted, and
+// `out` gets the outputs.  Where Out::kWhole (tiles of one reduction group), out.tile
+// gets the sums as they lie in the waves' registers, with the stage buffers free:
+// register r of acc[i][j] is row TM wm + 32 i + l32 of the tile, column
+// TN wn + 32 j + 8 (r / 4) + 4 hk + r % 4.  Else out.skip(m, n) says that a run is not wanted, and
 // out(m, n, v, lanes) takes the eight outputs of row m from column n on; `lanes`
 // neighbouring lanes, a constant, hold 8 lanes neighbouring columns of a row.
 template <typename T, bool AKC, bool BKC, typename C, bool TAIL, typename Out>
@@ -293,10 +327,15 @@ __device__ __forceinline__ void tile_product(const TileSource& g, int mt, int nt
     products(f1, mine, -1, f0);
   }
 
+  if constexpr (std::remove_reference_t<Out>::template kWhole<C>) {
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's last fragment reads are done
+    barrier_no_fence();                   // ... and every wave's
+    out.template tile<C>(acc, m0, n0, s_dyn);
+    return;
+  }
   // The fp32 tile leaves through the idle stage buffers, HC columns at a time
   // ([row][HC], 16-byte chunk c of row r at c ^ (r mod CH)), so that the epilogue
-  // reads and writes runs of eight neighbouring outputs.  Register r of
-  // acc[i][j] is row TM wm + 32 i + l32, column TN wn + 32 j + 8 (r / 4) + 4 hk + r % 4.
+  // reads and writes runs of eight neighbouring outputs.
   constexpr int FIT = C::FIT, HC = C::OUT_COLS;
   constexpr int CH = HC / 4 < 16 ? HC / 4 : 16;  // chunks that trade places
   static_assert(BM * HC * 4 <= STAGES * STAGE && HC % TN == 0 && BN % HC == 0, "staging");

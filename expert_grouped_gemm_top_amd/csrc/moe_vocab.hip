@@ -2,8 +2,7 @@
 // logits, and its gradients.
 //
 //   l_tv = x_t W_v,  loss_t = log sum_v exp(l_tv) - l_ty,  y = target[t]
-//   dz_tv = w_t (p_tv - [v = y]),  p = exp(l - lse)
-//   dx = c dz W^T,  dW = c x^T dz
+//   dz_tv = f_t (q_tv - [v = y]),  dx = c dz W^T,  dW = c x^T dz
 //
 // Tokens that are not counted are left out of every product: the first kernel
 // lists the others.  The forward's tiles of logits leave one maximum and sum of
@@ -11,14 +10,16 @@
 // in pieces: a piece's logits again, from them its dz, then both gradients' products
 // with it.
 //
-// The target's column is kept apart: with rest = sum_{v != y} exp(l_v - l_y),
-// loss = log(1 + rest), and its dz is expm1(-loss), both with all their digits where
-// a confident token's p is next to 1.
+// The target is kept apart from the other classes.  With rest = sum_{v != y} exp(l_v - l_y)
+// the loss is log(1 + rest); the gradient is the others' softmax q (q_y = 0, sum 1)
+// less the target's 1, times the others' probability f = rest / (1 + rest) =
+// -expm1(-loss), and the token's weight.  All have their digits where a confident
+// token's p is next to 1.
 //
-// dz is rounded to the element type, as the operand of both products.  It is held
-// without the common factor c, so that the targets' entries, mostly just above -1,
-// lose little by it; the others' errors go in all directions (bf16, 8192 tokens over
-// 65536 x 4096: dx 1.7e-3, dW 1.9e-3 of their norms off, 1.7e-3 of both by their own
+// The products take q - [v = y], rounded to the element type: its -1 is exact, and
+// the others' roundings go in all directions.  f is multiplied to dx's sums, and for
+// dW, which sums over the tokens, to their rows of x: rounded once more there
+// (bf16: dW is 2.4e-3 of its norm off, dx 1.7e-3, of which 1.7e-3 by their own
 // rounding).
 #include <algorithm>
 
@@ -38,9 +39,8 @@ struct Listed {
   int32_t* rows;  // [n] token
   int32_t* place; // [T] place of a token, -1 where not counted
   int32_t* y;     // [n] target
-  float* lse;     // [n] backward: as the forward left them
-  float* loss;
-  float* w;       // [n] backward: the token's weight
+  float* off;     // [n] backward: log of the others' sum of exponentials
+  float* f;       // [n] backward: their probability times the token's weight
 };
 
 // The tokens with a target in [0, vocab), in order, by one workgroup.  loss_out and lse_out (forward) become 0 for the others.
@@ -81,9 +81,9 @@ __global__ __launch_bounds__(1024) void vocab_list_kernel(int T, int vocab, cons
       out.rows[at] = (int)t;
       out.y[at] = y[j];
       if (loss_out == nullptr) {
-        out.loss[at] = loss[t];
-        out.lse[at] = lse[t];
-        out.w[at] = dloss != nullptr ? dloss[t] : 1.0f;
+        const float f = -expm1f(-loss[t]);
+        out.off[at] = f == 0.0f ? __builtin_inff() : lse[t] + logf(f);  // a loss of 0: no gradient
+        out.f[at] = dloss != nullptr ? dloss[t] * f : f;
       }
       ++at;
     }
@@ -105,13 +105,70 @@ __device__ __forceinline__ float exp_of(float v) {
 struct Run {
   float top, sum;
 };
+// Two runs of columns as one.  A NaN is in a sum, where it stays.
+__device__ __forceinline__ Run joined(const Run& a, const Run& b) {
+  const float top = fmaxf(a.top, b.top), base = top == -__builtin_inff() ? 0.0f : top;
+  return {top, a.sum * expf(a.top - base) + b.sum * expf(b.top - base)};
+}
 
+// Row statistics of a tile of logits.  Tiles of one reduction group (bf16) take them
+// from the waves' registers; where the groups' sums must be joined first they
+// come by eight columns.  At 256 x 256 over 2048 a tile's statistics cost
+// 3 of its 58 us (through LDS 7).
 template <typename T>
 struct LossOut {
+  template <typename C>
+  static constexpr bool kWhole = sizeof(T) == 2 && C::KG == 1;
   int n, vocab, pitch;
   const int32_t* y;
   float* own;  // [n] the targets' logits
   Run* runs;   // [run][pitch rows]
+
+  template <typename C, int MI, int NJ>
+  __device__ __forceinline__ void tile(f32x16 (&acc)[MI][NJ], int m0, int n0, unsigned char* s_dyn) const {
+    constexpr int BM = C::BM, WN = C::NW / C::WM, TM = BM / C::WM, TN = C::BN / WN;
+    const int tid = threadIdx.x, l32 = tid & 31, hk = (tid >> 5) & 1, w = tid >> 6, wm = w % C::WM, wn = w / C::WM;
+    const int first = n0 + TN * wn;  // this wave's columns
+    Run* s_run = reinterpret_cast<Run*>(s_dyn);  // [WN][BM]
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int row = TM * wm + 32 * i + l32, m = m0 + row;
+      const int at = (m < n ? y[m] : -1) - first;  // the target, if it is among them
+      if (__ballot(at >= 0 && at < TN) || first + TN > vocab) {  // a few waves, or the last columns
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int col = 32 * j + 8 * (r / 4) + 4 * hk + r % 4;
+            if (at == col) own[m] = acc[i][j][r];
+            if (at == col || first + col >= vocab) acc[i][j][r] = -__builtin_inff();
+          }
+      }
+      float top = -__builtin_inff();
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, acc[i][j][r]);
+      top = fmaxf(top, __shfl_xor(top, 32, kWave));
+      const float base = top == -__builtin_inff() ? 0.0f : top * 1.44269504f;
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sum += __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], 1.44269504f, -base));
+      sum += __shfl_xor(sum, 32, kWave);
+      if (hk == 0) s_run[wn * BM + row] = Run{top, sum};
+    }
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the waves' statistics are written
+    barrier_no_fence();
+    if (tid < BM && m0 + tid < n) {
+      Run a = s_run[tid];
+#pragma unroll
+      for (int i = 1; i < WN; ++i) a = joined(a, s_run[i * BM + tid]);
+      runs[(int64_t)(n0 / C::BN) * pitch + m0 + tid] = a;
+    }
+  }
+
   __device__ __forceinline__ bool skip(int, int) const { return false; }
   template <typename Lanes>
   __device__ __forceinline__ void operator()(int64_t m, int n0, float (&v)[8], Lanes) const {
@@ -162,7 +219,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void vocab_loss_kernel(LogitsArgs<
   tile_product<T, true, false, C, TAIL>(g, mt, nt, 0, a.K, s_dyn, LossOut<T>{g.M, vocab, pitch, a.list.y, own, runs});
 }
 
-// Joins the runs of 16 rows per workgroup, 16 threads each; the last workgroup adds up the mean.
+// Joins the runs of 16 rows per workgroup, 64 threads each; the last workgroup adds up the mean.
 struct JoinArgs {
   int n_runs, pitch;
   const Run* runs;
@@ -171,44 +228,36 @@ struct JoinArgs {
   double* part;  // a sum of losses of each workgroup
   float *loss, *lse, *mean;
 };
-__global__ __launch_bounds__(256) void vocab_join_kernel(JoinArgs a) {
-  __shared__ float s_top[16][17], s_sum[16][17];
+__global__ __launch_bounds__(1024) void vocab_join_kernel(JoinArgs a) {
+  __shared__ Run s_run[64][17];
   __shared__ double s_loss[16];
   __shared__ bool s_last;
   const int tid = threadIdx.x, r = tid & 15, q = tid >> 4, n = a.list.head[0];
   const int row = blockIdx.x * 16 + r;
   const int groups = max(1, (n + 15) / 16);
   if ((int)blockIdx.x >= groups) return;
-  float top = -__builtin_inff(), sum = 0.0f;
+  Run run{-__builtin_inff(), 0.0f};
   if (row < n)
-#pragma unroll 4
-    for (int i = q; i < a.n_runs; i += 16) {
-      const Run p = a.runs[(int64_t)i * a.pitch + row];
-      const float t = fmaxf(top, p.top);
-      const float base = t == -__builtin_inff() ? 0.0f : t;
-      sum = sum * expf(top - base) + p.sum * expf(p.top - base);
-      top = t;
-    }
-  s_top[q][r] = top;
-  s_sum[q][r] = sum;
+#pragma unroll 8
+    for (int i = q; i < a.n_runs; i += 64) run = joined(run, a.runs[(int64_t)i * a.pitch + row]);
+  s_run[q][r] = run;
   __syncthreads();
-  if (tid < 16) {
-    double l = 0.0;
-    if (row < n) {
-      for (int i = 1; i < 16; ++i) {
-        const float t = fmaxf(top, s_top[i][r]);
-        const float base = t == -__builtin_inff() ? 0.0f : t;
-        sum = sum * expf(top - base) + s_sum[i][r] * expf(s_top[i][r] - base);
-        top = t;
-      }
-      const float own = a.own[row], d = top + logf(sum) - own;  // log of the others' sum over the target's
-      const float loss = fmaxf(d, 0.0f) + log1pf(expf(-fabsf(d)));
-      const int t = a.list.rows[row];
+  // wave w joins row w: 64 runs over its lanes
+  const int w = tid >> 6, lane = tid & 63;
+  run = s_run[lane][w];
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) run = joined(run, Run{__shfl_xor(run.top, o, kWave), __shfl_xor(run.sum, o, kWave)});
+  if (lane == 0) {
+    const int at = blockIdx.x * 16 + w;
+    float loss = 0.0f;
+    if (at < n) {
+      const float own = a.own[at], d = run.top + logf(run.sum) - own;  // log of the others' sum over the target's
+      loss = fmaxf(d, 0.0f) + log1pf(expf(-fabsf(d)));
+      const int t = a.list.rows[at];
       a.loss[t] = loss;
       a.lse[t] = own + loss;
-      l = (double)loss;
     }
-    s_loss[tid] = l;
+    s_loss[w] = (double)loss;
   }
   __syncthreads();
   if (tid == 0) {
@@ -231,24 +280,61 @@ __global__ __launch_bounds__(256) void vocab_join_kernel(JoinArgs a) {
 
 // ---- the backward ---------------------------------------------------------------
 
+// q - [v = y] of a tile of logits.
 template <typename T>
 struct GradOut {
+  template <typename C>
+  static constexpr bool kWhole = sizeof(T) == 2 && C::KG == 1;
   int n, first, vocab;  // the piece's first column
   int pitch;
   Listed list;
   T* dz;
-  __device__ __forceinline__ bool skip(int, int) const { return false; }
+
+  template <typename C, int MI, int NJ>
+  __device__ __forceinline__ void tile(f32x16 (&acc)[MI][NJ], int m0, int n0, unsigned char* s_dyn) const {
+    constexpr int WN = C::NW / C::WM, TM = C::BM / C::WM, TN = C::BN / WN;
+    const int wv = threadIdx.x >> 6;
+    float base[MI];
+    int at[MI];
+    bool special = first + n0 + C::BN > vocab;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int m = m0 + TM * (wv % C::WM) + 32 * i + (threadIdx.x & 31);
+      base[i] = m < n ? list.off[m] * 1.44269504f : 0.0f;
+      at[i] = (m < n ? list.y[m] - first : -1) - n0;
+      const int in_wave = at[i] - TN * (wv / C::WM);
+      special |= __ballot(in_wave >= 0 && in_wave < TN) != 0;
+    }
+    auto go = [&](auto with) {
+      leave_bf16<C>(
+          acc, s_dyn,
+          [&](int i, int, int col, float (&v)[4]) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              v[e] = __builtin_amdgcn_exp2f(fmaf(v[e], 1.44269504f, -base[i]));
+              if (decltype(with)::value) {
+                if (first + n0 + col + e >= vocab) v[e] = 0.0f;
+                if (at[i] == col + e) v[e] = -1.0f;
+              }
+            }
+          },
+          [&](int row, int col, u32x4 q) {
+            if (m0 + row < n) *(u32x4*)(dz + (int64_t)(m0 + row) * pitch + n0 + col) = q;
+          });
+    };
+    if (special) go(std::true_type{});  // a few waves, or the last columns
+    else go(std::false_type{});
+  }
+
+  __device__ __forceinline__ bool skip(int m, int) const { return m >= n; }
   template <typename Lanes>
   __device__ __forceinline__ void operator()(int64_t m, int n0, float (&v)[8], Lanes) const {
-    if (m >= n) return;
-    const float lse = list.lse[m], w = list.w[m];
+    const float off = list.off[m];
     const int at = list.y[m] - first - n0, end = vocab - first - n0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < end ? w * exp_of<T>(v[j] - lse) : 0.0f;
-    if (at >= 0 && at < 8) {
-      const float own = w * expm1f(-list.loss[m]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = j == at ? own : v[j];
+    for (int j = 0; j < 8; ++j) {
+      v[j] = j < end ? exp_of<T>(v[j] - off) : 0.0f;
+      if (j == at) v[j] = -1.0f;
     }
     store8(dz + m * pitch + n0, v);
   }
@@ -265,19 +351,27 @@ __global__ __launch_bounds__(kTileThreads, 2) void vocab_dz_kernel(LogitsArgs<T>
   tile_product<T, true, false, C, TAIL>(g, mt, nt, 0, a.K, s_dyn, GradOut<T>{g.M, first, vocab, pitch, a.list, dz});
 }
 
-// The listed tokens' rows of x, one behind the other, for dW, which sums over them.
+// The listed tokens' rows of x times their f, one behind the other, for dW, which sums over them.
 template <typename T>
 __global__ __launch_bounds__(256) void vocab_gather_kernel(int H, const T* __restrict__ x, Listed list, T* __restrict__ out) {
   const int n = list.head[0];
   for (int64_t r = blockIdx.x; r < n; r += gridDim.x) {
-    const u32x4* src = (const u32x4*)(x + (int64_t)list.rows[r] * H);
-    u32x4* dst = (u32x4*)(out + r * H);
-    for (int i = threadIdx.x; i < H * (int)sizeof(T) / 16; i += 256) dst[i] = src[i];
+    const T* src = x + (int64_t)list.rows[r] * H;
+    const float f = list.f[r];
+    for (int i = 8 * threadIdx.x; i < H; i += 8 * 256) {
+      float v[8];
+      load8(src + i, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= f;
+      store8(out + r * H + i, v);
+    }
   }
 }
 
 // Sums of dx over the pieces, [slice][pitch rows][H].
 struct DxOut {
+  template <typename C>
+  static constexpr bool kWhole = false;
   int n, H, pitch, slice;
   bool add;
   float* sums;
@@ -297,10 +391,24 @@ struct DxOut {
 
 template <typename T>
 struct DwOut {
+  template <typename C>
+  static constexpr bool kWhole = sizeof(T) == 2 && C::KG == 1;
   int H, N;
   int64_t ld;
   float c;
   T* dw;
+  template <typename C, int MI, int NJ>
+  __device__ __forceinline__ void tile(f32x16 (&acc)[MI][NJ], int m0, int n0, unsigned char* s_dyn) const {
+    leave_bf16<C>(
+        acc, s_dyn,
+        [&](int, int, int, float (&v)[4]) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] *= c;
+        },
+        [&](int row, int col, u32x4 q) {  // N is a multiple of 8: a run is all in or all out
+          if (m0 + row < H && n0 + col < N) *(u32x4*)(dw + (int64_t)(m0 + row) * ld + n0 + col) = q;
+        });
+  }
   __device__ __forceinline__ bool skip(int h, int n) const { return h >= H || n >= N; }
   template <typename Lanes>
   __device__ __forceinline__ void operator()(int64_t h, int n, float (&v)[8], Lanes) const {
@@ -378,8 +486,9 @@ __global__ __launch_bounds__(256) void vocab_dx_kernel(int T_, int H, int slices
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = s == 0 ? u[j] : v[j] + u[j];
       }
+      const float f = c * list.f[place];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= c;
+      for (int j = 0; j < 8; ++j) v[j] *= f;
     }
     store8(dx + t * H + h, v);
   }
@@ -436,7 +545,8 @@ template <typename T>
 int run_cols(int tile) {
   int cols = 0;
   (void)with_tile<T>(tile, [&](auto t) {
-    cols = decltype(t)::OUT_COLS;
+    using C = decltype(t);
+    cols = LossOut<T>::template kWhole<C> ? C::BN : C::OUT_COLS;
     return hipSuccess;
   });
   return cols;
@@ -472,9 +582,8 @@ Space vocab_space(void* ws, int T, int H, int V, int esize, const VocabPlan& p, 
     const int cols = esize == 4 ? run_cols<float>(p.logits) : run_cols<uint16_t>(p.logits);
     s.runs = (Run*)take((size_t)((V + cols - 1) / cols) * p.pitch * sizeof(Run));
   } else {
-    s.list.lse = (float*)take(row);
-    s.list.loss = (float*)take(row);
-    s.list.w = (float*)take(row);
+    s.list.off = (float*)take(row);
+    s.list.f = (float*)take(row);
     s.x = take((size_t)p.pitch * H * esize);
     s.dz = take((size_t)p.pitch * p.piece * esize);
     s.sums = (float*)take((size_t)std::max(1, p.grads.x.slices) * p.pitch * H * 4);
@@ -536,7 +645,7 @@ hipError_t vocab_fwd_typed(const VocabArgs& g, float* loss, float* lse, float* m
   if (err != hipSuccess) return err;
   const int run = run_cols<T>(p.logits);
   const JoinArgs j{(cols + run - 1) / run, p.pitch, s.runs, s.own, s.list, s.part, loss, lse, mean};
-  MOE_LAUNCH(vocab_join_kernel, dim3((g.T + 15) / 16), dim3(256), 0, stream, j);
+  MOE_LAUNCH(vocab_join_kernel, dim3((g.T + 15) / 16), dim3(1024), 0, stream, j);
   return hipGetLastError();
 }
 
