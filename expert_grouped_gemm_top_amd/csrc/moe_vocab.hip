@@ -237,9 +237,21 @@ __global__ __launch_bounds__(1024) void vocab_join_kernel(JoinArgs a) {
   const int groups = max(1, (n + 15) / 16);
   if ((int)blockIdx.x >= groups) return;
   Run run{-__builtin_inff(), 0.0f};
-  if (row < n)
-#pragma unroll 8
-    for (int i = q; i < a.n_runs; i += 64) run = joined(run, a.runs[(int64_t)i * a.pitch + row]);
+  for (int first = q; first < a.n_runs; first += 64 * 8) {  // eight runs at a time
+    Run some[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = first + 64 * k;
+      some[k] = row < n && i < a.n_runs ? a.runs[(int64_t)i * a.pitch + row] : Run{-__builtin_inff(), 0.0f};
+    }
+    float top = run.top;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, some[k].top);
+    const float base = top == -__builtin_inff() ? 0.0f : top;
+    run = Run{top, run.sum * expf(run.top - base)};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) run.sum += some[k].sum * expf(some[k].top - base);
+  }
   s_run[q][r] = run;
   __syncthreads();
   // wave w joins row w: 64 runs over its lanes
@@ -340,41 +352,73 @@ struct GradOut {
   }
 };
 
-template <typename T, typename C, bool TAIL>
-__global__ __launch_bounds__(kTileThreads, 2) void vocab_dz_kernel(LogitsArgs<T> a, int first, int vocab, int pitch,
-                                                                   T* dz) {
-  extern __shared__ __attribute__((aligned(16))) unsigned char s_dyn[];
-  TileSource g = a.g;
-  g.M = a.list.head[0];
-  int mt, nt;
-  if (!row_tile<C>(group_id(), g.M, g.N, mt, nt)) return;
-  tile_product<T, true, false, C, TAIL>(g, mt, nt, 0, a.K, s_dyn, GradOut<T>{g.M, first, vocab, pitch, a.list, dz});
-}
-
-// The listed tokens' rows of x times their f, one behind the other, for dW, which sums over them.
+// What the first piece's launch does beside it, in workgroups of its own: the listed tokens' rows of x times their f, one
+// behind the other, for dW, which sums over them (out NULL: not wanted), and zeros for the other tokens' dx (NULL alike).
 template <typename T>
-__global__ __launch_bounds__(256) void vocab_gather_kernel(int H, const T* __restrict__ x, Listed list, T* __restrict__ out) {
-  const int n = list.head[0];
-  for (int64_t r = blockIdx.x; r < n; r += gridDim.x) {
-    const T* src = x + (int64_t)list.rows[r] * H;
-    const float f = list.f[r];
-    for (int i = 8 * threadIdx.x; i < H; i += 8 * 256) {
-      float v[8];
-      load8(src + i, v);
+struct Layout {
+  int T_, H;
+  const T* x;
+  T* out;
+  T* dx;
+  int64_t tiles;  // workgroups in front of these
+  int groups;
+};
+template <typename T>
+__device__ __forceinline__ void lay_out(const Layout<T>& g, const Listed& list, int group) {
+  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, step = g.groups * (kTileThreads / 64);
+  for (int t = group * (kTileThreads / 64) + w; t < g.T_; t += step) {  // a wave per token
+    const int place = list.place[t];
+    if (place < 0) {
+      const float zero[8] = {};
+      if (g.dx != nullptr)
+        for (int i = 8 * lane; i < g.H; i += 8 * 64) store8(g.dx + (int64_t)t * g.H + i, zero);
+    } else if (g.out != nullptr) {
+      const float f = list.f[place];
+      for (int i = 8 * lane; i < g.H; i += 8 * 64) {
+        float v[8];
+        load8(g.x + (int64_t)t * g.H + i, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= f;
-      store8(out + r * H + i, v);
+        for (int j = 0; j < 8; ++j) v[j] *= f;
+        store8(g.out + (int64_t)place * g.H + i, v);
+      }
     }
   }
 }
 
-// Sums of dx over the pieces, [slice][pitch rows][H].
+template <typename T, typename C, bool TAIL>
+__global__ __launch_bounds__(kTileThreads, 2) void vocab_dz_kernel(LogitsArgs<T> a, int first, int vocab, int pitch, T* dz,
+                                                                   Layout<T> beside) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char s_dyn[];
+  const int64_t item = group_id();
+  if (item >= beside.tiles) {
+    if (item - beside.tiles < beside.groups) lay_out(beside, a.list, (int)(item - beside.tiles));
+    return;
+  }
+  TileSource g = a.g;
+  g.M = a.list.head[0];
+  int mt, nt;
+  if (!row_tile<C>((int)item, g.M, g.N, mt, nt)) return;
+  tile_product<T, true, false, C, TAIL>(g, mt, nt, 0, a.K, s_dyn, GradOut<T>{g.M, first, vocab, pitch, a.list, dz});
+}
+
+// The factor that dz was held without.
+struct Factor {
+  float scale;
+  const float* per_mean;  // {mean, 1 / n}; NULL where tokens are weighted one by one
+  __device__ __forceinline__ float get() const { return per_mean != nullptr ? scale * per_mean[1] : scale; }
+};
+
+// Sums of dx over the pieces, [slice][pitch rows][H]; the last piece of a product in one slice leaves dx itself.
+template <typename T>
 struct DxOut {
   template <typename C>
   static constexpr bool kWhole = false;
   int n, H, pitch, slice;
   bool add;
   float* sums;
+  const Listed& list;
+  float c;
+  T* dx;  // NULL: sums
   __device__ __forceinline__ bool skip(int m, int h) const { return m >= n || h >= H; }
   template <typename Lanes>
   __device__ __forceinline__ void operator()(int64_t m, int h, float (&v)[8], Lanes) const {
@@ -385,7 +429,11 @@ struct DxOut {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] += u[j];
     }
-    store8(at, v);
+    if (dx == nullptr) return store8(at, v);
+    const float f = c * list.f[m];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= f;
+    store8(dx + (int64_t)list.rows[m] * H + h, v);
   }
 };
 
@@ -418,19 +466,13 @@ struct DwOut {
   }
 };
 
-// The factor that dz was held without.
-struct Factor {
-  float scale;
-  const float* per_mean;  // {mean, 1 / n}; NULL where tokens are weighted one by one
-  __device__ __forceinline__ float get() const { return per_mean != nullptr ? scale * per_mean[1] : scale; }
-};
-
 struct GradArgs {
   TileSource gx, gw;    // dz W^T (M: the batch's tokens) and x^T dz
   int Kx, slice, pitch; // the piece's columns, those of a slice, rows of dz and of a slice's sums
   Listed list;
   int add;              // not the first piece
   float* sums;
+  void* dx;             // the last piece of a product in one slice
   Factor c;
   void* dw;
   int64_t ldw;
@@ -457,7 +499,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void vocab_grads_kernel(GradArgs a
     int mt, nt;
     tile_of(item % tiles, mtiles, ntiles, 1024 / CX::BM, mt, nt);
     tile_product<T, true, true, CX, TAIL>(g, mt, nt, kb, min(a.Kx, kb + a.slice), s_dyn,
-                                           DxOut{n, g.N, a.pitch, s, a.add != 0, a.sums});
+                                           DxOut<T>{n, g.N, a.pitch, s, a.add != 0, a.sums, a.list, a.c.get(), (T*)a.dx});
   } else {
     const TileSource& g = a.gw;
     const int mtiles = (g.M + CW::BM - 1) / CW::BM, ntiles = (g.N + CW::BN - 1) / CW::BN;
@@ -469,7 +511,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void vocab_grads_kernel(GradArgs a
   }
 }
 
-// dx of every token from the slices' sums; zeros where not counted.
+// dx of the counted tokens from the slices' sums.
 template <typename T>
 __global__ __launch_bounds__(256) void vocab_dx_kernel(int T_, int H, int slices, int pitch, Listed list,
                                                        const float* __restrict__ sums, Factor f, T* __restrict__ dx) {
@@ -478,18 +520,18 @@ __global__ __launch_bounds__(256) void vocab_dx_kernel(int T_, int H, int slices
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)T_ * runs; i += (int64_t)gridDim.x * 256) {
     const int64_t t = i / runs;
     const int h = 8 * (int)(i % runs), place = list.place[t];
+    if (place < 0) continue;
     float v[8] = {};
-    if (place >= 0) {
-      for (int s = 0; s < slices; ++s) {
-        float u[8];
-        load8(sums + ((int64_t)s * pitch + place) * H + h, u);
+#pragma unroll 4
+    for (int s = 0; s < slices; ++s) {
+      float u[8];
+      load8(sums + ((int64_t)s * pitch + place) * H + h, u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = s == 0 ? u[j] : v[j] + u[j];
-      }
-      const float f = c * list.f[place];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= f;
+      for (int j = 0; j < 8; ++j) v[j] += u[j];
     }
+    const float f = c * list.f[place];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= f;
     store8(dx + t * H + h, v);
   }
 }
@@ -498,9 +540,26 @@ __global__ __launch_bounds__(256) void vocab_dx_kernel(int T_, int H, int slices
 
 int rounded_up(int64_t v, int to) { return (int)((v + to - 1) / to * to); }
 
+// Tiles of logits for few rows, beside those of moe_linear_plan.h: wide ones, whose stages hold 32 or 64 KiB of W, so
+// that enough of it is on its way.  One forward over 2048 x 131072, us by rows:
+//               1     64    128    192    256    384    512
+//   64 x 512   101    102    145    193    245    339    442
+//   128 x 256  103    108    110    163    167    235    300
+//   256 x 256  133    140    145    146    150    256    264
+//   128 x 128 in two reduction groups, two stages   139 to 149 up to 128 rows
+// and the dx products of one piece of 131072 columns on 128 x 128 tiles, frozen head, 128 rows: two groups of two
+// stages 244 us the call, one of four 233.
+enum { kTile64x512 = kTiles, kTile128x256, kTile128x128Deep };
+using WideTile = Tile<64, 512, 8, 1, 1, 2>;
+using FlatTile = Tile<128, 256, 8, 2, 1, 3>;
+using DeepTile = Tile<128, 128, 8, 2, 1, 4>;
+constexpr int kFewRows = 128;
+
 template <typename T, typename Fn>
 hipError_t with_tile(int tile, Fn&& run) {
   if constexpr (sizeof(T) == 2) {
+    if (tile == kTile64x512) return run(WideTile{});
+    if (tile == kTile128x256) return run(FlatTile{});
     if (tile == kTile256x256) return run(Tile0{});
     if (tile == kTile256x128) return run(Tile1{});
   }
@@ -512,31 +571,52 @@ hipError_t with_tile(int tile, Fn&& run) {
 
 struct VocabPlan {
   int logits;       // tile of the logits' products
-  int piece;        // columns of a piece of the backward, a multiple of 256
-  int pitch;        // rows of dz: T in whole tiles
+  int piece;        // columns of a piece of the backward, a multiple of 512
+  int pitch;        // rows of the statistics, of dz and of dx's sums
+  bool few;         // the gradients' products on the tiles for few rows
   Plan2 grads;
 };
 
-// The columns of a piece: dz of some 64 Mi elements, so that it is read again from the last-level cache.
-constexpr int64_t kPieceElements = 64 << 20;
+// The columns of a piece: dz of some 64 Mi elements and W's columns of 256 MiB at most, so that both are read again
+// from the last-level cache as far as that goes.
+constexpr int64_t kPieceElements = 64 << 20, kPieceBytes = 256 << 20;
 
-VocabPlan vocab_plan(int T, int H, int V, int esize, bool dx, bool dw) {
-  VocabPlan p{};
-  p.pitch = rounded_up(T, 256);
-  const int64_t cols = std::max<int64_t>(kPieceElements / p.pitch / 256 * 256, 1024);
-  p.piece = (int)std::min<int64_t>(cols, rounded_up(V, 256));
+int64_t group_count(int M, int N, int bm, int bn) { return (int64_t)((M + bm - 1) / bm) * ((N + bn - 1) / bn); }
+
+int logits_tile(int T, int N, int H, int esize) {
+  // the wide tiles where they fill the chip
+  if (esize == 2 && T <= 64 && group_count(T, N, 64, 512) >= kCus / 2) return kTile64x512;
+  if (esize == 2 && group_count(T, N, 128, 256) >= kCus && (T <= 128 || (T > 256 && T <= 384))) return kTile128x256;
+  int best_tile = 0;
   double best = -1.0;
   for (int tile = esize == 2 ? 0 : (int)kTile128x128; tile < kTiles; ++tile) {
-    const Cut c = cut_of(T, dx || dw ? p.piece : V, H, esize, tile, 1);
+    const Cut c = cut_of(T, N, H, esize, tile, 1);
     const int64_t rest = c.groups % kCus;
     double us = (double)(c.groups / kCus) * c.each;
     if (rest > 0) us += pass_us(cost_of(tile, esize), H, rest);
     if (best < 0.0 || us < best) {
       best = us;
-      p.logits = tile;
+      best_tile = tile;
     }
   }
-  if (dx || dw) p.grads = plan_bwd(T, H, p.piece, esize, dx, dw, false);
+  return best_tile;
+}
+
+VocabPlan vocab_plan(int T, int H, int V, int esize, bool dx, bool dw) {
+  VocabPlan p{};
+  p.pitch = rounded_up(T, 256);
+  const int64_t cols = std::max<int64_t>(
+      std::min<int64_t>(kPieceElements / p.pitch, kPieceBytes / ((int64_t)H * esize)) / 512 * 512, 1024);
+  p.piece = (int)std::min<int64_t>(cols, rounded_up(V, 512));
+  p.logits = logits_tile(T, dx || dw ? p.piece : V, H, esize);
+  if (!dx && !dw) return p;
+  p.grads = plan_bwd(T, H, p.piece, esize, dx, dw, false);
+  p.few = esize == 2 && T <= kFewRows && group_count(H, p.piece, 128, 128) >= kCus;
+  if (p.few && dx) {  // as many slices as fill the chip
+    const int64_t slices = std::max<int64_t>(1, kCus / group_count(T, H, 128, 128));
+    p.grads.x.slice = rounded_up((p.piece + slices - 1) / slices, 128);
+    p.grads.x.slices = (p.piece + p.grads.x.slice - 1) / p.grads.x.slice;
+  }
   return p;
 }
 
@@ -613,10 +693,11 @@ hipError_t run_loss(const LogitsArgs<T>& a, int vocab, int pitch, float* own, Ru
 }
 
 template <typename T, typename C, bool TAIL>
-hipError_t run_dz(const LogitsArgs<T>& a, int first, int vocab, int pitch, T* dz, hipStream_t stream) {
+hipError_t run_dz(const LogitsArgs<T>& a, int first, int vocab, int pitch, T* dz, Layout<T> beside, hipStream_t stream) {
   static PerDeviceOnce once;
-  return run_tiles(vocab_dz_kernel<T, C, TAIL>, C::LDS, tiles_of<C>(a.g.M, a.g.N), stream, once, a, first, vocab, pitch,
-                   dz);
+  beside.tiles = tiles_of<C>(a.g.M, a.g.N);
+  return run_tiles(vocab_dz_kernel<T, C, TAIL>, C::LDS, beside.tiles + beside.groups, stream, once, a, first, vocab, pitch,
+                   dz, beside);
 }
 
 template <typename T, typename CX, typename CW, bool TAIL>
@@ -658,21 +739,20 @@ hipError_t vocab_bwd_typed(const VocabArgs& g, const float* loss, const float* l
              dloss);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  if (dw != nullptr) {
-    MOE_LAUNCH(vocab_gather_kernel<T>, dim3(std::min(g.T, 2048)), dim3(256), 0, stream, g.H, (const T*)g.x, s.list, (T*)s.x);
-    if ((err = hipGetLastError()) != hipSuccess) return err;
-  }
   const Factor c{scale, dloss != nullptr ? nullptr : mean};
   T* dz = (T*)s.dz;
+  const int slices = dx != nullptr ? (std::min(p.piece, g.V) + p.grads.x.slice - 1) / p.grads.x.slice : 0;
   for (int first = 0; first < g.V; first += p.piece) {
     const int cols = std::min(p.piece, g.V - first);
+    const Layout<T> beside{g.T, g.H, (const T*)g.x, dw != nullptr ? (T*)s.x : nullptr, (T*)dx, 0,
+                           first == 0 ? std::min((g.T + 7) / 8, 256) : 0};
     const T* w = (const T*)g.w + first;
     LogitsArgs<T> a{{g.T, cols, g.x, g.H, w, g.V, s.list.rows}, g.H, s.list};
     err = with_tile<T>(p.logits, [&](auto tile) {
       using C = decltype(tile);
       const bool tail = g.H % (kStageK<T> * C::KG) != 0;
-      return tail ? run_dz<T, C, true>(a, first, g.vocab, p.piece, dz, stream)
-                  : run_dz<T, C, false>(a, first, g.vocab, p.piece, dz, stream);
+      return tail ? run_dz<T, C, true>(a, first, g.vocab, p.piece, dz, beside, stream)
+                  : run_dz<T, C, false>(a, first, g.vocab, p.piece, dz, beside, stream);
     });
     if (err != hipSuccess) return err;
     GradArgs b{};
@@ -684,10 +764,11 @@ hipError_t vocab_bwd_typed(const VocabArgs& g, const float* loss, const float* l
     b.list = s.list;
     b.add = first > 0;
     b.sums = s.sums;
+    b.dx = slices == 1 && first + cols == g.V ? dx : nullptr;
     b.c = c;
     b.dw = dw != nullptr ? (T*)dw + first : nullptr;
     b.ldw = g.V;
-    b.x_first = p.grads.x.each > p.grads.w.each;
+    b.x_first = p.few || p.grads.x.each > p.grads.w.each;
     auto run = [&](auto tx, auto tw) {
       using CX = decltype(tx);
       using CW = decltype(tw);
@@ -697,9 +778,10 @@ hipError_t vocab_bwd_typed(const VocabArgs& g, const float* loss, const float* l
       const bool tail_x = cols % SX != 0 || b.slice % SX != 0;
       return tail_x ? run_grads<T, CX, CW, true>(b, stream) : run_grads<T, CX, CW, false>(b, stream);
     };
-    const int pair = p.grads.pair;
+    const int pair = p.few ? -1 : p.grads.pair;
     err = hipErrorUnknown;
     if constexpr (sizeof(T) == 2) {
+      if (p.few) err = run(DeepTile{}, DeepTile{});
       if (pair == 0) err = run(Tile0{}, Tile0{});
       if (pair == 1) err = run(Tile0{}, Tile1{});
       if (pair == 2) err = run(Tile1{}, Tile0{});
@@ -711,10 +793,10 @@ hipError_t vocab_bwd_typed(const VocabArgs& g, const float* loss, const float* l
     if (pair == 7) err = run(Tile5{}, Tile4<T>{});
     if (err != hipSuccess) return err;
   }
-  if (dx == nullptr) return hipSuccess;
+  if (slices <= 1) return hipSuccess;
   const int64_t runs = (int64_t)g.T * (g.H / 8);
   MOE_LAUNCH(vocab_dx_kernel<T>, dim3((unsigned)std::min<int64_t>((runs + 255) / 256, 8192)), dim3(256), 0, stream, g.T, g.H,
-             (std::min(p.piece, g.V) + p.grads.x.slice - 1) / p.grads.x.slice, p.pitch, s.list, s.sums, c, (T*)dx);
+             slices, p.pitch, s.list, s.sums, c, (T*)dx);
   return hipGetLastError();
 }
 
