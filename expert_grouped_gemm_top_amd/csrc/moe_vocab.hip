@@ -33,7 +33,7 @@ namespace moe {
 
 namespace {
 
-// What the first kernel leaves: the counted tokens in order, and by their places in that list what the others read.
+// The counted tokens, in order.
 struct Listed {
   int32_t* head;  // [0] their number, [1] a ticket, set to 0
   int32_t* rows;  // [n] token
@@ -43,55 +43,117 @@ struct Listed {
   float* f;       // [n] backward: their probability times the token's weight
 };
 
-// The tokens with a target in [0, vocab), in order, by one workgroup.  loss_out and lse_out (forward) become 0 for the others.
+// What they are listed from.
+struct Tokens {
+  int T, vocab;
+  const int32_t* target;
+  float *loss_out, *lse_out;         // forward: become 0 for tokens that are not counted
+  const float *loss, *lse, *dloss;   // backward
+  __device__ __forceinline__ int y(int64_t t) const {
+    const int v = t < T ? target[t] : -1;
+    return v >= 0 && v < vocab ? v : -1;
+  }
+  __device__ __forceinline__ float f(int64_t t) const {
+    const float f = -expm1f(-loss[t]);
+    return dloss != nullptr ? dloss[t] * f : f;
+  }
+  __device__ __forceinline__ float off(int64_t t) const {
+    const float f = -expm1f(-loss[t]);
+    return f == 0.0f ? __builtin_inff() : lse[t] + logf(f);  // a loss of 0: no gradient
+  }
+  __device__ __forceinline__ bool bwd() const { return loss != nullptr; }
+};
+
+// RUN neighbouring tokens a thread from `first` on: their targets and this thread's place among the listed.
+// s_wave: an int a wave.
+template <int NT, int RUN>
+__device__ __forceinline__ int place_of(const Tokens& g, int64_t first, int (&y)[RUN], int& before, int* s_wave) {
+  int mine = 0;
+#pragma unroll
+  for (int j = 0; j < RUN; ++j) {
+    y[j] = g.y(first + j);
+    mine += y[j] >= 0;
+  }
+  const int upto = wave_inclusive_scan(mine), w = threadIdx.x >> 6;
+  __syncthreads();
+  if ((threadIdx.x & 63) == 63) s_wave[w] = upto;
+  __syncthreads();
+  int at = before + upto - mine;
+#pragma unroll
+  for (int i = 0; i < NT / 64; ++i) {
+    at += i < w ? s_wave[i] : 0;
+    before += s_wave[i];
+  }
+  return at;
+}
+
+// A token of that place, or -1 for none, into the list in memory.
+__device__ __forceinline__ void list_token(const Tokens& g, const Listed& out, int64_t t, int y, int at) {
+  if (t >= g.T) return;
+  out.place[t] = y >= 0 ? at : -1;
+  if (y < 0) {
+    if (!g.bwd()) g.loss_out[t] = g.lse_out[t] = 0.0f;
+    return;
+  }
+  out.rows[at] = (int)t;
+  out.y[at] = y;
+  if (g.bwd()) {
+    out.off[at] = g.off(t);
+    out.f[at] = g.f(t);
+  }
+}
+
+// Lists many tokens, by one workgroup.
 constexpr int kListRun = 8;
-__global__ __launch_bounds__(1024) void vocab_list_kernel(int T, int vocab, const int32_t* __restrict__ target, Listed out,
-                                                          float* loss_out, float* lse_out, const float* loss,
-                                                          const float* lse, const float* dloss) {
+__global__ __launch_bounds__(1024) void vocab_list_kernel(Tokens g, Listed out) {
   __shared__ int s_wave[16];
-  const int tid = threadIdx.x, w = tid >> 6;
   int before = 0;
-  for (int64_t base = 0; base < T; base += 1024 * kListRun) {
-    const int64_t first = base + (int64_t)tid * kListRun;
-    int y[kListRun], mine = 0;
+  for (int64_t base = 0; base < g.T; base += 1024 * kListRun) {
+    const int64_t first = base + (int64_t)threadIdx.x * kListRun;
+    int y[kListRun], at = place_of<1024>(g, first, y, before, s_wave);
 #pragma unroll
     for (int j = 0; j < kListRun; ++j) {
-      y[j] = first + j < T ? target[first + j] : -1;
-      if (y[j] < 0 || y[j] >= vocab) y[j] = -1;
-      mine += y[j] >= 0;
-    }
-    const int upto = wave_inclusive_scan(mine);
-    __syncthreads();
-    if ((tid & 63) == 63) s_wave[w] = upto;
-    __syncthreads();
-    int at = before + upto - mine;
-    for (int i = 0; i < 16; ++i) {
-      at += i < w ? s_wave[i] : 0;
-      before += s_wave[i];
-    }
-#pragma unroll
-    for (int j = 0; j < kListRun; ++j) {
-      const int64_t t = first + j;
-      if (t >= T) break;
-      out.place[t] = y[j] >= 0 ? at : -1;
-      if (y[j] < 0) {
-        if (loss_out != nullptr) loss_out[t] = lse_out[t] = 0.0f;
-        continue;
-      }
-      out.rows[at] = (int)t;
-      out.y[at] = y[j];
-      if (loss_out == nullptr) {
-        const float f = -expm1f(-loss[t]);
-        out.off[at] = f == 0.0f ? __builtin_inff() : lse[t] + logf(f);  // a loss of 0: no gradient
-        out.f[at] = dloss != nullptr ? dloss[t] * f : f;
-      }
-      ++at;
+      list_token(g, out, first + j, y[j], at);
+      at += y[j] >= 0;
     }
   }
-  if (tid == 0) {
+  if (threadIdx.x == 0) {
     out.head[0] = before;
     out.head[1] = 0;
   }
+}
+
+// Up to this many tokens every workgroup of the first product lists them for itself (in LDS), and one for the later
+// kernels: a launch less (fp32 backward of 333 tokens 27 -> 22 us).
+constexpr int kOwnListRows = 1024;
+constexpr size_t kOwnListBytes = kOwnListRows * 12 + 64;
+__device__ __forceinline__ int list_here(const Tokens& g, Listed& list, bool write, unsigned char* s) {
+  int* s_wave = reinterpret_cast<int*>(s);
+  int32_t* s_rows = reinterpret_cast<int32_t*>(s + 64);
+  int32_t* s_y = s_rows + kOwnListRows;
+  float* s_off = reinterpret_cast<float*>(s_y + kOwnListRows);
+  constexpr int RUN = kOwnListRows / kTileThreads;
+  int y[RUN], n = 0;
+  const int64_t first = (int64_t)threadIdx.x * RUN;
+  int at = place_of<kTileThreads>(g, first, y, n, s_wave);
+#pragma unroll
+  for (int j = 0; j < RUN; ++j) {
+    if (write) list_token(g, list, first + j, y[j], at);
+    if (y[j] < 0) continue;
+    s_rows[at] = (int)(first + j);
+    s_y[at] = y[j];
+    if (g.bwd()) s_off[at] = g.off(first + j);
+    ++at;
+  }
+  if (write && threadIdx.x == 0) {
+    list.head[0] = n;
+    list.head[1] = 0;
+  }
+  __syncthreads();
+  list.rows = s_rows;
+  list.y = s_y;
+  list.off = s_off;
+  return n;
 }
 
 template <typename T>
@@ -197,6 +259,8 @@ struct LogitsArgs {
   TileSource g;  // M: the batch's tokens; b from the piece's first column on
   int K;
   Listed list;
+  Tokens tokens;
+  bool own_list;
 };
 
 // Tile of the counted tokens' rows; false past the last.
@@ -212,11 +276,14 @@ template <typename T, typename C, bool TAIL>
 __global__ __launch_bounds__(kTileThreads, 2) void vocab_loss_kernel(LogitsArgs<T> a, int vocab, int pitch, float* own,
                                                                      Run* runs) {
   extern __shared__ __attribute__((aligned(16))) unsigned char s_dyn[];
+  const int item = group_id();
   TileSource g = a.g;
-  g.M = a.list.head[0];
+  Listed list = a.list;
+  g.M = a.own_list ? list_here(a.tokens, list, item == 0, s_dyn + C::LDS) : list.head[0];
+  g.rows = list.rows;
   int mt, nt;
-  if (!row_tile<C>(group_id(), g.M, g.N, mt, nt)) return;
-  tile_product<T, true, false, C, TAIL>(g, mt, nt, 0, a.K, s_dyn, LossOut<T>{g.M, vocab, pitch, a.list.y, own, runs});
+  if (!row_tile<C>(item, g.M, g.N, mt, nt)) return;
+  tile_product<T, true, false, C, TAIL>(g, mt, nt, 0, a.K, s_dyn, LossOut<T>{g.M, vocab, pitch, list.y, own, runs});
 }
 
 // Joins the runs of 16 rows per workgroup, 64 threads each; the last workgroup adds up the mean.
@@ -356,7 +423,7 @@ struct GradOut {
 // behind the other, for dW, which sums over them (out NULL: not wanted), and zeros for the other tokens' dx (NULL alike).
 template <typename T>
 struct Layout {
-  int T_, H;
+  int H;
   const T* x;
   T* out;
   T* dx;
@@ -364,41 +431,45 @@ struct Layout {
   int groups;
 };
 template <typename T>
-__device__ __forceinline__ void lay_out(const Layout<T>& g, const Listed& list, int group) {
-  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, step = g.groups * (kTileThreads / 64);
-  for (int t = group * (kTileThreads / 64) + w; t < g.T_; t += step) {  // a wave per token
-    const int place = list.place[t];
-    if (place < 0) {
-      const float zero[8] = {};
-      if (g.dx != nullptr)
-        for (int i = 8 * lane; i < g.H; i += 8 * 64) store8(g.dx + (int64_t)t * g.H + i, zero);
-    } else if (g.out != nullptr) {
-      const float f = list.f[place];
+__device__ __forceinline__ void lay_out(const Layout<T>& g, const Tokens& tokens, const int32_t* rows, int n, int group) {
+  const int lane = threadIdx.x & 63, step = g.groups * (kTileThreads / 64);
+  const int first = group * (kTileThreads / 64) + (threadIdx.x >> 6);  // a wave per row
+  if (g.out != nullptr)
+    for (int r = first; r < n; r += step) {
+      const int64_t t = rows[r];
+      const float f = tokens.f(t);
       for (int i = 8 * lane; i < g.H; i += 8 * 64) {
         float v[8];
-        load8(g.x + (int64_t)t * g.H + i, v);
+        load8(g.x + t * g.H + i, v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] *= f;
-        store8(g.out + (int64_t)place * g.H + i, v);
+        store8(g.out + (int64_t)r * g.H + i, v);
       }
     }
-  }
+  if (g.dx != nullptr)
+    for (int64_t t = first; t < tokens.T; t += step) {
+      if (tokens.y(t) >= 0) continue;
+      const float zero[8] = {};
+      for (int i = 8 * lane; i < g.H; i += 8 * 64) store8(g.dx + t * g.H + i, zero);
+    }
 }
 
 template <typename T, typename C, bool TAIL>
-__global__ __launch_bounds__(kTileThreads, 2) void vocab_dz_kernel(LogitsArgs<T> a, int first, int vocab, int pitch, T* dz,
+__global__ __launch_bounds__(kTileThreads, 2) void vocab_dz_kernel(LogitsArgs<T> a, int first, int pitch, T* dz,
                                                                    Layout<T> beside) {
   extern __shared__ __attribute__((aligned(16))) unsigned char s_dyn[];
   const int64_t item = group_id();
+  TileSource g = a.g;
+  Listed list = a.list;
+  g.M = a.own_list ? list_here(a.tokens, list, item == 0, s_dyn + C::LDS) : list.head[0];
+  g.rows = list.rows;
   if (item >= beside.tiles) {
-    if (item - beside.tiles < beside.groups) lay_out(beside, a.list, (int)(item - beside.tiles));
+    if (item - beside.tiles < beside.groups) lay_out(beside, a.tokens, list.rows, g.M, (int)(item - beside.tiles));
     return;
   }
-  TileSource g = a.g;
-  g.M = a.list.head[0];
   int mt, nt;
   if (!row_tile<C>((int)item, g.M, g.N, mt, nt)) return;
-  tile_product<T, true, false, C, TAIL>(g, mt, nt, 0, a.K, s_dyn, GradOut<T>{g.M, first, vocab, pitch, a.list, dz});
+  tile_product<T, true, false, C, TAIL>(g, mt, nt, 0, a.K, s_dyn, GradOut<T>{g.M, first, a.tokens.vocab, pitch, list, dz});
 }
 
 // The factor that dz was held without.
@@ -577,9 +648,8 @@ struct VocabPlan {
   Plan2 grads;
 };
 
-// The columns of a piece: dz of some 64 Mi elements and W's columns of 256 MiB at most, so that both are read again
-// from the last-level cache as far as that goes.
-constexpr int64_t kPieceElements = 64 << 20, kPieceBytes = 256 << 20;
+// The columns of a piece: dz of some 64 Mi elements, so that it is read again from the last-level cache.
+constexpr int64_t kPieceElements = 64 << 20;
 
 int64_t group_count(int M, int N, int bm, int bn) { return (int64_t)((M + bm - 1) / bm) * ((N + bn - 1) / bn); }
 
@@ -605,8 +675,7 @@ int logits_tile(int T, int N, int H, int esize) {
 VocabPlan vocab_plan(int T, int H, int V, int esize, bool dx, bool dw) {
   VocabPlan p{};
   p.pitch = rounded_up(T, 256);
-  const int64_t cols = std::max<int64_t>(
-      std::min<int64_t>(kPieceElements / p.pitch, kPieceBytes / ((int64_t)H * esize)) / 512 * 512, 1024);
+  const int64_t cols = std::max<int64_t>(kPieceElements / p.pitch / 512 * 512, 1024);
   p.piece = (int)std::min<int64_t>(cols, rounded_up(V, 512));
   p.logits = logits_tile(T, dx || dw ? p.piece : V, H, esize);
   if (!dx && !dw) return p;
@@ -685,19 +754,26 @@ int64_t tiles_of(int M, int N) {
   return (int64_t)((M + C::BM - 1) / C::BM) * ((N + C::BN - 1) / C::BN);
 }
 
+hipError_t list_tokens(const Tokens& tokens, const Listed& list, hipStream_t stream) {
+  MOE_LAUNCH(vocab_list_kernel, dim3(1), dim3(1024), 0, stream, tokens, list);
+  return hipGetLastError();
+}
+
 template <typename T, typename C, bool TAIL>
 hipError_t run_loss(const LogitsArgs<T>& a, int vocab, int pitch, float* own, Run* runs, hipStream_t stream) {
   static PerDeviceOnce once;
-  return run_tiles(vocab_loss_kernel<T, C, TAIL>, C::LDS, tiles_of<C>(a.g.M, a.g.N), stream, once, a, vocab, pitch, own,
+  constexpr size_t lds = C::LDS + kOwnListBytes;
+  static_assert(lds <= 160 * 1024, "one CU's LDS");
+  return run_tiles(vocab_loss_kernel<T, C, TAIL>, lds, tiles_of<C>(a.g.M, a.g.N), stream, once, a, vocab, pitch, own,
                    runs);
 }
 
 template <typename T, typename C, bool TAIL>
-hipError_t run_dz(const LogitsArgs<T>& a, int first, int vocab, int pitch, T* dz, Layout<T> beside, hipStream_t stream) {
+hipError_t run_dz(const LogitsArgs<T>& a, int first, int pitch, T* dz, Layout<T> beside, hipStream_t stream) {
   static PerDeviceOnce once;
   beside.tiles = tiles_of<C>(a.g.M, a.g.N);
-  return run_tiles(vocab_dz_kernel<T, C, TAIL>, C::LDS, beside.tiles + beside.groups, stream, once, a, first, vocab, pitch,
-                   dz, beside);
+  return run_tiles(vocab_dz_kernel<T, C, TAIL>, C::LDS + kOwnListBytes, beside.tiles + beside.groups, stream, once, a, first,
+                   pitch, dz, beside);
 }
 
 template <typename T, typename CX, typename CW, bool TAIL>
@@ -710,13 +786,13 @@ template <typename T>
 hipError_t vocab_fwd_typed(const VocabArgs& g, float* loss, float* lse, float* mean, void* ws, hipStream_t stream) {
   const VocabPlan p = vocab_plan(g.T, g.H, g.V, sizeof(T), false, false);
   const Space s = vocab_space(ws, g.T, g.H, g.V, sizeof(T), p, false);
-  MOE_LAUNCH(vocab_list_kernel, dim3(1), dim3(1024), 0, stream, g.T, g.vocab, g.target, s.list, loss, lse, nullptr, nullptr,
-             nullptr);
-  hipError_t err = hipGetLastError();
+  const Tokens tokens{g.T, g.vocab, g.target, loss, lse, nullptr, nullptr, nullptr};
+  const bool own_list = g.T <= kOwnListRows;
+  hipError_t err = own_list ? hipSuccess : list_tokens(tokens, s.list, stream);
   if (err != hipSuccess) return err;
   // columns past the vocabulary's end need no product
   const int cols = std::min(g.V, rounded_up(g.vocab, 8));
-  const LogitsArgs<T> a{{g.T, cols, g.x, g.H, g.w, g.V, s.list.rows}, g.H, s.list};
+  const LogitsArgs<T> a{{g.T, cols, g.x, g.H, g.w, g.V, s.list.rows}, g.H, s.list, tokens, own_list};
   err = with_tile<T>(p.logits, [&](auto tile) {
     using C = decltype(tile);
     const bool tail = g.H % (kStageK<T> * C::KG) != 0;
@@ -735,24 +811,24 @@ hipError_t vocab_bwd_typed(const VocabArgs& g, const float* loss, const float* l
                            float scale, void* dx, void* dw, void* ws, hipStream_t stream) {
   const VocabPlan p = vocab_plan(g.T, g.H, g.V, sizeof(T), dx != nullptr, dw != nullptr);
   const Space s = vocab_space(ws, g.T, g.H, g.V, sizeof(T), p, true);
-  MOE_LAUNCH(vocab_list_kernel, dim3(1), dim3(1024), 0, stream, g.T, g.vocab, g.target, s.list, nullptr, nullptr, loss, lse,
-             dloss);
-  hipError_t err = hipGetLastError();
+  const Tokens tokens{g.T, g.vocab, g.target, nullptr, nullptr, loss, lse, dloss};
+  const bool own_list = g.T <= kOwnListRows;
+  hipError_t err = own_list ? hipSuccess : list_tokens(tokens, s.list, stream);
   if (err != hipSuccess) return err;
   const Factor c{scale, dloss != nullptr ? nullptr : mean};
   T* dz = (T*)s.dz;
   const int slices = dx != nullptr ? (std::min(p.piece, g.V) + p.grads.x.slice - 1) / p.grads.x.slice : 0;
   for (int first = 0; first < g.V; first += p.piece) {
     const int cols = std::min(p.piece, g.V - first);
-    const Layout<T> beside{g.T, g.H, (const T*)g.x, dw != nullptr ? (T*)s.x : nullptr, (T*)dx, 0,
+    const Layout<T> beside{g.H, (const T*)g.x, dw != nullptr ? (T*)s.x : nullptr, (T*)dx, 0,
                            first == 0 ? std::min((g.T + 7) / 8, 256) : 0};
     const T* w = (const T*)g.w + first;
-    LogitsArgs<T> a{{g.T, cols, g.x, g.H, w, g.V, s.list.rows}, g.H, s.list};
+    LogitsArgs<T> a{{g.T, cols, g.x, g.H, w, g.V, s.list.rows}, g.H, s.list, tokens, own_list && first == 0};
     err = with_tile<T>(p.logits, [&](auto tile) {
       using C = decltype(tile);
       const bool tail = g.H % (kStageK<T> * C::KG) != 0;
-      return tail ? run_dz<T, C, true>(a, first, g.vocab, p.piece, dz, beside, stream)
-                  : run_dz<T, C, false>(a, first, g.vocab, p.piece, dz, beside, stream);
+      return tail ? run_dz<T, C, true>(a, first, p.piece, dz, beside, stream)
+                  : run_dz<T, C, false>(a, first, p.piece, dz, beside, stream);
     });
     if (err != hipSuccess) return err;
     GradArgs b{};
