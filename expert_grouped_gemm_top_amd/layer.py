@@ -7,7 +7,9 @@ grouped SwiGLU forward, combine; then optionally compaction, backward dx (+ dg),
 dW and the router's backward.  No step here computes anything itself: every
 value comes from libmoe's kernels.  ``MoeBlockBuffers`` puts the layer into its
 block the same way: layer norm, router with scored routing, routed experts, and
-a gated shared expert whose last product adds the routed sum.
+a gated shared expert whose last product adds the routed sum.  ``MoeHeadBuffers``
+(the vocabulary loss) and ``AdamWBuffers`` (the optimizer's states) make a training
+step of it: block forward, head forward and backward, block backward, AdamW.
 """
 from __future__ import annotations
 
@@ -29,9 +31,17 @@ class ScoredRouting:
     scale: float = 1.0
 
 
+@dataclasses.dataclass(frozen=True)
+class BalanceLoss:
+    """A balance loss of weight alpha over n_seq sequences of the batch (moe_balance_loss_fwd)."""
+    alpha: float
+    n_seq: int = 1
+
+
 class MoeLayerBuffers:
     def __init__(self, T, H, F, E, k, dtype=torch.bfloat16, device="cuda", rho=None, dw=True, dg=True,
-                 router=False, keep_graph=True, quota_cap=None, gather_rows=None, overlap_dw=False, routing=None):
+                 router=False, keep_graph=True, quota_cap=None, gather_rows=None, overlap_dw=False, routing=None,
+                 balance=None):
         """rho: quota ratio of the compacted backward (None: no compaction);
         quota_cap: the per-expert quota directly (e.g. from
         moe.moe_quota_cap_for_budget), instead of rho.  keep_graph=False: the
@@ -50,8 +60,10 @@ class MoeLayerBuffers:
         and dh complete (moe_signal_dh_ready); the caller's stream then waits
         for them.  Results are the same bit for bit.  routing: a ScoredRouting;
         tokens are then routed by scores (moe_route_scored) instead of by the
-        softmax over the selected logits."""
-        self.routing = routing
+        softmax over the selected logits.  balance: a BalanceLoss (of a layer with
+        its router): the forward leaves balance_loss [1] with balance_counts and
+        balance_mean [n_seq, E], the backward adds its gradient to the logits'."""
+        self.routing, self.balance = routing, balance
         self.T, self.H, self.F, self.E, self.k = T, H, F, E, k
         self.keep_graph = keep_graph
         self.N = N = T * k
@@ -115,16 +127,29 @@ class MoeLayerBuffers:
             self.dlogits = em(T, E, dt=f32)
             self.dw_r = em(H, E)
             self.router_ws = em(max(moe.moe_router_workspace_bytes(T, H, E), 16), dt=torch.uint8)
+        if balance is not None:
+            assert router, "the balance loss needs the router"
+            S = balance.n_seq
+            self.balance_counts = em(S, E, dt=i32)
+            self.balance_mean, self.balance_loss = em(S, E, dt=f32), em(1, dt=f32)
+            self.balance_ws = em(max(moe.moe_balance_loss_workspace_bytes(T, E, S), 16), dt=torch.uint8)
 
     # ------------------------------------------------------------------ forward
-    def forward(self, logits, x, w_gate, w_up, w_down, stream=None, w_r=None, wq=None, wt=None, route_bias=None):
+    def _balance_args(self, stream):
+        score = self.routing.score if self.routing is not None else moe.MOE_SCORE_SOFTMAX
+        return dict(score=score, alpha=self.balance.alpha, seq_offsets=self._seq_offsets, stream=stream)
+
+    def forward(self, logits, x, w_gate, w_up, w_down, stream=None, w_r=None, wq=None, wt=None, route_bias=None,
+                seq_offsets=None):
         """With w_r (a layer built with router=True) the logits are x W_r and
         the `logits` argument is ignored.  With wq (moe.Fp8Weights of the same
         frozen weights) the expert GEMMs read the fp8 copy.  With wt
         (moe.Fp8KMajorWeights) both expert GEMMs run on the fp8 matrix cores:
         the token rows are quantized per row, then gathered on load.
-        route_bias: the selection bias [E] of a layer with `routing`."""
+        route_bias: the selection bias [E] of a layer with `routing`.
+        seq_offsets: where the balance loss' sequences lie, [n_seq + 1]."""
         self._x = x  # the backward reads token rows through the pair ids
+        self._seq_offsets = seq_offsets
         if w_r is not None:
             moe.moe_router_fwd(x, w_r, self.logits, self.router_ws, stream)
             logits = self.logits
@@ -134,6 +159,9 @@ class MoeLayerBuffers:
         else:
             assert route_bias is None, "a selection bias needs a layer with scored routing"
             moe.moe_route_topk(logits, self.topk_idx, self.topk_w, self.k, stream)
+        if self.balance is not None:
+            moe.moe_balance_loss_fwd(logits, self.topk_idx, self.balance_counts, self.balance_mean, self.balance_loss,
+                                     self.balance_ws, **self._balance_args(stream))
         g = self.gather_rows or wt is not None  # index-only dispatch: the forward gathers x rows itself
         moe.moe_dispatch(self.topk_idx, None if g else x, self.counts, self.offsets, self.perm, self.inv_perm,
                          None if g else self.x_sorted, self.ws, self.E, stream)
@@ -176,12 +204,13 @@ class MoeLayerBuffers:
                               None if g or not self.dw else self.a_kept, None if g or not kg else self.h_kept, stream,
                               cap=self.quota_cap)
 
-    def backward(self, dy, w_gate, w_up, w_down, score=None, stream=None, w_r=None, wq=None):
+    def backward(self, dy, w_gate, w_up, w_down, score=None, stream=None, w_r=None, wq=None, dbalance=None):
         """dx (+ dg) and, for full fine-tuning, dW.  With a quota the backward
         runs on the compacted retained pairs; score: a pair-indexed fp32 tensor,
         None (the routing weights) or "metric" (moe_pair_scores: the norm of
         each pair's rank-one dW_down term).  With w_r, the router's backward
-        follows: dlogits, dw_r, and its share added to dx."""
+        follows: dlogits, dw_r, and its share added to dx.  dbalance [1] fp32: the
+        gradient that reaches the balance loss (None: 1)."""
         g, k = self.gather_rows, self.k
         if self.compacted:
             if isinstance(score, str):
@@ -229,10 +258,14 @@ class MoeLayerBuffers:
                                    self.dw_down, self.R, s_dw, x_src=x_src, x_div=k, a_src=a_src)
             if self.overlap_dw:
                 s_main.wait_stream(s_dw)
-        if w_r is not None and self.routing is not None:
-            r = self.routing
+        if w_r is not None and (self.routing is not None or self.balance is not None):
+            # without scored routing: the softmax over the selected logits is the renormalised softmax over all
+            r = self.routing or ScoredRouting(moe.MOE_SCORE_SOFTMAX)
             moe.moe_route_scored_bwd(self.logits, self.topk_idx, self.dg, self.dlogits, r.score, r.renormalize, r.scale,
                                      stream)
+            if self.balance is not None:
+                moe.moe_balance_loss_bwd(self.logits, self.balance_counts, self.dlogits, k, dloss=dbalance,
+                                         dl_add=self.dlogits, **self._balance_args(stream))
             moe.moe_router_bwd_dlogits(self._x, w_r, self.dlogits, self.dw_r, self.dx, True, self.router_ws, stream)
         elif w_r is not None:
             moe.moe_router_bwd(self._x, w_r, self.topk_idx, self.topk_w, self.dg, self.dlogits, self.dw_r, self.dx,
@@ -251,8 +284,9 @@ class MoeBlockBuffers:
     s_down [S, H], and route_bias [E] (optional); backward leaves the gradients
     in `grads` under the same names (the selection bias has none)."""
 
-    def __init__(self, T, H, F, E, k, S, routing=ScoredRouting(), dtype=torch.bfloat16, device="cuda", eps=1e-5):
-        self.layer = L = MoeLayerBuffers(T, H, F, E, k, dtype, device, router=True, routing=routing)
+    def __init__(self, T, H, F, E, k, S, routing=ScoredRouting(), dtype=torch.bfloat16, device="cuda", eps=1e-5,
+                 balance=None):
+        self.layer = L = MoeLayerBuffers(T, H, F, E, k, dtype, device, router=True, routing=routing, balance=balance)
         self.eps = eps
         em = lambda *s, dt=dtype: torch.empty(*s, dtype=dt, device=L.device)  # noqa: E731
         self.xn, self.y, self.dx = em(T, H), em(T, H), em(T, H)
@@ -265,21 +299,23 @@ class MoeBlockBuffers:
         self.grads = dict(gamma=em(H), beta=em(H), w_r=L.dw_r, w_gate=L.dw_gate, w_up=L.dw_up, w_down=L.dw_down,
                           s_gate=em(H, S), s_up=em(H, S), s_down=em(S, H))
 
-    def forward(self, x, p, stream=None):
+    def forward(self, x, p, stream=None, seq_offsets=None):
         self._x = x
         moe.moe_layernorm_fwd(x, p["gamma"], p.get("beta"), self.xn, self.mean, self.rstd, self.eps, stream)
         routed = self.layer.forward(None, self.xn, p["w_gate"], p["w_up"], p["w_down"], stream, w_r=p["w_r"],
-                                    route_bias=p.get("route_bias"))
+                                    route_bias=p.get("route_bias"), seq_offsets=seq_offsets)
         moe.moe_linear_fwd(self.xn, p["s_up"], None, self.up, workspace=self.ws, stream=stream)
         moe.moe_linear_fwd(self.xn, p["s_gate"], None, self.hidden, act=moe.MOE_ACT_SILU, mul=self.up,
                            z_save=self.z_gate, workspace=self.ws, stream=stream)
         moe.moe_linear_fwd(self.hidden, p["s_down"], None, self.y, residual=routed, workspace=self.ws, stream=stream)
         return self.y
 
-    def backward(self, dy, p, dx_add=None, stream=None):
-        """dx (+ dx_add, the gradient that reaches x past the block) and `grads`."""
+    def backward(self, dy, p, dx_add=None, stream=None, dbalance=None):
+        """dx (+ dx_add, the gradient that reaches x past the block) and `grads`;
+        dbalance: as for MoeLayerBuffers.backward."""
         g, ws, s = self.grads, self.ws, stream
-        dxn = self.layer.backward(dy, p["w_gate"], p["w_up"], p["w_down"], stream=stream, w_r=p["w_r"])
+        dxn = self.layer.backward(dy, p["w_gate"], p["w_up"], p["w_down"], stream=stream, w_r=p["w_r"],
+                                  dbalance=dbalance)
         moe.moe_linear_bwd(self.hidden, p["s_down"], dy, None, self.d_hidden, g["s_down"], workspace=ws, stream=s)
         moe.moe_linear_bwd(self.xn, p["s_gate"], self.d_hidden, self.dz, dxn, g["s_gate"], act=moe.MOE_ACT_SILU,
                            z=self.z_gate, mul=self.up, dmul=self.d_up, dx_add=dxn, workspace=ws, stream=s)
@@ -287,3 +323,60 @@ class MoeBlockBuffers:
         moe.moe_layernorm_bwd(self._x, p["gamma"], self.mean, self.rstd, dxn, self.dx, g["gamma"],
                               g["beta"] if p.get("beta") is not None else None, ws, dx_add, s)
         return self.dx
+
+
+class MoeHeadBuffers:
+    """The vocabulary loss over T tokens of width H: the head's weights [H, V], of
+    whose columns the first `vocab` (None: all) are classes.  forward leaves loss and
+    lse [T] and mean = {mean loss, 1 / counted tokens}; backward dx and, with dw, the
+    weights' gradient."""
+
+    def __init__(self, T, H, V, vocab=None, dtype=torch.bfloat16, device="cuda", dw=True):
+        dev = torch.device(device)
+        em = lambda *s, dt=torch.float32: torch.empty(*s, dtype=dt, device=dev)  # noqa: E731
+        self.vocab = vocab
+        self.loss, self.lse, self.mean = em(T), em(T), em(2)
+        self.dx = em(T, H, dt=dtype)
+        self.dw = em(H, V, dt=dtype) if dw else None
+        self.ws = em(max(moe.moe_vocab_loss_workspace_bytes(T, H, V, dtype), 16), dt=torch.uint8)
+
+    def forward(self, x, w, target, stream=None):
+        moe.moe_vocab_loss_fwd(x, w, target, self.loss, self.lse, self.mean, self.ws, self.vocab, stream)
+        return self.mean
+
+    def backward(self, x, w, target, dloss=None, scale=1.0, stream=None):
+        """Of scale times the mean loss, or with dloss [T] of scale times sum dloss loss."""
+        moe.moe_vocab_loss_bwd(x, w, target, self.loss, self.lse, self.mean, self.dx, self.dw, self.ws, dloss, scale,
+                               self.vocab, stream)
+        return self.dx
+
+
+class AdamWBuffers:
+    """AdamW over named parameters and their gradients (of one dtype, which stay where
+    they are): moments of `bits` 32 or 8 and, with `master`, fp32 copies of bf16
+    parameters.  weight_decay: of all, or a dict by name (0 for those that are not in
+    it).  lr [1] and counter live on the device, so a captured step takes each replay's
+    rate and counts on."""
+
+    def __init__(self, params, grads, lr, weight_decay=0.0, betas=(0.9, 0.999), eps=1e-8, bits=32, master=False, seed=0):
+        self.betas, self.eps, self.seed = betas, eps, seed
+        self.state, tensors = {}, []
+        for name, p in params.items():
+            dev, n = p.device, p.numel()
+            decay = weight_decay.get(name, 0.0) if isinstance(weight_decay, dict) else weight_decay
+            if bits == 8:
+                z = lambda dt, n=n: torch.zeros(n, dtype=dt, device=dev)  # noqa: E731
+                s = dict(m=z(torch.uint8), v=z(torch.uint8), m_scale=z(torch.float32, -(-n // 256)),
+                         v_scale=z(torch.float32, -(-n // 256)))
+            else:
+                s = dict(m=torch.zeros_like(p, dtype=torch.float32), v=torch.zeros_like(p, dtype=torch.float32))
+            if master:
+                s["master"] = p.detach().to(torch.float32, copy=True)
+            self.state[name] = s
+            tensors.append(moe.AdamWTensor(p, grads[name], weight_decay=decay, **s))
+        self.plan = moe.AdamWPlan(tensors)
+        self.counter = torch.zeros(2, dtype=torch.int32, device=dev)
+        self.lr = torch.full((1,), lr, dtype=torch.float32, device=dev)
+
+    def step(self, grad_scale=None, stream=None):
+        moe.moe_adamw_step(self.plan, self.counter, self.lr, *self.betas, self.eps, grad_scale, self.seed, stream)

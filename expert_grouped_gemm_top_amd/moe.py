@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import typing
 
 import torch
@@ -745,21 +746,28 @@ class AdamWPlan:
         self.device_index = dev = _device(tensors[0].param, "param")
         d, small = tensors[0].param.dtype, tensors[0].m.dtype == torch.uint8
         dt, state = _dt(tensors[0].param), torch.uint8 if small else F32
-        entries = (_AdamWEntry * len(tensors))()
-        for e, t in zip(entries, tensors):
-            n = t.param.numel()
+
+        def address(x, name, dtype, numel):
+            if x.dtype is dtype and x.numel() == numel and x.get_device() == dev and x.is_contiguous():
+                return x.data_ptr()
+            _ptr(x, name, dtype)
+            if x.numel() != numel:
+                raise MoeError(f"{name} holds {x.numel()} elements, needs {numel}")
+            raise MoeError(f"{name} is on {x.device} in a plan on the current device cuda:{dev}")
+
+        words = []
+        for t in tensors:
+            if any(not isinstance(x, torch.Tensor) for x in t[:4]):
+                raise MoeError("param, grad, m and v are tensors")
             if (t.m_scale is None or t.v_scale is None) == small:
                 raise MoeError("m_scale and v_scale are given with 8-bit moments, and only then")
-            for name, dtype, numel in (("param", d, n), ("grad", d, n), ("m", state, n), ("v", state, n),
-                                       ("m_scale", F32, -(-n // 256)), ("v_scale", F32, -(-n // 256)), ("master", F32, n)):
-                x = getattr(t, name)
-                p = _ptr(x, name, dtype, allow_none=name in ("m_scale", "v_scale", "master"))
-                if x is not None and x.numel() != numel:
-                    raise MoeError(f"{name} holds {x.numel()} elements, needs {numel}")
-                if x is not None and x.get_device() != dev:
-                    raise MoeError(f"{name} is on {x.device} in a plan on the current device cuda:{dev}")
-                setattr(e, name, p)
-            e.numel, e.weight_decay = n, t.weight_decay
+            n = t.param.numel()
+            scales = [address(x, name, F32, -(-n // 256)) if small else 0
+                      for x, name in ((t.m_scale, "m_scale"), (t.v_scale, "v_scale"))]
+            words += (address(t.param, "param", d, n), address(t.grad, "grad", d, n), address(t.m, "m", state, n),
+                      address(t.v, "v", state, n), *scales, 0 if t.master is None else address(t.master, "master", F32, n), n,
+                      float(t.weight_decay))
+        entries = struct.pack("8Qd" * len(tensors), *words)  # _AdamWEntry each
         size = int(lib().moe_adamw_plan_bytes(len(tensors)))
         if size == 0:
             raise MoeError(f"a plan of {len(tensors)} tensors is too large")
