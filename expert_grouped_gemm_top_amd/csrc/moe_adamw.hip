@@ -321,10 +321,34 @@ __device__ __forceinline__ void adamw_pass(const AdamwArgs& g, const Shared& sh,
   }
 }
 
+// The last of n tensors that begins at or before `chunk` (those before it are empty or done): 64 places are looked at
+// at a time.
+__device__ __forceinline__ int tensor_of(const int64_t* starts, int n, int64_t chunk) {
+  int lo = 0;
+  for (int left = n; left > 1;) {
+    const int step = (left + 63) / 64, at = lane_id() * step;
+    const bool before = at < left && get<int64_t>(starts + lo + at) <= chunk;
+    const int last = max(__popcll(__ballot(before)) - 1, 0) * step;
+    lo += last;
+    left = min(step, left - last);
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
 template <typename T, bool MASTER, bool SMALL>
 __global__ __launch_bounds__(256, SMALL ? 4 : 1) void adamw_kernel(AdamwArgs g) {
   __shared__ Shared s_sh;
   const int tid = threadIdx.x;
+  int i = 0;
+  int64_t from = 0, to = 0;  // chunks of tensor i
+  AdamwEntry e{};
+  auto find = [&](int64_t chunk) {
+    i += tensor_of(g.starts + i, g.n - i, chunk);
+    from = uniform(g.starts[i]);
+    to = uniform(g.starts[i + 1]);
+    e = uniform(g.entries[i]);
+  };
+  if (blockIdx.x < g.chunks) find(blockIdx.x);
   if (tid == 0) {
     const int t = g.counter[0] + 1;
     const double lr = *g.lr;
@@ -336,20 +360,8 @@ __global__ __launch_bounds__(256, SMALL ? 4 : 1) void adamw_kernel(AdamwArgs g) 
   }
   __syncthreads();
   const Shared sh = uniform(s_sh);
-  int i = 0;
-  int64_t from = 0, to = 0;  // chunks of tensor i
-  AdamwEntry e{};
   for (int64_t chunk = blockIdx.x; chunk < g.chunks; chunk += gridDim.x) {
-    if (chunk >= to) {
-      int hi = g.n;  // the last tensor that begins at or before the chunk: those before it are empty or done
-      while (hi - i > 1) {
-        const int mid = (i + hi) >> 1;
-        if (g.starts[mid] <= chunk) i = mid; else hi = mid;
-      }
-      from = g.starts[i];
-      to = g.starts[i + 1];
-      e = uniform(g.entries[i]);
-    }
+    if (chunk >= to) find(chunk);
     const int64_t first = (chunk - from) * kAdamwChunk;
     if (first + kAdamwChunk <= e.numel) adamw_pass<T, MASTER, SMALL, true>(g, sh, e, first + 8 * tid);
     else adamw_pass<T, MASTER, SMALL, false>(g, sh, e, first + 8 * tid);
