@@ -18,8 +18,7 @@
 // expected values are the exact ones.
 #include <algorithm>
 #include <cstring>
-#include <new>
-#include <vector>
+#include <type_traits>
 
 #include "moe_common.h"
 #include "moe_launch.h"
@@ -335,10 +334,13 @@ __device__ __forceinline__ int tensor_of(const int64_t* starts, int n, int64_t c
   return __builtin_amdgcn_readfirstlane(lo);
 }
 
-template <typename T, bool MASTER, bool SMALL>
-__global__ __launch_bounds__(256, SMALL ? 4 : 1) void adamw_kernel(AdamwArgs g) {
+// Workgroups of NT threads, of which every 256 take a chunk at a time.
+template <typename T, bool MASTER, bool SMALL, int NT>
+__global__ __launch_bounds__(NT, SMALL ? 4 : 1) void adamw_kernel(AdamwArgs g) {
+  constexpr int AT_ONCE = NT / 256;  // chunks
   __shared__ Shared s_sh;
   const int tid = threadIdx.x;
+  const int64_t begin = (int64_t)blockIdx.x * AT_ONCE + __builtin_amdgcn_readfirstlane(tid / 256);
   int i = 0;
   int64_t from = 0, to = 0;  // chunks of tensor i
   AdamwEntry e{};
@@ -348,7 +350,7 @@ __global__ __launch_bounds__(256, SMALL ? 4 : 1) void adamw_kernel(AdamwArgs g) 
     to = uniform(g.starts[i + 1]);
     e = uniform(g.entries[i]);
   };
-  if (blockIdx.x < g.chunks) find(blockIdx.x);
+  if (begin < g.chunks) find(begin);
   if (tid == 0) {
     const int t = g.counter[0] + 1;
     const double lr = *g.lr;
@@ -360,11 +362,11 @@ __global__ __launch_bounds__(256, SMALL ? 4 : 1) void adamw_kernel(AdamwArgs g) 
   }
   __syncthreads();
   const Shared sh = uniform(s_sh);
-  for (int64_t chunk = blockIdx.x; chunk < g.chunks; chunk += gridDim.x) {
+  for (int64_t chunk = begin; chunk < g.chunks; chunk += (int64_t)gridDim.x * AT_ONCE) {
     if (chunk >= to) find(chunk);
-    const int64_t first = (chunk - from) * kAdamwChunk;
-    if (first + kAdamwChunk <= e.numel) adamw_pass<T, MASTER, SMALL, true>(g, sh, e, first + 8 * tid);
-    else adamw_pass<T, MASTER, SMALL, false>(g, sh, e, first + 8 * tid);
+    const int64_t first = (chunk - from) * kAdamwChunk, at = first + 8 * (tid % 256);
+    if (first + kAdamwChunk <= e.numel) adamw_pass<T, MASTER, SMALL, true>(g, sh, e, at);
+    else adamw_pass<T, MASTER, SMALL, false>(g, sh, e, at);
   }
   // The last workgroup to get here counts the step: every one has read the counter.
   if (tid == 0 && (uint32_t)atomicAdd((uint32_t*)g.counter + 1, 1u) == gridDim.x - 1) {
@@ -449,23 +451,32 @@ hipError_t launch_adamw(const void* plan, const void* plan_device, const AdamwSt
   g.log_beta2 = a.beta2 > 0.0 ? log(a.beta2) : -__builtin_inf();
   g.eps = (float)a.eps;
   g.seed = a.seed;
-  // 32-bit moments are bound by HBM, best with one workgroup on a CU (151M weights with masters: 256 workgroups 808 us,
-  // 512 835, 2048 859); the codes' arithmetic wants every SIMD full (256 workgroups 660 us, 1024 395, 2048 375).
-  const int64_t most = h.small ? 2048 : 256;
-  const dim3 grid((unsigned)std::max<int64_t>(1, std::min(h.chunks, most))), block(256);
-  auto run = [&](auto kernel) {
-    MOE_LAUNCH(kernel, grid, block, 0, stream, g);
+  auto run = [&](auto kernel, int threads, int most) {
+    const int64_t groups = (h.chunks + threads / 256 - 1) / (threads / 256);
+    const dim3 grid((unsigned)std::max<int64_t>(1, std::min<int64_t>(groups, most)));
+    MOE_LAUNCH(kernel, grid, dim3(threads), 0, stream, g);
     return hipGetLastError();
   };
-  if (h.esize == 4) return h.small ? run(adamw_kernel<float, false, true>) : run(adamw_kernel<float, false, false>);
-  if (h.master)
-    return h.small ? run(adamw_kernel<uint16_t, true, true>) : run(adamw_kernel<uint16_t, true, false>);
-  return h.small ? run(adamw_kernel<uint16_t, false, true>) : run(adamw_kernel<uint16_t, false, false>);
+  // 32-bit moments are bound by HBM, best with one small workgroup on a CU (151M weights with masters: 256 workgroups of
+  // 256 threads 808 us, 512 835, 2048 859; 2M: 12.5, 15.3, 18.8, as workgroups queue up to say that they are done).
+  // The codes' arithmetic wants every SIMD full, by 256 workgroups of 1024 threads or, where the end counts for
+  // little, 2048 of 256 (2M weights 17.4 and 24.7 us, 8M 41 and 51, 32M 145 and 143, 151M 362 and 345).
+  constexpr int64_t kManyChunks = 8192;
+  auto of = [&](auto t, auto master) {
+    using T = decltype(t);
+    constexpr bool MASTER = decltype(master)::value;
+    if (!h.small) return run(adamw_kernel<T, MASTER, false, 256>, 256, 256);
+    if (h.chunks >= kManyChunks) return run(adamw_kernel<T, MASTER, true, 256>, 256, 2048);
+    return run(adamw_kernel<T, MASTER, true, 1024>, 1024, 256);
+  };
+  if (h.esize == 4) return of(0.0f, std::false_type{});
+  return h.master ? of(uint16_t{}, std::true_type{}) : of(uint16_t{}, std::false_type{});
 }
 
 hipError_t launch_adamw_moments(int64_t numel, const uint8_t* m, const uint8_t* v, const float* m_scale,
                                 const float* v_scale, float* m_out, float* v_out, hipStream_t stream) {
-  MOE_LAUNCH(adamw_moments_kernel, wide_grid((numel + 2047) / 2048), dim3(256), 0, stream, numel, m, v, m_scale, v_scale, m_out, v_out);
+  MOE_LAUNCH(adamw_moments_kernel, wide_grid((numel + 2047) / 2048), dim3(256), 0, stream, numel, m, v, m_scale, v_scale,
+             m_out, v_out);
   return hipGetLastError();
 }
 
