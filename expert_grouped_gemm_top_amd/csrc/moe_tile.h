@@ -218,19 +218,23 @@ using Tile4 = Tile<64, 64, 4, 2, 2, sizeof(T) == 2 ? 4 : 2>;
 // 2048 9.1 -> 7.3 us).
 using Tile5 = Tile<32, 32, 1, 1, 8, 2>;
 
-// Output tile (mt, nt) over k in [kb, ke), none where kb == ke.  A stage
+// Output tiles over k in [kb, ke), none where kb == ke, one after the other: `next`
+// gives them, next(mt, nt), until it says that there are no more.  A stage
 // is waited for before the last run of the one in front, so its first
 // fragments are read under those products, and its successor's loads go out in
 // two halves before the next two runs of products.
 // `out` gets the outputs.  Where Out::kWhole (tiles of one reduction group), out.tile
 // gets the sums as they lie in the waves' registers, with the stage buffers free:
 // register r of acc[i][j] is row TM wm + 32 i + l32 of the tile, column
-// TN wn + 32 j + 8 (r / 4) + 4 hk + r % 4.  Else out.skip(m, n) says that a run is not wanted, and
+// TN wn + 32 j + 8 (r / 4) + 4 hk + r % 4.  STREAM, for an out.tile that leaves
+// the stage buffers alone: the next tile's first stages load meanwhile, and what it
+// needs from memory out.ahead has put into LDS before the tile's products, so that no
+// wait for that waits for those loads.  Else out.skip(m, n) says that a run is not wanted, and
 // out(m, n, v, lanes) takes the eight outputs of row m from column n on; `lanes`
 // neighbouring lanes, a constant, hold 8 lanes neighbouring columns of a row.
-template <typename T, bool AKC, bool BKC, typename C, bool TAIL, typename Out>
-__device__ __forceinline__ void tile_product(const TileSource& g, int mt, int nt, int kb, int ke, unsigned char* s_dyn,
-                                             Out&& out) {
+template <typename T, bool AKC, bool BKC, typename C, bool TAIL, bool STREAM, typename Next, typename Out>
+__device__ __forceinline__ void tile_products(const TileSource& g, Next&& next, int kb, int ke, unsigned char* s_dyn,
+                                              Out&& out) {
   constexpr int BM = C::BM, BN = C::BN, NW = C::NW, WM = C::WM, KG = C::KG, STAGES = C::STAGES;
   constexpr int BK = kStageK<T>, RUN = kRunProducts<T>;
   constexpr int TM = BM / WM, TN = BN / (NW / WM), MI = TM / 32, NJ = TN / 32;
@@ -238,25 +242,32 @@ __device__ __forceinline__ void tile_product(const TileSource& g, int mt, int nt
   const int tid = threadIdx.x, l = tid & 63, l32 = l & 31, hk = l >> 5;
   const int kg = (tid >> 6) / NW, w = (tid >> 6) % NW;
   const int wm = w % WM, wn = w / WM;
-  const int m0 = mt * BM, n0 = nt * BN;
+  static_assert(!STREAM || std::remove_reference_t<Out>::template kWhole<C>, "no stage buffer for the outputs");
+  const int steps = (ke - kb + KG * BK - 1) / (KG * BK);
+  int mt, nt;
+  if (!next(mt, nt)) return;
+  int m0 = mt * BM, n0 = nt * BN;
 
   Loader<T, AKC, BM, NW, TAIL> la;
   Loader<T, BKC, BN, NW, TAIL> lb;
-  la.init(g.a, g.lda, g.rows, m0, g.M, kb + kg * BK, KG * BK, w, l);
-  lb.init(g.b, g.ldb, nullptr, n0, g.N, kb + kg * BK, KG * BK, w, l);
   constexpr int INS = Loader<T, AKC, BM, NW, TAIL>::INS + Loader<T, BKC, BN, NW, TAIL>::INS;  // loads of a stage
   // stage s lies in buffer s % STAGES; a group loads and reads its own part of it
   unsigned char* const mine = s_dyn + kg * GROUP;
   auto issue_a = [&](int buf) { la.issue(ke, KG * BK, mine + buf * STAGE, w); };
   auto issue_b = [&](int buf) { lb.issue(ke, KG * BK, mine + buf * STAGE + A_BYTES, w); };
 
+  // the first stages of tile (m0, n0)
+  auto start = [&] {
+    la.init(g.a, g.lda, g.rows, m0, g.M, kb + kg * BK, KG * BK, w, l);
+    lb.init(g.b, g.ldb, nullptr, n0, g.N, kb + kg * BK, KG * BK, w, l);
+    for (int s = 0; s < STAGES - 1 && s < steps; ++s) {
+      issue_a(s);
+      issue_b(s);
+    }
+  };
+  start();
+
   f32x16 acc[MI][NJ];
-#pragma unroll
-  for (int i = 0; i < MI; ++i)
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
   struct Frags {
     u32x4 a[MI], b[NJ];
   };
@@ -285,13 +296,16 @@ __device__ __forceinline__ void tile_product(const TileSource& g, int mt, int nt
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  const int steps = (ke - kb + KG * BK - 1) / (KG * BK);
+next_tile:
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  if constexpr (STREAM) out.template ahead<C>(m0);
   if (steps > 0) {
     Frags f0, f1;
-    for (int s = 0; s < STAGES - 1 && s < steps; ++s) {
-      issue_a(s);
-      issue_b(s);
-    }
     if (steps >= STAGES - 1) wait_vmcnt<(STAGES - 2) * INS>();  // stage 0 has landed, later ones need not have
     else wait_vmcnt<0>();
     barrier_no_fence();
@@ -330,7 +344,19 @@ __device__ __forceinline__ void tile_product(const TileSource& g, int mt, int nt
   if constexpr (std::remove_reference_t<Out>::template kWhole<C>) {
     __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's last fragment reads are done
     barrier_no_fence();                   // ... and every wave's
-    out.template tile<C>(acc, m0, n0, s_dyn);
+    if constexpr (STREAM) {
+      const int m = m0, n = n0;
+      const bool more = next(mt, nt);
+      if (more) {
+        m0 = mt * BM;
+        n0 = nt * BN;
+        start();
+      }
+      out.template tile<C>(acc, m, n, s_dyn);
+      if (more) goto next_tile;
+    } else {
+      out.template tile<C>(acc, m0, n0, s_dyn);
+    }
     return;
   }
   // The fp32 tile leaves through the idle stage buffers, HC columns at a time
@@ -378,6 +404,18 @@ __device__ __forceinline__ void tile_product(const TileSource& g, int mt, int nt
     }
     __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's reads of the staged rows are done
   }
+}
+
+// One output tile.
+template <typename T, bool AKC, bool BKC, typename C, bool TAIL, typename Out>
+__device__ __forceinline__ void tile_product(const TileSource& g, int mt, int nt, int kb, int ke, unsigned char* s_dyn,
+                                             Out&& out) {
+  auto once = [&](int& m, int& n) {
+    m = mt;
+    n = nt;
+    return true;
+  };
+  tile_products<T, AKC, BKC, C, TAIL, false>(g, once, kb, ke, s_dyn, out);
 }
 
 }  // namespace moe

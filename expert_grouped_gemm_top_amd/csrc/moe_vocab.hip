@@ -177,25 +177,46 @@ __device__ __forceinline__ Run joined(const Run& a, const Run& b) {
 // from the waves' registers; where the groups' sums must be joined first they
 // come by eight columns.  At 256 x 256 over 2048 a tile's statistics cost
 // 3 of its 58 us (through LDS 7).
+// LDS behind the stage buffers: the waves' statistics [WN][BM], then the targets of the tile's rows [BM].
+template <typename C>
+constexpr int kTileRuns = C::BM * (C::NW / C::WM);
+
 template <typename T>
 struct LossOut {
   template <typename C>
   static constexpr bool kWhole = sizeof(T) == 2 && C::KG == 1;
+  // The next tile's loads go out under the statistics (128 rows of 2048 by 131072 columns: 108 -> 104 us).  At
+  // 256 x 256 the addresses do not fit beside the sums, and spilled ones cost more (4096 rows: 1181 -> 1295 us).
+  template <typename C>
+  static constexpr bool kStream = kWhole<C> && C::BM * C::BN < 256 * 256;
+  template <typename C>
+  static constexpr size_t kBehind = kWhole<C> ? kTileRuns<C> * sizeof(Run) + C::BM * 4 : 0;
   int n, vocab, pitch;
   const int32_t* y;
   float* own;  // [n] the targets' logits
   Run* runs;   // [run][pitch rows]
+  unsigned char* behind;
 
+  template <typename C>
+  __device__ __forceinline__ int32_t* targets() const {
+    return reinterpret_cast<int32_t*>(behind + kTileRuns<C> * sizeof(Run));
+  }
+  template <typename C>
+  __device__ __forceinline__ void ahead(int m0) const {
+    const int m = m0 + (int)threadIdx.x;
+    if (threadIdx.x < C::BM) targets<C>()[threadIdx.x] = m < n ? y[m] : -1;
+  }
   template <typename C, int MI, int NJ>
-  __device__ __forceinline__ void tile(f32x16 (&acc)[MI][NJ], int m0, int n0, unsigned char* s_dyn) const {
+  __device__ __forceinline__ void tile(f32x16 (&acc)[MI][NJ], int m0, int n0, unsigned char*) const {
     constexpr int BM = C::BM, WN = C::NW / C::WM, TM = BM / C::WM, TN = C::BN / WN;
     const int tid = threadIdx.x, l32 = tid & 31, hk = (tid >> 5) & 1, w = tid >> 6, wm = w % C::WM, wn = w / C::WM;
     const int first = n0 + TN * wn;  // this wave's columns
-    Run* s_run = reinterpret_cast<Run*>(s_dyn);  // [WN][BM]
+    Run* s_run = reinterpret_cast<Run*>(behind);  // [WN][BM]
+    const int32_t* target = targets<C>();
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
       const int row = TM * wm + 32 * i + l32, m = m0 + row;
-      const int at = (m < n ? y[m] : -1) - first;  // the target, if it is among them
+      const int at = target[row] - first;  // the target, if it is among them
       if (__ballot(at >= 0 && at < TN) || first + TN > vocab) {  // a few waves, or the last columns
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
@@ -276,14 +297,27 @@ template <typename T, typename C, bool TAIL>
 __global__ __launch_bounds__(kTileThreads, 2) void vocab_loss_kernel(LogitsArgs<T> a, int vocab, int pitch, float* own,
                                                                      Run* runs) {
   extern __shared__ __attribute__((aligned(16))) unsigned char s_dyn[];
-  const int item = group_id();
+  int item = group_id();
   TileSource g = a.g;
   Listed list = a.list;
-  g.M = a.own_list ? list_here(a.tokens, list, item == 0, s_dyn + C::LDS) : list.head[0];
+  using Out = LossOut<T>;
+  unsigned char* behind = s_dyn + C::LDS;
+  g.M = a.own_list ? list_here(a.tokens, list, item == 0, behind + Out::template kBehind<C>) : list.head[0];
   g.rows = list.rows;
-  int mt, nt;
-  if (!row_tile<C>(item, g.M, g.N, mt, nt)) return;
-  tile_product<T, true, false, C, TAIL>(g, mt, nt, 0, a.K, s_dyn, LossOut<T>{g.M, vocab, pitch, list.y, own, runs});
+  const Out out{g.M, vocab, pitch, list.y, own, runs, behind};
+  if constexpr (Out::template kStream<C>) {
+    auto next = [&](int& mt, int& nt) {
+      const bool more = row_tile<C>(item, g.M, g.N, mt, nt);
+      item += gridDim.x * gridDim.y;
+      return more;
+    };
+    tile_products<T, true, false, C, TAIL, true>(g, next, 0, a.K, s_dyn, out);
+  } else {
+    int mt, nt;
+    if (!row_tile<C>(item, g.M, g.N, mt, nt)) return;
+    if constexpr (Out::template kWhole<C>) out.template ahead<C>(mt * C::BM);
+    tile_product<T, true, false, C, TAIL>(g, mt, nt, 0, a.K, s_dyn, out);
+  }
 }
 
 // Joins the runs of 16 rows per workgroup, 64 threads each; the last workgroup adds up the mean.
@@ -762,10 +796,12 @@ hipError_t list_tokens(const Tokens& tokens, const Listed& list, hipStream_t str
 template <typename T, typename C, bool TAIL>
 hipError_t run_loss(const LogitsArgs<T>& a, int vocab, int pitch, float* own, Run* runs, hipStream_t stream) {
   static PerDeviceOnce once;
-  constexpr size_t lds = C::LDS + kOwnListBytes;
+  // the forward's list needs no `off`: the wide tiles' waves have just enough room
+  constexpr size_t lds = C::LDS + LossOut<T>::template kBehind<C> + kOwnListBytes - 4 * kOwnListRows;
   static_assert(lds <= 160 * 1024, "one CU's LDS");
-  return run_tiles(vocab_loss_kernel<T, C, TAIL>, lds, tiles_of<C>(a.g.M, a.g.N), stream, once, a, vocab, pitch, own,
-                   runs);
+  int64_t groups = tiles_of<C>(a.g.M, a.g.N);
+  if (LossOut<T>::template kStream<C>) groups = std::min<int64_t>(groups, kCus);  // each takes tile after tile
+  return run_tiles(vocab_loss_kernel<T, C, TAIL>, lds, groups, stream, once, a, vocab, pitch, own, runs);
 }
 
 template <typename T, typename C, bool TAIL>
