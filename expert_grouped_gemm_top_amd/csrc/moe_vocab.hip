@@ -103,21 +103,26 @@ __device__ __forceinline__ void list_token(const Tokens& g, const Listed& out, i
   }
 }
 
-// Lists many tokens, by one workgroup.
-constexpr int kListRun = 8;
+// Lists many tokens, 1024 a workgroup, each of which counts the ones before its own for itself: a launch that waits for
+// nothing (8192 tokens, backward: FIXME us; by one workgroup 30).
 __global__ __launch_bounds__(1024) void vocab_list_kernel(Tokens g, Listed out) {
   __shared__ int s_wave[16];
-  int before = 0;
-  for (int64_t base = 0; base < g.T; base += 1024 * kListRun) {
-    const int64_t first = base + (int64_t)threadIdx.x * kListRun;
-    int y[kListRun], at = place_of<1024>(g, first, y, before, s_wave);
+  const int64_t first = (int64_t)blockIdx.x * 1024;
+  int mine = 0;
+  for (int64_t t = threadIdx.x; t < first; t += 1024 * 8) {
 #pragma unroll
-    for (int j = 0; j < kListRun; ++j) {
-      list_token(g, out, first + j, y[j], at);
-      at += y[j] >= 0;
-    }
+    for (int j = 0; j < 8; ++j) mine += t + 1024 * j < first && g.y(t + 1024 * j) >= 0;
   }
-  if (threadIdx.x == 0) {
+  mine = wave_inclusive_scan(mine);
+  if ((threadIdx.x & 63) == 63) s_wave[threadIdx.x >> 6] = mine;
+  __syncthreads();
+  int before = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) before += s_wave[i];
+  int y[1];
+  const int at = place_of<1024>(g, first + threadIdx.x, y, before, s_wave);
+  list_token(g, out, first + threadIdx.x, y[0], at);
+  if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) {
     out.head[0] = before;
     out.head[1] = 0;
   }
@@ -571,13 +576,34 @@ struct DwOut {
   }
 };
 
+// The slices of dx's product.  They are laid out for the batch's tokens; where fewer are counted their tiles leave
+// workgroups over, and each slice is cut into as many as those do, on the device, which knows the count (T 1703 with 307
+// counted, H 360, V 42516, fp32: 1068 -> FIXME us).  Their sums lie in the rows that are not needed either.
+struct Slices {
+  int many, slice;  // for the batch's tokens: how many, and their columns
+  int tiles;        // ... and row tiles
+  int piece;        // columns of all but the last piece
+  int pitch;
+  bool again;       // whether to cut them
+  struct Cut {
+    int slice, pitch, many;
+  };
+  __device__ __forceinline__ Cut cut(int n, int bm) const {
+    const int times = again ? tiles / max(1, (n + bm - 1) / bm) : 1;
+    if (times <= 1) return {slice, pitch, many};
+    const int cols = (slice + times - 1) / times, c = (cols + 127) / 128 * 128;
+    return {c, (n + bm - 1) / bm * bm, (piece + c - 1) / c};
+  }
+};
+
 struct GradArgs {
   TileSource gx, gw;    // dz W^T (M: the batch's tokens) and x^T dz
-  int Kx, slice, pitch; // the piece's columns, those of a slice, rows of dz and of a slice's sums
+  int Kx;               // the piece's columns
+  Slices slices;
   Listed list;
   int add;              // not the first piece
   float* sums;
-  void* dx;             // the last piece of a product in one slice
+  void* dx;             // the last piece: written from here where there is one slice
   Factor c;
   void* dw;
   int64_t ldw;
@@ -599,12 +625,15 @@ __global__ __launch_bounds__(kTileThreads, 2) void vocab_grads_kernel(GradArgs a
     const int mtiles = (n + CX::BM - 1) / CX::BM, ntiles = (g.N + CX::BN - 1) / CX::BN, tiles = mtiles * ntiles;
     const int item = (int)(a.x_first ? b : b - a.nw);
     if (tiles == 0) return;
-    const int s = item / tiles, kb = s * a.slice;
-    if (s * (int64_t)a.slice >= a.Kx) return;
+    const Slices::Cut cut = a.slices.cut(n, CX::BM);
+    const int s = item / tiles;
+    if (s * (int64_t)cut.slice >= a.Kx) return;
+    const int kb = s * cut.slice;
     int mt, nt;
     tile_of(item % tiles, mtiles, ntiles, 1024 / CX::BM, mt, nt);
-    tile_product<T, true, true, CX, TAIL>(g, mt, nt, kb, min(a.Kx, kb + a.slice), s_dyn,
-                                           DxOut<T>{n, g.N, a.pitch, s, a.add != 0, a.sums, a.list, a.c.get(), (T*)a.dx});
+    tile_product<T, true, true, CX, TAIL>(g, mt, nt, kb, min(a.Kx, kb + cut.slice), s_dyn,
+                                           DxOut<T>{n, g.N, cut.pitch, s, a.add != 0, a.sums, a.list, a.c.get(),
+                                                    cut.many == 1 ? (T*)a.dx : nullptr});
   } else {
     const TileSource& g = a.gw;
     const int mtiles = (g.M + CW::BM - 1) / CW::BM, ntiles = (g.N + CW::BN - 1) / CW::BN;
@@ -618,8 +647,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void vocab_grads_kernel(GradArgs a
 
 // dx of the counted tokens from the slices' sums.
 template <typename T>
-__global__ __launch_bounds__(256) void vocab_dx_kernel(int T_, int H, int slices, int pitch, Listed list,
+__global__ __launch_bounds__(256) void vocab_dx_kernel(int T_, int H, Slices slices, int bm, Listed list,
                                                        const float* __restrict__ sums, Factor f, T* __restrict__ dx) {
+  const Slices::Cut cut = slices.cut(list.head[0], bm);
+  if (cut.many == 1) return;  // the last piece has left dx
   const float c = f.get();
   const int runs = H / 8;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)T_ * runs; i += (int64_t)gridDim.x * 256) {
@@ -628,9 +659,9 @@ __global__ __launch_bounds__(256) void vocab_dx_kernel(int T_, int H, int slices
     if (place < 0) continue;
     float v[8] = {};
 #pragma unroll 4
-    for (int s = 0; s < slices; ++s) {
+    for (int s = 0; s < cut.many; ++s) {
       float u[8];
-      load8(sums + ((int64_t)s * pitch + place) * H + h, u);
+      load8(sums + ((int64_t)s * cut.pitch + place) * H + h, u);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] += u[j];
     }
@@ -789,7 +820,7 @@ int64_t tiles_of(int M, int N) {
 }
 
 hipError_t list_tokens(const Tokens& tokens, const Listed& list, hipStream_t stream) {
-  MOE_LAUNCH(vocab_list_kernel, dim3(1), dim3(1024), 0, stream, tokens, list);
+  MOE_LAUNCH(vocab_list_kernel, dim3((unsigned)((tokens.T + 1023) / 1024)), dim3(1024), 0, stream, tokens, list);
   return hipGetLastError();
 }
 
@@ -853,7 +884,15 @@ hipError_t vocab_bwd_typed(const VocabArgs& g, const float* loss, const float* l
   if (err != hipSuccess) return err;
   const Factor c{scale, dloss != nullptr ? nullptr : mean};
   T* dz = (T*)s.dz;
-  const int slices = dx != nullptr ? (std::min(p.piece, g.V) + p.grads.x.slice - 1) / p.grads.x.slice : 0;
+  Slices slices{};
+  int bm = 1;
+  if (dx != nullptr) {
+    slices.slice = p.grads.x.slice;
+    slices.piece = std::min(p.piece, g.V);
+    slices.many = (slices.piece + slices.slice - 1) / slices.slice;
+    slices.pitch = p.pitch;
+    slices.again = slices.many > 1 || !own_list;  // few tokens in one slice: not worth a launch
+  }
   for (int first = 0; first < g.V; first += p.piece) {
     const int cols = std::min(p.piece, g.V - first);
     const Layout<T> beside{g.H, (const T*)g.x, dw != nullptr ? (T*)s.x : nullptr, (T*)dx, 0,
@@ -871,12 +910,10 @@ hipError_t vocab_bwd_typed(const VocabArgs& g, const float* loss, const float* l
     b.gx = TileSource{g.T, g.H, dz, p.piece, w, g.V, nullptr};
     b.gw = TileSource{g.H, dw != nullptr ? cols : 0, s.x, g.H, dz, p.piece, nullptr};
     b.Kx = dx != nullptr ? cols : 0;
-    b.slice = p.grads.x.slice;
-    b.pitch = p.pitch;
     b.list = s.list;
     b.add = first > 0;
     b.sums = s.sums;
-    b.dx = slices == 1 && first + cols == g.V ? dx : nullptr;
+    b.dx = first + cols == g.V ? dx : nullptr;
     b.c = c;
     b.dw = dw != nullptr ? (T*)dw + first : nullptr;
     b.ldw = g.V;
@@ -884,10 +921,13 @@ hipError_t vocab_bwd_typed(const VocabArgs& g, const float* loss, const float* l
     auto run = [&](auto tx, auto tw) {
       using CX = decltype(tx);
       using CW = decltype(tw);
-      b.nx = dx != nullptr ? tiles_of<CX>(g.T, g.H) * ((cols + b.slice - 1) / b.slice) : 0;
+      bm = CX::BM;
+      slices.tiles = (g.T + bm - 1) / bm;
+      b.slices = slices;
+      b.nx = tiles_of<CX>(g.T, g.H) * slices.many;
       b.nw = dw != nullptr ? tiles_of<CW>(g.H, cols) : 0;
       constexpr int SX = kStageK<T> * CX::KG;
-      const bool tail_x = cols % SX != 0 || b.slice % SX != 0;
+      const bool tail_x = cols % SX != 0 || slices.slice % SX != 0 || (slices.again && 128 % SX != 0);
       return tail_x ? run_grads<T, CX, CW, true>(b, stream) : run_grads<T, CX, CW, false>(b, stream);
     };
     const int pair = p.few ? -1 : p.grads.pair;
@@ -905,10 +945,10 @@ hipError_t vocab_bwd_typed(const VocabArgs& g, const float* loss, const float* l
     if (pair == 7) err = run(Tile5{}, Tile4<T>{});
     if (err != hipSuccess) return err;
   }
-  if (slices <= 1) return hipSuccess;
+  if (!slices.again) return hipSuccess;
   const int64_t runs = (int64_t)g.T * (g.H / 8);
   MOE_LAUNCH(vocab_dx_kernel<T>, dim3((unsigned)std::min<int64_t>((runs + 255) / 256, 8192)), dim3(256), 0, stream, g.T, g.H,
-             slices, p.pitch, s.list, s.sums, c, (T*)dx);
+             slices, bm, s.list, s.sums, c, (T*)dx);
   return hipGetLastError();
 }
 

@@ -125,8 +125,8 @@ int moe_abi_version(void);
  *   moe_linear_fwd                          1, plus 1 when its reduction is split
  *   moe_balance_loss_fwd                    1 for one sequence of T <= 256, else 2
  *   moe_vocab_loss_fwd                      2, plus 1 for T > 1024
- *   moe_vocab_loss_bwd                      1 for T > 1024, plus 2 for each piece of the vocabulary, plus 1 where
- *                                           dx's products are split
+ *   moe_vocab_loss_bwd                      1 for T > 1024, plus 2 for each piece of the vocabulary, plus 1 for dx
+ *                                           where T > 1024 or its products are split
  *   moe_balance_loss_bwd, moe_adamw_step,
  *   moe_adamw_moments                       1
  *   moe_linear_bwd                          1 for dz or dbias (0 without activation, gate and

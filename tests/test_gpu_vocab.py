@@ -87,10 +87,11 @@ def test_larger_bf16(T, H, V, vocab):
     check(T, H, V, "bf16", seed=T, vocab=vocab, weighted=True)
 
 
-def test_several_pieces():
+@pytest.mark.parametrize("ignored", [0.3, 0.99])
+def test_several_pieces(ignored):
     """Vocabularies of more than one piece, the last of odd width."""
     T = 20000
-    x, w, y, vocab = case(T, 64, 9000, "bf16", 3, 8997)
+    x, w, y, vocab = case(T, 64, 9000, "bf16", 3, 8997, ignored)
     b = Buffers(T, 64, 9000, "bf16")
     d = [dev(x, "bf16"), dev(w, "bf16"), torch.from_numpy(y).cuda()]
     before = moe.moe_launch_count()
@@ -125,6 +126,14 @@ def test_either_gradient_alone(dx, dw, dtype):
 @pytest.mark.parametrize("ignored", [0.0, 0.5, 0.97, 1.0])
 def test_rows_that_are_not_counted_may_hold_anything(ignored, dtype):
     check(150, 96, 520, dtype, seed=5, vocab=515, ignored=ignored, spoil=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H,V,ignored", [(2100, 264, 2056, 0.6), (2100, 264, 2056, 0.97), (1700, 136, 4104, 0.9),
+                                           (1025, 72, 1000, 1.0), (1030, 512, 24, 0.8), (900, 128, 3000, 0.95)])
+def test_few_of_many_tokens_are_counted(T, H, V, ignored, dtype):
+    """The slices of dx are cut again where most tokens are not counted."""
+    check(T, H, V, dtype, seed=T, vocab=V - 3, ignored=ignored, weighted=True, spoil=True)
 
 
 def test_targets_outside_are_not_counted():
