@@ -202,6 +202,35 @@ __device__ __forceinline__ void leave_bf16(f32x16 (&acc)[MI][NJ], unsigned char*
   }
 }
 
+// The same without LDS, for stage buffers that are being loaded: the two lanes of a row exchange their halves, and each
+// leaves every other 16-byte run.
+template <typename C, int MI, int NJ, typename Make, typename Put>
+__device__ __forceinline__ void leave_bf16_direct(f32x16 (&acc)[MI][NJ], Make&& make, Put&& put) {
+  const int tid = threadIdx.x, l32 = tid & 31, hk = (tid >> 5) & 1, w = tid >> 6;
+  const int row0 = C::BM / C::WM * (w % C::WM) + l32, col0 = C::BN / (C::NW / C::WM) * (w / C::WM);
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; q += 2) {
+        const int row = row0 + 32 * i, col = col0 + 32 * j + 8 * q;
+        uint32_t half[2][2];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          float v[4] = {acc[i][j][4 * (q + p)], acc[i][j][4 * (q + p) + 1], acc[i][j][4 * (q + p) + 2],
+                        acc[i][j][4 * (q + p) + 3]};
+          make(i, row, col + 8 * p + 4 * hk, v);
+          half[p][0] = pack_bf2(v[0], v[1]);
+          half[p][1] = pack_bf2(v[2], v[3]);
+        }
+        // lanes 32 to 63 of run q change places with lanes 0 to 31 of run q + 1
+        const auto a = __builtin_amdgcn_permlane32_swap(half[0][0], half[1][0], false, false);
+        const auto b = __builtin_amdgcn_permlane32_swap(half[0][1], half[1][1], false, false);
+        put(row, col + 8 * hk, u32x4{a[0], b[0], a[1], b[1]});
+      }
+}
+
 // The tiles of moe_linear_plan.h.
 using Tile0 = Tile<256, 256, 8, 2, 1, 2>;
 using Tile1 = Tile<256, 128, 8, 4, 1, 3>;
@@ -228,8 +257,8 @@ using Tile5 = Tile<32, 32, 1, 1, 8, 2>;
 // register r of acc[i][j] is row TM wm + 32 i + l32 of the tile, column
 // TN wn + 32 j + 8 (r / 4) + 4 hk + r % 4.  STREAM, for an out.tile that leaves
 // the stage buffers alone: the next tile's first stages load meanwhile, and what it
-// needs from memory out.ahead has put into LDS before the tile's products, so that no
-// wait for that waits for those loads.  Else out.skip(m, n) says that a run is not wanted, and
+// needs from memory out.ahead has put into LDS before the tile's products (behind a
+// barrier of the last out.tile), so that no wait for that waits for those loads.  Else out.skip(m, n) says that a run is not wanted, and
 // out(m, n, v, lanes) takes the eight outputs of row m from column n on; `lanes`
 // neighbouring lanes, a constant, hold 8 lanes neighbouring columns of a row.
 template <typename T, bool AKC, bool BKC, typename C, bool TAIL, bool STREAM, typename Next, typename Out>
