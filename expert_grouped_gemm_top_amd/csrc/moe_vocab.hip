@@ -104,7 +104,7 @@ __device__ __forceinline__ void list_token(const Tokens& g, const Listed& out, i
 }
 
 // Lists many tokens, 1024 a workgroup, each of which counts the ones before its own for itself: a launch that waits for
-// nothing (8192 tokens, backward: FIXME us; by one workgroup 30).
+// nothing (8192 tokens, 5.6 us; by one workgroup 30).
 __global__ __launch_bounds__(1024) void vocab_list_kernel(Tokens g, Listed out) {
   __shared__ int s_wave[16];
   const int64_t first = (int64_t)blockIdx.x * 1024;
@@ -178,6 +178,12 @@ __device__ __forceinline__ Run joined(const Run& a, const Run& b) {
   return {top, a.sum * expf(a.top - base) + b.sum * expf(b.top - base)};
 }
 
+// Whether a workgroup takes tile after tile of logits, the next one's loads under what becomes of the last one's sums
+// (128 rows of 2048 by 131072 columns: the loss 108 -> 104 us, the frozen head's backward 232 -> 226).  At 256 x 256 the
+// addresses do not fit beside the sums, and spilled ones cost more (loss of 4096 rows: 1181 -> 1295 us).
+template <typename T, typename C>
+constexpr bool streams = sizeof(T) == 2 && C::KG == 1 && C::BM * C::BN < 256 * 256;
+
 // Row statistics of a tile of logits.  Tiles of one reduction group (bf16) take them
 // from the waves' registers; where the groups' sums must be joined first they
 // come by eight columns.  At 256 x 256 over 2048 a tile's statistics cost
@@ -190,10 +196,6 @@ template <typename T>
 struct LossOut {
   template <typename C>
   static constexpr bool kWhole = sizeof(T) == 2 && C::KG == 1;
-  // The next tile's loads go out under the statistics (128 rows of 2048 by 131072 columns: 108 -> 104 us).  At
-  // 256 x 256 the addresses do not fit beside the sums, and spilled ones cost more (4096 rows: 1181 -> 1295 us).
-  template <typename C>
-  static constexpr bool kStream = kWhole<C> && C::BM * C::BN < 256 * 256;
   template <typename C>
   static constexpr size_t kBehind = kWhole<C> ? kTileRuns<C> * sizeof(Run) + C::BM * 4 : 0;
   int n, vocab, pitch;
@@ -310,7 +312,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void vocab_loss_kernel(LogitsArgs<
   g.M = a.own_list ? list_here(a.tokens, list, item == 0, behind + Out::template kBehind<C>) : list.head[0];
   g.rows = list.rows;
   const Out out{g.M, vocab, pitch, list.y, own, runs, behind};
-  if constexpr (Out::template kStream<C>) {
+  if constexpr (streams<T, C>) {
     auto next = [&](int& mt, int& nt) {
       const bool more = row_tile<C>(item, g.M, g.N, mt, nt);
       item += gridDim.x * gridDim.y;
@@ -407,7 +409,15 @@ struct GradOut {
   int pitch;
   Listed list;
   T* dz;
+  float2* rows;  // LDS, [BM] of the tile's rows, where it streams: log of the others' sum in base 2, target (its bits)
 
+  __device__ __forceinline__ float2 row_of(int m) const {
+    return m < n ? float2{list.off[m] * 1.44269504f, __int_as_float(list.y[m] - first)} : float2{0.0f, __int_as_float(-1)};
+  }
+  template <typename C>
+  __device__ __forceinline__ void ahead(int m0) const {
+    if (threadIdx.x < C::BM) rows[threadIdx.x] = row_of(m0 + (int)threadIdx.x);
+  }
   template <typename C, int MI, int NJ>
   __device__ __forceinline__ void tile(f32x16 (&acc)[MI][NJ], int m0, int n0, unsigned char* s_dyn) const {
     constexpr int WN = C::NW / C::WM, TM = C::BM / C::WM, TN = C::BN / WN;
@@ -417,28 +427,33 @@ struct GradOut {
     bool special = first + n0 + C::BN > vocab;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      const int m = m0 + TM * (wv % C::WM) + 32 * i + (threadIdx.x & 31);
-      base[i] = m < n ? list.off[m] * 1.44269504f : 0.0f;
-      at[i] = (m < n ? list.y[m] - first : -1) - n0;
+      const int row = TM * (wv % C::WM) + 32 * i + (threadIdx.x & 31);
+      const float2 r = streams<T, C> ? rows[row] : row_of(m0 + row);
+      base[i] = r.x;
+      at[i] = __float_as_int(r.y) - n0;
       const int in_wave = at[i] - TN * (wv / C::WM);
       special |= __ballot(in_wave >= 0 && in_wave < TN) != 0;
     }
+    if constexpr (streams<T, C>) {
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave has its rows
+      barrier_no_fence();                   // ... and every wave: the next tile's may come
+    }
     auto go = [&](auto with) {
-      leave_bf16<C>(
-          acc, s_dyn,
-          [&](int i, int, int col, float (&v)[4]) {
+      auto make = [&](int i, int, int col, float (&v)[4]) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              v[e] = __builtin_amdgcn_exp2f(fmaf(v[e], 1.44269504f, -base[i]));
-              if (decltype(with)::value) {
-                if (first + n0 + col + e >= vocab) v[e] = 0.0f;
-                if (at[i] == col + e) v[e] = -1.0f;
-              }
-            }
-          },
-          [&](int row, int col, u32x4 q) {
-            if (m0 + row < n) *(u32x4*)(dz + (int64_t)(m0 + row) * pitch + n0 + col) = q;
-          });
+        for (int e = 0; e < 4; ++e) {
+          v[e] = __builtin_amdgcn_exp2f(fmaf(v[e], 1.44269504f, -base[i]));
+          if (decltype(with)::value) {
+            if (first + n0 + col + e >= vocab) v[e] = 0.0f;
+            if (at[i] == col + e) v[e] = -1.0f;
+          }
+        }
+      };
+      auto put = [&](int row, int col, u32x4 q) {
+        if (m0 + row < n) *(u32x4*)(dz + (int64_t)(m0 + row) * pitch + n0 + col) = q;
+      };
+      if constexpr (streams<T, C>) leave_bf16_direct<C>(acc, make, put);
+      else leave_bf16<C>(acc, s_dyn, make, put);
     };
     if (special) go(std::true_type{});  // a few waves, or the last columns
     else go(std::false_type{});
@@ -458,7 +473,7 @@ struct GradOut {
   }
 };
 
-// What the first piece's launch does beside it, in workgroups of its own: the listed tokens' rows of x times their f, one
+// What the first piece's launch does beside it, in workgroups of its own or behind their tiles: the listed tokens' rows of x times their f, one
 // behind the other, for dW, which sums over them (out NULL: not wanted), and zeros for the other tokens' dx (NULL alike).
 template <typename T>
 struct Layout {
@@ -502,13 +517,26 @@ __global__ __launch_bounds__(kTileThreads, 2) void vocab_dz_kernel(LogitsArgs<T>
   Listed list = a.list;
   g.M = a.own_list ? list_here(a.tokens, list, item == 0, s_dyn + C::LDS) : list.head[0];
   g.rows = list.rows;
-  if (item >= beside.tiles) {
-    if (item - beside.tiles < beside.groups) lay_out(beside, a.tokens, list.rows, g.M, (int)(item - beside.tiles));
-    return;
+  GradOut<T> out{g.M, first, a.tokens.vocab, pitch, list, dz, nullptr};
+  if constexpr (streams<T, C>) {
+    out.rows = reinterpret_cast<float2*>(s_dyn + C::LDS + kOwnListBytes);
+    int tile = (int)item;
+    auto next = [&](int& mt, int& nt) {
+      const bool more = row_tile<C>(tile, g.M, g.N, mt, nt);
+      tile += (int)beside.tiles;
+      return more;
+    };
+    if (item < beside.tiles) tile_products<T, true, false, C, TAIL, true>(g, next, 0, a.K, s_dyn, out);
+    if (item < beside.groups) lay_out(beside, a.tokens, list.rows, g.M, (int)item);
+  } else {
+    if (item >= beside.tiles) {
+      if (item - beside.tiles < beside.groups) lay_out(beside, a.tokens, list.rows, g.M, (int)(item - beside.tiles));
+      return;
+    }
+    int mt, nt;
+    if (!row_tile<C>((int)item, g.M, g.N, mt, nt)) return;
+    tile_product<T, true, false, C, TAIL>(g, mt, nt, 0, a.K, s_dyn, out);
   }
-  int mt, nt;
-  if (!row_tile<C>((int)item, g.M, g.N, mt, nt)) return;
-  tile_product<T, true, false, C, TAIL>(g, mt, nt, 0, a.K, s_dyn, GradOut<T>{g.M, first, a.tokens.vocab, pitch, list, dz});
 }
 
 // The factor that dz was held without.
@@ -578,7 +606,7 @@ struct DwOut {
 
 // The slices of dx's product.  They are laid out for the batch's tokens; where fewer are counted their tiles leave
 // workgroups over, and each slice is cut into as many as those do, on the device, which knows the count (T 1703 with 307
-// counted, H 360, V 42516, fp32: 1068 -> FIXME us).  Their sums lie in the rows that are not needed either.
+// counted, H 360, V 42516, fp32: 1068 -> 538 us).  Their sums lie in the rows that are not needed either.
 struct Slices {
   int many, slice;  // for the batch's tokens: how many, and their columns
   int tiles;        // ... and row tiles
@@ -831,7 +859,7 @@ hipError_t run_loss(const LogitsArgs<T>& a, int vocab, int pitch, float* own, Ru
   constexpr size_t lds = C::LDS + LossOut<T>::template kBehind<C> + kOwnListBytes - 4 * kOwnListRows;
   static_assert(lds <= 160 * 1024, "one CU's LDS");
   int64_t groups = tiles_of<C>(a.g.M, a.g.N);
-  if (LossOut<T>::template kStream<C>) groups = std::min<int64_t>(groups, kCus);  // each takes tile after tile
+  if (streams<T, C>) groups = std::min<int64_t>(groups, kCus);  // each takes tile after tile
   return run_tiles(vocab_loss_kernel<T, C, TAIL>, lds, groups, stream, once, a, vocab, pitch, own, runs);
 }
 
@@ -839,8 +867,15 @@ template <typename T, typename C, bool TAIL>
 hipError_t run_dz(const LogitsArgs<T>& a, int first, int pitch, T* dz, Layout<T> beside, hipStream_t stream) {
   static PerDeviceOnce once;
   beside.tiles = tiles_of<C>(a.g.M, a.g.N);
-  return run_tiles(vocab_dz_kernel<T, C, TAIL>, C::LDS + kOwnListBytes, beside.tiles + beside.groups, stream, once, a, first,
-                   pitch, dz, beside);
+  size_t lds = C::LDS + kOwnListBytes;
+  int64_t groups = beside.tiles + beside.groups;
+  if constexpr (streams<T, C>) {
+    static_assert(C::LDS + kOwnListBytes + C::BM * sizeof(float2) <= 160 * 1024, "one CU's LDS");
+    lds += C::BM * sizeof(float2);
+    beside.tiles = std::min<int64_t>(beside.tiles, kCus);  // each takes tile after tile, then lays out its share
+    groups = std::max<int64_t>(beside.tiles, beside.groups);
+  }
+  return run_tiles(vocab_dz_kernel<T, C, TAIL>, lds, groups, stream, once, a, first, pitch, dz, beside);
 }
 
 template <typename T, typename CX, typename CW, bool TAIL>
