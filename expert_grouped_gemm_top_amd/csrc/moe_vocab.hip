@@ -371,11 +371,12 @@ __global__ __launch_bounds__(1024) void vocab_join_kernel(JoinArgs a) {
     const int at = blockIdx.x * 16 + w;
     float loss = 0.0f;
     if (at < n) {
-      const float own = a.own[at], d = run.top + logf(run.sum) - own;  // log of the others' sum over the target's
-      loss = fmaxf(d, 0.0f) + log1pf(expf(-fabsf(d)));
+      const float own = a.own[at], others = run.top + logf(run.sum), d = others - own;
+      const float less = log1pf(expf(-fabsf(d)));
+      loss = fmaxf(d, 0.0f) + less;
       const int t = a.list.rows[at];
       a.loss[t] = loss;
-      a.lse[t] = own + loss;
+      a.lse[t] = fmaxf(others, own) + less;  // not own + loss: a target far below would take the others' digits
     }
     s_loss[w] = (double)loss;
   }

@@ -163,6 +163,106 @@ def test_confident_tokens_keep_their_digits():
     assert (np.abs(host(b.dx)[diag, diag] - ref["dx"][diag, diag]) <= 300 * 2.0 ** -24 * np.abs(ref["dx"][diag, diag])).all()
 
 
+@pytest.mark.parametrize("far", [2.0 ** 20, 2.0 ** 40, float("inf")])
+def test_a_target_far_below_leaves_the_others_their_digits(far):
+    """lse and the others' gradients do not pass through the target's logit.  All logits are whole: lse is off by the
+    exponentials' and the logarithm's roundings, below 64 2^-24, a gradient by that, its own and its product's."""
+    H = V = 16
+    x, w = np.zeros((3, H)), np.eye(H)
+    x[0, :4], x[1, 5:9], x[2, 3] = [1, 2, 3, 4], [7, 0, 7, 1], 2
+    y = np.array([15, 14, 13], np.int32)
+    if np.isfinite(far):
+        x[np.arange(3), y] = -far
+    else:  # W alone reaches it: an infinite x would make every logit NaN
+        x[:, H - 1] = 1
+        w[H - 1] = 0
+        w[H - 1, 13:] = -far
+        y[:] = 15
+    with np.errstate(invalid="ignore"):
+        l = np.where(np.isinf(w[H - 1])[None, :] & (x[:, H - 1:] != 0), -np.inf, x @ np.where(np.isinf(w), 0, w))
+    others = np.where(np.arange(V)[None, :] == y[:, None], -np.inf, l)
+    top = others.max(1, keepdims=True)
+    lse = (top + np.log(np.exp(others - top).sum(1, keepdims=True)))[:, 0]
+    b = Buffers(3, H, V, "f32")
+    b.step(dev(x, "f32"), dev(w, "f32"), torch.from_numpy(y).cuda(), V, torch.ones(3, device="cuda"))
+    torch.cuda.synchronize()
+    within("lse", host(b.lse), lse, 64 * 2.0 ** -24 + np.abs(lse) * 2.0 ** -23)
+    if np.isfinite(far):
+        own = l[np.arange(3), y]
+        within("loss", host(b.loss), lse - own, 64 * 2.0 ** -24 + np.abs(lse - own) * 2.0 ** -23)
+        q = np.exp(others - lse[:, None])
+        q[np.arange(3), y] = -1
+        within("dx", host(b.dx), q @ w.T, 300 * 2.0 ** -24 * (np.abs(q) @ np.abs(w).T))
+    else:
+        assert (host(b.loss) == np.inf).all()
+        q = np.exp(others - lse[:, None])
+        q[np.arange(3), y] = -1
+        within("dw", host(b.dw), x.T @ q, 300 * 2.0 ** -24 * (np.abs(x).T @ np.abs(q)))
+
+
+def test_more_tokens_than_the_list_kernels_first_rounds():
+    """Two million tokens: their list, 1024 a workgroup, and the products' rows behind it."""
+    T, H, V = (1 << 21) + 5, 8, 16
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(T, H, device="cuda", generator=g)
+    w = torch.randn(H, V, device="cuda", generator=g)
+    y = torch.randint(-8, V, (T,), device="cuda", generator=g, dtype=torch.int32)
+    b = Buffers(T, H, V, "f32")
+    b.step(x, w, y, V)
+    keep, rows = y >= 0, torch.arange(T, device="cuda")
+    l = (x.double()[:, :, None] * w.double()[None]).sum(1)
+    lse = torch.logsumexp(l, 1)
+    loss = (lse - l[rows, y.long().clamp(min=0)]) * keep
+    assert ((b.lse.double() - lse) * keep).abs().max() <= 64 * 2.0 ** -23 * l.abs().max()
+    assert (b.loss.double() - loss).abs().max() <= 64 * 2.0 ** -23 * l.abs().max()
+    n = int(keep.sum())
+    assert float(b.mean[1]) == np.float32(1 / n) and abs(float(b.mean[0]) - float(loss.sum()) / n) <= 1e-5
+    p = torch.exp(l - lse[:, None])
+    p[rows, y.long().clamp(min=0)] -= 1
+    p *= keep[:, None] / n
+    dx = (p[:, None, :] * w.double()[None]).sum(2)
+    assert (b.dx.double() - dx).abs().max() <= 200 * 2.0 ** -23 * float((p.abs()[:, None, :] * w.double().abs()[None]).sum(2).max())
+    # sums of n terms in fp32, 32 to 64 k at a time in a matrix core's chain: n 2^-24 of their sizes at the most
+    dw, size = (x.double()[:, :, None] * p[:, None, :]).sum(0), (x.double().abs()[:, :, None] * p.abs()[:, None, :]).sum(0)
+    assert ((b.dw.double() - dw).abs() <= n * 2.0 ** -24 * size).all()
+
+
+def test_weights_past_32_bit_offsets():
+    """4.3e9 weights: their last columns and rows, with classes on both sides of 2^31 and 2^32 elements."""
+    T, H, V = 5, 4104, 1 << 20
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(H, V, dtype=torch.bfloat16, device="cuda")
+    y = torch.tensor([0, V - 1, V // 2, -1, V - 2], dtype=torch.int32, device="cuda")
+    x[:, H - 1] = torch.tensor([1.0, 2.0, -1.0, float("nan"), 0.5])
+    x[:, 3] = 1
+    w[H - 1, V - 1], w[H - 1, 0], w[3, V // 2], w[H - 1, V - 2] = 8, 4, 6, -3
+    b = Buffers(T, H, V, "bf16")
+    b.step(x, w, y, V)
+    torch.cuda.synchronize()
+    # the logits of all but four columns are 0
+    at = [0, V // 2, V - 2, V - 1]
+    X, W = x[[0, 1, 2, 4]].double().cpu(), w[:, at].double().cpu()
+    l = X[:, [3, H - 1]] @ W[[3, H - 1]]
+    lse = torch.log(torch.exp(l).sum(1) + (V - 4))
+    own = l[torch.arange(4), torch.tensor([0, 3, 1, 2])]
+    got = b.loss.double().cpu()[[0, 1, 2, 4]]
+    assert (got - (lse - own)).abs().max() <= 1e-4 and float(b.loss[3]) == 0  # a sum of 2^20 terms, and 64 2^-23 of 24
+    p = torch.exp(l - lse[:, None])
+    p[torch.arange(4), torch.tensor([0, 3, 1, 2])] -= 1
+    p /= 4
+    dw = X[:, [3, H - 1]].T @ p
+    got = b.dw[[3, H - 1]][:, at].double().cpu()
+    size = X[:, [3, H - 1]].abs().T @ p.abs()
+    assert ((got - dw).abs() <= (3.01 * U["bf16"] + 2e-4) * size).all()  # both factors and the result rounded
+    dx = p @ W[[3, H - 1]].T
+    got = b.dx[[0, 1, 2, 4]][:, [3, H - 1]].double().cpu()
+    assert ((got - dx).abs() <= (2.01 * U["bf16"] + 2e-4) * (p.abs() @ W[[3, H - 1]].T.abs())).all()
+    assert (b.dx[3] == 0).all() and int((b.dx != 0).sum()) <= 8
+    assert int((b.dw[4:H - 1] != 0).sum()) == 0 and int((b.dw[:3] != 0).sum()) == 0
+    del b, w
+    torch.cuda.empty_cache()
+
+
 def test_a_difference_quotient():
     x, w, y, vocab = case(12, 16, 40, "f32", 7, 37)
     b = Buffers(12, 16, 40, "f32")
