@@ -198,6 +198,35 @@ def test_captured_replays():
                 assert torch.equal(x, y)
 
 
+def test_logits_past_32_bit_offsets():
+    """2.1e9 logits in two sequences, all equal but in the last row: its share and its gradient."""
+    T, E = (1 << 23) + 5, 256
+    l = torch.zeros(T, E, device="cuda")
+    l[T - 1, E - 1] = 8
+    idx = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    idx[T - 3:] = E - 1
+    off = torch.tensor([0, T - 3, T], dtype=torch.int32, device="cuda")
+    counts, mean = torch.zeros(2, E, dtype=torch.int32, device="cuda"), torch.zeros(2, E, device="cuda")
+    loss = torch.zeros(1, device="cuda")
+    ws = torch.empty(moe.moe_balance_loss_workspace_bytes(T, E, 2), dtype=torch.uint8, device="cuda")
+    moe.moe_balance_loss_fwd(l, idx, counts, mean, loss, ws, seq_offsets=off)
+    d = torch.full((T, E), 7.0, device="cuda")
+    moe.moe_balance_loss_bwd(l, counts, d, 1, seq_offsets=off)
+    torch.cuda.synchronize()
+    assert counts[0, 0] == T - 3 and counts[1, E - 1] == 3 and int(counts.sum()) == T
+    assert (mean[0].double() - 1 / E).abs().max() <= 200 * 2.0 ** -23 / E + (T / 1024 / 64) * 2.0 ** -24 / E
+    top = np.exp(8.0) / (np.exp(8.0) + E - 1)
+    want = E / T * ((T - 3) / E + 3 * (2 / E + top) / 3)
+    assert abs(float(loss) - want) <= 1e-3 * want
+    f = E / T / 3  # of the last sequence's rows
+    assert abs(float(d[T - 1, E - 1]) - f * top * 3 * (1 - top)) <= 1e-5 * f * top * 3 * (1 - top)
+    assert abs(float(d[T - 2, 0]) + f / E * 3 / E) <= 1e-5 * f / E * 3 / E
+    first = E / T / (T - 3) / E * (T - 3) * (1 - 1 / E)
+    assert abs(float(d[0, 0]) - first) <= 1e-5 * first and abs(float(d[T - 4, 0]) - first) <= 1e-5 * first
+    del l, d
+    torch.cuda.empty_cache()
+
+
 def test_launches():
     for T, n in ((256, 1), (257, 2)):
         l, idx = case(T, 16, 2, 8)
