@@ -268,6 +268,61 @@ def test_on_another_stream_and_two_at_once():
             assert torch.equal(t.param, u.param) and torch.equal(t.m, u.m) and torch.equal(t.v, u.v)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_no_eps_and_gradients_whose_squares_are_subnormal(bits):
+    """m / sqrt(v) is a sign where both decays are 0: of squares down to 2^-140, as fp32 keeps them (half a step of
+    2^-149 of v, half of that of its root, and 16 roundings)."""
+    g = np.array([2.0 ** -e * s * f for e in (30, 60, 62, 63, 64, 66, 68, 70) for s in (1, -1) for f in (1.0, 1.4)])
+    n = len(g)
+    for i in range(n) if bits == 8 else [slice(None)]:  # 8 bits: a block of its own for each
+        a = np.atleast_1d(g[i])
+        e = lambda dt=torch.float32: torch.zeros(len(a), dtype=dt, device="cuda")  # noqa: E731
+        extra = dict(m_scale=e()[:1], v_scale=e()[:1]) if bits == 8 else {}
+        d = torch.uint8 if bits == 8 else torch.float32
+        t = moe.AdamWTensor(e(), gpu(a), e(d), e(d), **extra)
+        c = torch.zeros(2, dtype=torch.int32, device="cuda")
+        moe.moe_adamw_step(moe.AdamWPlan([t]), c, torch.ones(1, device="cuda"), 0.0, 0.0, 0.0)
+        a = fp32(a)
+        err = 16 * U["f32"] + 2.0 ** -150 / a ** 2
+        assert (np.abs(host(t.param) + np.sign(a)) <= err).all(), (a, host(t.param))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_tensors_past_32_bit_offsets(bits):
+    """4.3e9 weights in one tensor and a small one behind it: their ends move as the formula says, the zeros between stay."""
+    n = (1 << 32) + 4096 + 77 if bits == 8 else (1 << 31) + 4096 + 77
+    h = torch.bfloat16
+    z = lambda n, dt: torch.zeros(n, dtype=dt, device="cuda")  # noqa: E731
+    d = torch.uint8 if bits == 8 else torch.float32
+    make = lambda n: moe.AdamWTensor(z(n, h), z(n, h), z(n, d), z(n, d), **(  # noqa: E731
+        dict(m_scale=z(-(-n // 256), torch.float32), v_scale=z(-(-n // 256), torch.float32)) if bits == 8 else {}))
+    t, u = make(n), make(300)
+    for a in (t, u):
+        a.grad[-300:] = 0.5
+        a.param[-300:] = 1.0
+    t.grad[:300], t.param[:300] = 0.5, 1.0
+    c = z(2, torch.int32)
+    moe.moe_adamw_step(moe.AdamWPlan([t, u]), c, torch.full((1,), 0.125, device="cuda"), 0.5, 0.5, 0.0)
+    torch.cuda.synchronize()
+    # the first step of equal gradients is lr: 1 - 0.125, a bf16 value (or, from an fp32 one a rounding off, its neighbour)
+    for a in (t.param[:300], t.param[-300:], u.param):
+        assert (a.float() - 0.875).abs().max() <= 2.0 ** -8
+        assert (a.float() == 0.875).float().mean() > 0.9
+    for a in ([t.m[:300], t.m[-300:], u.m] if bits == 32 else []):
+        assert (a == 0.25).all()
+    if bits == 8:
+        mo, vo = z(n, torch.float32), z(n, torch.float32)
+        moe.moe_adamw_moments(t.m, t.v, t.m_scale, t.v_scale, mo, vo)
+        for a in (slice(0, 300), slice(n - 300, n)):  # 0.25 and 0.125 are codes at their blocks' scales
+            assert (mo[a] == 0.25).all() and (vo[a] == 0.125).all()
+        assert int((t.m[300:-300] != 0).sum()) == 0
+        del mo, vo
+    # 0 / (0 + 0) is NaN with eps 0: the formula's
+    assert torch.isnan(t.param[300:400]).all() and torch.isnan(t.param[-400:-300]).all()
+    del t, u
+    torch.cuda.empty_cache()
+
+
 def test_nothing_to_do_is_a_step():
     t = Model([0, 0], "f32", 32, False)
     t.step(0)
