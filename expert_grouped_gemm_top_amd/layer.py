@@ -148,6 +148,8 @@ class MoeLayerBuffers:
         the token rows are quantized per row, then gathered on load.
         route_bias: the selection bias [E] of a layer with `routing`.
         seq_offsets: where the balance loss' sequences lie, [n_seq + 1]."""
+        assert self.balance is None or w_r is not None, "the balance loss needs the router's logits"
+        assert self.balance is not None or seq_offsets is None, "sequences are the balance loss'"
         self._x = x  # the backward reads token rows through the pair ids
         self._seq_offsets = seq_offsets
         if w_r is not None:
@@ -210,7 +212,9 @@ class MoeLayerBuffers:
         None (the routing weights) or "metric" (moe_pair_scores: the norm of
         each pair's rank-one dW_down term).  With w_r, the router's backward
         follows: dlogits, dw_r, and its share added to dx.  dbalance [1] fp32: the
-        gradient that reaches the balance loss (None: 1)."""
+        gradient that reaches the balance loss (None: 1), whose own joins the
+        logits' there."""
+        assert dbalance is None or (self.balance is not None and w_r is not None), "no balance loss in this backward"
         g, k = self.gather_rows, self.k
         if self.compacted:
             if isinstance(score, str):

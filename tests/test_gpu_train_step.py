@@ -146,6 +146,19 @@ def test_plain_routing_with_a_balance_loss():
     assert (off <= (4 * np.abs(l).max() + 60) * 3 * 2.0 ** -23 * size + 2.0 ** -22 * np.abs(R.host(full.dlogits))).all()
 
 
+def test_a_balance_loss_that_would_be_lost_is_refused():
+    """One of other logits than the router's, sequences without a loss, a gradient that nothing takes."""
+    f = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+    ws, x = (f(E, H, F), f(E, H, F), f(E, F, H)), f(8, H)
+    offsets = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    with_loss, without = (MoeLayerBuffers(8, H, F, E, K, torch.float32, router=True, balance=b) for b in (BalanceLoss(1.0), None))
+    for call in (lambda: with_loss.forward(f(8, E), x, *ws), lambda: without.forward(None, x, *ws, w_r=f(H, E), seq_offsets=offsets),
+                 lambda: without.backward(x, *ws, w_r=f(H, E), dbalance=f(1)), lambda: with_loss.backward(x, *ws, dbalance=f(1)),
+                 lambda: MoeLayerBuffers(8, H, F, E, K, torch.float32, balance=BalanceLoss(1.0))):
+        with pytest.raises(AssertionError, match="balance"):
+            call()
+
+
 def batch(T, seed):
     rng = np.random.default_rng(seed)
     y = rng.integers(0, VOCAB, T).astype(np.int32)
