@@ -21,6 +21,11 @@
 // dW, which sums over the tokens, to their rows of x: rounded once more there
 // (bf16: dW is 2.4e-3 of its norm off, dx 1.7e-3, of which 1.7e-3 by their own
 // rounding).
+//
+// With few rows HBM bounds it: the forward of 128 over 2048 x 131072 reads W at 5.2
+// TB/s (103 us), the frozen head's backward twice at 4.8 (226 us).  With many the
+// matrix cores' feeding through LDS does: 1.1 PFLOP/s over the forward's 256 x 256
+// tiles, 1.2 over the backward's three products of 8192 x 4096 x 65536 (10.9 ms).
 #include <algorithm>
 
 #include "moe_common.h"
@@ -129,7 +134,7 @@ __global__ __launch_bounds__(1024) void vocab_list_kernel(Tokens g, Listed out) 
 }
 
 // Up to this many tokens every workgroup of the first product lists them for itself (in LDS), and one for the later
-// kernels: a launch less (fp32 backward of 333 tokens 27 -> 22 us).
+// kernels: a launch less (fp32 backward of 333 tokens 27 -> 21 us).
 constexpr int kOwnListRows = 1024;
 constexpr size_t kOwnListBytes = kOwnListRows * 12 + 64;
 __device__ __forceinline__ int list_here(const Tokens& g, Listed& list, bool write, unsigned char* s) {
@@ -707,14 +712,15 @@ int rounded_up(int64_t v, int to) { return (int)((v + to - 1) / to * to); }
 
 // Tiles of logits for few rows, beside those of moe_linear_plan.h: wide ones, whose stages hold 32 or 64 KiB of W, so
 // that enough of it is on its way.  One forward over 2048 x 131072, us by rows:
-//               1     64    128    192    256    384    512
-//   64 x 512   101    102    145    193    245    339    442
-//   128 x 256  103    108    110    163    167    235    300
-//   256 x 256  133    140    145    146    150    256    264
+//               1     64    128    192    256    320    384    512   1024
+//   64 x 512    99     98    141    183    233    277    323    426    838
+//   128 x 256   99    103    104    157    163    220    227    289    549
+//   256 x 256  128    134    137    143    146    246    250    258    483
+//   256 x 128  141    148    154    159    161    279    283    290    551
 //   128 x 128 in two reduction groups, two stages   139 to 149 up to 128 rows
 // and the dx products of one piece of 131072 columns on 128 x 128 tiles, frozen head, 128 rows: two groups of two
 // stages 244 us the call, one of four 233.
-enum { kTile64x512 = kTiles, kTile128x256, kTile128x128Deep };
+enum { kTile64x512 = kTiles, kTile128x256 };
 using WideTile = Tile<64, 512, 8, 1, 1, 2>;
 using FlatTile = Tile<128, 256, 8, 2, 1, 3>;
 using DeepTile = Tile<128, 128, 8, 2, 1, 4>;
