@@ -332,21 +332,6 @@ size_t dbias_bytes(int T, int O) { return ((size_t)dz_slots(T, O) * O * sizeof(f
 
 // ---- launchers -------------------------------------------------------------------
 
-// The last plans of this thread by their sizes: a training or decoding loop asks
-// for the same few shapes, and a search costs a few us of the host's time.
-template <typename P, typename Fn>
-const P& remembered(int T, int I, int O, int kind, Fn&& search) {
-  struct Entry {
-    int T, I, O, kind;
-    P plan;
-  };
-  thread_local Entry entries[64] = {};
-  const uint32_t h = ((uint32_t)T * 0x9e3779b1u) ^ ((uint32_t)I * 0x85ebca77u) ^ ((uint32_t)O * 0xc2b2ae3du) ^
-                     ((uint32_t)kind * 0x27d4eb2fu);
-  Entry& e = entries[(h >> 16) & 63];
-  if (e.T != T || e.I != I || e.O != O || e.kind != kind) e = Entry{T, I, O, kind, search()};
-  return e.plan;
-}
 const Cut& fwd_cut(int T, int I, int O, int esize) {
   return remembered<Cut>(T, I, O, esize, [&] { return plan_fwd(T, O, I, esize); });
 }

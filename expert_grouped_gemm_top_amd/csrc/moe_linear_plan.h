@@ -1,5 +1,5 @@
 // moe_linear_plan.h -- which workgroup tiles and reduction slices run the
-// products of moe_linear.hip.  Host code only, a rule on sizes: the plan of
+// products of moe_linear.hip and moe_vocab.hip.  Host code only, a rule on sizes: the plan of
 // least estimated time, from the tiles' measured costs.
 #pragma once
 
@@ -151,6 +151,22 @@ inline Plan2 plan_bwd(int T, int I, int O, int esize, bool dx, bool dw, bool spl
     else each_cut(T, I, O, esize, tiles.x, [&](const Cut& x) { with_w(&x); });
   }
   return best;
+}
+
+// The last plans of this thread by their sizes: a training or decoding loop asks
+// for the same few shapes, and a search costs a few us of the host's time.
+template <typename P, typename Fn>
+const P& remembered(int T, int I, int O, int kind, Fn&& search) {
+  struct Entry {
+    int T, I, O, kind;
+    P plan;
+  };
+  thread_local Entry entries[64] = {};
+  const uint32_t h = ((uint32_t)T * 0x9e3779b1u) ^ ((uint32_t)I * 0x85ebca77u) ^ ((uint32_t)O * 0xc2b2ae3du) ^
+                     ((uint32_t)kind * 0x27d4eb2fu);
+  Entry& e = entries[(h >> 16) & 63];
+  if (e.T != T || e.I != I || e.O != O || e.kind != kind) e = Entry{T, I, O, kind, search()};
+  return e.plan;
 }
 
 }  // namespace moe

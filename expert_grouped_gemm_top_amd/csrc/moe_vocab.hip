@@ -772,7 +772,7 @@ int logits_tile(int T, int N, int H, int esize) {
   return best_tile;
 }
 
-VocabPlan vocab_plan(int T, int H, int V, int esize, bool dx, bool dw) {
+VocabPlan make_plan(int T, int H, int V, int esize, bool dx, bool dw) {
   VocabPlan p{};
   p.pitch = rounded_up(T, 256);
   const int64_t cols = std::max<int64_t>(kPieceElements / p.pitch / 512 * 512, 1024);
@@ -787,6 +787,11 @@ VocabPlan vocab_plan(int T, int H, int V, int esize, bool dx, bool dw) {
     p.grads.x.slices = (p.piece + p.grads.x.slice - 1) / p.grads.x.slice;
   }
   return p;
+}
+
+const VocabPlan& vocab_plan(int T, int H, int V, int esize, bool dx, bool dw) {
+  return remembered<VocabPlan>(T, H, V, esize + (dx ? 8 : 0) + (dw ? 16 : 0),
+                               [&] { return make_plan(T, H, V, esize, dx, dw); });
 }
 
 // The columns of a run that a tile of the forward leaves.
@@ -893,7 +898,7 @@ hipError_t run_grads(const GradArgs& a, hipStream_t stream) {
 
 template <typename T>
 hipError_t vocab_fwd_typed(const VocabArgs& g, float* loss, float* lse, float* mean, void* ws, hipStream_t stream) {
-  const VocabPlan p = vocab_plan(g.T, g.H, g.V, sizeof(T), false, false);
+  const VocabPlan& p = vocab_plan(g.T, g.H, g.V, sizeof(T), false, false);
   const Space s = vocab_space(ws, g.T, g.H, g.V, sizeof(T), p, false);
   const Tokens tokens{g.T, g.vocab, g.target, loss, lse, nullptr, nullptr, nullptr};
   const bool own_list = g.T <= kOwnListRows;
@@ -918,7 +923,7 @@ hipError_t vocab_fwd_typed(const VocabArgs& g, float* loss, float* lse, float* m
 template <typename T>
 hipError_t vocab_bwd_typed(const VocabArgs& g, const float* loss, const float* lse, const float* mean, const float* dloss,
                            float scale, void* dx, void* dw, void* ws, hipStream_t stream) {
-  const VocabPlan p = vocab_plan(g.T, g.H, g.V, sizeof(T), dx != nullptr, dw != nullptr);
+  const VocabPlan& p = vocab_plan(g.T, g.H, g.V, sizeof(T), dx != nullptr, dw != nullptr);
   const Space s = vocab_space(ws, g.T, g.H, g.V, sizeof(T), p, true);
   const Tokens tokens{g.T, g.vocab, g.target, nullptr, nullptr, loss, lse, dloss};
   const bool own_list = g.T <= kOwnListRows;
@@ -997,10 +1002,12 @@ hipError_t vocab_bwd_typed(const VocabArgs& g, const float* loss, const float* l
 }  // namespace
 
 size_t vocab_workspace_bytes(int T, int H, int V, int esize) {
-  size_t need = vocab_space(nullptr, T, H, V, esize, vocab_plan(T, H, V, esize, false, false), false).bytes;
-  for (int want = 1; want < 4; ++want)
-    need = std::max(need, vocab_space(nullptr, T, H, V, esize, vocab_plan(T, H, V, esize, want & 1, want & 2), true).bytes);
-  return need;
+  return remembered<size_t>(T, H, V, esize + 64, [&] {
+    size_t need = vocab_space(nullptr, T, H, V, esize, vocab_plan(T, H, V, esize, false, false), false).bytes;
+    for (int want = 1; want < 4; ++want)
+      need = std::max(need, vocab_space(nullptr, T, H, V, esize, vocab_plan(T, H, V, esize, want & 1, want & 2), true).bytes);
+    return need;
+  });
 }
 
 hipError_t launch_vocab_fwd(const VocabArgs& g, int esize, float* loss, float* lse, float* mean, void* ws,
