@@ -115,7 +115,24 @@ __device__ __forceinline__ int rows_each(int n, int most) {
   return max(kRowsAtOnce, ((n + most - 1) / most + kRowsAtOnce - 1) / kRowsAtOnce * kRowsAtOnce);
 }
 
-// Workgroup (j, s): the j-th run of sequence s' rows.  ONE: it is the only workgroup, and writes the results itself.
+// Sequence and run of its rows that workgroup j of a flat grid takes: the runs of all sequences in a row, which every wave
+// adds up for itself.
+constexpr int kFlatSeqs = 64;
+__device__ __forceinline__ void find_run(const BalanceArgs& g, int most, int& s, int& run) {
+  const int lane = lane_id(), j = blockIdx.x;
+  int runs = 0;
+  if (lane < g.n_seq) {
+    const Rows rows = rows_of(g.offsets, lane, g.T);
+    const int n = rows.end - rows.begin, each = rows_each(n, most);
+    runs = (n + each - 1) / each;
+  }
+  const int upto = wave_inclusive_scan(runs);
+  s = __popcll(__ballot(upto <= j));  // past the last: kWave
+  run = j - (s > 0 ? __shfl(upto, s - 1, kWave) : 0);
+}
+
+// Workgroup (j, s): the j-th run of sequence s' rows; up to 64 sequences in a flat grid.  ONE: it is the only workgroup,
+// and writes the results itself.
 template <typename Tok, bool ONE>
 __global__ __launch_bounds__(kRowThreads) void balance_rows_kernel(BalanceArgs g, BalanceParts part,
                                                                    int32_t* __restrict__ counts,
@@ -124,11 +141,16 @@ __global__ __launch_bounds__(kRowThreads) void balance_rows_kernel(BalanceArgs g
   __shared__ float s_p[NT / 64][kMaxExperts];
   __shared__ int s_c[kMaxExperts];
   __shared__ double s_sum[NT / 64];
-  const int tid = threadIdx.x, li = tid & 15, s = blockIdx.y;
+  const int tid = threadIdx.x, li = tid & 15;
+  int s = blockIdx.y, run = blockIdx.x;
+  if (!ONE && run == 0 && s == 0 && tid == 0) *part.done = 0;
+  if (!ONE && g.n_seq <= kFlatSeqs) {
+    find_run(g, part.most, s, run);
+    if (s >= g.n_seq) return;
+  }
   const Rows rows = rows_of(g.offsets, s, g.T);
   const int n = rows.end - rows.begin;
-  if (!ONE && blockIdx.x == 0 && s == 0 && tid == 0) *part.done = 0;
-  const int64_t each = ONE ? n : rows_each(n, part.most), begin = rows.begin + each * blockIdx.x;
+  const int64_t each = ONE ? n : rows_each(n, part.most), begin = rows.begin + each * run;
   const int64_t end = min(begin + each, (int64_t)rows.end);
   if (!ONE && begin >= end) return;
   for (int e = tid; e < kMaxExperts; e += NT) s_c[e] = 0;
@@ -168,7 +190,7 @@ __global__ __launch_bounds__(kRowThreads) void balance_rows_kernel(BalanceArgs g
       mean_p[tid] = mean;
       term = (double)s_c[tid] * mean;
     } else {
-      const size_t at = ((size_t)s * part.most + blockIdx.x) * g.E + tid;
+      const size_t at = ((size_t)s * part.most + run) * g.E + tid;
       part.p[at] = v;
       part.c[at] = s_c[tid];
     }
@@ -310,8 +332,9 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(BalanceArgs g, const i
   }
 }
 
-// Workgroups that a sequence may have: 1024 in all.  Those past its rows end at once, so ragged sequences are shared
-// out nearly as evenly as equal ones (16384 tokens in 8 of them, both kernels: 1024 workgroups 14.8 us, 2048 16.5).
+// Workgroups that a sequence may have: 1024 in all, so that ragged ones are shared out nearly as evenly as equal ones.  Up
+// to 64 sequences there are only as many as have rows; else those past a sequence's rows end at once (16384 tokens in 8
+// sequences, both kernels: 13.6 us, 14.8 with 1024 of which most have none).
 int balance_most(int T, int n_seq) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(((int64_t)T + kRowsAtOnce - 1) / kRowsAtOnce, 1024 / n_seq));
 }
@@ -367,8 +390,10 @@ hipError_t launch_balance_fwd(const BalanceArgs& g, int32_t* counts, float* mean
   size_t bytes;
   const BalanceParts part = balance_parts(g.T, g.E, g.n_seq, ws, &bytes);
   hipError_t err = with_token(g.E, aligned, [&](auto tok) {
-    MOE_LAUNCH((balance_rows_kernel<decltype(tok), false>), dim3(part.most, g.n_seq), dim3(kRowThreads), 0, stream, g, part,
-               counts, mean_p, loss);
+    // runs of a flat grid: no sequence has more than one that is not whole
+    const dim3 grid = g.n_seq <= kFlatSeqs ? dim3(std::min(g.n_seq * part.most, g.T / kRowsAtOnce + g.n_seq))
+                                           : dim3(part.most, g.n_seq);
+    MOE_LAUNCH((balance_rows_kernel<decltype(tok), false>), grid, dim3(kRowThreads), 0, stream, g, part, counts, mean_p, loss);
     return hipGetLastError();
   });
   if (err != hipSuccess) return err;
