@@ -1258,6 +1258,9 @@ int moe_adamw_step(const void* plan, const void* plan_device, int32_t* counter, 
   REQUIRE(beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0, MOE_ERR_INVALID_ARGUMENT,
           "%s: beta1 and beta2 must be in [0, 1)", fn);
   REQUIRE(eps >= 0.0 && std::isfinite(eps), MOE_ERR_INVALID_ARGUMENT, "%s: eps must be finite and not negative", fn);
+  // as fp32, whose reciprocal the kernel takes where v is 0
+  REQUIRE(eps == 0.0 || (eps >= 0x1p-126 && eps < 0x1p126), MOE_ERR_UNSUPPORTED, "%s: eps=%g is not 0 or from 2^-126 to 2^126", fn,
+          eps);
   const moe::AdamwStep a{counter, lr, grad_scale, beta1, beta2, eps, seed};
   hipStream_t s = as_stream(stream);
   return hip_status(timed(MOE_K_ADAMW, s, [&] { return moe::launch_adamw(plan, plan_device, a, s); }), fn);

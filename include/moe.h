@@ -773,7 +773,7 @@ int moe_adamw_plan(int n, const moe_adamw_tensor* tensors, int dtype, int state_
  * 2^127: m in E4M3; v without a sign, c = (8 + c % 8) 2^(c / 8 - 34) for c = 1 to
  * 254, 0 for 0, and what is not zero has at least code 1.  Codes are decided in 64
  * bits; what is not finite has a NaN code (0x7f, 255).
- * 0 <= beta1, beta2 < 1, eps >= 0.  Steps that may overlap in time share no
+ * 0 <= beta1, beta2 < 1; eps 0 or from 2^-126 to 2^126.  Steps that may overlap in time share no
  * tensors and no counter. */
 int moe_adamw_step(const void* plan, const void* plan_device, int32_t* counter, const float* lr, double beta1,
                    double beta2, double eps, const float* grad_scale, uint32_t seed, void* stream);

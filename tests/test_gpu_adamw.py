@@ -345,7 +345,7 @@ def test_refusals():
             moe.AdamWPlan(bad)
     plan = moe.AdamWPlan([T(f(64), f(64), f(64), f(64))])
     c = torch.zeros(2, dtype=torch.int32, device="cuda")
-    for kw, text in ((dict(beta1=1.0), "beta"), (dict(beta2=-0.1), "beta"), (dict(eps=-1.0), "eps"), (dict(eps=float("nan")), "eps"),
+    for kw, text in ((dict(beta1=1.0), "beta"), (dict(beta2=-0.1), "beta"), (dict(eps=-1.0), "eps"), (dict(eps=float("nan")), "eps"), (dict(eps=1e-40), "eps"), (dict(eps=1e-300), "eps"), (dict(eps=1e38), "eps"),
                      (dict(grad_scale=f(2)), "grad_scale"), (dict(lr=f(2)), "lr"), (dict(lr=None), "lr"), (dict(counter=c[:1]), "counter")):
         with pytest.raises(moe.MoeError, match=text):
             moe.moe_adamw_step(plan, **{**dict(counter=c, lr=f(1)), **kw})

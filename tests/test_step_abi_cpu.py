@@ -139,7 +139,7 @@ def test_adamw_step_and_moments(lib):  # noqa: F811
     refuses(lib, lib.moe_adamw_step, ok, [
         ({0: NULL}, 1, "plan"), ({1: NULL}, 1, "plan_device"), ({1: off(1, 8)}, 1, "plan_device must be 16"), ({2: NULL}, 1, "counter"),
         ({3: NULL}, 1, "lr"), ({4: 1.0}, 1, "beta"), ({4: -0.1}, 1, "beta"), ({5: 1.0}, 1, "beta"), ({5: float("nan")}, 1, "beta"),
-        ({6: -1e-8}, 1, "eps"), ({6: float("inf")}, 1, "eps")])
+        ({6: -1e-8}, 1, "eps"), ({6: float("inf")}, 1, "eps"), ({6: 1e-40}, 2, "eps"), ({6: 1e38}, 2, "eps")])
     ok = [1000] + [P(i) for i in range(6)] + [NULL]
     refuses(lib, lib.moe_adamw_moments, ok, [({0: 0}, 1, "numel=0"), ({0: 1 << 40}, 2, "too large")] +
             [({i + 1: NULL}, 1, n) for i, n in enumerate(("m must", "v must", "m_scale", "v_scale", "m_out", "v_out"))] +
