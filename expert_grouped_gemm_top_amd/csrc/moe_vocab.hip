@@ -108,11 +108,12 @@ __device__ __forceinline__ void list_token(const Tokens& g, const Listed& out, i
   }
 }
 
-// Lists many tokens, 1024 a workgroup, each of which counts the ones before its own for itself: a launch that waits for
-// nothing (8192 tokens, 5.6 us; by one workgroup 30).
-__global__ __launch_bounds__(1024) void vocab_list_kernel(Tokens g, Listed out) {
+// Lists many tokens, `each` a workgroup (a multiple of 1024), each of which counts the ones before its own for itself: a
+// launch that waits for nothing (8192 tokens, 5.6 us; by one workgroup 30).  Past 256 workgroups each takes more tokens, or
+// the counting would grow with the square (16 Mi tokens of 16 classes: the call 97 -> 28 ms).
+__global__ __launch_bounds__(1024) void vocab_list_kernel(Tokens g, Listed out, int each) {
   __shared__ int s_wave[16];
-  const int64_t first = (int64_t)blockIdx.x * 1024;
+  const int64_t first = (int64_t)blockIdx.x * each;
   int mine = 0;
   for (int64_t t = threadIdx.x; t < first; t += 1024 * 8) {
 #pragma unroll
@@ -124,9 +125,11 @@ __global__ __launch_bounds__(1024) void vocab_list_kernel(Tokens g, Listed out) 
   int before = 0;
 #pragma unroll
   for (int i = 0; i < 16; ++i) before += s_wave[i];
-  int y[1];
-  const int at = place_of<1024>(g, first + threadIdx.x, y, before, s_wave);
-  list_token(g, out, first + threadIdx.x, y[0], at);
+  for (int64_t t = first + threadIdx.x; t < first + each; t += 1024) {
+    int y[1];
+    const int at = place_of<1024>(g, t, y, before, s_wave);
+    list_token(g, out, t, y[0], at);
+  }
   if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) {
     out.head[0] = before;
     out.head[1] = 0;
@@ -860,7 +863,8 @@ int64_t tiles_of(int M, int N) {
 }
 
 hipError_t list_tokens(const Tokens& tokens, const Listed& list, hipStream_t stream) {
-  MOE_LAUNCH(vocab_list_kernel, dim3((unsigned)((tokens.T + 1023) / 1024)), dim3(1024), 0, stream, tokens, list);
+  const int each = rounded_up(((int64_t)tokens.T + kCus - 1) / kCus, 1024);
+  MOE_LAUNCH(vocab_list_kernel, dim3((unsigned)((tokens.T + each - 1) / each)), dim3(1024), 0, stream, tokens, list, each);
   return hipGetLastError();
 }
 
