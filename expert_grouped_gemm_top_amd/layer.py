@@ -213,8 +213,9 @@ class MoeLayerBuffers:
         each pair's rank-one dW_down term).  With w_r, the router's backward
         follows: dlogits, dw_r, and its share added to dx.  dbalance [1] fp32: the
         gradient that reaches the balance loss (None: 1), whose own joins the
-        logits' there."""
-        assert dbalance is None or (self.balance is not None and w_r is not None), "no balance loss in this backward"
+        logits' there; a layer with a balance loss needs w_r."""
+        assert dbalance is None or self.balance is not None, "no balance loss in this backward"
+        assert self.balance is None or w_r is not None, "the balance loss' gradient needs the router's backward"
         g, k = self.gather_rows, self.k
         if self.compacted:
             if isinstance(score, str):
