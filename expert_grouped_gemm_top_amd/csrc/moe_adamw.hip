@@ -15,7 +15,8 @@
 // 0.02 is a tenth of half a bf16 step: rounded to nearest it would never come
 // about), and 8-bit moments (v moves by a thousandth of its distance to g^2, a
 // sixtieth of a code's half step: to nearest it would stand still).  So the
-// expected values are the exact ones.
+// expected values are the exact ones, to 2^-32 of a bf16 step and 2^-16 of a
+// code's, but for v below its smallest code, which is raised to it.
 #include <algorithm>
 #include <cstring>
 #include <type_traits>
@@ -212,9 +213,9 @@ struct Shared {
   uint32_t key;
 };
 
-// Root and reciprocal by the hardware's, each within 2^-23 of its value.
-__device__ __forceinline__ float updated(float p, float keep, float m, float root, const Shared& sh, float eps) {
-  return p * keep - sh.step1 * (m * __builtin_amdgcn_rcpf(root * sh.inv_root2 + eps));
+// What p goes down by but for the decay.  Root and reciprocal by the hardware's, each within 2^-23 of its value.
+__device__ __forceinline__ float update(float m, float root, const Shared& sh, float eps) {
+  return sh.step1 * (m * __builtin_amdgcn_rcpf(root * sh.inv_root2 + eps));
 }
 // The hardware's root of a subnormal is 0: what is near them is taken 2^100 times as large.
 __device__ __forceinline__ float root_of(float v) {
@@ -222,9 +223,9 @@ __device__ __forceinline__ float root_of(float v) {
   return __builtin_amdgcn_sqrtf(v * (tiny ? 0x1p100f : 1.0f)) * (tiny ? 0x1p-50f : 1.0f);
 }
 // Only where a wave has such a v: everywhere it costs a step with 32 bits 7 % (151M weights 802 -> 859 us), and one with
-// 8 bits 2 %, where the check would cost 4 (599, 611, 625).
-__device__ __forceinline__ void update8(float (&p)[8], float keep, const float (&m)[8], const float (&v)[8],
-                                        const Shared& sh, float eps) {
+// 8 bits and its read-back 2 %, where the check would cost 4 (599, 611, 625).
+__device__ __forceinline__ void update8(const float (&m)[8], const float (&v)[8], const Shared& sh, float eps,
+                                        float (&u)[8]) {
   uint32_t least = 0xffffffffu;
 #pragma unroll
   for (int j = 0; j < 8; ++j) least = min(least, __float_as_uint(v[j]) - 1);  // zeros count as large
@@ -237,22 +238,29 @@ __device__ __forceinline__ void update8(float (&p)[8], float keep, const float (
     for (int j = 0; j < 8; ++j) root[j] = __builtin_amdgcn_sqrtf(v[j]);
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) p[j] = updated(p[j], keep, m[j], root[j], sh, eps);
+  for (int j = 0; j < 8; ++j) u[j] = update(m[j], root[j], sh, eps);
 }
 
-// bf16 of p, rounded by 16 of the hash's bits.
-__device__ __forceinline__ uint32_t dithered(float p, uint32_t r) {
-  const uint32_t bits = __float_as_uint(p);
-  const uint32_t up = (bits + ((r * 0x9e3779b1u) >> 16)) >> 16;  // infinities stay: nothing is below their 16 bits
-  return p != p ? 0x7fc0u : up;
+// Where 1 - lr decay were taken as fp32 it would be a multiple of 2^-24, the same way for every element and step: a decay
+// of 1e-7 came out as 1.15e-7, one of 1e-8 as none.  So p goes down by p (lr decay) + u in one rounding ...
+__device__ __forceinline__ float moved(float p, double decay, float u) { return p - fmaf(p, (float)decay, u); }
+// ... or, as bf16, up for the hash's share of what is left over: by an addition below the seven bits of mantissa, whose
+// carry rounds up.  In 64 bits, as fp32 would round to 2^-24 of p first, where p may go down by less (151M weights with
+// 8-bit moments 355 -> 370 us; with 32 bits HBM hides it, 620).
+__device__ __forceinline__ uint32_t dithered(float p, double decay, float u, uint32_t r) {
+  const double to = fma((double)p, 1.0 - decay, -(double)u);
+  const uint64_t share = (uint64_t)(r * 0x9e3779b1u) << 13;  // 52 - 7 - 32
+  const uint64_t bits = ((uint64_t)__double_as_longlong(to) + share) >> 45 << 45;
+  const uint32_t q = __float_as_uint((float)__longlong_as_double((long long)bits)) >> 16;
+  return to != to ? 0x7fc0u : q;  // infinities stay: a share has none of their mantissa's bits
 }
 
 // One pass over a chunk: eight elements a thread, from element `at` of tensor e on.
 template <typename T, bool MASTER, bool SMALL, bool FULL>
 __device__ __forceinline__ void adamw_pass(const AdamwArgs& g, const Shared& sh, const AdamwEntry& e, int64_t at) {
   const int live = FULL ? 8 : (int)min((int64_t)8, max((int64_t)0, e.numel - at));
-  const float keep = (float)(1.0 - (double)sh.lr * e.decay);
-  float p[8], gr[8];
+  const double decay = (double)sh.lr * e.decay;
+  float p[8], gr[8], u[8];
   get8<FULL>((const T*)e.grad + at, live, gr);
   if constexpr (MASTER) get8<FULL>(e.master + at, live, p);
   else get8<FULL>((const T*)e.param + at, live, p);
@@ -277,7 +285,7 @@ __device__ __forceinline__ void adamw_pass(const AdamwArgs& g, const Shared& sh,
       m[j] = b1 * m[j] + a1 * gj;
       v[j] = b2 * v[j] + a2 * gj * gj;
     }
-    update8(p, keep, m, v, sh, g.eps);
+    update8(m, v, sh, g.eps, u);
     put8<FULL>(mp, live, m);
     put8<FULL>(vp, live, v);
   } else {
@@ -296,7 +304,7 @@ __device__ __forceinline__ void adamw_pass(const AdamwArgs& g, const Shared& sh,
       m[j] = fma(gj, am, (double)value_m(mc[j >> 2], j & 3) * bm);
       v[j] = fma(gj * gj, av, value_v((vc[j >> 2] >> (8 * (j & 3))) & 255) * bv);
       const float mf = (float)m[j], vf = (float)v[j];
-      p[j] = updated(p[j], keep, mf, root_of(vf), sh, g.eps);
+      u[j] = update(mf, root_of(vf), sh, g.eps);
       const bool ok = finite(m[j]);
       top_m = max(top_m, ok ? __float_as_uint(mf) & 0x7fffffffu : 0u);
       top_v = max(top_v, ok ? __float_as_uint(vf) : 0u);
@@ -332,11 +340,20 @@ __device__ __forceinline__ void adamw_pass(const AdamwArgs& g, const Shared& sh,
     }
   }
   if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j] = moved(p[j], decay, u[j]);
     put8<FULL>((float*)e.param + at, live, p);
   } else {
     uint32_t q[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = MASTER ? f2bf(p[j]) : dithered(p[j], r[j]);
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (MASTER) {
+        p[j] = moved(p[j], decay, u[j]);
+        q[j] = f2bf(p[j]);
+      } else {
+        q[j] = dithered(p[j], decay, u[j], r[j]);
+      }
+    }
     if constexpr (MASTER) put8<FULL>(e.master + at, live, p);
     put_bits<FULL>((uint16_t*)e.param + at, live, q);
   }
