@@ -7,7 +7,7 @@
 //   dl_te = dloss alpha E / (k N n_s) p_te (c_se - sum_j p_tj c_sj) [(1 - sigmoid(l_te))]
 //
 // Sixteen lanes share a token; one pass over the logits each way.  Sums run in
-// one fixed order: a workgroup's rows, then the workgroups of a sequence.
+// one fixed order: a workgroup's rows, then the runs of a sequence.
 #include <algorithm>
 
 #include "moe_common.h"
@@ -100,39 +100,36 @@ __device__ __forceinline__ double group_sum(double v, double* s) {
   return v;
 }
 
-// Partial sums of the workgroups, `most` at most for a sequence, and what the last kernel joins.
+// Runs of rows that a workgroup sums up: the batch in blocks of `each` rows, cut again where a sequence ends.  Along
+// the rows either the block or the sequence moves on, so block + sequence numbers the runs: a workgroup each, and a
+// place among the partial sums.  So long sequences are shared out whatever others there are (500000 rows, nearly all of
+// them in one of 1000 sequences: 127 us, 9600 where the workgroups were divided by sequences).
 struct BalanceParts {
-  int most;
-  float* p;       // [n_seq][most][E]
-  int32_t* c;     // [n_seq][most][E]
-  double* loss;   // a term of each workgroup of the second kernel
-  uint32_t* done; // how many of them have ended, set to 0 by the first kernel
+  int each, runs;  // runs: as many as there may be
+  float* p;        // [runs][E]
+  int32_t* c;      // [runs][E]
+  double* loss;    // a term of each workgroup of the second kernel
+  uint32_t* done;  // how many of them have ended, set to 0 by the first kernel
 };
 
 constexpr int kRowThreads = 1024, kRowsAtOnce = kRowThreads / kRow;
-// Rows of a workgroup for a sequence of n: as many as it takes at once, or what `most` workgroups must take.
-__device__ __forceinline__ int rows_each(int n, int most) {
-  return max(kRowsAtOnce, ((n + most - 1) / most + kRowsAtOnce - 1) / kRowsAtOnce * kRowsAtOnce);
-}
 
-// Sequence and run of its rows that workgroup j of a flat grid takes: the runs of all sequences in a row, which every wave
-// adds up for itself.
-constexpr int kFlatSeqs = 64;
-__device__ __forceinline__ void find_run(const BalanceArgs& g, int most, int& s, int& run) {
-  const int lane = lane_id(), j = blockIdx.x;
-  int runs = 0;
-  if (lane < g.n_seq) {
-    const Rows rows = rows_of(g.offsets, lane, g.T);
-    const int n = rows.end - rows.begin, each = rows_each(n, most);
-    runs = (n + each - 1) / each;
+// The sequence of run j: the last one whose first run is not behind j.  64 places are looked at at a time.
+__device__ __forceinline__ int sequence_of(const BalanceArgs& g, int each, int j) {
+  int lo = 0;
+  for (int left = g.n_seq; left > 1;) {
+    const int step = (left + 63) / 64, at = lane_id() * step;
+    bool before = false;
+    if (at < left) before = (int)((uint32_t)rows_of(g.offsets, lo + at, g.T).begin / (uint32_t)each) + lo + at <= j;
+    const int found = (int)__popcll(__ballot(before));  // (unsigned: none less one would be 2^32 - 1)
+    const int last = max(found - 1, 0) * step;          // none: a run in front of the first sequence's, without rows
+    lo += last;
+    left = min(step, left - last);
   }
-  const int upto = wave_inclusive_scan(runs);
-  s = __popcll(__ballot(upto <= j));  // past the last: kWave
-  run = j - (s > 0 ? __shfl(upto, s - 1, kWave) : 0);
+  return lo;
 }
 
-// Workgroup (j, s): the j-th run of sequence s' rows; up to 64 sequences in a flat grid.  ONE: it is the only workgroup,
-// and writes the results itself.
+// Workgroup j: run j.  ONE: it is the only workgroup, and writes the results itself.
 template <typename Tok, bool ONE>
 __global__ __launch_bounds__(kRowThreads) void balance_rows_kernel(BalanceArgs g, BalanceParts part,
                                                                    int32_t* __restrict__ counts,
@@ -141,17 +138,17 @@ __global__ __launch_bounds__(kRowThreads) void balance_rows_kernel(BalanceArgs g
   __shared__ float s_p[NT / 64][kMaxExperts];
   __shared__ int s_c[kMaxExperts];
   __shared__ double s_sum[NT / 64];
-  const int tid = threadIdx.x, li = tid & 15;
-  int s = blockIdx.y, run = blockIdx.x;
-  if (!ONE && run == 0 && s == 0 && tid == 0) *part.done = 0;
-  if (!ONE && g.n_seq <= kFlatSeqs) {
-    find_run(g, part.most, s, run);
-    if (s >= g.n_seq) return;
-  }
+  const int tid = threadIdx.x, li = tid & 15, run = blockIdx.x;
+  if (!ONE && run == 0 && tid == 0) *part.done = 0;
+  const int s = ONE ? 0 : sequence_of(g, part.each, run);
   const Rows rows = rows_of(g.offsets, s, g.T);
   const int n = rows.end - rows.begin;
-  const int64_t each = ONE ? n : rows_each(n, part.most), begin = rows.begin + each * run;
-  const int64_t end = min(begin + each, (int64_t)rows.end);
+  int64_t begin = rows.begin, end = rows.end;
+  if (!ONE) {
+    const int64_t block = (int64_t)(run - s) * part.each;
+    begin = max(begin, block);
+    end = min(end, block + part.each);
+  }
   if (!ONE && begin >= end) return;
   for (int e = tid; e < kMaxExperts; e += NT) s_c[e] = 0;
   __syncthreads();
@@ -190,7 +187,7 @@ __global__ __launch_bounds__(kRowThreads) void balance_rows_kernel(BalanceArgs g
       mean_p[tid] = mean;
       term = (double)s_c[tid] * mean;
     } else {
-      const size_t at = ((size_t)s * part.most + run) * g.E + tid;
+      const size_t at = (size_t)run * g.E + tid;
       part.p[at] = v;
       part.c[at] = s_c[tid];
     }
@@ -204,21 +201,21 @@ __global__ __launch_bounds__(kRowThreads) void balance_rows_kernel(BalanceArgs g
 constexpr int kJoinCols = 32;
 __global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs g, BalanceParts part, int32_t* __restrict__ counts,
                                                             float* __restrict__ mean_p, float* __restrict__ loss) {
-  __shared__ float s_p[32][kJoinCols];
+  __shared__ double s_p[32][kJoinCols];
   __shared__ int s_c[32][kJoinCols];
   __shared__ double s_sum[16];
   __shared__ bool s_last;
   const int tid = threadIdx.x, q = tid / kJoinCols, e = blockIdx.x * kJoinCols + tid % kJoinCols, s = blockIdx.y;
   const Rows rows = rows_of(g.offsets, s, g.T);
   const int n = rows.end - rows.begin;
-  float p = 0.0f;
+  double p = 0.0;
   int c = 0;
-  if (e < g.E) {
-    const int each = rows_each(n, part.most), runs = (n + each - 1) / each;
-    const size_t first = (size_t)s * part.most * g.E + e;
+  if (e < g.E && n > 0) {
+    const int b0 = (uint32_t)rows.begin / (uint32_t)part.each, b1 = (uint32_t)(rows.end - 1) / (uint32_t)part.each;
+    const size_t first = (size_t)(b0 + s) * g.E + e;
 #pragma unroll 8
-    for (int i = q; i < runs; i += 32) {
-      p += part.p[first + (size_t)i * g.E];
+    for (int i = q; i <= b1 - b0; i += 32) {
+      p += (double)part.p[first + (size_t)i * g.E];
       c += part.c[first + (size_t)i * g.E];
     }
   }
@@ -227,14 +224,14 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs g, Balan
   __syncthreads();
   double term = 0.0;
   if (tid < kJoinCols && e < g.E) {
-    p = 0.0f;
+    p = 0.0;
     c = 0;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
       p += s_p[i][tid];
       c += s_c[i][tid];
     }
-    const float mean = n > 0 ? p / (float)n : 0.0f;
+    const float mean = n > 0 ? (float)(p / n) : 0.0f;
     counts[(size_t)s * g.E + e] = c;
     mean_p[(size_t)s * g.E + e] = mean;
     term = (double)c * mean;
@@ -332,11 +329,13 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(BalanceArgs g, const i
   }
 }
 
-// Workgroups that a sequence may have: 1024 in all, so that ragged ones are shared out nearly as evenly as equal ones.  Up
-// to 64 sequences there are only as many as have rows; else those past a sequence's rows end at once (16384 tokens in 8
-// sequences, both kernels: 13.6 us, 14.8 with 1024 of which most have none).
-int balance_most(int T, int n_seq) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>(((int64_t)T + kRowsAtOnce - 1) / kRowsAtOnce, 1024 / n_seq));
+// Rows of a block: 512 of them share the batch out, each a multiple of what a workgroup takes at once (65536 rows of 128
+// experts, both kernels: 15.3 us, 20.1 by 1024 blocks, 14.3 by 256; 131072 rows in 32 sequences 24.8, 22.9, 25.4; 65536 of
+// 256 experts in 16 sequences 22.3, 25.6, 25.4), up to 8192, so that a thread adds at most 128 rows in fp32; the runs are
+// added in 64 bits.
+int balance_each(int T) {
+  constexpr int64_t kBlocks = 512;
+  return (int)std::min<int64_t>((T + kBlocks * kRowsAtOnce - 1) / (kBlocks * kRowsAtOnce) * kRowsAtOnce, 8192);
 }
 constexpr int kOneGroupRows = 256;  // up to here one workgroup does it all
 int join_groups(int E) { return (E + kJoinCols - 1) / kJoinCols; }
@@ -346,8 +345,9 @@ bool balance_alone(int T, int n_seq) { return n_seq == 1 && T <= kOneGroupRows; 
 BalanceParts balance_parts(int T, int E, int n_seq, void* ws, size_t* bytes) {
   char* at = (char*)ws;
   BalanceParts p;
-  p.most = balance_most(T, n_seq);
-  const size_t n = (size_t)n_seq * p.most * E * 4;
+  p.each = balance_each(T);
+  p.runs = (int)(((int64_t)T + p.each - 1) / p.each) + n_seq - 1;
+  const size_t n = (size_t)p.runs * E * 4;
   p.loss = (double*)at;
   at += (size_t)n_seq * join_groups(E) * sizeof(double);
   p.done = (uint32_t*)at;
@@ -390,10 +390,8 @@ hipError_t launch_balance_fwd(const BalanceArgs& g, int32_t* counts, float* mean
   size_t bytes;
   const BalanceParts part = balance_parts(g.T, g.E, g.n_seq, ws, &bytes);
   hipError_t err = with_token(g.E, aligned, [&](auto tok) {
-    // runs of a flat grid: no sequence has more than one that is not whole
-    const dim3 grid = g.n_seq <= kFlatSeqs ? dim3(std::min(g.n_seq * part.most, g.T / kRowsAtOnce + g.n_seq))
-                                           : dim3(part.most, g.n_seq);
-    MOE_LAUNCH((balance_rows_kernel<decltype(tok), false>), grid, dim3(kRowThreads), 0, stream, g, part, counts, mean_p, loss);
+    MOE_LAUNCH((balance_rows_kernel<decltype(tok), false>), dim3(part.runs), dim3(kRowThreads), 0, stream, g, part, counts,
+               mean_p, loss);
     return hipGetLastError();
   });
   if (err != hipSuccess) return err;
