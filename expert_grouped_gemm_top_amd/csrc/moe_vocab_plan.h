@@ -29,7 +29,8 @@ struct VocabPlan {
   Plan2 grads;
 };
 
-// The columns of a piece: dz of some 64 Mi elements, so that it is read again from the last-level cache.
+// The columns of a piece: dz of 64 Mi elements, so that it is read again from the last-level cache, but at least 1024, so
+// that the products keep their tiles.
 constexpr int64_t kPieceElements = 64 << 20;
 
 inline int64_t group_count(int M, int N, int bm, int bn) { return (int64_t)((M + bm - 1) / bm) * ((N + bn - 1) / bn); }

@@ -704,7 +704,8 @@ def moe_vocab_loss_fwd(x, w, target, loss, lse, mean, workspace, vocab: int | No
 def moe_vocab_loss_bwd(x, w, target, loss, lse, mean, dx, dw, workspace, dloss=None, scale: float = 1.0,
                        vocab: int | None = None, stream=None):
     """dx and dw (either may be None) of scale times the mean loss, or of scale times
-    the sum of dloss [T] loss (mean may then be None)."""
+    the sum of dloss [T] loss (mean may then be None).  A term of dx has one factor that
+    is rounded to the type, one of dw two (include/moe.h)."""
     dev = _device(x, "x")
     T, H = rows = _rows(x, "x")
     V = _rows(w, "w")[1]

@@ -153,7 +153,7 @@ typedef enum moe_kernel {
   MOE_K_LAYERNORM = 13,    /* moe_layernorm_fwd, moe_layernorm_bwd */
   MOE_K_LINEAR_FWD = 14,   /* moe_linear_fwd */
   MOE_K_LINEAR_BWD = 15,   /* moe_linear_bwd */
-  /* 16 names no kernel */
+  /* 16 stays free: moe_profile_kernel refuses it, as it did when it was the first number past the kernels */
   MOE_K_BALANCE = 17,      /* moe_balance_loss_fwd, moe_balance_loss_bwd */
   MOE_K_ADAMW = 18,        /* moe_adamw_step */
   MOE_K_VOCAB_FWD = 19,    /* moe_vocab_loss_fwd */
@@ -697,8 +697,9 @@ int moe_balance_loss_bwd(int T, int E, int k, int n_seq, int score, float alpha,
 
 /* Workspace (device bytes) of moe_vocab_loss_fwd and moe_vocab_loss_bwd: the list of
  * counted tokens, and the forward's row statistics (8 bytes for each token and run
- * of 32 to 512 columns) or the backward's piece of dz (some 64 Mi elements), its
- * rows of x and the fp32 sums of dx.  Host-only. */
+ * of 32 to 512 columns) or the backward's piece of dz, its rows of x and the fp32
+ * sums of dx.  A piece has as many columns as make 64 Mi elements with the tokens,
+ * but 1024 at least: from 64 Ki tokens on, 1024 elements a token.  Host-only. */
 size_t moe_vocab_loss_workspace_bytes(int T, int H, int V, int dtype);
 
 /* Softmax cross entropy of the logits x W over the classes 0 .. vocab - 1, which are
@@ -722,12 +723,18 @@ int moe_vocab_loss_fwd(int T, int H, int V, int vocab, int dtype, const void* x,
  * loss[t], in pieces of the vocabulary whose logits are computed again:
  *   dz_tv = w_t (exp(x_t W_v - lse[t]) - [v = target[t]]),  w_t = 1 or dloss[t]
  *   dx = c dz W^T,  dw = c x^T dz,                          c = scale / n or scale
- * dz is rounded to `dtype` as the operand of both products; sums in fp32 over all
- * pieces, dx and dw rounded once.  Rows of tokens that are not counted, and padding
- * columns, get zeros.  loss, lse: as the forward left them; mean [2] as well (not
- * read with dloss, else needed); dloss [T] fp32 (device) or NULL.  dx [T, H] and
- * dw [H, V] of `dtype` (device, out), either may be NULL (a frozen head); 16-byte
- * aligned.  The rest as for the forward. */
+ * With q the softmax over the classes other than the target (0 there) and f_t = w_t
+ * times their probability, dz_tv = f_t (q_tv - [v = target[t]]).  What the products
+ * take is q_tv - [v = target[t]], rounded to `dtype` (its -1 is exact).  f_t is
+ * multiplied to dx's fp32 sums, and for dw, which sums over the tokens, to the rows
+ * of x, which are rounded to `dtype` once more.  So with u half a step of `dtype`
+ * (bf16 2^-8, fp32 2^-24) the roundings leave a term of dx off by at most u of its
+ * size and one of dw by 2 u + u^2, beside those of fp32.  Sums in fp32 over all
+ * pieces; dx and dw are rounded as they are stored.  Rows of tokens that are not
+ * counted, and padding columns, get zeros.  loss, lse: as the forward left them;
+ * mean [2] as well (not read with dloss, else needed); dloss [T] fp32 (device) or
+ * NULL.  dx [T, H] and dw [H, V] of `dtype` (device, out), either may be NULL (a
+ * frozen head); 16-byte aligned.  The rest as for the forward. */
 int moe_vocab_loss_bwd(int T, int H, int V, int vocab, int dtype, const void* x, const void* w, const int32_t* target,
                        const float* loss, const float* lse, const float* mean, const float* dloss, float scale, void* dx,
                        void* dw, void* workspace, size_t workspace_bytes, void* stream);
@@ -748,7 +755,9 @@ size_t moe_adamw_plan_bytes(int n);
 
 /* Lays out a step over n tensors in `plan` (host memory of plan_bytes); the caller
  * keeps it and a copy of it on the device for moe_adamw_step, as long as the
- * tensors stay where they are.  All tensors of a plan have the same dtype and
+ * tensors stay where they are.  A plan is bound to their addresses, the gradients'
+ * too: gradients that lie elsewhere in every step need a new plan and a new copy
+ * for each, so keep them in place where steps are short.  All tensors of a plan have the same dtype and
  * state_bits (32 or 8), and all have a master or none; no two buffers share
  * memory.  New 8-bit moments are zeros throughout (codes and scales).  Host-only. */
 int moe_adamw_plan(int n, const moe_adamw_tensor* tensors, int dtype, int state_bits, void* plan, size_t plan_bytes);
