@@ -31,6 +31,8 @@ namespace {
 
 // ---- the hash ------------------------------------------------------------------
 
+// Shifts and multiplications in turn; the multipliers here and in dithered() are three of the five 32-bit primes that the
+// specification of the xxHash algorithm publishes.
 __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   x = (x ^ (x >> 16)) * 0x85ebca77u;
   x = (x ^ (x >> 15)) * 0xc2b2ae3du;
@@ -366,7 +368,7 @@ __device__ __forceinline__ int tensor_of(const int64_t* starts, int n, int64_t c
   for (int left = n; left > 1;) {
     const int step = (left + 63) / 64, at = lane_id() * step;
     const bool before = at < left && get<int64_t>(starts + lo + at) <= chunk;
-    const int last = max(__popcll(__ballot(before)) - 1, 0) * step;
+    const int last = max((int)__popcll(__ballot(before)) - 1, 0) * step;
     lo += last;
     left = min(step, left - last);
   }

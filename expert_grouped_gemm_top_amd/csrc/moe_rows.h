@@ -62,8 +62,6 @@ struct Raw8<uint16_t> {
   __device__ __forceinline__ void load(const uint16_t* p) { v = *(const u32x4*)p; }
   __device__ __forceinline__ float get(int j) const { return (j & 1) ? bf_hi(v[j >> 1]) : bf_lo(v[j >> 1]); }
 };
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ float load1(const uint16_t* p) { return bf2f(*p); }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = (uint16_t)f2bf(v); }
 
