@@ -361,9 +361,12 @@ class AdamWBuffers:
     they are): moments of `bits` 32 or 8 and, with `master`, fp32 copies of bf16
     parameters.  weight_decay: of all, or a dict by name (0 for those that are not in
     it).  lr [1] and counter live on the device, so a captured step takes each replay's
-    rate and counts on."""
+    rate and counts on.  The plan is made once, of the gradients' addresses: gradients
+    that moved would need a new one (moe.AdamWPlan, 0.16 ms of the host's time for 64
+    tensors and 0.8 for 400, beside a step of 8 us over 64 small ones)."""
 
     def __init__(self, params, grads, lr, weight_decay=0.0, betas=(0.9, 0.999), eps=1e-8, bits=32, master=False, seed=0):
+        assert bits in (32, 8), f"moments of {bits} bits"
         self.betas, self.eps, self.seed = betas, eps, seed
         self.state, tensors = {}, []
         for name, p in params.items():
