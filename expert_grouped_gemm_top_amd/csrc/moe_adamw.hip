@@ -244,8 +244,11 @@ __device__ __forceinline__ void update8(const float (&m)[8], const float (&v)[8]
 }
 
 // Where 1 - lr decay were taken as fp32 it would be a multiple of 2^-24, the same way for every element and step: a decay
-// of 1e-7 came out as 1.15e-7, one of 1e-8 as none.  So p goes down by p (lr decay) + u in one rounding ...
-__device__ __forceinline__ float moved(float p, double decay, float u) { return p - fmaf(p, (float)decay, u); }
+// of 1e-7 came out as 1.15e-7, one of 1e-8 as none.  So p goes down by p (lr decay) + u in one rounding (an infinite one
+// by u alone: infinity less itself would be NaN) ...
+__device__ __forceinline__ float moved(float p, double decay, float u) {
+  return p - (__builtin_isinf(p) ? u : fmaf(p, (float)decay, u));
+}
 // ... or, as bf16, up for the hash's share of what is left over: by an addition below the seven bits of mantissa, whose
 // carry rounds up.  In 64 bits, as fp32 would round to 2^-24 of p first, where p may go down by less (151M weights with
 // 8-bit moments 355 -> 370 us; with 32 bits HBM hides it, 620).

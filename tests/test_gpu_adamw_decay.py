@@ -97,3 +97,17 @@ def test_shares_below_2_to_16_of_a_step():
         assert np.array_equal(down[sure], (r < 2 ** (32 - shift))[sure]), shift
         assert shift > 18 or down.any()  # 64 are expected of 2^-18, one of 2^-24
         assert (t.param[torch.from_numpy(down).cuda()] == 1 - 2.0 ** -8).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("dtype,master", [(torch.float32, False), (torch.bfloat16, True), (torch.bfloat16, False)])
+@pytest.mark.parametrize("decay", [0.0, 0.1])
+def test_infinite_weights_stay(dtype, master, bits, decay):
+    w = torch.full((300,), 0.5, device="cuda")
+    w[3], w[299] = float("inf"), -float("inf")
+    t = tensor(w, dtype, bits, master, decay, torch.ones(300, device="cuda"))
+    steps(t, 1e-3, 2)
+    p = t.param.float()
+    assert p[3] == float("inf") and p[299] == -float("inf") and int(torch.isfinite(p).sum()) == 298
+    if master:
+        assert t.master[3] == float("inf") and t.master[299] == -float("inf")
