@@ -711,15 +711,13 @@ __global__ __launch_bounds__(256) void vocab_dx_kernel(int T_, int H, Slices sli
 
 // ---- plans and launchers -----------------------------------------------------------
 
-// kTile64x512, kTile128x256, and the few-row gradients' tile.
-using WideTile = Tile<64, 512, 8, 1, 1, 2>;
+// kTile128x256, and dx's tile for few rows.
 using FlatTile = Tile<128, 256, 8, 2, 1, 3>;
 using DeepTile = Tile<128, 128, 8, 2, 1, 4>;
 
 template <typename T, typename Fn>
 hipError_t with_tile(int tile, Fn&& run) {
   if constexpr (sizeof(T) == 2) {
-    if (tile == kTile64x512) return run(WideTile{});
     if (tile == kTile128x256) return run(FlatTile{});
     if (tile == kTile256x256) return run(Tile0{});
     if (tile == kTile256x128) return run(Tile1{});
@@ -809,7 +807,7 @@ hipError_t list_tokens(const Tokens& tokens, const Listed& list, hipStream_t str
 template <typename T, typename C, bool TAIL>
 hipError_t run_loss(const LogitsArgs<T>& a, int vocab, int pitch, float* own, Run* runs, hipStream_t stream) {
   static PerDeviceOnce once;
-  // the forward's list needs no `off`: the wide tiles' waves have just enough room
+  // the forward's list needs no `off`: the 128 x 256 tile leaves no more room
   constexpr size_t lds = C::LDS + LossOut<T>::template kBehind<C> + kOwnListBytes - 4 * kOwnListRows;
   static_assert(lds <= 160 * 1024, "one CU's LDS");
   int64_t groups = tiles_of<C>(a.g.M, a.g.N);

@@ -8,24 +8,34 @@ namespace moe {
 
 inline int rounded_up(int64_t v, int to) { return (int)((v + to - 1) / to * to); }
 
-// Tiles of logits for few rows, beside those of moe_linear_plan.h: wide ones, whose stages hold 32 or 64 KiB of W, so
-// that enough of it is on its way.  One forward over 2048 x 131072, us by rows:
-//               1     64    128    192    256    320    384    512   1024
-//   64 x 512    99     98    141    183    233    277    323    426    838
-//   128 x 256   99    103    104    157    163    220    227    289    549
-//   256 x 256  128    134    137    143    146    246    250    258    483
-//   256 x 128  141    148    154    159    161    279    283    290    551
-//   128 x 128 in two reduction groups, two stages   139 to 149 up to 128 rows
-// and the dx products of one piece of 131072 columns on 128 x 128 tiles, frozen head, 128 rows: two groups of two
-// stages 244 us the call, one of four 233.
-enum { kTile64x512 = kTiles, kTile128x256 };
-constexpr int kFewRows = 128;
+// The tile of logits for few rows, beside those of moe_linear_plan.h: a wide one, whose stages hold 32 KiB of W, so that
+// enough of it is on its way.  One forward, us by rows:
+//                          1     64    128    192    256    320    384    512
+//   2048 x 131072
+//     128 x 256          102    104    107    171    170    225    219    290
+//     256 x 256          141    154    144    139    153    250    245    255
+//     256 x 128          179    171    168    164    161    277    277    283
+//   2048 x 151936
+//     128 x 256          126    129    135    189    190    254    259    340
+//     256 x 256          173    176    176    182    186    287    299    300
+//     256 x 128          169    171    180    185    186    331    334    338
+//   4096 x 151552
+//     128 x 256          239    247    254    341    350    481    478    645
+//     256 x 256          322    328    335    335    347    545    549    565
+//   2048 x 65536
+//     128 x 256           57     59     59     83     84    120    115    149
+//     256 x 256           69     74     76     75     74    133    127    136
+//   1024 x 32000 (125 tiles a row of them: the estimate decides)
+//     128 x 256           27     30     30     32     33     48     48     51
+//     256 x 256           35     38     39     39     41     44     45     46
+// (A 64 x 512 tile took 100 us where 128 x 256 takes 102 at one row of 131072 columns, 153 against 126 at 151936.)
+enum { kTile128x256 = kTiles };
 
 struct VocabPlan {
   int logits;       // tile of the logits' products
   int piece;        // columns of a piece of the backward, a multiple of 512
   int pitch;        // rows of the statistics, of dz and of dx's sums
-  bool few;         // the gradients' products on the tiles for few rows
+  bool few;         // dx's products on the tiles for few rows
   Plan2 grads;
 };
 
@@ -36,8 +46,7 @@ constexpr int64_t kPieceElements = 64 << 20;
 inline int64_t group_count(int M, int N, int bm, int bn) { return (int64_t)((M + bm - 1) / bm) * ((N + bn - 1) / bn); }
 
 inline int logits_tile(int T, int N, int H, int esize) {
-  // the wide tiles where they fill the chip
-  if (esize == 2 && T <= 64 && group_count(T, N, 64, 512) >= kCus / 2) return kTile64x512;
+  // the wide tile where it fills the chip
   if (esize == 2 && group_count(T, N, 128, 256) >= kCus && (T <= 128 || (T > 256 && T <= 384))) return kTile128x256;
   int best_tile = 0;
   double best = -1.0;
@@ -62,11 +71,16 @@ inline VocabPlan make_vocab_plan(int T, int H, int V, int esize, bool dx, bool d
   p.logits = logits_tile(T, dx || dw ? p.piece : V, H, esize);
   if (!dx && !dw) return p;
   p.grads = plan_bwd(T, H, p.piece, esize, dx, dw, false);
-  p.few = esize == 2 && T <= kFewRows && group_count(H, p.piece, 128, 128) >= kCus;
-  if (p.few && dx) {  // as many slices as fill the chip
-    const int64_t slices = std::max<int64_t>(1, kCus / group_count(T, H, 128, 128));
-    p.grads.x.slice = rounded_up((p.piece + slices - 1) / slices, 128);
-    p.grads.x.slices = (p.piece + p.grads.x.slice - 1) / p.grads.x.slice;
+  // dx alone, of 65 to 128 rows: 128 x 128 tiles in one reduction group of four stages and as many slices as fill the
+  // chip, where those are long.  The call with and without, us: 128 rows, 2048 x 131072 (slices of 8192) 242 and 260,
+  // 2048 x 151936 289 and 303, 4096 x 151552 529 and 561, 2048 x 65536 (4096) 142 and 142, 1024 x 32000 (1024) 56 and 52;
+  // 64 rows of 2048 x 131072 215 and 210; with dW beside it 600 and 490.
+  const int64_t slices = std::max<int64_t>(1, kCus / group_count(T, H, 128, 128));
+  const int slice = rounded_up((p.piece + slices - 1) / slices, 128);
+  p.few = esize == 2 && dx && !dw && T > 64 && T <= 128 && slice >= 8192;
+  if (p.few) {
+    p.grads.x.slice = slice;
+    p.grads.x.slices = (p.piece + slice - 1) / slice;
   }
   return p;
 }

@@ -697,7 +697,7 @@ int moe_balance_loss_bwd(int T, int E, int k, int n_seq, int score, float alpha,
 
 /* Workspace (device bytes) of moe_vocab_loss_fwd and moe_vocab_loss_bwd: the list of
  * counted tokens, and the forward's row statistics (8 bytes for each token and run
- * of 32 to 512 columns) or the backward's piece of dz, its rows of x and the fp32
+ * of 32 to 256 columns) or the backward's piece of dz, its rows of x and the fp32
  * sums of dx.  A piece has as many columns as make 64 Mi elements with the tokens,
  * but 1024 at least: from 64 Ki tokens on, 1024 elements a token.  Host-only. */
 size_t moe_vocab_loss_workspace_bytes(int T, int H, int V, int dtype);

@@ -68,12 +68,31 @@ def test_plans_cover_the_vocabulary(plan):
 
 
 def test_the_tile_cases_reach_their_kernels(plan):
-    r = plan(*[v for c in CASES for v in (c.T, c.H, c.V, 3)])
-    for c, line in zip(CASES, r.stdout.splitlines()):
+    both, alone = (plan(*[v for c in CASES for v in (c.T, c.H, c.V, want)]).stdout.splitlines() for want in (3, 1))
+    assert len(both) == len(alone) == len(CASES)
+    for c, line, dx in zip(CASES, both, alone):
         loss, dz, pieces, few, pair, slices = map(int, line.split())
         bm, bn = TILES[c.loss]
-        assert (loss, -(-c.T // bm) * -(-c.V // bn), dz, pieces, bool(few), None if few else pair, slices) == \
-            (c.loss, c.tiles, c.dz, c.pieces, c.few, c.pair, c.slices), c
-    assert len(r.stdout.splitlines()) == len(CASES)
-    assert {c.loss for c in CASES if c.tiles > 256 and c.loss != 0} == {1, 6, 7}  # every streamed tile, twice a workgroup
+        assert (loss, -(-c.T // bm) * -(-c.V // bn), dz, pieces, few, pair, slices, bool(int(dx.split()[3]))) == \
+            (c.loss, c.tiles, c.loss, c.pieces, 0, c.pair, c.slices, c.few), c
+    assert {c.loss for c in CASES if c.tiles > 256 and c.loss != 0} == {1, 6}  # every streamed tile, twice a workgroup
     assert {c.pair for c in CASES} >= {0, 1, 2, 3} and {c.pair for c in CASES if c.pieces > 1} >= {0, 1}
+    assert sum(c.few for c in CASES) > 1
+
+
+def choice(plan, T, H, V, want):
+    """Tiles of the loss and of dz, and whether the products take the tiles for few rows."""
+    loss, dz, _, few, _, _ = map(int, plan(T, H, V, want).stdout.split())
+    return loss, dz, bool(few)
+
+
+def test_few_rows_by_what_was_measured(plan):
+    """The wide tile up to 128 rows and from 257 to 384 where it fills the chip, at vocabularies that divide over 256
+    workgroups or not; the few-row tiles for dx alone, of 65 to 128 rows and long slices, never with dW beside it."""
+    for H, V in ((2048, 131072), (2048, 151936), (4096, 151552), (2048, 65536)):
+        for T in (1, 64, 65, 128, 257, 384):
+            for want in (1, 2, 3):
+                assert choice(plan, T, H, V, want) == (6, 6, want == 1 and 65 <= T <= 128 and V > 65536), (T, H, V, want)
+        for T in (129, 256, 385, 512):
+            assert choice(plan, T, H, V, 1)[0] != 6 and not choice(plan, T, H, V, 1)[2], (T, H, V)
+    assert not choice(plan, 128, 1024, 32000, 1)[2]  # 32 slices of 1000 columns
