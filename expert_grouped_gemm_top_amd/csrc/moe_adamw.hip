@@ -504,9 +504,9 @@ hipError_t launch_adamw(const void* plan, const void* plan_device, const AdamwSt
   // 32-bit moments are bound by HBM, best with one small workgroup on a CU (151M weights with masters: 256 workgroups of
   // 256 threads 783 us or 5.4 TB/s, 512 827, 2048 840; 2M: 12.7, 14.8, 19.2, as workgroups queue up to say that they are
   // done).  The codes' arithmetic wants every SIMD full, by 256 workgroups of 1024 threads or, where the end counts for
-  // little, 2048 of 256 (with the moments read back, 2M weights 16.0 and 23.9 us, 8M 41.8 and 49.6, 32M 152 and 145,
-  // 151M 635 and 611).
-  constexpr int64_t kManyChunks = 8192;
+  // little, 2048 of 256 (2M bf16 weights 10.7 and 17.4 us, 8M 25.6 and 33.2, 24M 64.3 and 65.5, 32M 84 either way, 151M
+  // 388 and 369).
+  constexpr int64_t kManyChunks = 16384;
   auto of = [&](auto t, auto master) {
     using T = decltype(t);
     constexpr bool MASTER = decltype(master)::value;
