@@ -15,8 +15,8 @@
 // 0.02 is a tenth of half a bf16 step: rounded to nearest it would never come
 // about), and 8-bit moments (v moves by a thousandth of its distance to g^2, a
 // sixtieth of a code's half step: to nearest it would stand still).  So the
-// expected values are the exact ones, to 2^-32 of a bf16 step and 2^-16 of a
-// code's, but for v below its smallest code, which is raised to it.
+// expected values are the exact ones, to 2^-12 of what a weight moves by and 2^-16
+// of a code's step, but for v below its smallest code, which is raised to it.
 #include <algorithm>
 #include <cstring>
 #include <type_traits>
@@ -251,10 +251,14 @@ __device__ __forceinline__ float moved(float p, double decay, float u) {
 }
 // ... or, as bf16, up for the hash's share of what is left over: by an addition below the seven bits of mantissa, whose
 // carry rounds up.  In 64 bits, as fp32 would round to 2^-24 of p first, where p may go down by less (151M weights with
-// 8-bit moments 355 -> 370 us; with 32 bits HBM hides it, 620).
+// 8-bit moments 355 -> 380 to 387 us; with 32 bits HBM hides it, 620).  A share of 16 bits is up to 2^-24 of p off; where p
+// moves by less than 2^-12 of itself, beside which that would count, it has 32 (367 us where all have 32, but ordinary
+// steps keep to the 16 that the formula has for them).
 __device__ __forceinline__ uint32_t dithered(float p, double decay, float u, uint32_t r) {
   const double to = fma((double)p, 1.0 - decay, -(double)u);
-  const uint64_t share = (uint64_t)(r * 0x9e3779b1u) << 13;  // 52 - 7 - 32
+  const bool little = fabsf(fmaf(p, (float)decay, u)) < fabsf(p) * 0x1p-12f;
+  const uint32_t h = (r * 0x9e3779b1u) & (little ? 0xffffffffu : 0xffff0000u);
+  const uint64_t share = (uint64_t)h << 13;  // 52 - 7 - 32
   const uint64_t bits = ((uint64_t)__double_as_longlong(to) + share) >> 45 << 45;
   const uint32_t q = __float_as_uint((float)__longlong_as_double((long long)bits)) >> 16;
   return to != to ? 0x7fc0u : q;  // infinities stay: a share has none of their mantissa's bits
@@ -504,8 +508,8 @@ hipError_t launch_adamw(const void* plan, const void* plan_device, const AdamwSt
   // 32-bit moments are bound by HBM, best with one small workgroup on a CU (151M weights with masters: 256 workgroups of
   // 256 threads 783 us or 5.4 TB/s, 512 827, 2048 840; 2M: 12.7, 14.8, 19.2, as workgroups queue up to say that they are
   // done).  The codes' arithmetic wants every SIMD full, by 256 workgroups of 1024 threads or, where the end counts for
-  // little, 2048 of 256 (2M bf16 weights 10.7 and 17.4 us, 8M 25.6 and 33.2, 24M 64.3 and 65.5, 32M 84 either way, 151M
-  // 388 and 369).
+  // little, 2048 of 256 (2M bf16 weights 10.9 and 17.4 us, 8M 27.5 and 33.5, 24M 68 either way, 32M 89 and 87, 151M 408
+  // and 380).
   constexpr int64_t kManyChunks = 16384;
   auto of = [&](auto t, auto master) {
     using T = decltype(t);

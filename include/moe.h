@@ -775,7 +775,8 @@ int moe_adamw_plan(int n, const moe_adamw_tensor* tensors, int dtype, int state_
  * blocks of 256 begun by the tensors in front of it; with
  *   mix(x): x = (x ^ x >> 16) 0x85ebca77; x = (x ^ x >> 15) 0xc2b2ae3d; x ^ x >> 16
  *   r = mix(place ^ mix(mix(t) + seed))      (32 bits; places below 2^32)
- * a param goes up for the share (r 0x9e3779b1 mod 2^32) / 2^32 of a bf16 step, m's
+ * a param goes up for the share (h >> 16) / 2^16 of a bf16 step, h = r 0x9e3779b1
+ * mod 2^32, or h / 2^32 where it moves by less than 2^-12 of itself; m's
  * code for (r % 2^16 + 1/3) / 2^16 of its step, v's for (r >> 16 + 1/3) / 2^16.
  * Codes of 8 bits, times the block's scale, the smallest power of two that keeps
  * its largest value (as fp32) within 448 for m and 1.75 for v, from 2^-126 to

@@ -99,6 +99,25 @@ def test_shares_below_2_to_16_of_a_step():
         assert (t.param[torch.from_numpy(down).cuda()] == 1 - 2.0 ** -8).all()
 
 
+@pytest.mark.parametrize("shift,fine", [(11, False), (12, False), (14, True), (16, True)])
+def test_shares_of_16_and_of_32_bits(shift, fine):
+    """Weights of 1 that go down by 2^-shift and 2^-25 more: 2^(8 - shift) of a step of 2^-8, and 2^-17.  Of those whose
+    h >> 16 is at that border, half go down by 32 bits, and by 16 all or none."""
+    n, k = 1 << 24, 4
+    t = tensor(torch.ones(n, device="cuda"), torch.bfloat16, 32, False, 0.0, torch.ones(n, device="cuda"))
+    steps(t, 2.0 ** -shift + 2.0 ** -25, 1, seed=k)
+    h = (S.dither(0, n, 1, k) * np.uint64(0x9e3779b1) & np.uint64(0xffffffff)).astype(np.int64)
+    down, border = t.param.float().cpu().numpy() != 1, 1 << (24 - shift)
+    assert np.array_equal(down[h >> 16 != border], (h >> 16 < border)[h >> 16 != border])
+    at = h >> 16 == border
+    assert at.sum() > 100
+    if fine:  # the update is lr to 2^-20 of it
+        sure = at & (np.abs((h & 0xffff) - 2 ** 15) > 2.0 ** (32 + 8 - shift - 20) + 1)
+        assert np.array_equal(down[sure], ((h & 0xffff) < 2 ** 15)[sure]) and sure.sum() > 50
+    else:
+        assert down[at].all() or not down[at].any()
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("dtype,master", [(torch.float32, False), (torch.bfloat16, True), (torch.bfloat16, False)])
 @pytest.mark.parametrize("decay", [0.0, 0.1])
