@@ -250,10 +250,8 @@ __device__ __forceinline__ float moved(float p, double decay, float u) {
   return p - (__builtin_isinf(p) ? u : fmaf(p, (float)decay, u));
 }
 // ... or, as bf16, up for the hash's share of what is left over: by an addition below the seven bits of mantissa, whose
-// carry rounds up.  In 64 bits, as fp32 would round to 2^-24 of p first, where p may go down by less (151M weights with
-// 8-bit moments 355 -> 380 to 387 us; with 32 bits HBM hides it, 620).  A share of 16 bits is up to 2^-24 of p off; where p
-// moves by less than 2^-12 of itself, beside which that would count, it has 32 (367 us where all have 32, but ordinary
-// steps keep to the 16 that the formula has for them).
+// carry rounds up.  In 64 bits, as fp32 rounds to 2^-24 of p, where p may go down by less.  A share of 16 bits is up to
+// as much off; where p moves by less than 2^-12 of itself, beside which that would count, it has 32.
 __device__ __forceinline__ uint32_t dithered(float p, double decay, float u, uint32_t r) {
   const double to = fma((double)p, 1.0 - decay, -(double)u);
   const bool little = fabsf(fmaf(p, (float)decay, u)) < fabsf(p) * 0x1p-12f;
@@ -262,6 +260,27 @@ __device__ __forceinline__ uint32_t dithered(float p, double decay, float u, uin
   const uint64_t bits = ((uint64_t)__double_as_longlong(to) + share) >> 45 << 45;
   const uint32_t q = __float_as_uint((float)__longlong_as_double((long long)bits)) >> 16;
   return to != to ? 0x7fc0u : q;  // infinities stay: a share has none of their mantissa's bits
+}
+// Eight weights so.  fp32 and the upper 16 bits of the hash decide but where their sum is within four of a carry: fp32 is
+// off by a step and a half (1 - decay, and the difference), the lower bits by one, for weights that keep half their
+// size.  (One wave in sixteen has such a weight; 151M with 8-bit moments 352 -> 361 us, 385 with 64 bits everywhere;
+// with 32-bit moments HBM hides it, 620.)
+__device__ __forceinline__ void round8(const float (&p)[8], double decay, const float (&u)[8], const uint32_t (&r)[8],
+                                       uint32_t (&q)[8]) {
+  const float keep = (float)(1.0 - decay);
+  bool close[8], any = false;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float x = fmaf(p[j], keep, -u[j]);
+    const uint32_t sum = __float_as_uint(x) + ((r[j] * 0x9e3779b1u) >> 16);
+    close[j] = (uint16_t)(sum + 4) < 8;
+    any |= close[j];
+    q[j] = x != x ? 0x7fc0u : sum >> 16;
+  }
+  if (__ballot(any)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = close[j] ? dithered(p[j], decay, u[j], r[j]) : q[j];
+  }
 }
 
 // One pass over a chunk: eight elements a thread, from element `at` of tensor e on.
@@ -354,14 +373,14 @@ __device__ __forceinline__ void adamw_pass(const AdamwArgs& g, const Shared& sh,
     put8<FULL>((float*)e.param + at, live, p);
   } else {
     uint32_t q[8];
+    if constexpr (MASTER) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if constexpr (MASTER) {
+      for (int j = 0; j < 8; ++j) {
         p[j] = moved(p[j], decay, u[j]);
         q[j] = f2bf(p[j]);
-      } else {
-        q[j] = dithered(p[j], decay, u[j], r[j]);
       }
+    } else {
+      round8(p, decay, u, r, q);
     }
     if constexpr (MASTER) put8<FULL>(e.master + at, live, p);
     put_bits<FULL>((uint16_t*)e.param + at, live, q);
@@ -508,8 +527,8 @@ hipError_t launch_adamw(const void* plan, const void* plan_device, const AdamwSt
   // 32-bit moments are bound by HBM, best with one small workgroup on a CU (151M weights with masters: 256 workgroups of
   // 256 threads 783 us or 5.4 TB/s, 512 827, 2048 840; 2M: 12.7, 14.8, 19.2, as workgroups queue up to say that they are
   // done).  The codes' arithmetic wants every SIMD full, by 256 workgroups of 1024 threads or, where the end counts for
-  // little, 2048 of 256 (2M bf16 weights 10.9 and 17.4 us, 8M 27.5 and 33.5, 24M 68 either way, 32M 89 and 87, 151M 408
-  // and 380).
+  // little, 2048 of 256 (2M bf16 weights 10.7 and 17.5 us, 8M 26 and 33, 24M 64 either way, 32M 83.5 and 82, 151M 382 and
+  // 358).
   constexpr int64_t kManyChunks = 16384;
   auto of = [&](auto t, auto master) {
     using T = decltype(t);
